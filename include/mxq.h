@@ -43,7 +43,9 @@
  *     when an input element is Inf or NaN (outputs are then undefined),
  *     MXQ_DEV_WAIT_TIMEOUT when a bounded inter-CTA wait gave up (outputs
  *     are then undefined), MXQ_DEV_INVALID_SCALE when a caller-given global
- *     scale is negative or not finite (that group's outputs are undefined).  `status` may be NULL on the MX entry point
+ *     scale is negative or not finite (that group's outputs are undefined),
+ *     MXQ_DEV_INVALID_EXPERT when an expert id is not below the number of
+ *     experts (it is left out).  `status` may be NULL on the MX entry point
  *     only (the check is then skipped); elsewhere it is required.
  *   - Input bf16 data must be 16-byte aligned; code and scale outputs
  *     must be 16-byte aligned; fp32 / fp64 arrays naturally aligned.
@@ -104,11 +106,14 @@ typedef enum mxq_status {
 #define MXQ_DEV_NONFINITE_INPUT 0x1u
 #define MXQ_DEV_WAIT_TIMEOUT 0x2u
 #define MXQ_DEV_INVALID_SCALE 0x4u
+#define MXQ_DEV_INVALID_EXPERT 0x8u
 
 typedef enum mxq_fmt {
     MXQ_FMT_NVFP4 = 0,
     MXQ_FMT_MXFP4 = 1,
-    MXQ_FMT_MXFP8 = 2
+    MXQ_FMT_MXFP8 = 2,
+    MXQ_FMT_FP8_BLOCK = 3    /* E4M3 values, one fp32 scale per 128 x 128 block
+                                (mxq_moe_forward only) */
 } mxq_fmt;
 
 typedef enum mxq_scale_mode {
@@ -398,6 +403,73 @@ MXQ_API mxq_status mxq_dequant_relerr_noalloc(const uint16_t *x, const uint8_t *
                                               int64_t cols, int64_t tensors_per_scale,
                                               double *sum_sq_err, double *sum_sq_ref,
                                               double *relerr, cudaStream_t stream);
+
+/* Block-FP8 quantization: E4M3 values with one fp32 scale per brows x bcols
+ * block, the format mxq_requant_fp8_mx reads, mxq_gemm_fp8 multiplies and
+ * mxq_moe_forward takes as MXQ_FMT_FP8_BLOCK.
+ * Source: MJPansa/Qwen3.8-Flash-Next-MXFP4-FP8-R12, "Quantization format"
+ * (retained layers keep the source block-FP8 format; the block shape and the
+ * rounding are readings).
+ *   x       bf16 [rows, cols], cols % 16 == 0 (MXQ_ERR_SHAPE).
+ *   brows, bcols  1 x 128 (a token tile: a scale per token and 128 channels)
+ *           or 128 x 128 (weights); others MXQ_ERR_UNSUPPORTED.  The last
+ *           blocks of a row or column may be smaller.
+ *   codes   out, E4M3 bytes [rows, cols].
+ *   scales  out, fp32 [ceil(rows / brows), ceil(cols / 128)].
+ *   status  required (MXQ_DEV_NONFINITE_INPUT).
+ * scale = RN32(amax / 448) of the block; code = E4M3(RN32(x / scale)), round
+ * to nearest even, sign kept; a block of zeros has scale 0 and codes 0.  One
+ * read of x, no workspace.  A stack [E, rows, cols] whose rows are a multiple
+ * of brows may be passed as [E * rows, cols]. */
+MXQ_API mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows,
+                                    int64_t bcols, uint8_t *codes, float *scales, uint32_t *status,
+                                    cudaStream_t stream);
+
+/* Bytes of device workspace of mxq_moe_forward: fp32 [T * topk, inter] and
+ * [T * topk, hidden], each padded to 256 bytes (0 for sizes it refuses). */
+MXQ_API size_t mxq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t hidden, int64_t inter);
+
+/* A routed-expert layer for a few tokens over quantized weights:
+ *   y[t] = sum_j w[t,j] D_e (silu(G_e x_t) * (U_e x_t)),  e = ids[t,j],
+ * silu(a) = a / (1 + exp(-a)), with the experts' matrices as the quantizers
+ * write them (weight-only: activations are not quantized).
+ * Source: dabsLabs/Qwen3.8-Flash-Next-NVFP4, "What makes this build
+ * different" (stacked experts, fused gate_up, 16-bit activations);
+ * azampatti/Qwen3.8-Flash-Next-FP4-Local-AZ, "The shared expert" (silu of the
+ * gate times up); MJPansa/Qwen3.8-Flash-Next-MXFP4-FP8-R12, "Retained layers"
+ * (routed layers in MXFP4 or block FP8).
+ *   x        bf16 [T, hidden].
+ *   topk_ids int32 [T, topk]; an id below 0 stands for no expert (a token
+ *            whose ids are all negative gives a row of zeros); an id >=
+ *            experts sets MXQ_DEV_INVALID_EXPERT and counts as none.  The
+ *            same expert may appear twice; both weights count.
+ *   topk_weights fp32 [T, topk], used as given.
+ *   fmt      MXQ_FMT_NVFP4, MXQ_FMT_MXFP4, MXQ_FMT_MXFP8 or
+ *            MXQ_FMT_FP8_BLOCK, of both stacks.
+ *   gate_up_codes, gate_up_scales, gate_up_s2   the stack [experts, 2 inter,
+ *            hidden], gate rows first: codes and linear scales as
+ *            mxq_quantize_nvfp4 (one group per expert, with s2 [experts]),
+ *            mxq_quantize_mx, or mxq_quantize_fp8 with 128 x 128 blocks (fp32
+ *            scales) writes them; s2 is read for NVFP4 only.  16-byte aligned.
+ *   down_codes, down_scales, down_s2   the stack [experts, hidden, inter].
+ *   y        out, bf16 [T, hidden], 16-byte aligned.
+ *   status   required.  MXQ_DEV_NONFINITE_INPUT when a token that has an
+ *            expert holds Inf or NaN (that token's row is then undefined, the
+ *            others are not touched by it).  NaN codes or scales of a chosen
+ *            expert give NaN.
+ *   workspace at least mxq_moe_workspace_bytes(T, topk, hidden, inter).  Two
+ *            calls that overlap in time need one each.
+ * hidden and inter must be multiples of 128 (MXQ_ERR_SHAPE) and at most 8192,
+ * T * topk and T at most 2048, experts at most 4096 (MXQ_ERR_UNSUPPORTED).
+ * Sums are fp32 in a fixed order: repeated calls give the same bits. */
+MXQ_API mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden,
+                                   const int32_t *topk_ids, const float *topk_weights, int64_t topk,
+                                   mxq_fmt fmt, int64_t experts, int64_t inter,
+                                   const uint8_t *gate_up_codes, const void *gate_up_scales,
+                                   const float *gate_up_s2, const uint8_t *down_codes,
+                                   const void *down_scales, const float *down_s2, uint16_t *y,
+                                   uint32_t *status, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
 
 /* Zero a census (enqueued on `stream`).  census: device mxq_census. */
 MXQ_API mxq_status mxq_census_reset(mxq_census *census, cudaStream_t stream);

@@ -70,7 +70,7 @@ using namespace mxq;
 
 extern "C" {
 
-int mxq_version(void) { return 10200; }
+int mxq_version(void) { return 10300; }
 
 const char *mxq_status_string(mxq_status s)
 {
@@ -515,6 +515,119 @@ mxq_status mxq_dequant_relerr(const uint16_t *x, const uint8_t *codes, const uin
                                   tensors_per_scale < 1 ? 1 : tensors_per_scale,
                                   static_cast<double *>(workspace), sum_sq_err, sum_sq_ref, relerr, stream);
     return e == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows, int64_t bcols,
+                            uint8_t *codes, float *scales, uint32_t *status, cudaStream_t stream)
+{
+    const ApiRange range_("mxq_quantize_fp8");
+    if (rows < 0 || cols < 0 || brows < 1 || bcols < 1)
+        return MXQ_ERR_INVALID_ARG;
+    if (bcols != 128 || (brows != 1 && brows != 128))
+        return MXQ_ERR_UNSUPPORTED;
+    if (cols % 16 != 0)
+        return MXQ_ERR_SHAPE;
+    int64_t total;
+    if (!mul_ok(rows, cols, &total) || rows > 0xFFFFFF00ll || cols > 0xFFFFFF00ll)
+        return MXQ_ERR_SHAPE;
+    const int64_t nbr = (rows + brows - 1) / brows, nbc = (cols + 127) / 128;
+    int64_t blocks;
+    if (!mul_ok(nbr, nbc, &blocks) || blocks > (brows == 1 ? 0xFFFFFFFFll : 0x7FFFFFFFll))
+        return MXQ_ERR_SHAPE;   // the kernels index the blocks in 32 bits
+    if (total == 0)
+        return MXQ_OK;
+    if (!x || !codes || !scales || !status)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(status, 4))
+        return MXQ_ERR_ALIGN;
+    return launch_quantize_fp8(x, rows, cols, brows, codes, scales, status, stream) == cudaSuccess ? MXQ_OK
+                                                                                                : MXQ_ERR_CUDA;
+}
+
+// Sizes the layer kernels take; *h_bytes, *z_bytes: the two parts of the workspace.
+static mxq_status moe_sizes(int64_t T, int64_t topk, int64_t hidden, int64_t inter, size_t *h_bytes,
+                            size_t *z_bytes)
+{
+    if (T < 0 || topk < 0 || hidden < 0 || inter < 0)
+        return MXQ_ERR_INVALID_ARG;
+    if (hidden % 128 != 0 || inter % 128 != 0)
+        return MXQ_ERR_SHAPE;
+    int64_t a;
+    if (!mul_ok(T, topk, &a) || a > kMoeMaxAssignments || T > kMoeMaxAssignments || hidden > kMoeMaxWidth ||
+        inter > kMoeMaxWidth)
+        return MXQ_ERR_UNSUPPORTED;
+    *h_bytes = align_up((size_t)(a * inter) * sizeof(float), 256);
+    *z_bytes = align_up((size_t)(a * hidden) * sizeof(float), 256);
+    return MXQ_OK;
+}
+
+size_t mxq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t hidden, int64_t inter)
+{
+    size_t h, z;
+    return moe_sizes(T, topk, hidden, inter, &h, &z) == MXQ_OK ? h + z : 0;
+}
+
+mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const int32_t *topk_ids,
+                           const float *topk_weights, int64_t topk, mxq_fmt fmt, int64_t experts,
+                           int64_t inter, const uint8_t *gate_up_codes, const void *gate_up_scales,
+                           const float *gate_up_s2, const uint8_t *down_codes, const void *down_scales,
+                           const float *down_s2, uint16_t *y, uint32_t *status, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream)
+{
+    const ApiRange range_("mxq_moe_forward");
+    if (fmt != MXQ_FMT_NVFP4 && fmt != MXQ_FMT_MXFP4 && fmt != MXQ_FMT_MXFP8 && fmt != MXQ_FMT_FP8_BLOCK)
+        return MXQ_ERR_INVALID_ARG;
+    if (experts < 0)
+        return MXQ_ERR_INVALID_ARG;
+    size_t h_bytes, z_bytes;
+    const mxq_status st = moe_sizes(T, topk, hidden, inter, &h_bytes, &z_bytes);
+    if (st != MXQ_OK)
+        return st;
+    if (experts > kMoeMaxExperts)
+        return MXQ_ERR_UNSUPPORTED;
+    if (T == 0 || hidden == 0)
+        return MXQ_OK;
+    if (!y || !status)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(status, 4))
+        return MXQ_ERR_ALIGN;
+    if (topk == 0 || inter == 0)    // nothing to add up
+        return cudaMemsetAsync(y, 0, (size_t)(T * hidden) * sizeof(uint16_t), stream) == cudaSuccess ? MXQ_OK
+                                                                                                    : MXQ_ERR_CUDA;
+    if (!x || !topk_ids || !topk_weights)
+        return MXQ_ERR_INVALID_ARG;
+    const bool s2 = fmt == MXQ_FMT_NVFP4;
+    if (experts > 0 && (!gate_up_codes || !gate_up_scales || !down_codes || !down_scales ||
+                        (s2 && (!gate_up_s2 || !down_s2))))
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(gate_up_codes, 16) ||
+        !aligned(gate_up_scales, 16) || !aligned(down_codes, 16) || !aligned(down_scales, 16) ||
+        (s2 && (!aligned(gate_up_s2, 4) || !aligned(down_s2, 4))))
+        return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < h_bytes + z_bytes)
+        return MXQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return MXQ_ERR_ALIGN;
+    MoeLayer m;
+    m.x = x;
+    m.T = T;
+    m.hidden = hidden;
+    m.inter = inter;
+    m.topk = topk;
+    m.experts = experts;
+    m.ids = topk_ids;
+    m.weights = topk_weights;
+    m.gu_codes = gate_up_codes;
+    m.gu_scales = gate_up_scales;
+    m.gu_s2 = gate_up_s2;
+    m.dn_codes = down_codes;
+    m.dn_scales = down_scales;
+    m.dn_s2 = down_s2;
+    m.y = y;
+    m.status = status;
+    m.h = static_cast<float *>(workspace);
+    m.z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + h_bytes);
+    return launch_moe(m, (int)fmt, stream) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
 mxq_status mxq_census_reset(mxq_census *census, cudaStream_t stream)

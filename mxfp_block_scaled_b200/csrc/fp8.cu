@@ -1,0 +1,164 @@
+// fp8.cu -- block-FP8 quantization: E4M3 values with one fp32 scale per
+// 1 x 128 (token tiles) or 128 x 128 (weights) block (sm_100a).
+//
+// Method (the format mxq_requant_fp8_mx reads): scale = RN32(amax / 448),
+// code = E4M3(RN32(x / scale)), round to nearest even, saturating; a block
+// whose amax is 0 has scale 0 and codes 0.  amax of a non-zero bf16 block is
+// at least 2^-133, so its scale is never rounded to 0.
+//
+// Both kernels read x once into registers, so HBM is the bound: 2 B in,
+// 1 B out and a scale per block.  The quotient is a correctly rounded
+// reciprocal of the scale and one FMA correction (div2_bf16) while the scale
+// lies in [2^-60, 2^60]; there the quotient is the IEEE one, except where it
+// is so small (below 2^-60) that its code is a signed 0 either way.  Outside
+// that range the IEEE division is called.
+#include "mxq_device.cuh"
+#include "mxq_internal.h"
+#include "mxq.h"
+
+namespace mxq {
+
+// Eight bf16 (four words) of a block with scale d and reciprocal r -> eight
+// E4M3 codes.
+__device__ __forceinline__ uint2 fp8_codes8(const uint4 &v, float d, float r, bool mid)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+    if (mid) {
+        const float2 dd = make_float2(d, d), nr = make_float2(-r, -r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = div2_bf16(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), dd, nr);
+            h[i] = e4m3x2(y.x, y.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = d > 0.0f ? e4m3x2(__fdiv_rn(bf16_lo(w[i]), d), __fdiv_rn(bf16_hi(w[i]), d)) : 0u;
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+__device__ __forceinline__ uint32_t absmax8(const uint4 &v)
+{
+    uint32_t m = absmax_bf16x2(0u, v.x);
+    m = absmax_bf16x2(m, v.y);
+    m = absmax_bf16x2(m, v.z);
+    return fold_halves(absmax_bf16x2(m, v.w));
+}
+
+// Scale of a block from the bits of its amax; r is its reciprocal where mid.
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits, float &r, bool &mid)
+{
+    const float d = __fdiv_rn(__uint_as_float(amax_bits << 16), 448.0f);
+    mid = d >= 0x1p-60f && d <= 0x1p60f;
+    r = mid ? rcp_rn_mid(d) : 0.0f;
+    return d;
+}
+
+// 1 x 128 blocks: 16 lanes of 8 values hold one; a thread keeps kRowUnroll
+// blocks in flight.
+constexpr int kRowUnroll = 4;
+
+__global__ void __launch_bounds__(256)
+fp8_row_kernel(const uint16_t *__restrict__ x, uint32_t nblk, uint32_t cols, const FastDiv nbc,
+               uint8_t *__restrict__ codes, float *__restrict__ scales, uint32_t *__restrict__ status)
+{
+    const uint32_t half = (blockIdx.x * 256u + threadIdx.x) >> 4, l8 = (threadIdx.x & 15u) * 8u;
+    const uint32_t nhalf = gridDim.x * 16u;
+    uint32_t bad = 0;
+    // every lane of a warp runs the same iterations (the reductions below
+    // name all 32 lanes); blocks past the end hold zeros and are not stored
+    for (uint64_t b0 = half & ~1u; b0 < nblk; b0 += (uint64_t)nhalf * kRowUnroll) {
+        uint4 v[kRowUnroll];
+        uint64_t at[kRowUnroll];
+        bool in[kRowUnroll];
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; ++u) {
+            const uint64_t b = b0 + (half & 1u) + (uint64_t)u * nhalf;
+            const uint32_t row = fastdiv((uint32_t)b, nbc), c = ((uint32_t)b - row * nbc.d) * 128u + l8;
+            in[u] = b < nblk && c < cols;
+            at[u] = (uint64_t)row * cols + c;
+            v[u] = in[u] ? __ldg(reinterpret_cast<const uint4 *>(x + at[u])) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; ++u) {
+            uint32_t m = absmax8(v[u]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            bad |= m >= 0x7F80u;
+            float r;
+            bool mid;
+            const float d = fp8_scale(m, r, mid);
+            if (in[u]) {
+                *reinterpret_cast<uint2 *>(codes + at[u]) = fp8_codes8(v[u], d, r, mid);
+                if (l8 == 0)
+                    scales[b0 + (half & 1u) + (uint64_t)u * nhalf] = d;
+            }
+        }
+    }
+    if (bad)
+        atomicOr(status, MXQ_DEV_NONFINITE_INPUT);
+}
+
+// 128 x 128 blocks: one CTA of 256 threads holds one in registers (64 values
+// a thread), so x is read once although the amax spans 128 rows.
+__global__ void __launch_bounds__(256)
+fp8_block_kernel(const uint16_t *__restrict__ x, uint32_t rows, uint32_t cols, uint32_t nbc,
+                 uint8_t *__restrict__ codes, float *__restrict__ scales, uint32_t *__restrict__ status)
+{
+    __shared__ uint32_t part[8];
+    const uint32_t br = blockIdx.x / nbc, bc = blockIdx.x - br * nbc;
+    const uint32_t c = bc * 128u + (threadIdx.x & 15u) * 8u, r0 = br * 128u + (threadIdx.x >> 4);
+    uint4 v[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = r0 + 16u * i < rows && c < cols
+                   ? __ldg(reinterpret_cast<const uint4 *>(x + (uint64_t)(r0 + 16u * i) * cols + c))
+                   : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, absmax8(v[i]));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31u) == 0)
+        part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, part[i]);
+    float r;
+    bool mid;
+    const float d = fp8_scale(m, r, mid);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (r0 + 16u * i < rows && c < cols)
+            *reinterpret_cast<uint2 *>(codes + (uint64_t)(r0 + 16u * i) * cols + c) = fp8_codes8(v[i], d, r, mid);
+    if (threadIdx.x == 0) {
+        scales[blockIdx.x] = d;
+        if (m >= 0x7F80u)
+            atomicOr(status, MXQ_DEV_NONFINITE_INPUT);
+    }
+}
+
+cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows, uint8_t *codes,
+                                float *scales, uint32_t *status, cudaStream_t s)
+{
+    const uint32_t nbc = (uint32_t)((cols + 127) / 128);
+    if (brows == 1) {
+        const uint64_t nblk = (uint64_t)rows * nbc;
+        uint64_t grid = (nblk + 16 * kRowUnroll - 1) / (16 * kRowUnroll);
+        if (nblk <= 148 * 16)   // few blocks: one each, no thread waits for four
+            grid = (nblk + 15) / 16;
+        fp8_row_kernel<<<(unsigned)grid, 256, 0, s>>>(x, (uint32_t)nblk, (uint32_t)cols, make_fastdiv(nbc), codes,
+                                                      scales, status);
+    } else {
+        const uint64_t grid = (uint64_t)((rows + 127) / 128) * nbc;
+        fp8_block_kernel<<<(unsigned)grid, 256, 0, s>>>(x, (uint32_t)rows, (uint32_t)cols, nbc, codes, scales,
+                                                        status);
+    }
+    return cudaGetLastError();
+}
+
+} // namespace mxq

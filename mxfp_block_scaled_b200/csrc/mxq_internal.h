@@ -116,6 +116,27 @@ cudaError_t launch_requant_fp8_mx(const uint8_t *fp8, const float *bscale, int64
                                   int64_t brows, int64_t bcols, int fmt, uint8_t *codes,
                                   uint8_t *scales, const ScaleLayout &sl, uint32_t *status,
                                   cudaStream_t s);
+// Block-FP8 quantization; rows * ceil(cols / 128) < 2^32, brows 1 or 128.
+cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows, uint8_t *codes,
+                                float *scales, uint32_t *status, cudaStream_t s);
+
+// Mixture-of-experts layer for a few tokens.
+constexpr int64_t kMoeMaxAssignments = 2048;   // T * topk
+constexpr int64_t kMoeMaxWidth = 8192;         // hidden, inter
+constexpr int64_t kMoeMaxExperts = 4096;       // their counts fit the activation rows' space
+struct MoeLayer {
+    const uint16_t *x;
+    int64_t T, hidden, inter, topk, experts;
+    const int32_t *ids;
+    const float *weights;
+    const uint8_t *gu_codes, *dn_codes;
+    const void *gu_scales, *dn_scales;
+    const float *gu_s2, *dn_s2;
+    uint16_t *y;
+    uint32_t *status;
+    float *h, *z;               // workspace: fp32 [T * topk, inter], [T * topk, hidden]
+};
+cudaError_t launch_moe(const MoeLayer &m, int fmt, cudaStream_t s);
 cudaError_t launch_census_add(mxq_census *c, int64_t n_tensors, const double *err, const double *ref,
                               const double *rel, const double *err_rtn, int64_t n_groups, const uint32_t *m4,
                               int64_t blocks_per_group, cudaStream_t s);

@@ -24,8 +24,9 @@ STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "shape", 3: "align", 4: "work
 DEV_NONFINITE_INPUT = 0x1
 DEV_WAIT_TIMEOUT = 0x2
 DEV_INVALID_SCALE = 0x4
+DEV_INVALID_EXPERT = 0x8
 
-FMT = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
+FMT = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2, "fp8_block": 3}
 SCALE_MODE = {"rtn": 0, "four_six": 1}
 LAYOUT = {"linear": 0, "swizzled_128x4": 1}
 OP = {"quantize_nvfp4": 0, "quantize_act": 1, "dequant_relerr": 2}
@@ -33,7 +34,8 @@ OP = {"quantize_nvfp4": 0, "quantize_act": 1, "dequant_relerr": 2}
 EXPORTED = ("mxq_version", "mxq_status_string", "mxq_scale_bytes", "mxq_workspace_bytes",
             "mxq_quantize_nvfp4", "mxq_global_scale_nvfp4", "mxq_quantize_nvfp4_s2", "mxq_quantize_nvfp4_weighted",
             "mxq_quantize_mx", "mxq_requant_fp8_mx", "mxq_quantize_act", "mxq_dequant_relerr",
-            "mxq_dequant_relerr_noalloc", "mxq_census_reset", "mxq_census_add")
+            "mxq_dequant_relerr_noalloc", "mxq_census_reset", "mxq_census_add", "mxq_quantize_fp8",
+            "mxq_moe_workspace_bytes", "mxq_moe_forward")
 
 # Fields of struct mxq_census (include/mxq.h), in order, each 8 bytes.
 CENSUS_FIELDS = ("sum_relerr", "max_relerr", "sum_sq_err", "sum_sq_ref", "sum_sq_err_rtn",
@@ -93,6 +95,13 @@ def load(path=LIB_PATH):
                                      vp]
     L.mxq_dequant_relerr_noalloc.restype = i32
     L.mxq_dequant_relerr_noalloc.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp]
+    L.mxq_quantize_fp8.restype = i32
+    L.mxq_quantize_fp8.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp]
+    L.mxq_moe_workspace_bytes.restype = sz
+    L.mxq_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.mxq_moe_forward.restype = i32
+    L.mxq_moe_forward.argtypes = [vp, i64, i64, vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp,
+                                  vp, sz, vp]
     L.mxq_test_stall_next_single_pass.restype = None
     L.mxq_test_stall_next_single_pass.argtypes = [i32]
     if path == LIB_PATH:
@@ -315,6 +324,58 @@ def mxq_dequant_relerr_noalloc(x, codes, scales, s2, fmt, n_tensors, rows, cols,
     _check("mxq_dequant_relerr_noalloc", rc)
 
 
+# The layer operators run on the device of their first tensor, whichever is
+# current, and refuse buffers that lie on different ones.
+def _buf(name, t, nbytes, dev):
+    _need(name, t, nbytes)
+    if t is not None and t.device != dev:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+    return _p(t)
+
+
+def _launch(name, dev, args, stream):
+    fn = getattr(load(), name)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    else:
+        rc = fn(*args, _stream(stream))
+    _check(name, rc)
+
+
+def mxq_quantize_fp8(x, rows, cols, brows, bcols, codes, scales, status, stream=None):
+    dev, n = x.device, rows * cols
+    nblk = -(-rows // brows) * -(-cols // bcols) if brows > 0 and bcols > 0 else 0
+    _launch("mxq_quantize_fp8", dev,
+            (_buf("x", x, 2 * n, dev), rows, cols, brows, bcols, _buf("codes", codes, n, dev),
+             _buf("scales", scales, 4 * nblk, dev), _buf("status", status, 4, dev)), stream)
+
+
+def moe_weight_bytes(fmt, experts, rows, cols):
+    """(codes, scales) bytes of a stack [experts, rows, cols] as mxq_moe_forward reads it."""
+    n = experts * rows * cols
+    if fmt == "fp8_block":
+        return n, 4 * experts * -(-rows // 128) * -(-cols // 128)
+    return _code_bytes(fmt, n), n // (16 if fmt == "nvfp4" else 32)
+
+
+def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, inter, gate_up_codes,
+                    gate_up_scales, gate_up_s2, down_codes, down_scales, down_s2, y, status, workspace,
+                    stream=None):
+    dev = x.device
+    gc, gs = moe_weight_bytes(fmt, experts, 2 * inter, hidden)
+    dc, ds = moe_weight_bytes(fmt, experts, hidden, inter)
+    s2 = 4 * experts if fmt == "nvfp4" else 0
+    _launch("mxq_moe_forward", dev,
+            (_buf("x", x, 2 * T * hidden, dev), T, hidden, _buf("topk_ids", topk_ids, 4 * T * topk, dev),
+             _buf("topk_weights", topk_weights, 4 * T * topk, dev), topk, FMT[fmt], experts, inter,
+             _buf("gate_up_codes", gate_up_codes, gc, dev), _buf("gate_up_scales", gate_up_scales, gs, dev),
+             _buf("gate_up_s2", gate_up_s2, s2, dev), _buf("down_codes", down_codes, dc, dev),
+             _buf("down_scales", down_scales, ds, dev), _buf("down_s2", down_s2, s2, dev),
+             _buf("y", y, 2 * T * hidden, dev), _buf("status", status, 4, dev),
+             _buf("workspace", workspace, 0, dev), _nbytes(workspace)), stream)
+
+
 # ------------------------------------------------------------ allocating --
 def _bf16(x):
     if x.dtype != torch.bfloat16 or not x.is_contiguous():
@@ -461,6 +522,74 @@ def requant_fp8_mx(fp8, bscale, brows, bcols, fmt, stream=None, layout="linear")
     }
     mxq_requant_fp8_mx(fp8, bscale, R, C, brows, bcols, fmt, layout, out["codes"], out["scales"],
                        out["status"], stream)
+    return out
+
+
+def quantize_fp8(x, brows=1, stream=None):
+    """x: bf16 [..., C], quantized as one [rows, C] matrix to E4M3 with one
+    fp32 scale per brows x 128 block (1: token tiles, 128: weights).  Returns
+    dict codes [..., C] u8, scales [ceil(rows/brows), ceil(C/128)] f32 (a stack
+    [E, R, C] of weights with R a multiple of 128: [E, R/128, ceil(C/128)]),
+    status."""
+    _bf16(x)
+    C = x.shape[-1]
+    R = x.numel() // C if C else 0
+    lead = (-(-R // brows),)
+    if x.dim() == 3 and brows == 128 and x.shape[1] % 128 == 0:
+        lead = (x.shape[0], x.shape[1] // 128)
+    dev = x.device
+    out = {
+        "codes": torch.empty(x.shape, dtype=torch.uint8, device=dev),
+        "scales": torch.empty(lead + (-(-C // 128),), dtype=torch.float32, device=dev),
+        "status": torch.zeros(1, dtype=torch.int32, device=dev),
+    }
+    mxq_quantize_fp8(x, R, C, brows, 128, out["codes"], out["scales"], out["status"], stream)
+    return out
+
+
+def moe_workspace(T, topk, hidden, inter, device="cuda"):
+    """A workspace for mxq_moe_forward at these sizes, to keep from call to call."""
+    return torch.empty(max(load().mxq_moe_workspace_bytes(T, topk, hidden, inter), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _typed(name, t, dtype, shape):
+    if t is None or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("expected %s as contiguous %s %s" % (name, dtype, list(shape)))
+    return t
+
+
+def moe_forward(x, topk_ids, topk_weights, gate_up, down, fmt, stream=None):
+    """A routed-expert layer for a few tokens.  x: bf16 [T, H]; topk_ids int32
+    and topk_weights fp32 [T, k] (an id below 0: no expert); gate_up, down:
+    dicts with codes, scales (and s2 for "nvfp4") of the stacks [E, 2I, H] and
+    [E, H, I], as quantize_nvfp4, quantize_mx or quantize_fp8 with brows=128
+    (fmt "fp8_block") return them with linear scales.  Returns dict y bf16
+    [T, H], status."""
+    _bf16(x)
+    T, H = x.shape
+    E = gate_up["codes"].shape[0]
+    I = gate_up["codes"].shape[1] // 2
+    k = topk_ids.shape[1]
+    _typed("topk_ids", topk_ids, torch.int32, (T, k))
+    _typed("topk_weights", topk_weights, torch.float32, (T, k))
+    per = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32, "fp8_block": 128}[fmt]
+    for name, q, rows, cols in (("gate_up", gate_up, 2 * I, H), ("down", down, H, I)):
+        _typed(name + " codes", q["codes"], torch.uint8,
+               (E, rows, cols // 2 if fmt in ("nvfp4", "mxfp4") else cols))
+        if fmt == "fp8_block":
+            _typed(name + " scales", q["scales"], torch.float32, (E, rows // per, cols // per))
+        else:
+            _typed(name + " scales", q["scales"], torch.uint8, (E, rows, cols // per))
+        if fmt == "nvfp4":
+            _typed(name + " s2", q["s2"], torch.float32, (E,))
+    dev = x.device
+    out = {"y": torch.empty((T, H), dtype=torch.bfloat16, device=dev),
+           "status": torch.zeros(1, dtype=torch.int32, device=dev)}
+    mxq_moe_forward(x, T, H, topk_ids, topk_weights, k, fmt, E, I, gate_up["codes"], gate_up["scales"],
+                    gate_up.get("s2") if fmt == "nvfp4" else None, down["codes"], down["scales"],
+                    down.get("s2") if fmt == "nvfp4" else None, out["y"], out["status"],
+                    moe_workspace(T, k, H, I, dev), stream)
     return out
 
 
