@@ -126,6 +126,11 @@ typedef enum mxq_layout {
     MXQ_LAYOUT_SWIZZLED_128X4 = 1   /* 128 x 4 tiles, see the conventions */
 } mxq_layout;
 
+typedef enum mxq_out {
+    MXQ_OUT_BF16 = 0,
+    MXQ_OUT_F32 = 1
+} mxq_out;
+
 typedef enum mxq_op {
     MXQ_OP_QUANTIZE_NVFP4 = 0,
     MXQ_OP_QUANTIZE_ACT = 1,
@@ -424,6 +429,27 @@ MXQ_API mxq_status mxq_dequant_relerr_noalloc(const uint16_t *x, const uint8_t *
 MXQ_API mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows,
                                     int64_t bcols, uint8_t *codes, float *scales, uint32_t *status,
                                     cudaStream_t stream);
+
+/* Product of block-FP8 matrices, c = a b^T with both operands dequantized:
+ *   c[m, n] = sum_kb a_scales[m, kb] b_scales[n / 128, kb]
+ *             sum_{k in block kb} E4M3(a[m, k]) E4M3(b[n, k]).
+ * Source: MJPansa/Qwen3.8-Flash-Next-MXFP4-FP8-R12, "Quantization format"
+ * (retained layers keep block FP8 and run on quantized activations; the
+ * activation blocks and the order of the sums are readings).
+ *   a, a_scales   E4M3 [M, K] and fp32 [M, ceil(K / 128)]: a token tile as
+ *            mxq_quantize_fp8 with 1 x 128 blocks writes it.
+ *   b, b_scales   E4M3 [N, K] and fp32 [ceil(N / 128), ceil(K / 128)]: a
+ *            weight matrix [out, in] with 128 x 128 blocks.
+ *   K        a multiple of 16 (MXQ_ERR_SHAPE); a, b and c 16-byte aligned.
+ *   out, c   MXQ_OUT_BF16 or MXQ_OUT_F32, out, [M, N].
+ *   status   required (MXQ_DEV_WAIT_TIMEOUT).
+ * Products are exact; their sums and the scaled sums of the blocks are fp32,
+ * in an order that does not depend on scheduling (repeated calls give the
+ * same bits; the order differs between small and large M).  A NaN code makes
+ * its row or column NaN.  No workspace. */
+MXQ_API mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b,
+                                const float *b_scales, int64_t M, int64_t N, int64_t K, mxq_out out,
+                                void *c, uint32_t *status, cudaStream_t stream);
 
 /* Bytes of device workspace of mxq_moe_forward: fp32 [T * topk, inter] and
  * [T * topk, hidden], each padded to 256 bytes (0 for sizes it refuses). */

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxq.so")
 SOURCES = ["api.cu", "nvfp4.cu", "weighted.cu", "mx.cu", "verify.cu", "noalloc.cu",
-           "fp8.cu", "moe.cu"]
+           "fp8.cu", "gemm.cu", "moe.cu"]
 HEADERS = ["mxq_device.cuh", "mxq_internal.h", "nvfp4_block.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

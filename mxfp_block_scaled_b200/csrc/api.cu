@@ -29,6 +29,16 @@ static size_t verify_workspace_bytes(int64_t n_tensors, int64_t rows, int64_t co
     return align_up((size_t)(n_tensors * cpt) * 2 * sizeof(double), 256);
 }
 
+// Status of a launch.  The runtime keeps a failed call's error until it is
+// asked for; taken here, it does not turn up in a later call.
+static mxq_status launched(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return MXQ_OK;
+    (void)cudaGetLastError();
+    return MXQ_ERR_CUDA;
+}
+
 static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 static bool layout_ok(mxq_layout l) { return l == MXQ_LAYOUT_LINEAR || l == MXQ_LAYOUT_SWIZZLED_128X4; }
@@ -540,8 +550,46 @@ mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64
         return MXQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(status, 4))
         return MXQ_ERR_ALIGN;
-    return launch_quantize_fp8(x, rows, cols, brows, codes, scales, status, stream) == cudaSuccess ? MXQ_OK
-                                                                                                : MXQ_ERR_CUDA;
+    return launched(launch_quantize_fp8(x, rows, cols, brows, codes, scales, status, stream));
+}
+
+mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b, const float *b_scales,
+                        int64_t M, int64_t N, int64_t K, mxq_out out, void *c, uint32_t *status,
+                        cudaStream_t stream)
+{
+    const ApiRange range_("mxq_gemm_fp8");
+    if (M < 0 || N < 0 || K < 0 || (out != MXQ_OUT_BF16 && out != MXQ_OUT_F32))
+        return MXQ_ERR_INVALID_ARG;
+    if (K % 16 != 0)
+        return MXQ_ERR_SHAPE;
+    const int64_t kMax = 0x7FFFFF00ll;      // rows, columns and values are indexed in 32 bits
+    int64_t mn, mk, nk;
+    if (M > kMax || N > kMax || K > kMax || !mul_ok(M, N, &mn) || !mul_ok(M, K, &mk) || !mul_ok(N, K, &nk) ||
+        ((M + 127) / 128) * ((N + 63) / 64) > kMax || (M + 7) / 8 > kMax)
+        return MXQ_ERR_SHAPE;
+    if (mn == 0)
+        return MXQ_OK;
+    if (!c || !status)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(c, 16) || !aligned(status, 4))
+        return MXQ_ERR_ALIGN;
+    if (K == 0)                             // an empty sum
+        return launched(cudaMemsetAsync(c, 0, (size_t)mn * (out == MXQ_OUT_F32 ? 4 : 2), stream));
+    if (!a || !a_scales || !b || !b_scales)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4))
+        return MXQ_ERR_ALIGN;
+    GemmArgs g;
+    g.a = a;
+    g.b = b;
+    g.sa = a_scales;
+    g.sb = b_scales;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.c = c;
+    g.status = status;
+    return launched(launch_gemm_fp8(g, out == MXQ_OUT_F32, stream));
 }
 
 // Sizes the layer kernels take; *h_bytes, *z_bytes: the two parts of the workspace.
@@ -592,8 +640,7 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     if (!aligned(y, 16) || !aligned(status, 4))
         return MXQ_ERR_ALIGN;
     if (topk == 0 || inter == 0)    // nothing to add up
-        return cudaMemsetAsync(y, 0, (size_t)(T * hidden) * sizeof(uint16_t), stream) == cudaSuccess ? MXQ_OK
-                                                                                                    : MXQ_ERR_CUDA;
+        return launched(cudaMemsetAsync(y, 0, (size_t)(T * hidden) * sizeof(uint16_t), stream));
     if (!x || !topk_ids || !topk_weights)
         return MXQ_ERR_INVALID_ARG;
     const bool s2 = fmt == MXQ_FMT_NVFP4;
@@ -627,7 +674,7 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     m.status = status;
     m.h = static_cast<float *>(workspace);
     m.z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + h_bytes);
-    return launch_moe(m, (int)fmt, stream) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+    return launched(launch_moe(m, (int)fmt, stream));
 }
 
 mxq_status mxq_census_reset(mxq_census *census, cudaStream_t stream)

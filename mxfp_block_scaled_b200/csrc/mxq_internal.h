@@ -120,6 +120,16 @@ cudaError_t launch_requant_fp8_mx(const uint8_t *fp8, const float *bscale, int64
 cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, int64_t brows, uint8_t *codes,
                                 float *scales, uint32_t *status, cudaStream_t s);
 
+// Product of block-FP8 matrices, M, N, K >= 1, K % 16 == 0.
+struct GemmArgs {
+    const uint8_t *a, *b;
+    const float *sa, *sb;
+    int64_t M, N, K;
+    void *c;
+    uint32_t *status;
+};
+cudaError_t launch_gemm_fp8(const GemmArgs &g, int out_f32, cudaStream_t s);
+
 // Mixture-of-experts layer for a few tokens.
 constexpr int64_t kMoeMaxAssignments = 2048;   // T * topk
 constexpr int64_t kMoeMaxWidth = 8192;         // hidden, inter

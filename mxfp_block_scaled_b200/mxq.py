@@ -29,13 +29,14 @@ DEV_INVALID_EXPERT = 0x8
 FMT = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2, "fp8_block": 3}
 SCALE_MODE = {"rtn": 0, "four_six": 1}
 LAYOUT = {"linear": 0, "swizzled_128x4": 1}
+OUT = {"bf16": 0, "f32": 1}
 OP = {"quantize_nvfp4": 0, "quantize_act": 1, "dequant_relerr": 2}
 
 EXPORTED = ("mxq_version", "mxq_status_string", "mxq_scale_bytes", "mxq_workspace_bytes",
             "mxq_quantize_nvfp4", "mxq_global_scale_nvfp4", "mxq_quantize_nvfp4_s2", "mxq_quantize_nvfp4_weighted",
             "mxq_quantize_mx", "mxq_requant_fp8_mx", "mxq_quantize_act", "mxq_dequant_relerr",
             "mxq_dequant_relerr_noalloc", "mxq_census_reset", "mxq_census_add", "mxq_quantize_fp8",
-            "mxq_moe_workspace_bytes", "mxq_moe_forward")
+            "mxq_gemm_fp8", "mxq_moe_workspace_bytes", "mxq_moe_forward")
 
 # Fields of struct mxq_census (include/mxq.h), in order, each 8 bytes.
 CENSUS_FIELDS = ("sum_relerr", "max_relerr", "sum_sq_err", "sum_sq_ref", "sum_sq_err_rtn",
@@ -97,6 +98,8 @@ def load(path=LIB_PATH):
     L.mxq_dequant_relerr_noalloc.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp]
     L.mxq_quantize_fp8.restype = i32
     L.mxq_quantize_fp8.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp]
+    L.mxq_gemm_fp8.restype = i32
+    L.mxq_gemm_fp8.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, vp]
     L.mxq_moe_workspace_bytes.restype = sz
     L.mxq_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
     L.mxq_moe_forward.restype = i32
@@ -351,6 +354,14 @@ def mxq_quantize_fp8(x, rows, cols, brows, bcols, codes, scales, status, stream=
              _buf("scales", scales, 4 * nblk, dev), _buf("status", status, 4, dev)), stream)
 
 
+def mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, c, status, stream=None):
+    dev, kb = a.device, -(-K // 128)
+    _launch("mxq_gemm_fp8", dev,
+            (_buf("a", a, M * K, dev), _buf("a_scales", a_scales, 4 * M * kb, dev), _buf("b", b, N * K, dev),
+             _buf("b_scales", b_scales, 4 * -(-N // 128) * kb, dev), M, N, K, OUT[out],
+             _buf("c", c, M * N * (4 if out == "f32" else 2), dev), _buf("status", status, 4, dev)), stream)
+
+
 def moe_weight_bytes(fmt, experts, rows, cols):
     """(codes, scales) bytes of a stack [experts, rows, cols] as mxq_moe_forward reads it."""
     n = experts * rows * cols
@@ -545,6 +556,24 @@ def quantize_fp8(x, brows=1, stream=None):
     }
     mxq_quantize_fp8(x, R, C, brows, 128, out["codes"], out["scales"], out["status"], stream)
     return out
+
+
+def gemm_fp8(a, a_scales, b, b_scales, out="bf16", stream=None):
+    """c = a b^T of block-FP8 matrices.  a: uint8 E4M3 codes [M, K] with fp32
+    scales [M, ceil(K/128)] (quantize_fp8 of a token tile); b: codes [N, K]
+    with scales [ceil(N/128), ceil(K/128)] (brows=128).  Returns dict c [M, N]
+    (bf16, or fp32 for out="f32"), status."""
+    M, K = a.shape
+    N = b.shape[0]
+    kb = -(-K // 128)
+    _typed("a", a, torch.uint8, (M, K))
+    _typed("a_scales", a_scales, torch.float32, (M, kb))
+    _typed("b", b, torch.uint8, (N, K))
+    _typed("b_scales", b_scales, torch.float32, (-(-N // 128), kb))
+    res = {"c": torch.empty((M, N), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=a.device),
+           "status": torch.zeros(1, dtype=torch.int32, device=a.device)}
+    mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, res["c"], res["status"], stream)
+    return res
 
 
 def moe_workspace(T, topk, hidden, inter, device="cuda"):
