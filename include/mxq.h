@@ -452,7 +452,8 @@ MXQ_API mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const u
                                 void *c, uint32_t *status, cudaStream_t stream);
 
 /* Bytes of device workspace of mxq_moe_forward: fp32 [T * topk, inter] and
- * [T * topk, hidden], each padded to 256 bytes (0 for sizes it refuses). */
+ * [T * topk, hidden], each padded to 256 bytes (0 for sizes it refuses).
+ * Nothing in it needs to start at zero. */
 MXQ_API size_t mxq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t hidden, int64_t inter);
 
 /* A routed-expert layer for a few tokens over quantized weights:

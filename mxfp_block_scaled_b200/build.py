@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxq.so")
 SOURCES = ["api.cu", "nvfp4.cu", "weighted.cu", "mx.cu", "verify.cu", "noalloc.cu",
            "fp8.cu", "gemm.cu", "moe.cu"]
-HEADERS = ["mxq_device.cuh", "mxq_internal.h", "nvfp4_block.cuh"]
+HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_tma.cuh", "nvfp4_block.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 # No --use_fast_math: denormals are kept and every division / reciprocal

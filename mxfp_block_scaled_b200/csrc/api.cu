@@ -625,7 +625,7 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     const ApiRange range_("mxq_moe_forward");
     if (fmt != MXQ_FMT_NVFP4 && fmt != MXQ_FMT_MXFP4 && fmt != MXQ_FMT_MXFP8 && fmt != MXQ_FMT_FP8_BLOCK)
         return MXQ_ERR_INVALID_ARG;
-    if (experts < 0)
+    if (experts < 1)
         return MXQ_ERR_INVALID_ARG;
     size_t h_bytes, z_bytes;
     const mxq_status st = moe_sizes(T, topk, hidden, inter, &h_bytes, &z_bytes);
@@ -644,8 +644,7 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     if (!x || !topk_ids || !topk_weights)
         return MXQ_ERR_INVALID_ARG;
     const bool s2 = fmt == MXQ_FMT_NVFP4;
-    if (experts > 0 && (!gate_up_codes || !gate_up_scales || !down_codes || !down_scales ||
-                        (s2 && (!gate_up_s2 || !down_s2))))
+    if (!gate_up_codes || !gate_up_scales || !down_codes || !down_scales || (s2 && (!gate_up_s2 || !down_s2)))
         return MXQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(gate_up_codes, 16) ||
         !aligned(gate_up_scales, 16) || !aligned(down_codes, 16) || !aligned(down_scales, 16) ||
@@ -672,8 +671,9 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     m.dn_s2 = down_s2;
     m.y = y;
     m.status = status;
-    m.h = static_cast<float *>(workspace);
-    m.z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + h_bytes);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    m.h = reinterpret_cast<float *>(ws);
+    m.z = reinterpret_cast<float *>(ws + h_bytes);
     return launched(launch_moe(m, (int)fmt, stream));
 }
 

@@ -32,8 +32,7 @@
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq.h"
-
-#include <cuda.h>
+#include "mxq_tma.cuh"
 
 namespace mxq {
 
@@ -176,12 +175,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, TileBar
     return false;
 }
 
-__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-                 ::"r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
-}
-
 // Shared-memory descriptor of a K-major operand tile, rows of 128 bytes with
 // the 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
@@ -320,8 +313,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                         break;
                     char *dst = smem + s * T::bytes;
                     mbar_arrive_expect_tx(&bars.full[s], T::bytes);
-                    tma_load(dst, &ma, kb * 128u, m * 128u, &bars.full[s]);
-                    tma_load(dst + 128 * 128, &mb, kb * 128u, n * BN, &bars.full[s]);
+                    tma_load_2d(dst, &ma, kb * 128u, m * 128u, &bars.full[s]);
+                    tma_load_2d(dst + 128 * 128, &mb, kb * 128u, n * BN, &bars.full[s]);
                     if (++s == T::stages) {
                         s = 0;
                         ph ^= 1u;
@@ -461,41 +454,13 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
 
 namespace {
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder of tensor maps (the library links the runtime only).
-EncodeFn encode_fn()
-{
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-}
-
-// Row-major [rows, K] bytes in boxes of 128 bytes by box_rows rows.
-bool make_map(EncodeFn f, CUtensorMap *m, const uint8_t *p, uint64_t rows, uint64_t K, uint32_t box_rows)
-{
-    const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
-    const cuuint32_t box[2] = {128, box_rows}, step[2] = {1, 1};
-    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int BN, typename Out>
 cudaError_t run_tile(const GemmArgs &g, int sms, cudaStream_t s)
 {
     using T = Tile<BN>;
-    static EncodeFn encode = encode_fn();     // a function of the driver, the same for every device
-    if (!encode)
-        return cudaErrorNotSupported;
     CUtensorMap ma, mb;
-    if (!make_map(encode, &ma, g.a, (uint64_t)g.M, (uint64_t)g.K, 128) ||
-        !make_map(encode, &mb, g.b, (uint64_t)g.N, (uint64_t)g.K, BN))
+    if (!make_byte_map(&ma, g.a, (uint64_t)g.M, (uint64_t)g.K, 128) ||
+        !make_byte_map(&mb, g.b, (uint64_t)g.N, (uint64_t)g.K, BN))
         return cudaErrorInvalidValue;
     TileArgs p;
     p.sa = g.sa;

@@ -20,16 +20,17 @@
 //
 // moe_kernel.  One CTA of 16 warps per SM.  Every CTA builds the list of
 // chosen experts itself (at most 2048 assignments).  An expert's assignments
-// are cut into groups of at most 8; a task is 16 weight rows (gate_up: 8 gate
-// rows and the same 8 up rows, so the activation is local to a thread) of one
-// group, over the whole length K; a CTA takes a contiguous run of tasks, so
-// it reads contiguous rows and needs the activations of few groups.
+// are cut into groups of at most 8 (4 in very wide layers); a task is 16 weight
+// rows (gate_up: 8 gate rows and the same 8 up rows, so the activation is local
+// to a thread) of one group, over the whole length K; a CTA takes a contiguous
+// run of tasks, so it reads contiguous rows and needs the activations of few
+// groups.
 //
 // Weights.  A warp streams its tasks through its own ring of chunks (16 rows
-// of 128 bytes of codes and their scales) in shared memory with cp.async, so
-// no warp waits for another one's data; with few tasks 2, 4, ... warps split K
-// and add their sums in a fixed order.  The 16-byte pieces of a row are
-// permuted (xor) so that the fragment loads have no bank conflicts.
+// of 256 bytes of codes and their scales) in shared memory with cp.async, so
+// no warp waits for another one's data; with few tasks 2, 4 or 8 warps split K
+// and add their sums in a fixed order.  Rows are padded so that the fragment
+// loads have no bank conflicts.
 //
 // Product.  mma.sync m16n8k16 with f16 operands and fp32 sums: 16 weight rows
 // by 8 assignments.  Few columns are filled, and the tensor pipe is idle most
@@ -55,9 +56,14 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCodeBytes = 16 * 128;             // codes of one chunk
-constexpr int kSlotBytes = kCodeBytes + 256;     // and its scales
-constexpr int kGroup = 8;                        // assignments of a group (columns of the product)
+// One chunk in shared memory: 16 rows of 256 bytes of codes, then the rows'
+// scales.  With rows 272 bytes apart a fragment load (one word of each lane
+// from 8 rows) touches every bank once; so do the scales, 48 bytes apart.
+constexpr int kChunkBytes = 256;
+constexpr int kPitch = kChunkBytes + 16;
+constexpr int kScaleAt = 16 * kPitch;
+constexpr int kScalePitch = 48;
+constexpr int kSlotBytes = kScaleAt + 16 * kScalePitch;
 
 struct MoeArgs {
     const uint16_t *x;          // gate_up: bf16 tokens [T, K]
@@ -74,9 +80,11 @@ struct MoeArgs {
     uint32_t row_bytes;         // codes of one row
     uint32_t row_scales;        // scales of one row (bytes); block-FP8: of one row of blocks
     uint32_t A, topk, E, K;
+    uint32_t group;             // assignments of a group: 8, or 4 where 8 rows do not fit the stage
     uint32_t nrows;             // rows of an output: I or H
     uint32_t tiles;             // tasks of a group
     uint32_t chunks;            // chunks of a row
+    uint32_t ks;                // warps that share a task
     uint32_t cap;               // activation rows the stage holds
     uint32_t xstride;           // bytes of a staged row
     FastDiv tilesdiv, topkdiv;
@@ -85,12 +93,11 @@ struct MoeArgs {
 template <int FMT>
 struct Fmt {
     static constexpr bool fp4 = FMT == MXQ_FMT_NVFP4 || FMT == MXQ_FMT_MXFP4;
-    static constexpr int chunk_k = fp4 ? 256 : 128;                       // values of a row in a chunk
-    // scale bytes of a row in a chunk
-    static constexpr int sbytes = FMT == MXQ_FMT_NVFP4 ? 16 : FMT == MXQ_FMT_MXFP4 ? 8 : 4;
-    // 4-bit fragments take one word of each of 8 rows at one piece, 8-bit
-    // ones two words of each of 4 rows at two pieces
-    static __device__ __forceinline__ uint32_t swz(uint32_t row) { return fp4 ? (row & 7u) : (row & 3u) << 1; }
+    static constexpr int group_bytes = fp4 ? 64 : 128;                    // of 128 codes of a row
+    static constexpr int chunk_k = 128 * kChunkBytes / group_bytes;       // values of a row in a chunk
+    // scale bytes of 128 values of a row, and the bytes a lane copies at a time
+    static constexpr int sbytes = FMT == MXQ_FMT_NVFP4 ? 8 : 4;
+    static constexpr int schunk = sbytes * (kChunkBytes / group_bytes);   // of a chunk
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src)
@@ -123,15 +130,54 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// UE8M0 byte -> fp32 2^(b - 127); 255 is NaN.
-__device__ __forceinline__ float ue8m0(uint32_t b)
+// Four UE8M0 bytes -> fp32 2^(b - 127) (255 is NaN), through bf16, which
+// holds them all.
+__device__ __forceinline__ void ue8m0x4(uint32_t w, float (&d)[4])
 {
-    const uint32_t bits = b ? b << 23 : 0x00400000u;
-    return __uint_as_float(b == 255u ? 0x7FC00000u : bits);
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    d[0] = bf16_lo(lo);
+    d[1] = bf16_hi(lo);
+    d[2] = bf16_lo(hi);
+    d[3] = bf16_hi(hi);
+}
+
+// The four bytes of `w` (eight E2M1 codes) -> four f16x2 values, exact; the
+// bytes are named inside one asm so that no shift is spent on them.
+__device__ __forceinline__ void e2m1x8_unpack(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// Four E4M3 codes -> two f16x2, exact.
+__device__ __forceinline__ void e4m3x4_unpack(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// The low half of an f16x2 in both halves (an operand selector, no instruction).
+__device__ __forceinline__ uint32_t low2(uint32_t h)
+{
+    const __half2 r = __low2half2(*reinterpret_cast<const __half2 *>(&h));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The chosen experts.  list: assignments sorted by expert; group g holds
-// list[start[g] .. start[g + 1]) of expert expert[g], at most kGroup of them.
+// list[start[g] .. start[g + 1]) of expert expert[g], at most MoeArgs::group.
 struct Route {
     uint16_t *list, *start, *expert;
     uint32_t groups;
@@ -149,7 +195,7 @@ __device__ __forceinline__ uint32_t route_warp(const MoeArgs &a, const Route &r,
     const uint32_t n = __popc(peers), rank = __popc(peers & below);
     const bool lead = id >= 0 && rank == 0;
     // exclusive sums over the leaders below: groups (high half), assignments
-    uint32_t v = lead ? (((n + kGroup - 1) / kGroup) << 16) | n : 0u;
+    uint32_t v = lead ? (((n + a.group - 1) / a.group) << 16) | n : 0u;
     const uint32_t own = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -161,9 +207,9 @@ __device__ __forceinline__ uint32_t route_warp(const MoeArgs &a, const Route &r,
     const uint32_t base = __shfl_sync(0xFFFFFFFFu, v - own, __ffs(peers) - 1);
     if (id >= 0) {
         r.list[(base & 0xFFFFu) + rank] = (uint16_t)lane;
-        if (rank % kGroup == 0) {
-            r.start[(base >> 16) + rank / kGroup] = (uint16_t)((base & 0xFFFFu) + rank);
-            r.expert[(base >> 16) + rank / kGroup] = (uint16_t)id;
+        if (rank % a.group == 0) {
+            r.start[(base >> 16) + rank / a.group] = (uint16_t)((base & 0xFFFFu) + rank);
+            r.expert[(base >> 16) + rank / a.group] = (uint16_t)id;
         }
     }
     if (lane == 0)
@@ -171,28 +217,34 @@ __device__ __forceinline__ uint32_t route_warp(const MoeArgs &a, const Route &r,
     return total >> 16;
 }
 
-// More: counts per expert in shared memory (E words at `cnt`), a scan, and a
-// scatter by the first warp, 32 assignments at a time in their order: an
-// expert's groups have to be the same in every CTA.  The list is complete at
-// the next barrier of the CTA; groups and experts are at the return.
+// More: ids, then counts and places of the experts in shared memory (E words
+// at `cnt`), a scan, and a scatter.  The order of a group's assignments is
+// free (each is a column of its own), but an expert's groups have to be the
+// same in every CTA, so the list of an expert with more than one is put in
+// ascending order.
 __device__ __forceinline__ uint32_t route_block(const MoeArgs &a, const Route &r, uint32_t *cnt, uint32_t *wsum)
 {
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    for (uint32_t e = tid; e < a.E; e += kThreads)
-        cnt[e] = 0u;
-    __syncthreads();
+    constexpr uint32_t none = 0xFFFFu;
+    uint16_t *ids = reinterpret_cast<uint16_t *>(cnt + a.E);
     for (uint32_t i = tid; i < a.A; i += kThreads) {
         const int id = a.ids[i];
         if (id >= (int)a.E)
             atomicOr(a.status, MXQ_DEV_INVALID_EXPERT);
-        else if (id >= 0)
-            atomicAdd(&cnt[id], 1u);
+        ids[i] = (uint16_t)(id >= 0 && id < (int)a.E ? (uint32_t)id : none);
     }
+    for (uint32_t e = tid; e < a.E; e += kThreads)
+        cnt[e] = 0u;
     __syncthreads();
+    for (uint32_t i = tid; i < a.A; i += kThreads)
+        if (ids[i] != none)
+            atomicAdd(&cnt[ids[i]], 1u);
+    __syncthreads();
+    // groups (high half) and assignments of the experts below
     const uint32_t per = (a.E + kThreads - 1) / kThreads, e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
     uint32_t own = 0;
     for (uint32_t e = e0; e < e1; ++e)
-        own += (((cnt[e] + kGroup - 1) / kGroup) << 16) | cnt[e];
+        own += (((cnt[e] + a.group - 1) / a.group) << 16) | cnt[e];
     uint32_t v = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -204,40 +256,55 @@ __device__ __forceinline__ uint32_t route_block(const MoeArgs &a, const Route &r
         wsum[warp] = v;
     __syncthreads();
     uint32_t total = 0;
+#pragma unroll
     for (uint32_t i = 0; i < kWarps; ++i) {
         if (i < warp)
             v += wsum[i];
         total += wsum[i];
     }
     v -= own;
+    bool more = false;
     for (uint32_t e = e0; e < e1; ++e) {
         const uint32_t n = cnt[e];
-        cnt[e] = v & 0xFFFFu;
-        for (uint32_t i = 0; i < n; i += kGroup) {
+        cnt[e] = (n << 16) | (v & 0xFFFFu);
+        more |= n > a.group;
+        for (uint32_t i = 0; i < n; i += a.group) {
             r.start[v >> 16] = (uint16_t)(v & 0xFFFFu);
             r.expert[v >> 16] = (uint16_t)e;
-            v += (1u << 16) + min(n - i, (uint32_t)kGroup);
+            v += (1u << 16) + min(n - i, a.group);
         }
     }
     if (tid == 0)
         r.start[total >> 16] = (uint16_t)(total & 0xFFFFu);
+    more = __syncthreads_or(more);
+    for (uint32_t i = tid; i < a.A; i += kThreads)
+        if (ids[i] != none)
+            r.list[atomicAdd(&cnt[ids[i]], 1u) & 0xFFFFu] = (uint16_t)i;
     __syncthreads();
-    if (warp == 0)
-        for (uint32_t i = lane; i < ((a.A + 31u) & ~31u); i += 32u) {
-            int id = i < a.A ? a.ids[i] : -1;
-            if (id >= (int)a.E)
-                id = -1;
-            const uint32_t peers = __match_any_sync(0xFFFFFFFFu, id), rank = __popc(peers & ((1u << lane) - 1u));
-            uint32_t at = 0;
-            if (id >= 0) {
-                at = cnt[id];
-                r.list[at + rank] = (uint16_t)i;
+    if (more) {
+        constexpr int most = (int)((kMoeMaxAssignments + kThreads - 1) / kThreads);
+        uint32_t val[most], to[most];
+#pragma unroll
+        for (int k = 0; k < most; ++k) {
+            const uint32_t pos = tid + k * kThreads;
+            to[k] = none;
+            if (pos < (total & 0xFFFFu)) {
+                val[k] = r.list[pos];
+                const uint32_t c = cnt[ids[val[k]]], n = c >> 16, end = c & 0xFFFFu;    // past its last place now
+                if (n > a.group) {
+                    to[k] = end - n;
+                    for (uint32_t j = end - n; j < end; ++j)
+                        to[k] += r.list[j] < val[k];
+                }
             }
-            __syncwarp();
-            if (id >= 0 && rank == 0)
-                cnt[id] = at + __popc(peers);
-            __syncwarp();
         }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < most; ++k)
+            if (to[k] != none)
+                r.list[to[k]] = (uint16_t)val[k];
+        __syncthreads();
+    }
     return total >> 16;
 }
 
@@ -258,14 +325,26 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Where four values lie in a staged row.  4-bit formats: in order; a lane's
+// word holds 8 codes.  8-bit formats: a lane has one word (4 codes) of two
+// neighbouring pieces, so of every 32 values the quads 0, 4, 1, 5, ... follow
+// one another.
+template <int FMT>
+__device__ __forceinline__ uint32_t staged(uint32_t k)
+{
+    const uint32_t q = (k >> 2) & 7u;
+    return Fmt<FMT>::fp4 ? k * 2u : ((k & ~31u) + ((q & 3u) * 2u + (q >> 2)) * 4u) * 2u;
+}
+
 // One warp: row `a` of the activations -> f16 at `dst`, its inverse factor
 // returned.
-template <bool GATE_UP>
+template <int FMT, bool GATE_UP>
 __device__ __forceinline__ float stage_row(const MoeArgs &g, uint32_t a, char *dst, uint32_t lane)
 {
     uint32_t m = 0;
     if (GATE_UP) {
         const uint16_t *src = g.x + (uint64_t)fastdiv(a, g.topkdiv) * g.K;
+#pragma unroll 8
         for (uint32_t k = lane * 8u; k < g.K; k += 256u) {
             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + k));
             uint32_t q = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, v.x), v.y), v.z), v.w);
@@ -275,6 +354,7 @@ __device__ __forceinline__ float stage_row(const MoeArgs &g, uint32_t a, char *d
         if (m >= 0x7F800000u && lane == 0)
             atomicOr(g.status, MXQ_DEV_NONFINITE_INPUT);
         const float f = row_factor(m);
+#pragma unroll 8
         for (uint32_t k = lane * 8u; k < g.K; k += 256u) {
             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + k));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -282,11 +362,17 @@ __device__ __forceinline__ float stage_row(const MoeArgs &g, uint32_t a, char *d
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 h[i] = half2_bits(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
-            *reinterpret_cast<uint4 *>(dst + k * 2u) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (Fmt<FMT>::fp4)
+                *reinterpret_cast<uint4 *>(dst + k * 2u) = make_uint4(h[0], h[1], h[2], h[3]);
+            else {
+                *reinterpret_cast<uint2 *>(dst + staged<FMT>(k)) = make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2 *>(dst + staged<FMT>(k + 4u)) = make_uint2(h[2], h[3]);
+            }
         }
         return 1.0f / f;
     }
     const float *src = g.hin + (uint64_t)a * g.K;
+#pragma unroll 6
     for (uint32_t k = lane * 4u; k < g.K; k += 128u) {
         const float4 v = *reinterpret_cast<const float4 *>(src + k);
         m = max(max(m, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
@@ -294,9 +380,10 @@ __device__ __forceinline__ float stage_row(const MoeArgs &g, uint32_t a, char *d
     }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     const float f = row_factor(m >= 0x7F800000u ? 0u : m);
+#pragma unroll 6
     for (uint32_t k = lane * 4u; k < g.K; k += 128u) {
         const float4 v = *reinterpret_cast<const float4 *>(src + k);
-        *reinterpret_cast<uint2 *>(dst + k * 2u) =
+        *reinterpret_cast<uint2 *>(dst + staged<FMT>(k)) =
             make_uint2(half2_bits(v.x * f, v.y * f), half2_bits(v.z * f, v.w * f));
     }
     return 1.0f / f;
@@ -323,7 +410,7 @@ moe_kernel(const MoeArgs a)
     // shared memory: rings, activation rows, row factors, lists, partial sums
     char *ring = smem + warp * (D * kSlotBytes);
     char *xs = smem + kWarps * D * kSlotBytes;
-    float *xf = reinterpret_cast<float *>(xs + a.cap * a.xstride);
+    float *xf = reinterpret_cast<float *>(xs + (a.cap + 1u) * a.xstride);
     float *part = xf + ((a.cap + 3u) & ~3u);
     Route r;
     r.list = reinterpret_cast<uint16_t *>(part + kWarps * 128);
@@ -339,22 +426,22 @@ moe_kernel(const MoeArgs a)
         r.groups = groups_s;
     } else
         r.groups = route_block(a, r, reinterpret_cast<uint32_t *>(xs), wsum);
+    for (uint32_t k = tid * 16u; k < a.xstride; k += kThreads * 16u)
+        *reinterpret_cast<uint4 *>(xs + a.cap * a.xstride + k) = make_uint4(0u, 0u, 0u, 0u);
     // this CTA's run of tasks
     const uint32_t ntask = r.groups * a.tiles;
     const uint32_t t0 = (uint32_t)((uint64_t)ntask * blockIdx.x / gridDim.x);
     const uint32_t t1 = (uint32_t)((uint64_t)ntask * (blockIdx.x + 1) / gridDim.x);
-    // warps that share a task: doubled while every warp of the grid still gets
-    // at most one and each has a chunk
-    uint32_t ks = 1;
-    while (ks * 2u <= kWarps && ks * 2u <= a.chunks && (uint64_t)ntask * ks * 2u <= (uint64_t)gridDim.x * kWarps)
-        ks *= 2u;
-    const uint32_t teams = kWarps / ks, team = warp / ks, q = warp - team * ks;
+    const uint32_t ks = a.ks, teams = kWarps / ks, team = warp / ks, q = warp - team * ks;
     const uint32_t c0 = a.chunks * q / ks, c1 = a.chunks * (q + 1) / ks;
 
     const uint32_t half = GATE_UP ? a.nrows : 8u;    // distance of the second 8 rows from the first
     const uint32_t tile_rows = GATE_UP ? 8u : 16u;
-    const uint32_t piece = lane & 7u;
+    const uint32_t piece = lane & 7u, half8 = (t4 >> 1) * 8u;
     const uint32_t ring_s = smem_addr(ring);
+    // scale pieces of a row: 4 (4-bit formats: the lanes cover 8 rows, twice) or 2
+    constexpr uint32_t spieces = F::fp4 ? 4 : 2;
+    const uint32_t srow = lane / spieces, spiece = lane % spieces;
     Walk p;
     p.task = t0 + team;
     p.ch = c0;
@@ -363,39 +450,41 @@ moe_kernel(const MoeArgs a)
         const uint32_t r0 = tile * tile_rows;
         p.code = a.codes + e * a.expert_bytes + (uint64_t)(r0 + (lane >> 3)) * a.row_bytes + piece * 16u;
         const char *se = static_cast<const char *>(a.scales) + e * a.expert_scales;
-        if (FMT == MXQ_FMT_FP8_BLOCK)      // lanes 0, 1: the block rows of the two halves
-            p.scale = se + (uint64_t)((r0 + (lane & 1u) * half) >> 7) * a.row_scales;
-        else {
-            // fp4: two lanes a row, half of its bytes each; MXFP8: one lane a row
-            const uint32_t row = F::fp4 ? lane >> 1 : lane & 15u;
-            p.scale = se + (uint64_t)(r0 + (row & 7u) + (row >> 3) * half) * a.row_scales +
-                      (F::fp4 ? (lane & 1u) * (F::sbytes / 2) : 0u);
-        }
+        if (FMT == MXQ_FMT_FP8_BLOCK)      // lanes 0-1 and 2-3: the block rows of the two halves
+            p.scale = se + (uint64_t)((r0 + ((lane >> 1) & 1u) * half) >> 7) * a.row_scales;
+        else                               // pieces of sbytes, spieces to a row
+            p.scale = se + (uint64_t)(r0 + (srow & 7u) + (srow >> 3) * half) * a.row_scales;
     };
+    const uint32_t code_dst = ring_s + (lane >> 3) * kPitch + piece * 16u;
+    const uint32_t scale_dst = ring_s + kScaleAt + (FMT == MXQ_FMT_FP8_BLOCK ? (lane >> 1) * 8u : srow) * kScalePitch +
+                               spiece * F::sbytes;
+    const uint64_t r4 = 4ull * a.row_bytes, hb = (uint64_t)half * a.row_bytes;
+    const uint64_t s8 = (uint64_t)half * a.row_scales;
     auto issue = [&](uint32_t slot) {
         if (p.task < t1) {
-            const uint32_t dst = ring_s + slot * kSlotBytes, off = p.ch * 128u, row = lane >> 3;
-            if (off + piece * 16u < a.row_bytes) {
-                const uint8_t *s = p.code + off;
-                const uint64_t r4 = 4ull * a.row_bytes, hb = (uint64_t)half * a.row_bytes;
-                // row + 4 i: its swizzle, too, follows from the row
-                cp16(dst + row * 128u + ((piece ^ F::swz(row)) << 4), s);
-                cp16(dst + (row + 4u) * 128u + ((piece ^ F::swz(row + 4u)) << 4), s + r4);
-                cp16(dst + (row + 8u) * 128u + ((piece ^ F::swz(row)) << 4), s + hb);
-                cp16(dst + (row + 12u) * 128u + ((piece ^ F::swz(row + 4u)) << 4), s + hb + r4);
+            const uint32_t dst = code_dst + slot * kSlotBytes, sd = scale_dst + slot * kSlotBytes;
+            const uint32_t left = a.row_bytes - p.ch * kChunkBytes;      // of the row, from this chunk on
+            const uint8_t *q0 = p.code + p.ch * kChunkBytes, *q1 = q0 + r4, *q2 = q0 + hb, *q3 = q2 + r4;
+            if (piece * 16u < left) {
+                cp16(dst, q0);
+                cp16(dst + 4 * kPitch, q1);
+                cp16(dst + 8 * kPitch, q2);
+                cp16(dst + 12 * kPitch, q3);
             }
-            const uint32_t sd = dst + kCodeBytes;
-            if (FMT == MXQ_FMT_NVFP4) {
-                if (p.ch * 16u + (lane & 1u) * 8u < a.row_scales)
-                    cp_small<8>(sd + lane * 8u, p.scale + p.ch * 16u);
-            } else if (FMT == MXQ_FMT_MXFP4) {
-                if (p.ch * 8u + (lane & 1u) * 4u < a.row_scales)
-                    cp_small<4>(sd + lane * 4u, p.scale + p.ch * 8u);
-            } else if (FMT == MXQ_FMT_MXFP8) {
-                if (lane < 16u)
-                    cp_small<4>(sd + lane * 4u, p.scale + p.ch * 4u);
-            } else if (lane < 2u)
-                cp_small<4>(sd + lane * 4u, p.scale + p.ch * 4u);
+            if (piece * 16u + 128u < left) {
+                cp16(dst + 128, q0 + 128);
+                cp16(dst + 4 * kPitch + 128, q1 + 128);
+                cp16(dst + 8 * kPitch + 128, q2 + 128);
+                cp16(dst + 12 * kPitch + 128, q3 + 128);
+            }
+            const char *s = p.scale + p.ch * F::schunk + spiece * F::sbytes;
+            if (spiece * F::group_bytes < left) {
+                if (F::fp4) {                       // rows 0-7, rows 8-15
+                    cp_small<F::sbytes>(sd, s);
+                    cp_small<F::sbytes>(sd + 8 * kScalePitch, s + s8);
+                } else if (FMT == MXQ_FMT_MXFP8 || lane < 4u)
+                    cp_small<4>(sd, s);
+            }
             if (++p.ch == c1) {
                 p.ch = c0;
                 p.task += teams;
@@ -407,9 +496,8 @@ moe_kernel(const MoeArgs a)
     };
     if (p.task < t1)
         locate();
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i)
-        issue(i);
+    if (D == 2)
+        issue(0);
     if (!GATE_UP)
         cudaGridDependencySynchronize();     // h is written by the launch before
     cudaTriggerProgrammaticLaunchCompletion();
@@ -425,7 +513,7 @@ moe_kernel(const MoeArgs a)
         const uint32_t end = min(t1, gl * a.tiles), nr = (uint32_t)r.start[gl] - row0;
         __syncthreads();
         for (uint32_t i = warp; i < nr; i += kWarps) {
-            const float f = stage_row<GATE_UP>(a, r.list[row0 + i], xs + i * a.xstride, lane);
+            const float f = stage_row<FMT, GATE_UP>(a, r.list[row0 + i], xs + i * a.xstride, lane);
             if (lane == 0)
                 xf[i] = f;
         }
@@ -433,106 +521,87 @@ moe_kernel(const MoeArgs a)
         for (; task < end; task += teams) {
             const uint32_t grp = fastdiv(task, a.tilesdiv), tile = task - grp * a.tiles;
             const uint32_t first = r.start[grp], cnt = r.start[grp + 1] - first;
-            const bool col = g8 < cnt;
-            const char *xrow = xs + (first - row0 + (col ? g8 : 0u)) * a.xstride + t4 * 16u;
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            // columns without an assignment read the row of zeros
+            const char *xrow = xs + (g8 < cnt ? first - row0 + g8 : a.cap) * a.xstride + t4 * 16u;
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, acc2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (uint32_t ch = c0; ch < c1; ++ch) {
-                cp_wait<D - 2>();
-                __syncwarp();
-                issue(slot == 0 ? D - 1 : slot - 1);     // the slot read in the step before
-                const char *base = ring + slot * kSlotBytes, *sb = base + kCodeBytes;
-                slot = slot == D - 1 ? 0 : slot + 1;
+                if (D == 1) {
+                    __syncwarp();
+                    issue(0);
+                    cp_wait<0>();
+                    __syncwarp();
+                } else {
+                    cp_wait<0>();
+                    __syncwarp();
+                    issue(slot ^ 1u);            // the slot read in the step before
+                }
+                // this lane's words of rows g8 and g8 + 8, and their scales
+                const char *cw = ring + slot * kSlotBytes + g8 * kPitch + t4 * 4u;
+                const char *sb = ring + slot * kSlotBytes + kScaleAt +
+                                 (FMT == MXQ_FMT_FP8_BLOCK ? 0u : g8 * kScalePitch);
+                slot = D == 2 ? slot ^ 1u : 0u;
                 const char *xk = xrow + ch * (F::chunk_k * 2u);
-                const uint32_t nk = min((uint32_t)F::chunk_k, a.K - ch * F::chunk_k);
-                if (FMT == MXQ_FMT_NVFP4) {
-                    const uint4 s0 = lds128(sb + g8 * 16u), s1 = lds128(sb + 128u + g8 * 16u);
-                    const uint32_t w0[4] = {s0.x, s0.y, s0.z, s0.w}, w1[4] = {s1.x, s1.y, s1.z, s1.w};
+                const uint32_t groups = min((uint32_t)F::chunk_k, a.K - ch * F::chunk_k) >> 7;
+#pragma unroll 2
+                for (uint32_t hk = 0; hk < groups; ++hk, cw += F::group_bytes, sb += F::sbytes, xk += 256) {
+                    float d0[4], d1[4], c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t s0[4], s1[4];
+                    if (FMT == MXQ_FMT_NVFP4) {
+                        // pairs of scales of 32 values, the one of this lane's 16 first
+                        const uint2 n0 = lds64(sb), n1 = lds64(sb + 8 * kScalePitch);
+                        e4m3x4_unpack(n0.x >> half8, s0[0], s0[1]);
+                        e4m3x4_unpack(n0.y >> half8, s0[2], s0[3]);
+                        e4m3x4_unpack(n1.x >> half8, s1[0], s1[1]);
+                        e4m3x4_unpack(n1.y >> half8, s1[2], s1[3]);
+                    } else if (FMT == MXQ_FMT_FP8_BLOCK) {
+                        d0[0] = __uint_as_float(lds32(sb));
+                        d1[0] = __uint_as_float(lds32(sb + 8 * kScalePitch));
+                    } else {
+                        ue8m0x4(lds32(sb), d0);
+                        ue8m0x4(lds32(sb + 8 * kScalePitch), d1);
+                    }
 #pragma unroll
-                    for (uint32_t hk = 0; hk < 2; ++hk) {
-                        if (hk * 128u >= nk)
-                            break;
-#pragma unroll
-                        for (uint32_t u2 = 0; u2 < 4; ++u2) {
-                            const uint32_t u = hk * 4u + u2, sel = ((u & 1u) * 2u + (t4 >> 1)) * 0x11u;
-                            const uint32_t d0 = e4m3x2_to_f16x2(__byte_perm(w0[u >> 1], 0u, sel));
-                            const uint32_t d1 = e4m3x2_to_f16x2(__byte_perm(w1[u >> 1], 0u, sel));
-                            const char *at = base + g8 * 128u + ((u ^ g8) << 4) + t4 * 4u;
-                            uint32_t p0[4], p1[4];
-                            e2m1x8_to_f16x2(lds32(at), p0);
-                            e2m1x8_to_f16x2(lds32(at + 1024u), p1);
+                    for (uint32_t u = 0; u < 4; ++u) {           // 32 values of a row
+                        uint32_t p0[4], p1[4];
+                        if (F::fp4) {
+                            e2m1x8_unpack(lds32(cw + u * 16u), p0);
+                            e2m1x8_unpack(lds32(cw + u * 16u + 8 * kPitch), p1);
+                        } else {
+                            e4m3x4_unpack(lds32(cw + u * 32u), p0[0], p0[1]);
+                            e4m3x4_unpack(lds32(cw + u * 32u + 16), p0[2], p0[3]);
+                            e4m3x4_unpack(lds32(cw + u * 32u + 8 * kPitch), p1[0], p1[1]);
+                            e4m3x4_unpack(lds32(cw + u * 32u + 8 * kPitch + 16), p1[2], p1[3]);
+                        }
+                        const uint4 b = lds128(xk + u * 64u);
+                        if (FMT == MXQ_FMT_NVFP4) {
+                            const uint32_t e0 = low2(s0[u]), e1 = low2(s1[u]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                p0[i] = hmul2_bits(p0[i], d0);
-                                p1[i] = hmul2_bits(p1[i], d1);
+                                p0[i] = hmul2_bits(p0[i], e0);
+                                p1[i] = hmul2_bits(p1[i], e1);
                             }
-                            uint4 b = lds128(xk + u * 64u);
-                            if (!col)
-                                b = make_uint4(0u, 0u, 0u, 0u);
                             mma16816(acc, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
-                            mma16816(acc, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+                            mma16816(acc2, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+                            continue;
                         }
-                    }
-                } else if (FMT == MXQ_FMT_MXFP4) {
-                    const uint2 s0 = lds64(sb + g8 * 8u), s1 = lds64(sb + 64u + g8 * 8u);
-                    const uint32_t w0[2] = {s0.x, s0.y}, w1[2] = {s1.x, s1.y};
-#pragma unroll
-                    for (uint32_t hk = 0; hk < 2; ++hk) {
-                        if (hk * 128u >= nk)
-                            break;
-#pragma unroll
-                        for (uint32_t u2 = 0; u2 < 4; ++u2) {
-                            const uint32_t u = hk * 4u + u2;
-                            const char *at = base + g8 * 128u + ((u ^ g8) << 4) + t4 * 4u;
-                            uint32_t p0[4], p1[4];
-                            e2m1x8_to_f16x2(lds32(at), p0);
-                            e2m1x8_to_f16x2(lds32(at + 1024u), p1);
-                            uint4 b = lds128(xk + u * 64u);
-                            if (!col)
-                                b = make_uint4(0u, 0u, 0u, 0u);
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(c, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
-                            mma16816(c, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
-                            const float d0 = ue8m0((w0[hk] >> (8u * u2)) & 255u);
-                            const float d1 = ue8m0((w1[hk] >> (8u * u2)) & 255u);
-                            acc[0] = fmaf(c[0], d0, acc[0]);
-                            acc[1] = fmaf(c[1], d0, acc[1]);
-                            acc[2] = fmaf(c[2], d1, acc[2]);
-                            acc[3] = fmaf(c[3], d1, acc[3]);
-                        }
-                    }
-                } else {
-                    const uint32_t w0 = lds32(sb + (FMT == MXQ_FMT_MXFP8 ? g8 * 4u : 0u));
-                    const uint32_t w1 = lds32(sb + (FMT == MXQ_FMT_MXFP8 ? 32u + g8 * 4u : 4u));
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (uint32_t u = 0; u < 4; ++u) {
-                        const char *at = base + g8 * 128u + (((2u * u + (t4 >> 1)) ^ F::swz(g8)) << 4) + (t4 & 1u) * 8u;
-                        const uint2 v0 = lds64(at), v1 = lds64(at + 1024u);
-                        uint4 b = lds128(xk + u * 64u);
-                        if (!col)
-                            b = make_uint4(0u, 0u, 0u, 0u);
-                        mma16816(c, e4m3x2_to_f16x2(v0.x), e4m3x2_to_f16x2(v1.x), e4m3x2_to_f16x2(v0.x >> 16),
-                                 e4m3x2_to_f16x2(v1.x >> 16), b.x, b.y);
-                        mma16816(c, e4m3x2_to_f16x2(v0.y), e4m3x2_to_f16x2(v1.y), e4m3x2_to_f16x2(v0.y >> 16),
-                                 e4m3x2_to_f16x2(v1.y >> 16), b.z, b.w);
-                        if (FMT == MXQ_FMT_MXFP8) {
-                            const float d0 = ue8m0((w0 >> (8u * u)) & 255u), d1 = ue8m0((w1 >> (8u * u)) & 255u);
-                            acc[0] = fmaf(c[0], d0, acc[0]);
-                            acc[1] = fmaf(c[1], d0, acc[1]);
-                            acc[2] = fmaf(c[2], d1, acc[2]);
-                            acc[3] = fmaf(c[3], d1, acc[3]);
+                        mma16816(c, p0[0], p1[0], p0[1], p1[1], b.x, b.y);
+                        mma16816(c, p0[2], p1[2], p0[3], p1[3], b.z, b.w);
+                        if (FMT == MXQ_FMT_FP8_BLOCK ? u == 3 : true) {      // a scale block is complete
+                            const float f0 = d0[FMT == MXQ_FMT_FP8_BLOCK ? 0 : u];
+                            const float f1 = d1[FMT == MXQ_FMT_FP8_BLOCK ? 0 : u];
+                            acc[0] = fmaf(c[0], f0, acc[0]);
+                            acc[1] = fmaf(c[1], f0, acc[1]);
+                            acc[2] = fmaf(c[2], f1, acc[2]);
+                            acc[3] = fmaf(c[3], f1, acc[3]);
                             c[0] = c[1] = c[2] = c[3] = 0.0f;
                         }
                     }
-                    if (FMT == MXQ_FMT_FP8_BLOCK) {
-                        const float d0 = __uint_as_float(w0), d1 = __uint_as_float(w1);
-                        acc[0] = fmaf(c[0], d0, acc[0]);
-                        acc[1] = fmaf(c[1], d0, acc[1]);
-                        acc[2] = fmaf(c[2], d1, acc[2]);
-                        acc[3] = fmaf(c[3], d1, acc[3]);
-                    }
                 }
             }
+            if (FMT == MXQ_FMT_NVFP4)   // two chains of products
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] += acc2[i];
             if (ks > 1) {       // the team's partial sums, in warp order
                 *reinterpret_cast<float4 *>(part + warp * 128u + lane * 4u) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 named_barrier_sync(1 + (int)team, (int)(ks * 32u));
@@ -639,16 +708,28 @@ cudaError_t moe_gemm(MoeArgs a, int ctas, cudaStream_t s)
     a.tilesdiv = make_fastdiv(a.tiles);
     a.topkdiv = make_fastdiv(a.topk);
     a.chunks = (a.K + Fmt<FMT>::chunk_k - 1) / Fmt<FMT>::chunk_k;
+    // Warps that share a task: doubled while every warp of the grid still gets
+    // at most one and each has a chunk, were all assignments of different
+    // experts.  Not by the experts really chosen: a token's sums are then added
+    // in the same order whatever its company chose.
+    a.ks = 1;
+    while (a.ks < 8 && a.ks * 2 <= a.chunks && (uint64_t)a.A * a.tiles * a.ks * 2 <= (uint64_t)ctas * kWarps)
+        a.ks *= 2;
     a.xstride = a.K * 2 + 64;       // 64 mod 128: the rows of a fragment load fall on different banks
     const size_t lists = (3 * (size_t)a.A + 2) * 2 + 64;
-    const size_t fixed = kWarps * 128 * 4 + lists;
-    // ring of 4 chunks a warp where 8 activation rows fit beside it, else 2
-    const int depth = kWarps * 4 * kSlotBytes + fixed + 8 * (a.xstride + 4) + 16 <= kSmemMax ? 4 : 2;
-    const size_t ring = (size_t)kWarps * depth * kSlotBytes;
-    uint32_t cap = (uint32_t)((kSmemMax - ring - fixed - 16) / (a.xstride + 4));
-    a.cap = cap > 64 ? 64 : cap;    // at least 16 KB in all: the expert counts lie there first
-    const size_t smem = ring + fixed + a.cap * (size_t)a.xstride + (((size_t)a.cap + 3) & ~3ull) * 4;
-    return depth == 4 ? run<FMT, GATE_UP, 4>(a, smem, ctas, s) : run<FMT, GATE_UP, 2>(a, smem, ctas, s);
+    const size_t fixed = kWarps * 128 * 4 + lists, row = a.xstride + 4;
+    // Stage: 8 activation rows and one of zeros at least, beside rings of 2
+    // chunks a warp; in layers too wide for that 4 rows, and then 1 chunk.
+    const auto fits = [&](size_t rows, size_t depth) {
+        return kWarps * depth * kSlotBytes + fixed + (rows + 1) * row + 16 <= kSmemMax;
+    };
+    a.group = fits(8, 2) ? 8 : 4;
+    const size_t depth = fits(4, 2) ? 2 : 1;
+    const size_t ring = kWarps * depth * kSlotBytes;
+    const size_t cap = (kSmemMax - ring - fixed - 16) / row - 1;
+    a.cap = (uint32_t)(cap > 64 ? 64 : cap);      // at least 20 KB in all: ids and expert counts lie there first
+    const size_t smem = ring + fixed + (a.cap + 1) * (size_t)a.xstride + (((size_t)a.cap + 3) & ~3ull) * 4;
+    return depth == 2 ? run<FMT, GATE_UP, 2>(a, smem, ctas, s) : run<FMT, GATE_UP, 1>(a, smem, ctas, s);
 }
 
 template <int FMT>

@@ -133,7 +133,7 @@ cudaError_t launch_gemm_fp8(const GemmArgs &g, int out_f32, cudaStream_t s);
 // Mixture-of-experts layer for a few tokens.
 constexpr int64_t kMoeMaxAssignments = 2048;   // T * topk
 constexpr int64_t kMoeMaxWidth = 8192;         // hidden, inter
-constexpr int64_t kMoeMaxExperts = 4096;       // their counts fit the activation rows' space
+constexpr int64_t kMoeMaxExperts = 4096;       // their ids and counts fit the activation rows' space
 struct MoeLayer {
     const uint16_t *x;
     int64_t T, hidden, inter, topk, experts;

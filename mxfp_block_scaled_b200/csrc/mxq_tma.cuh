@@ -1,0 +1,46 @@
+// mxq_tma.cuh -- tensor maps of byte matrices and the TMA load that uses them
+// (sm_100a; PTX ISA, cp.async.bulk.tensor).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mxq_device.cuh"
+
+namespace mxq {
+
+// Box at byte column x (a multiple of 16) and row y of the map's matrix ->
+// shared memory, counted in bytes on `bar`; what lies past the matrix is 0.
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+                 ::"r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
+}
+
+// Map of the row-major byte matrix [rows, cols] at p (16-byte aligned, cols a
+// multiple of 16) in boxes of 128 bytes by box_rows (at most 256) rows, with
+// the 128-byte swizzle: 16-byte piece i of row r of a box lies at piece
+// i ^ (r % 8).  The encoder is the driver's (the library links the runtime
+// only); its address is looked up once.  False if either is refused.
+inline bool make_byte_map(CUtensorMap *m, const uint8_t *p, uint64_t rows, uint64_t cols, uint32_t box_rows)
+{
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
+    const cuuint32_t box[2] = {128, box_rows}, step[2] = {1, 1};
+    return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+} // namespace mxq

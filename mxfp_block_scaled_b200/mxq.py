@@ -327,39 +327,52 @@ def mxq_dequant_relerr_noalloc(x, codes, scales, s2, fmt, n_tensors, rows, cols,
     _check("mxq_dequant_relerr_noalloc", rc)
 
 
-# The layer operators run on the device of their first tensor, whichever is
+# The layer operators are called once per layer and token, so their checks are
+# kept light.  They run on the device of their first tensor, whichever is
 # current, and refuse buffers that lie on different ones.
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libmxq takes device tensors")
+    return dev
+
+
 def _buf(name, t, nbytes, dev):
-    _need(name, t, nbytes)
-    if t is not None and t.device != dev:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
-    return _p(t)
+    if t is None:
+        return None
+    if t.nbytes < nbytes or not t.is_contiguous():
+        _need(name, t, nbytes)
+    if t.get_device() != dev:
+        raise ValueError("%s is not on the device of the first tensor" % name)
+    return t.data_ptr()
 
 
-def _launch(name, dev, args, stream):
-    fn = getattr(load(), name)
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
-    else:
-        rc = fn(*args, _stream(stream))
-    _check(name, rc)
+def _enqueue(fn, args, dev, stream):
+    """fn(*args, stream) on device `dev`; stream: a torch stream of it, or its current one."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
 
 
 def mxq_quantize_fp8(x, rows, cols, brows, bcols, codes, scales, status, stream=None):
-    dev, n = x.device, rows * cols
+    dev, n = _device(x), rows * cols
     nblk = -(-rows // brows) * -(-cols // bcols) if brows > 0 and bcols > 0 else 0
-    _launch("mxq_quantize_fp8", dev,
-            (_buf("x", x, 2 * n, dev), rows, cols, brows, bcols, _buf("codes", codes, n, dev),
-             _buf("scales", scales, 4 * nblk, dev), _buf("status", status, 4, dev)), stream)
+    rc = _enqueue(load().mxq_quantize_fp8,
+                  (_buf("x", x, 2 * n, dev), rows, cols, brows, bcols, _buf("codes", codes, n, dev),
+                   _buf("scales", scales, 4 * nblk, dev), _buf("status", status, 4, dev)), dev, stream)
+    _check("mxq_quantize_fp8", rc)
 
 
 def mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, c, status, stream=None):
-    dev, kb = a.device, -(-K // 128)
-    _launch("mxq_gemm_fp8", dev,
-            (_buf("a", a, M * K, dev), _buf("a_scales", a_scales, 4 * M * kb, dev), _buf("b", b, N * K, dev),
-             _buf("b_scales", b_scales, 4 * -(-N // 128) * kb, dev), M, N, K, OUT[out],
-             _buf("c", c, M * N * (4 if out == "f32" else 2), dev), _buf("status", status, 4, dev)), stream)
+    dev, kb = _device(a), -(-K // 128)
+    rc = _enqueue(load().mxq_gemm_fp8,
+                  (_buf("a", a, M * K, dev), _buf("a_scales", a_scales, 4 * M * kb, dev), _buf("b", b, N * K, dev),
+                   _buf("b_scales", b_scales, 4 * -(-N // 128) * kb, dev), M, N, K, OUT[out],
+                   _buf("c", c, M * N * (4 if out == "f32" else 2), dev), _buf("status", status, 4, dev)),
+                  dev, stream)
+    _check("mxq_gemm_fp8", rc)
 
 
 def moe_weight_bytes(fmt, experts, rows, cols):
@@ -373,18 +386,19 @@ def moe_weight_bytes(fmt, experts, rows, cols):
 def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, inter, gate_up_codes,
                     gate_up_scales, gate_up_s2, down_codes, down_scales, down_s2, y, status, workspace,
                     stream=None):
-    dev = x.device
+    dev = _device(x)
     gc, gs = moe_weight_bytes(fmt, experts, 2 * inter, hidden)
     dc, ds = moe_weight_bytes(fmt, experts, hidden, inter)
     s2 = 4 * experts if fmt == "nvfp4" else 0
-    _launch("mxq_moe_forward", dev,
-            (_buf("x", x, 2 * T * hidden, dev), T, hidden, _buf("topk_ids", topk_ids, 4 * T * topk, dev),
-             _buf("topk_weights", topk_weights, 4 * T * topk, dev), topk, FMT[fmt], experts, inter,
-             _buf("gate_up_codes", gate_up_codes, gc, dev), _buf("gate_up_scales", gate_up_scales, gs, dev),
-             _buf("gate_up_s2", gate_up_s2, s2, dev), _buf("down_codes", down_codes, dc, dev),
-             _buf("down_scales", down_scales, ds, dev), _buf("down_s2", down_s2, s2, dev),
-             _buf("y", y, 2 * T * hidden, dev), _buf("status", status, 4, dev),
-             _buf("workspace", workspace, 0, dev), _nbytes(workspace)), stream)
+    rc = _enqueue(load().mxq_moe_forward,
+                  (_buf("x", x, 2 * T * hidden, dev), T, hidden, _buf("topk_ids", topk_ids, 4 * T * topk, dev),
+                   _buf("topk_weights", topk_weights, 4 * T * topk, dev), topk, FMT[fmt], experts, inter,
+                   _buf("gate_up_codes", gate_up_codes, gc, dev), _buf("gate_up_scales", gate_up_scales, gs, dev),
+                   _buf("gate_up_s2", gate_up_s2, s2, dev), _buf("down_codes", down_codes, dc, dev),
+                   _buf("down_scales", down_scales, ds, dev), _buf("down_s2", down_s2, s2, dev),
+                   _buf("y", y, 2 * T * hidden, dev), _buf("status", status, 4, dev),
+                   _buf("workspace", workspace, 0, dev), _nbytes(workspace)), dev, stream)
+    _check("mxq_moe_forward", rc)
 
 
 # ------------------------------------------------------------ allocating --
