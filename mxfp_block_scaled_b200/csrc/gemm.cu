@@ -9,15 +9,18 @@
 // added to fp32 sums in registers.
 //
 // gemm_tile_kernel (M above kSmallM).  One persistent CTA per SM, tiles of 128
-// rows by BN columns.  A producer thread fetches the 128-byte-wide K blocks of
-// a and b by TMA (128-byte swizzle; rows, columns and a last K block past the
-// ends arrive as zeros), one thread issues tcgen05.mma kind::f8f6f4 (four of
-// K = 32 a block) into one of NB TMEM buffers, and 16 warps move each finished
-// buffer into their sums: acc += (sa sb) P.  A warp has 32 rows (its TMEM
-// lanes) and BN / 4 columns, so all of a thread's sums share one row scale and
-// one column scale.  A scale warp brings the 128 row scales and the column
-// scales of each block into shared memory ahead of time; read by the 16 warps
-// themselves, 32 lines a load, they would cost as many cycles as the product.
+// rows by BN columns.  A producer warp fetches the 128-byte-wide K blocks of a
+// and b by TMA (128-byte swizzle; rows, columns and a last K block past the ends
+// arrive as zeros), another issues tcgen05.mma kind::f8f6f4 (four of K = 32 a
+// block) into one of several TMEM buffers, and 8 warps move each finished buffer
+// into their sums: acc += (sa sb) P.  A warp has 32 rows (its TMEM lanes) and
+// BN / 2 columns, so all of a thread's sums share one row scale and one column
+// scale.  Two more warps bring the scales of each block into shared memory, four
+// blocks ahead: loaded by the summing warps themselves, 32 lines a load, they
+// took 17 % more time.  The service warps hand most of their registers to the
+// summing ones
+// (setmaxnreg), whose 128 sums a thread leave room to read one part of a buffer
+// while the part before is added.
 //
 // gemm_small_kernel (few rows: decoding).  The read of b is the bound.  A
 // warp multiplies 16 rows of b by up to 8 NT rows of a with mma.sync
@@ -125,16 +128,26 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
 
 // ------------------------------------------------------------ many rows --
 
-constexpr int kEpiWarps = 16;
-constexpr int kTileThreads = 32 * (kEpiWarps + 4);   // sums, producer, product, scales, one idle warp
-constexpr int kStageOut = 2048;                      // bytes a warp stages its result through
+constexpr int kEpiWarps = 8;
+constexpr int kTileThreads = 32 * (kEpiWarps + 4);   // sums, producer, product, two of scales
+// Registers of a thread: kTileThreads x 168 at launch (what __launch_bounds__
+// allows), of which the four service warps give up the most.  The sum of the
+// shares must not pass what the block was launched with.
+constexpr int kLaunchRegs = 168, kSumRegs = 232, kServiceRegs = 40;
+static_assert(kEpiWarps * kSumRegs + 4 * kServiceRegs <= (kEpiWarps + 4) * kLaunchRegs, "register shares");
+constexpr int kStageOut = 4096;                      // bytes a warp stages its result through
 
 template <int BN>
 struct Tile {
+    // 256 columns are two products of 128, each with its own buffers and its own
+    // four summing warps: a buffer's next product is then a whole step away while
+    // it is read
+    static constexpr int halves = BN == 256 ? 2 : 1;
+    static constexpr int hc = BN / halves;                            // columns of a product
     static constexpr int bytes = (128 + BN) * 128;                    // one K block of a and b
-    static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 5 : 7;   // 227 KB in all
-    static constexpr int bufs = BN == 256 ? 2 : 4;                    // TMEM buffers of BN columns
-    static constexpr int cols = BN / 4;                               // a warp's columns
+    static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 5 : 7;  // 227 KB in all
+    static constexpr int bufs = BN == 256 ? 2 : 4;                    // TMEM buffers of each half
+    static constexpr int cols = BN / 2;                               // a warp's columns
 };
 
 struct TileArgs {
@@ -144,10 +157,11 @@ struct TileArgs {
     uint32_t M, N, K, KB;
     uint32_t mt, nt;            // tiles in each direction
     uint32_t group;             // column tiles of a group; groups are walked one after the other
+    uint32_t tma_out;           // c is stored by TMA (rows of a multiple of 16 bytes)
 };
 
 struct TileBars {
-    uint64_t full[8], empty[8], tfull[4], tempty[4], drain;
+    uint64_t full[8], empty[8], tfull[4], tempty[4], sempty[4], drain;
     uint32_t tmem, abort;
 };
 
@@ -182,37 +196,137 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// 1 in one lane of the (whole) warp.
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// The instructions below are issued by the lane whose `one` is 1, inside code
+// that the whole warp runs: their descriptors and addresses then stay in
+// uniform registers.  In a branch of one thread each product took 85 cycles to
+// issue, and a step of four with its commits 710 instead of 512.
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+                 "setp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one) : "memory");
 }
 
-__device__ __forceinline__ void umma_commit(uint64_t *bar)
+// The products so far arrive on `bar` when done.
+__device__ __forceinline__ void umma_commit(uint64_t *bar, uint32_t one)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_addr(bar)) : "memory");
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(smem_addr(bar)), "r"(one) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16])
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes, uint32_t one)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15}, [%16];"
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %2, 0;\n\t"
+                 "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}"
+                 ::"r"(smem_addr(bar)), "r"(bytes), "r"(one) : "memory");
+}
+
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint64_t *bar,
+                                         uint32_t one)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %5, 0;\n\t"
+                 "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];\n\t}"
+                 ::"r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(one) : "memory");
+}
+
+// 32 columns of this warp's 32 TMEM lanes, one lane a thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                 "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                    "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
-                   "=r"(v[15])
+                   "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+                   "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+                   "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
                  : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads so far are done; v is named so that no use of it moves above.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// One warp's 32 rows x COLS sums -> global, through 2 KB of shared memory: 64
+// Sums of 16 bytes' worth of results -> their bits.
+template <typename Out>
+__device__ __forceinline__ uint4 out_bits(const float2 *s)
+{
+    if constexpr (sizeof(Out) == 4)
+        return make_uint4(__float_as_uint(s[0].x), __float_as_uint(s[0].y), __float_as_uint(s[1].x),
+                          __float_as_uint(s[1].y));
+    else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(s[i].x, s[i].y);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// One warp's 32 rows x COLS sums -> global by TMA: 128 bytes of each row at a
+// time, through 4 KB of shared memory in the map's swizzle.  The copy reads them
+// while the warp goes on; the next one waits for that.  Rows and columns past
+// the ends are left out by the copy.
+template <int COLS, typename Out>
+__device__ __forceinline__ void store_tma(const float2 *acc, char *buf, const CUtensorMap *map, uint32_t m0,
+                                          uint32_t n0, const TileArgs &p, uint32_t lane)
+{
+    constexpr int per = 128 / sizeof(Out);      // columns of a copy
+    constexpr int used = COLS < per ? COLS : per;
+#pragma unroll
+    for (int r = 0; r < COLS / used; ++r) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < used * (int)sizeof(Out) / 16; ++q)
+            *reinterpret_cast<uint4 *>(buf + lane * 128u + (((uint32_t)q ^ (lane & 7u)) << 4)) =
+                out_bits<Out>(acc + (r * used + q * (16 / (int)sizeof(Out))) / 2);
+        fence_proxy_async_smem();
+        __syncwarp();
+        const uint32_t n = n0 + r * used;
+        if (lane == 0 && m0 < p.M && n < p.N)
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                         ::"l"(map), "r"(smem_addr(buf)), "r"(n), "r"(m0) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+// The same by plain stores, for rows that are no multiple of 16 bytes and for
+// warps of less than 128 bytes a row: 64
 // bytes of each row at a time, their 16-byte pieces permuted against bank
-// conflicts, written out in whole rows.
+// conflicts, written out along the rows.
 template <int COLS, typename Out>
 __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c, uint32_t m0, uint32_t n0,
                                            const TileArgs &p, uint32_t lane)
@@ -221,31 +335,17 @@ __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c,
     constexpr int rounds = (COLS + per - 1) / per;
     constexpr int used = COLS < per ? COLS : per;
     constexpr int pieces = used * (int)sizeof(Out) / 16;
-    const bool vec = (p.N * sizeof(Out)) % 16 == 0;
     const uint32_t swz = (lane >> 1) & 3u;
 #pragma unroll
     for (int r = 0; r < rounds; ++r) {
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < pieces; ++q) {
-            uint4 v;
-            const float2 *s = acc + (r * used + q * (16 / (int)sizeof(Out))) / 2;
-            if (sizeof(Out) == 2) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(s[i].x, s[i].y);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                v = make_uint4(w[0], w[1], w[2], w[3]);
-            } else
-                v = make_uint4(__float_as_uint(s[0].x), __float_as_uint(s[0].y), __float_as_uint(s[1].x),
-                               __float_as_uint(s[1].y));
-            *reinterpret_cast<uint4 *>(buf + lane * 64u + (((uint32_t)q ^ swz) << 4)) = v;
-        }
+        for (int q = 0; q < pieces; ++q)
+            *reinterpret_cast<uint4 *>(buf + lane * 64u + (((uint32_t)q ^ swz) << 4)) =
+                out_bits<Out>(acc + (r * used + q * (16 / (int)sizeof(Out))) / 2);
         __syncwarp();
         const uint32_t nr = n0 + r * used;
-        if (vec) {
+        if (p.tma_out) {        // whole pieces
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t row = i * 8u + (lane >> 2), q = lane & 3u, n = nr + q * (16u / sizeof(Out));
@@ -253,13 +353,13 @@ __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c,
                     *reinterpret_cast<uint4 *>(c + (uint64_t)(m0 + row) * p.N + n) =
                         *reinterpret_cast<const uint4 *>(buf + row * 64u + ((q ^ ((row >> 1) & 3u)) << 4));
             }
-        } else {
-            for (uint32_t i = lane; i < 32u * used; i += 32u) {
-                const uint32_t row = i / used, col = i % used, q = col * (uint32_t)sizeof(Out) / 16u;
-                if (m0 + row < p.M && nr + col < p.N)
-                    c[(uint64_t)(m0 + row) * p.N + nr + col] = *reinterpret_cast<const Out *>(
-                        buf + row * 64u + ((q ^ ((row >> 1) & 3u)) << 4) + (col * sizeof(Out)) % 16u);
-            }
+            continue;
+        }
+        for (uint32_t i = lane; i < 32u * used; i += 32u) {
+            const uint32_t row = i / used, col = i % used, q = col * (uint32_t)sizeof(Out) / 16u;
+            if (m0 + row < p.M && nr + col < p.N)
+                c[(uint64_t)(m0 + row) * p.N + nr + col] = *reinterpret_cast<const Out *>(
+                    buf + row * 64u + ((q ^ ((row >> 1) & 3u)) << 4) + (col * sizeof(Out)) % 16u);
         }
     }
 }
@@ -268,32 +368,37 @@ __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c,
 
 template <int BN, typename Out>
 __global__ void __launch_bounds__(kTileThreads, 1)
-gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const TileArgs p)
+gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                 const __grid_constant__ CUtensorMap mc, const TileArgs p)
 {
     using T = Tile<BN>;
+    constexpr int kCols = T::halves * T::bufs * T::hc;      // TMEM columns: 256 or 512
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ TileBars bars;
-    __shared__ float srow[T::bufs][128], scol[T::bufs][4];
+    __shared__ float srow[T::bufs][128], scol[T::bufs][2];
     // operand tiles start on 1024-byte boundaries (the swizzle repeats there)
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    // the same value in every lane, and known to be
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     const uint32_t ntile = p.mt * p.nt;
     if (threadIdx.x == 0) {
         for (int i = 0; i < T::stages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
-        for (int i = 0; i < T::bufs; ++i) {
-            mbar_init(&bars.tfull[i], 2);            // the product and the scales
-            mbar_init(&bars.tempty[i], kEpiWarps);
+        for (int i = 0; i < T::bufs * T::halves; ++i) {
+            mbar_init(&bars.tfull[i], 3);                        // the product and two warps' scales
+            mbar_init(&bars.tempty[i], kEpiWarps / T::halves);   // for the product
         }
+        for (int i = 0; i < T::bufs; ++i)
+            mbar_init(&bars.sempty[i], kEpiWarps);               // for the scales
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_mbar_init();
     }
     if (warp == kEpiWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_addr(&bars.tmem)), "n"(T::bufs * BN) : "memory");
+                     ::"r"(smem_addr(&bars.tmem)), "n"(kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     fence_before();
@@ -301,20 +406,22 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
     fence_after();
     const uint32_t tmem = bars.tmem;
 
-    if (warp == kEpiWarps) {                         // producer
-        if (lane == 0) {
+    if (warp >= kEpiWarps) {
+        regs_down<kServiceRegs>();
+        if (warp == kEpiWarps) {                     // producer
+            const uint32_t one = elect_one();
             uint32_t s = 0, ph = 1;                  // a fresh barrier passes the wait for its odd phase
             bool ok = true;
             for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x) {
                 uint32_t m, n;
                 tile_at(p, i, m, n);
                 for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                    if (!(ok = wait_bar(&bars.empty[s], ph, bars, p.status)))
+                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.empty[s], ph, bars, p.status))))
                         break;
                     char *dst = smem + s * T::bytes;
-                    mbar_arrive_expect_tx(&bars.full[s], T::bytes);
-                    tma_load_2d(dst, &ma, kb * 128u, m * 128u, &bars.full[s]);
-                    tma_load_2d(dst + 128 * 128, &mb, kb * 128u, n * BN, &bars.full[s]);
+                    expect_tx(&bars.full[s], T::bytes, one);
+                    tma_load(dst, &ma, kb * 128u, m * 128u, &bars.full[s], one);
+                    tma_load(dst + 128 * 128, &mb, kb * 128u, n * BN, &bars.full[s], one);
                     if (++s == T::stages) {
                         s = 0;
                         ph ^= 1u;
@@ -322,34 +429,41 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 }
             }
             if (!ok) {
-                // copies in flight: the last fill of every stage.  Stages
-                // before s were filled in the current pass over the ring
-                // (phase ph ^ 1), the others in the pass before.
+                // copies in flight: the last fill of every stage.  Stages before
+                // s were filled in the current pass over the ring (phase ph ^ 1),
+                // the others in the pass before.
                 for (uint32_t k = 0; k < (uint32_t)T::stages; ++k) {
                     const uint32_t par = k < s ? ph ^ 1u : ph;
                     for (uint32_t n = 0; n < kGemmSpin && !mbar_try_wait(&bars.full[k], par); ++n)
                         ;
                 }
             }
-        }
-    } else if (warp == kEpiWarps + 1) {              // product
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN / 8) << 17) | ((128u / 16u) << 24);
+        } else if (warp == kEpiWarps + 1) {          // product
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(T::hc / 8) << 17) | ((128u / 16u) << 24);
+            const uint32_t one = elect_one();
             uint32_t s = 0, ph = 0, d = 0, dph = 1;
             bool ok = true;
             for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x)
                 for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                    if (!(ok = wait_bar(&bars.tempty[d], dph, bars, p.status) &&
-                               wait_bar(&bars.full[s], ph, bars, p.status)))
-                        break;
-                    fence_after();
+                    ok = wait_bar(&bars.full[s], ph, bars, p.status);
                     const uint32_t at = smem_addr(smem + s * T::bytes);
-                    const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * 128);
+                    const uint64_t da = operand_desc(at);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)      // 32 values: 32 bytes along the row
-                        umma(tmem + d * BN, da + k * 2, db + k * 2, idesc, k > 0);
-                    umma_commit(&bars.empty[s]);
-                    umma_commit(&bars.tfull[d]);
+                    for (uint32_t h = 0; h < (uint32_t)T::halves; ++h) {
+                        const uint32_t buf = h * T::bufs + d;
+                        ok = __all_sync(0xFFFFFFFFu, ok && wait_bar(&bars.tempty[buf], dph, bars, p.status));
+                        if (!ok)
+                            break;
+                        fence_after();
+                        const uint64_t db = operand_desc(at + (128 + h * T::hc) * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 32 values: 32 bytes along the row
+                            umma(tmem + buf * T::hc, da + k * 2, db + k * 2, idesc, k > 0, one);
+                        umma_commit(&bars.tfull[buf], one);
+                    }
+                    if (!ok)
+                        break;
+                    umma_commit(&bars.empty[s], one);
                     if (++s == T::stages) {
                         s = 0;
                         ph ^= 1u;
@@ -360,51 +474,77 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     }
                 }
             if (!ok) {                               // products in flight
-                umma_commit(&bars.drain);
+                umma_commit(&bars.drain, one);
                 for (uint32_t n = 0; n < kGemmSpin && !mbar_try_wait(&bars.drain, 0); ++n)
                     ;
             }
-        }
-    } else if (warp == kEpiWarps + 2) {              // scales
-        uint32_t d = 0, dph = 1;
-        bool ok = true;
-        for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x) {
-            uint32_t m, n;
-            tile_at(p, i, m, n);
-            const uint32_t row = m * 128u + lane, cb = (n * BN + (lane & 3u) * T::cols) >> 7;
-            const float *sa = p.sa + (uint64_t)row * p.KB, *sb = p.sb + (uint64_t)cb * p.KB;
-            const bool col = lane < 4u && n * BN + lane * T::cols < p.N;
-            float v[4], w;
-            auto load = [&](uint32_t kb) {
-#pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    v[j] = row + j * 32u < p.M ? __ldg(sa + j * 32ull * p.KB + kb) : 0.0f;
-                w = col ? __ldg(sb + kb) : 0.0f;
-            };
-            load(0);
-            for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tempty[d], dph, bars, p.status))))
-                    break;
-#pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    srow[d][j * 32u + lane] = v[j];
-                if (lane < 4u)
-                    scol[d][lane] = w;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bars.tfull[d]);
-                if (kb + 1 < p.KB)
-                    load(kb + 1);
-                if (++d == T::bufs) {
-                    d = 0;
-                    dph ^= 1u;
+        } else {                                         // scales: two warps, 64 rows each
+            // kAhead steps' scales at a time, and those of the steps after them on
+            // the way: a load takes longer than a step.
+            constexpr uint32_t kAhead = 4;
+            const uint32_t sw = warp - (kEpiWarps + 2), r0 = sw * 64u + lane;
+            float now[3][kAhead], next[3][kAhead];       // this lane's two rows, and (lanes 0, 1 of the first warp) its columns
+            uint32_t d = 0, dph = 1, ni = blockIdx.x, nkb = 0;    // the chunk to load next
+            bool ok = true;
+            auto load = [&]() {
+                if (ni >= ntile)
+                    return;
+                uint32_t m, n;
+                tile_at(p, ni, m, n);
+                const uint32_t row = m * 128u + r0, c0 = n * BN + lane * T::cols;
+                const float *sa = p.sa + (uint64_t)row * p.KB + nkb, *sb = p.sb + (uint64_t)(c0 >> 7) * p.KB + nkb;
+                const bool in0 = row < p.M, in1 = row + 32u < p.M, inc = sw == 0 && lane < 2u && c0 < p.N;
+    #pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j) {
+                    const bool in = nkb + j < p.KB;
+                    next[0][j] = in && in0 ? __ldg(sa + j) : 0.0f;
+                    next[1][j] = in && in1 ? __ldg(sa + 32ull * p.KB + j) : 0.0f;
+                    next[2][j] = in && inc ? __ldg(sb + j) : 0.0f;
                 }
-            }
+                nkb += kAhead;
+                if (nkb >= p.KB) {
+                    nkb = 0;
+                    ni += gridDim.x;
+                }
+            };
+            load();
+            for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x)
+                for (uint32_t kb = 0; kb < p.KB && ok; kb += kAhead) {
+    #pragma unroll
+                    for (uint32_t j = 0; j < kAhead; ++j) {
+                        now[0][j] = next[0][j];
+                        now[1][j] = next[1][j];
+                        now[2][j] = next[2][j];
+                    }
+                    load();
+    #pragma unroll
+                    for (uint32_t j = 0; j < kAhead; ++j) {
+                        if (kb + j >= p.KB || !ok)
+                            break;
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.sempty[d], dph, bars, p.status));
+                        if (!ok)
+                            break;
+                        srow[d][r0] = now[0][j];
+                        srow[d][r0 + 32u] = now[1][j];
+                        if (sw == 0 && lane < 2u)
+                            scol[d][lane] = now[2][j];
+                        __syncwarp();
+                        if (lane < (uint32_t)T::halves)
+                            mbar_arrive(&bars.tfull[lane * T::bufs + d]);
+                        if (++d == T::bufs) {
+                            d = 0;
+                            dph ^= 1u;
+                        }
+                    }
+                }
         }
-    } else if (warp < kEpiWarps) {                   // sums
-        const uint32_t quad = warp & 3u, part = warp >> 2;
-        const uint32_t taddr = tmem + ((quad * 32u) << 16) + part * T::cols;
+    } else {                                         // sums
+        regs_up<kSumRegs>();
+        const uint32_t quad = warp & 3u, part = warp >> 2, half = T::halves == 2 ? part : 0u;
+        const uint32_t taddr = tmem + ((quad * 32u) << 16) + half * T::bufs * T::hc + (T::halves == 2 ? 0u : part * T::cols);
         char *buf = smem + T::stages * T::bytes + warp * kStageOut;
+        uint64_t *const tfull = &bars.tfull[half * T::bufs], *const tempty = &bars.tempty[half * T::bufs];
+        const float *const rows = &srow[0][quad * 32u + lane], *const col = &scol[0][part];
         uint32_t d = 0, dph = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x) {
@@ -415,40 +555,55 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             for (int j = 0; j < T::cols / 2; ++j)
                 acc[j] = make_float2(0.0f, 0.0f);
             for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tfull[d], dph, bars, p.status))))
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(tfull + d, dph, bars, p.status));
+                if (!ok)
                     break;
                 fence_after();
-                const float s = srow[d][quad * 32u + lane] * scol[d][part];
-                const float2 ss = make_float2(s, s);
+                const float f = rows[d * 128u] * col[d * 2u];
+                const float2 ff = make_float2(f, f);
+                const uint32_t at = taddr + d * T::hc;
+                uint32_t v[2][32];
+                tmem_ld32(at, v[0]);
+                tmem_ld_wait(v[0]);
 #pragma unroll
-                for (int j = 0; j < T::cols; j += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(taddr + d * BN + j, v);
-                    tmem_ld_wait();
+                for (int j = 0; j < T::cols / 32; ++j) {
+                    uint32_t(&now)[32] = v[j & 1], (&next)[32] = v[(j + 1) & 1];
+                    if ((j + 1) * 32 < T::cols)
+                        tmem_ld32(at + (j + 1) * 32, next);
+                    else {                           // all of the buffer is read
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(tempty + d);
+                            mbar_arrive(&bars.sempty[d]);
+                        }
+                    }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        acc[j / 2 + q] = __ffma2_rn(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])),
-                                                    ss, acc[j / 2 + q]);
+                    for (int q = 0; q < 16; ++q)
+                        acc[j * 16 + q] = __ffma2_rn(make_float2(__uint_as_float(now[2 * q]), __uint_as_float(now[2 * q + 1])),
+                                                     ff, acc[j * 16 + q]);
+                    if ((j + 1) * 32 < T::cols)
+                        tmem_ld_wait(next);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bars.tempty[d]);
                 if (++d == T::bufs) {
                     d = 0;
                     dph ^= 1u;
                 }
             }
-            if (ok)
-                store_rows<T::cols, Out>(acc, buf, static_cast<Out *>(p.c), m * 128u + quad * 32u,
-                                         n * BN + part * T::cols, p, lane);
+            const uint32_t m0 = m * 128u + quad * 32u, n0 = n * BN + part * T::cols;
+            if (ok && p.tma_out && T::cols * sizeof(Out) >= 128)
+                store_tma<T::cols, Out>(acc, buf, &mc, m0, n0, p, lane);
+            else if (ok)
+                store_rows<T::cols, Out>(acc, buf, static_cast<Out *>(p.c), m0, n0, p, lane);
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    __syncwarp();
     fence_before();
     __syncthreads();
     if (warp == kEpiWarps + 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::bufs * BN));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols));
     }
 }
 
@@ -458,10 +613,6 @@ template <int BN, typename Out>
 cudaError_t run_tile(const GemmArgs &g, int sms, cudaStream_t s)
 {
     using T = Tile<BN>;
-    CUtensorMap ma, mb;
-    if (!make_byte_map(&ma, g.a, (uint64_t)g.M, (uint64_t)g.K, 128) ||
-        !make_byte_map(&mb, g.b, (uint64_t)g.N, (uint64_t)g.K, BN))
-        return cudaErrorInvalidValue;
     TileArgs p;
     p.sa = g.sa;
     p.sb = g.sb;
@@ -476,13 +627,20 @@ cudaError_t run_tile(const GemmArgs &g, int sms, cudaStream_t s)
     // a group's part of b: at most 32 MB, a quarter of L2
     const uint64_t fit = (32ull << 20) / ((uint64_t)BN * (p.K + 1)) + 1;
     p.group = fit < p.nt ? (uint32_t)fit : p.nt;
+    p.tma_out = (g.N * sizeof(Out)) % 16 == 0;
+    CUtensorMap ma, mb, mc;
+    if (!make_byte_map(&ma, g.a, (uint64_t)g.M, (uint64_t)g.K, 128) ||
+        !make_byte_map(&mb, g.b, (uint64_t)g.N, (uint64_t)g.K, BN))
+        return cudaErrorInvalidValue;
+    if (p.tma_out && !make_out_map(&mc, g.c, (uint64_t)g.M, (uint64_t)g.N, sizeof(Out) == 4, 32))
+        return cudaErrorInvalidValue;
     const size_t smem = (size_t)T::stages * T::bytes + kEpiWarps * kStageOut + 1024;
     const auto k = gemm_tile_kernel<BN, Out>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
     const uint64_t tiles = (uint64_t)p.mt * p.nt;
-    k<<<(unsigned)(tiles < (uint64_t)sms ? tiles : sms), kTileThreads, smem, s>>>(ma, mb, p);
+    k<<<(unsigned)(tiles < (uint64_t)sms ? tiles : sms), kTileThreads, smem, s>>>(ma, mb, mc, p);
     return cudaGetLastError();
 }
 
@@ -511,21 +669,16 @@ cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    // Tile width: the fewest column-steps of work on the busiest SM.  A
-    // narrower tile fetches a more often, so its step is priced up.
+    // Tile width: the fewest rounds of tiles on the SMs, each at what a step of
+    // that width took (0.66, 0.38 and 0.28 us: 65536 x 2560 x 2048).
     const int64_t mt = (g.M + 127) / 128;
-    int best = 256;
-    double cost = 0;
-    for (int bn = 256; bn >= 64; bn /= 2) {
-        const int64_t tiles = mt * ((g.N + bn - 1) / bn), rounds = (tiles + sms - 1) / sms;
-        const double c = (double)rounds * (bn + 32);
-        if (bn == 256 || c < cost) {
-            cost = c;
-            best = bn;
-        }
-    }
-    return best == 256 ? run_tile<256, Out>(g, sms, s)
-                       : best == 128 ? run_tile<128, Out>(g, sms, s) : run_tile<64, Out>(g, sms, s);
+    const auto cost = [&](int64_t bn, double step) {
+        return (double)((mt * ((g.N + bn - 1) / bn) + sms - 1) / sms) * step;
+    };
+    const double c256 = cost(256, 0.66), c128 = cost(128, 0.38), c64 = cost(64, 0.28);
+    if (c256 <= c128 && c256 <= c64)
+        return run_tile<256, Out>(g, sms, s);
+    return c128 <= c64 ? run_tile<128, Out>(g, sms, s) : run_tile<64, Out>(g, sms, s);
 }
 
 } // namespace
