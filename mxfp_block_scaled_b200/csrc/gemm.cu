@@ -139,14 +139,9 @@ constexpr int kStageOut = 4096;                      // bytes a warp stages its 
 
 template <int BN>
 struct Tile {
-    // 256 columns are two products of 128, each with its own buffers and its own
-    // four summing warps: a buffer's next product is then a whole step away while
-    // it is read
-    static constexpr int halves = BN == 256 ? 2 : 1;
-    static constexpr int hc = BN / halves;                            // columns of a product
     static constexpr int bytes = (128 + BN) * 128;                    // one K block of a and b
     static constexpr int stages = BN == 256 ? 4 : BN == 128 ? 5 : 7;  // 227 KB in all
-    static constexpr int bufs = BN == 256 ? 2 : 4;                    // TMEM buffers of each half
+    static constexpr int bufs = BN == 256 ? 2 : 4;                    // TMEM buffers of BN columns
     static constexpr int cols = BN / 2;                               // a warp's columns
 };
 
@@ -161,7 +156,7 @@ struct TileArgs {
 };
 
 struct TileBars {
-    uint64_t full[8], empty[8], tfull[4], tempty[4], sempty[4], drain;
+    uint64_t full[8], empty[8], tfull[4], tempty[4], drain;
     uint32_t tmem, abort;
 };
 
@@ -372,7 +367,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                  const __grid_constant__ CUtensorMap mc, const TileArgs p)
 {
     using T = Tile<BN>;
-    constexpr int kCols = T::halves * T::bufs * T::hc;      // TMEM columns: 256 or 512
+    constexpr int kCols = T::bufs * BN;      // TMEM columns: 256 or 512
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ TileBars bars;
     __shared__ float srow[T::bufs][128], scol[T::bufs][2];
@@ -386,12 +381,10 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
-        for (int i = 0; i < T::bufs * T::halves; ++i) {
-            mbar_init(&bars.tfull[i], 3);                        // the product and two warps' scales
-            mbar_init(&bars.tempty[i], kEpiWarps / T::halves);   // for the product
+        for (int i = 0; i < T::bufs; ++i) {
+            mbar_init(&bars.tfull[i], 3);            // the product and two warps' scales
+            mbar_init(&bars.tempty[i], kEpiWarps);
         }
-        for (int i = 0; i < T::bufs; ++i)
-            mbar_init(&bars.sempty[i], kEpiWarps);               // for the scales
         mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_mbar_init();
@@ -439,30 +432,22 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 }
             }
         } else if (warp == kEpiWarps + 1) {          // product
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(T::hc / 8) << 17) | ((128u / 16u) << 24);
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN / 8) << 17) | ((128u / 16u) << 24);
             const uint32_t one = elect_one();
             uint32_t s = 0, ph = 0, d = 0, dph = 1;
             bool ok = true;
             for (uint32_t i = blockIdx.x; i < ntile && ok; i += gridDim.x)
                 for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                    ok = wait_bar(&bars.full[s], ph, bars, p.status);
-                    const uint32_t at = smem_addr(smem + s * T::bytes);
-                    const uint64_t da = operand_desc(at);
-#pragma unroll
-                    for (uint32_t h = 0; h < (uint32_t)T::halves; ++h) {
-                        const uint32_t buf = h * T::bufs + d;
-                        ok = __all_sync(0xFFFFFFFFu, ok && wait_bar(&bars.tempty[buf], dph, bars, p.status));
-                        if (!ok)
-                            break;
-                        fence_after();
-                        const uint64_t db = operand_desc(at + (128 + h * T::hc) * 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 32 values: 32 bytes along the row
-                            umma(tmem + buf * T::hc, da + k * 2, db + k * 2, idesc, k > 0, one);
-                        umma_commit(&bars.tfull[buf], one);
-                    }
-                    if (!ok)
+                    ok = wait_bar(&bars.tempty[d], dph, bars, p.status) && wait_bar(&bars.full[s], ph, bars, p.status);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
+                    fence_after();
+                    const uint32_t at = smem_addr(smem + s * T::bytes);
+                    const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)      // 32 values: 32 bytes along the row
+                        umma(tmem + d * BN, da + k * 2, db + k * 2, idesc, k > 0, one);
+                    umma_commit(&bars.tfull[d], one);
                     umma_commit(&bars.empty[s], one);
                     if (++s == T::stages) {
                         s = 0;
@@ -521,7 +506,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     for (uint32_t j = 0; j < kAhead; ++j) {
                         if (kb + j >= p.KB || !ok)
                             break;
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.sempty[d], dph, bars, p.status));
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tempty[d], dph, bars, p.status));
                         if (!ok)
                             break;
                         srow[d][r0] = now[0][j];
@@ -529,8 +514,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                         if (sw == 0 && lane < 2u)
                             scol[d][lane] = now[2][j];
                         __syncwarp();
-                        if (lane < (uint32_t)T::halves)
-                            mbar_arrive(&bars.tfull[lane * T::bufs + d]);
+                        if (lane == 0)
+                            mbar_arrive(&bars.tfull[d]);
                         if (++d == T::bufs) {
                             d = 0;
                             dph ^= 1u;
@@ -540,10 +525,9 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
         }
     } else {                                         // sums
         regs_up<kSumRegs>();
-        const uint32_t quad = warp & 3u, part = warp >> 2, half = T::halves == 2 ? part : 0u;
-        const uint32_t taddr = tmem + ((quad * 32u) << 16) + half * T::bufs * T::hc + (T::halves == 2 ? 0u : part * T::cols);
+        const uint32_t quad = warp & 3u, part = warp >> 2;
+        const uint32_t taddr = tmem + ((quad * 32u) << 16) + part * T::cols;
         char *buf = smem + T::stages * T::bytes + warp * kStageOut;
-        uint64_t *const tfull = &bars.tfull[half * T::bufs], *const tempty = &bars.tempty[half * T::bufs];
         const float *const rows = &srow[0][quad * 32u + lane], *const col = &scol[0][part];
         uint32_t d = 0, dph = 0;
         bool ok = true;
@@ -555,13 +539,13 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             for (int j = 0; j < T::cols / 2; ++j)
                 acc[j] = make_float2(0.0f, 0.0f);
             for (uint32_t kb = 0; kb < p.KB; ++kb) {
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(tfull + d, dph, bars, p.status));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tfull[d], dph, bars, p.status));
                 if (!ok)
                     break;
                 fence_after();
                 const float f = rows[d * 128u] * col[d * 2u];
                 const float2 ff = make_float2(f, f);
-                const uint32_t at = taddr + d * T::hc;
+                const uint32_t at = taddr + d * BN;
                 uint32_t v[2][32];
                 tmem_ld32(at, v[0]);
                 tmem_ld_wait(v[0]);
@@ -573,10 +557,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     else {                           // all of the buffer is read
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(tempty + d);
-                            mbar_arrive(&bars.sempty[d]);
-                        }
+                        if (lane == 0)
+                            mbar_arrive(&bars.tempty[d]);
                     }
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
@@ -670,12 +652,12 @@ cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     // Tile width: the fewest rounds of tiles on the SMs, each at what a step of
-    // that width took (0.66, 0.38 and 0.28 us: 65536 x 2560 x 2048).
+    // that width took (0.57, 0.38 and 0.28 us).
     const int64_t mt = (g.M + 127) / 128;
     const auto cost = [&](int64_t bn, double step) {
         return (double)((mt * ((g.N + bn - 1) / bn) + sms - 1) / sms) * step;
     };
-    const double c256 = cost(256, 0.66), c128 = cost(128, 0.38), c64 = cost(64, 0.28);
+    const double c256 = cost(256, 0.57), c128 = cost(128, 0.38), c64 = cost(64, 0.28);
     if (c256 <= c128 && c256 <= c64)
         return run_tile<256, Out>(g, sms, s);
     return c128 <= c64 ? run_tile<128, Out>(g, sms, s) : run_tile<64, Out>(g, sms, s);
