@@ -8,7 +8,7 @@
 // cannot take them: every block's P (exact products, fp32 sums) is scaled and
 // added to fp32 sums in registers.
 //
-// gemm_tile_kernel (M above kSmallM).  One persistent CTA per SM, tiles of 128
+// gemm_tile_kernel (many rows).  One persistent CTA per SM, tiles of 128
 // rows by BN columns.  A producer warp fetches the 128-byte-wide K blocks of a
 // and b by TMA (128-byte swizzle; rows, columns and a last K block past the ends
 // arrive as zeros), another issues tcgen05.mma kind::f8f6f4 (four of K = 32 a
@@ -45,7 +45,12 @@ namespace {
 // hardware, so this is well above any wait that makes progress and below a
 // second or two.
 constexpr uint32_t kGemmSpin = 1u << 20;
-constexpr int kSmallM = 64;
+// Rows that stream b through mma.sync: up to 16, and more while the whole product
+// is small.  Measured, tiles against streaming: 16 x 2560 x 2048 7.1 against
+// 3.8 us, 24 rows of it 7.2 against 7.8; 32 x 1536 x 2048 (0.1 G) 7.2 against
+// 5.7, 48 x 2048 x 1280 (0.13 G) 5.7 against 7.9; 128 x 512 x 512 4.2 against 2.9.
+// (At most 1024 rows of it, far inside the grid's second dimension.)
+constexpr int64_t kSmallM = 16, kSmallMaxM = 1024, kSmallWork = 100 << 20;
 
 template <typename T>
 __device__ __forceinline__ T to_out(float v);
@@ -638,7 +643,7 @@ cudaError_t run_small(const GemmArgs &g, cudaStream_t s)
 template <typename Out>
 cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
 {
-    if (g.M <= kSmallM) {
+    if (g.M <= kSmallM || (g.M <= kSmallMaxM && g.M * g.N <= kSmallWork / g.K)) {
         if (g.M <= 8)
             return run_small<1, Out>(g, s);
         if (g.M <= 16)
