@@ -30,8 +30,10 @@
  *   - All pointers are DEVICE pointers unless stated; the caller owns every
  *     buffer.  The library allocates nothing.  State kept between calls:
  *     the device address of the fixed scratch array of
- *     mxq_dequant_relerr_noalloc (per device and context, see there) and the
- *     one-shot request flag of the test hook in mxq_test.h; nothing else.
+ *     mxq_dequant_relerr_noalloc (per device and context, see there), the
+ *     host address of the driver's tensor-map encoder (mxq_gemm_fp8, looked
+ *     up once) and the one-shot request flag of the test hook in mxq_test.h;
+ *     nothing else.
  *   - All work is enqueued asynchronously on `stream` (0 = legacy default
  *     stream).  The call returns after enqueueing; results are valid once
  *     the stream has reached that point.
@@ -417,8 +419,9 @@ MXQ_API mxq_status mxq_dequant_relerr_noalloc(const uint16_t *x, const uint8_t *
  * rounding are readings).
  *   x       bf16 [rows, cols], cols % 16 == 0 (MXQ_ERR_SHAPE).
  *   brows, bcols  1 x 128 (a token tile: a scale per token and 128 channels)
- *           or 128 x 128 (weights); others MXQ_ERR_UNSUPPORTED.  The last
- *           blocks of a row or column may be smaller.
+ *           or 128 x 128 (weights); others MXQ_ERR_UNSUPPORTED (below 1
+ *           MXQ_ERR_INVALID_ARG).  The last blocks of a row or column may be
+ *           smaller.
  *   codes   out, E4M3 bytes [rows, cols].
  *   scales  out, fp32 [ceil(rows / brows), ceil(cols / 128)].
  *   status  required (MXQ_DEV_NONFINITE_INPUT).
@@ -487,7 +490,9 @@ MXQ_API size_t mxq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t hidden, 
  *   workspace at least mxq_moe_workspace_bytes(T, topk, hidden, inter).  Two
  *            calls that overlap in time need one each.
  * hidden and inter must be multiples of 128 (MXQ_ERR_SHAPE) and at most 8192,
- * T * topk and T at most 2048, experts at most 4096 (MXQ_ERR_UNSUPPORTED).
+ * T * topk and T at most 2048, experts at most 4096 (MXQ_ERR_UNSUPPORTED) and
+ * at least 1 (MXQ_ERR_INVALID_ARG).  T or hidden 0 leaves everything as it is;
+ * topk or inter 0 gives rows of zeros.
  * Sums are fp32 in a fixed order: repeated calls give the same bits. */
 MXQ_API mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden,
                                    const int32_t *topk_ids, const float *topk_weights, int64_t topk,

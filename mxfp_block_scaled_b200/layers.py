@@ -14,6 +14,10 @@ Argument marshalling only; every step runs in libmxq.so.
 * A mixed-format model keeps a per-layer format list
   (MJPansa/Qwen3.8-Flash-Next-MXFP4-FP8-R12, "Quantization format" and
   "Retained layers": some routed-expert layers MXFP4, the others in another
+  format).  Layers kept in block FP8 are block_fp8_layer results.
+* A converted layer is run as it is stored: routed_forward reads the
+  experts' codes (a few tokens), fp8_linear quantizes the tokens and
+  multiplies in block FP8 (projections and shared experts kept in that
   format).
 """
 import torch
@@ -43,6 +47,39 @@ def quantize_routed_layer(gate_up, down, fmt="nvfp4", mode="four_six", stream=No
         q.update(fmt=fmt, sum_sq_err=err, sum_sq_ref=ref, relerr=rel)
         out[name] = q
     return out
+
+
+def block_fp8_layer(gate_up, down, stream=None):
+    """A stacked routed-expert layer in block FP8 (E4M3, one fp32 scale per
+    128 x 128 block), the format of the layers a mixed model retains; 2I and H
+    multiples of 128.  {"gate_up": q, "down": q} for routed_forward."""
+    out = {}
+    for name, x in (("gate_up", gate_up), ("down", down)):
+        if x.dim() != 3 or x.shape[1] % 128:
+            raise ValueError("%s: a stack [E, R, C] with R a multiple of 128" % name)
+        out[name] = dict(mxq.quantize_fp8(x, 128, stream=stream), fmt="fp8_block")
+    return out
+
+
+def routed_forward(layer_q, x, topk_ids, topk_weights, workspace=None, stream=None):
+    """y[t] = sum_j w[t, j] down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j],
+    of a converted layer (a quantize_routed_layer or block_fp8_layer result)
+    for a few tokens.  x: bf16 [T, H]; topk_ids int32, topk_weights fp32
+    [T, k].  Returns dict y bf16 [T, H], status."""
+    gu, dn = layer_q["gate_up"], layer_q["down"]
+    if gu["fmt"] != dn["fmt"]:
+        raise ValueError("gate_up is %s, down is %s" % (gu["fmt"], dn["fmt"]))
+    return mxq.moe_forward(x, topk_ids, topk_weights, gu, dn, gu["fmt"], workspace=workspace, stream=stream)
+
+
+def fp8_linear(x, w_q, out="bf16", stream=None):
+    """x w^T with both sides in block FP8: the token tile x (bf16 [T, K]) is
+    quantized with one scale per token and 128 channels, w_q is
+    mxq.quantize_fp8(w, 128) of w [N, K].  Returns dict c [T, N] (bf16, or
+    fp32 for out="f32"), status (of both steps)."""
+    t = mxq.quantize_fp8(x, stream=stream)
+    return mxq.gemm_fp8(t["codes"], t["scales"], w_q["codes"], w_q["scales"], out, status=t["status"],
+                        stream=stream)
 
 
 def unstack_expert(layer_q, e):

@@ -10,6 +10,7 @@ tensors for every buffer.  ``quantize_nvfp4``, ``quantize_mx``,
 ``quantize_act`` and ``dequant_relerr`` allocate the outputs and workspace
 with torch and return them.
 """
+import contextlib
 import ctypes
 import os
 
@@ -402,6 +403,12 @@ def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, in
 
 
 # ------------------------------------------------------------ allocating --
+def _on(stream):
+    """Results and workspaces made on the stream that the call runs on: what is
+    freed on return is then handed out again only behind the call."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
 def _bf16(x):
     if x.dtype != torch.bfloat16 or not x.is_contiguous():
         raise ValueError("expected a contiguous bf16 tensor")
@@ -557,26 +564,29 @@ def quantize_fp8(x, brows=1, stream=None):
     [E, R, C] of weights with R a multiple of 128: [E, R/128, ceil(C/128)]),
     status."""
     _bf16(x)
+    if brows not in (1, 128):
+        raise ValueError("blocks of 1 x 128 or 128 x 128")
     C = x.shape[-1]
-    R = x.numel() // C if C else 0
+    R = x.shape[:-1].numel()
     lead = (-(-R // brows),)
     if x.dim() == 3 and brows == 128 and x.shape[1] % 128 == 0:
         lead = (x.shape[0], x.shape[1] // 128)
     dev = x.device
-    out = {
-        "codes": torch.empty(x.shape, dtype=torch.uint8, device=dev),
-        "scales": torch.empty(lead + (-(-C // 128),), dtype=torch.float32, device=dev),
-        "status": torch.zeros(1, dtype=torch.int32, device=dev),
-    }
-    mxq_quantize_fp8(x, R, C, brows, 128, out["codes"], out["scales"], out["status"], stream)
+    with _on(stream):
+        out = {
+            "codes": torch.empty(x.shape, dtype=torch.uint8, device=dev),
+            "scales": torch.empty(lead + (-(-C // 128),), dtype=torch.float32, device=dev),
+            "status": torch.zeros(1, dtype=torch.int32, device=dev),
+        }
+        mxq_quantize_fp8(x, R, C, brows, 128, out["codes"], out["scales"], out["status"], stream)
     return out
 
 
-def gemm_fp8(a, a_scales, b, b_scales, out="bf16", stream=None):
+def gemm_fp8(a, a_scales, b, b_scales, out="bf16", status=None, stream=None):
     """c = a b^T of block-FP8 matrices.  a: uint8 E4M3 codes [M, K] with fp32
     scales [M, ceil(K/128)] (quantize_fp8 of a token tile); b: codes [N, K]
     with scales [ceil(N/128), ceil(K/128)] (brows=128).  Returns dict c [M, N]
-    (bf16, or fp32 for out="f32"), status."""
+    (bf16, or fp32 for out="f32"), status (a given one is added to)."""
     M, K = a.shape
     N = b.shape[0]
     kb = -(-K // 128)
@@ -584,9 +594,12 @@ def gemm_fp8(a, a_scales, b, b_scales, out="bf16", stream=None):
     _typed("a_scales", a_scales, torch.float32, (M, kb))
     _typed("b", b, torch.uint8, (N, K))
     _typed("b_scales", b_scales, torch.float32, (-(-N // 128), kb))
-    res = {"c": torch.empty((M, N), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=a.device),
-           "status": torch.zeros(1, dtype=torch.int32, device=a.device)}
-    mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, res["c"], res["status"], stream)
+    if out not in OUT:
+        raise ValueError("out is one of %s" % sorted(OUT))
+    with _on(stream):
+        res = {"c": torch.empty((M, N), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=a.device),
+               "status": torch.zeros(1, dtype=torch.int32, device=a.device) if status is None else status}
+        mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, res["c"], res["status"], stream)
     return res
 
 
@@ -602,37 +615,40 @@ def _typed(name, t, dtype, shape):
     return t
 
 
-def moe_forward(x, topk_ids, topk_weights, gate_up, down, fmt, stream=None):
+def moe_forward(x, topk_ids, topk_weights, gate_up, down, fmt, workspace=None, stream=None):
     """A routed-expert layer for a few tokens.  x: bf16 [T, H]; topk_ids int32
     and topk_weights fp32 [T, k] (an id below 0: no expert); gate_up, down:
     dicts with codes, scales (and s2 for "nvfp4") of the stacks [E, 2I, H] and
     [E, H, I], as quantize_nvfp4, quantize_mx or quantize_fp8 with brows=128
-    (fmt "fp8_block") return them with linear scales.  Returns dict y bf16
+    (fmt "fp8_block") return them with linear scales; workspace: a
+    moe_workspace to use again, not by two calls at once.  Returns dict y bf16
     [T, H], status."""
     _bf16(x)
+    per = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32, "fp8_block": 128}.get(fmt)
+    if per is None:
+        raise ValueError("unknown format %r" % (fmt,))
     T, H = x.shape
-    E = gate_up["codes"].shape[0]
-    I = gate_up["codes"].shape[1] // 2
+    E, I = gate_up["codes"].shape[0], gate_up["codes"].shape[1] // 2
     k = topk_ids.shape[1]
     _typed("topk_ids", topk_ids, torch.int32, (T, k))
     _typed("topk_weights", topk_weights, torch.float32, (T, k))
-    per = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32, "fp8_block": 128}[fmt]
     for name, q, rows, cols in (("gate_up", gate_up, 2 * I, H), ("down", down, H, I)):
         _typed(name + " codes", q["codes"], torch.uint8,
                (E, rows, cols // 2 if fmt in ("nvfp4", "mxfp4") else cols))
         if fmt == "fp8_block":
-            _typed(name + " scales", q["scales"], torch.float32, (E, rows // per, cols // per))
+            _typed(name + " scales", q["scales"], torch.float32, (E, -(-rows // per), -(-cols // per)))
         else:
             _typed(name + " scales", q["scales"], torch.uint8, (E, rows, cols // per))
         if fmt == "nvfp4":
             _typed(name + " s2", q["s2"], torch.float32, (E,))
     dev = x.device
-    out = {"y": torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-           "status": torch.zeros(1, dtype=torch.int32, device=dev)}
-    mxq_moe_forward(x, T, H, topk_ids, topk_weights, k, fmt, E, I, gate_up["codes"], gate_up["scales"],
-                    gate_up.get("s2") if fmt == "nvfp4" else None, down["codes"], down["scales"],
-                    down.get("s2") if fmt == "nvfp4" else None, out["y"], out["status"],
-                    moe_workspace(T, k, H, I, dev), stream)
+    with _on(stream):
+        out = {"y": torch.empty((T, H), dtype=torch.bfloat16, device=dev),
+               "status": torch.zeros(1, dtype=torch.int32, device=dev)}
+        mxq_moe_forward(x, T, H, topk_ids, topk_weights, k, fmt, E, I, gate_up["codes"], gate_up["scales"],
+                        gate_up["s2"] if fmt == "nvfp4" else None, down["codes"], down["scales"],
+                        down["s2"] if fmt == "nvfp4" else None, out["y"], out["status"],
+                        moe_workspace(T, k, H, I, dev) if workspace is None else workspace, stream)
     return out
 
 
