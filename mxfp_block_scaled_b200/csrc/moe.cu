@@ -11,14 +11,14 @@
 //
 // Three launches, each allowed to start while the one before drains
 // (programmatic dependent launch; the second fetches its first weights before
-// it waits):
+// it waits for h, which the first's own wait at its start allows):
 //   moe_kernel<FMT, true>   h[a] = silu(G x) * (U x)        fp32 [A, I]
 //   moe_kernel<FMT, false>  z[a] = w[a] D h[a]              fp32 [A, H]
 //   moe_combine_kernel      y[t] = sum_j z[t k + j]         fixed order
 // a = t k + j numbers the assignments.  Each z row is written by one warp and
 // summed in the order of j, so repeated calls give the same bits.
 //
-// moe_kernel.  One CTA of 16 warps per SM.  Every CTA builds the list of
+// moe_kernel.  One CTA of 16 warps (8 with few tasks) per SM.  Every CTA builds the list of
 // chosen experts itself (at most 2048 assignments).  An expert's assignments
 // are cut into groups of at most 8 (4 in very wide layers); a task is 16 weight
 // rows (gate_up: 8 gate rows and the same 8 up rows, so the activation is local
@@ -49,13 +49,12 @@
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq.h"
+#include <algorithm>
 
 namespace mxq {
 
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
 // One chunk in shared memory: 16 rows of 256 bytes of codes, then the rows'
 // scales.  With rows 272 bytes apart a fragment load (one word of each lane
 // from 8 rows) touches every bank once; so do the scales, 48 bytes apart.
@@ -84,10 +83,10 @@ struct MoeArgs {
     uint32_t nrows;             // rows of an output: I or H
     uint32_t tiles;             // tasks of a group
     uint32_t chunks;            // chunks of a row
-    uint32_t ks;                // warps that share a task
+    uint32_t kslog;             // log2 of the warps that share a task
     uint32_t cap;               // activation rows the stage holds
     uint32_t xstride;           // bytes of a staged row
-    FastDiv tilesdiv, topkdiv;
+    FastDiv tilesdiv, topkdiv, griddiv;
 };
 
 template <int FMT>
@@ -222,8 +221,10 @@ __device__ __forceinline__ uint32_t route_warp(const MoeArgs &a, const Route &r,
 // free (each is a column of its own), but an expert's groups have to be the
 // same in every CTA, so the list of an expert with more than one is put in
 // ascending order.
+template <int kWarps>
 __device__ __forceinline__ uint32_t route_block(const MoeArgs &a, const Route &r, uint32_t *cnt, uint32_t *wsum)
 {
+    constexpr uint32_t kThreads = 32 * kWarps;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     constexpr uint32_t none = 0xFFFFu;
     uint16_t *ids = reinterpret_cast<uint16_t *>(cnt + a.E);
@@ -398,15 +399,18 @@ struct Walk {
 
 } // namespace
 
-template <int FMT, bool GATE_UP, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int FMT, bool GATE_UP, int D, int kWarps, bool SPLIT>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
 moe_kernel(const MoeArgs a)
 {
+    constexpr uint32_t kThreads = 32 * kWarps;
     using F = Fmt<FMT>;
     extern __shared__ __align__(128) char smem[];
     __shared__ uint32_t wsum[kWarps];
     __shared__ uint32_t groups_s;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3u;
+    if (GATE_UP)
+        cudaGridDependencySynchronize();     // whatever ran before may have written what this reads
     // shared memory: rings, activation rows, row factors, lists, partial sums
     char *ring = smem + warp * (D * kSlotBytes);
     char *xs = smem + kWarps * D * kSlotBytes;
@@ -416,7 +420,7 @@ moe_kernel(const MoeArgs a)
     r.list = reinterpret_cast<uint16_t *>(part + kWarps * 128);
     r.start = r.list + a.A;
     r.expert = r.start + a.A + 1;
-    if (a.A <= 32u) {
+    if (kWarps < 16 || a.A <= 32u) {
         if (warp == 0) {
             const uint32_t n = route_warp(a, r, lane);
             if (lane == 0)
@@ -425,15 +429,14 @@ moe_kernel(const MoeArgs a)
         __syncthreads();
         r.groups = groups_s;
     } else
-        r.groups = route_block(a, r, reinterpret_cast<uint32_t *>(xs), wsum);
+        r.groups = route_block<kWarps>(a, r, reinterpret_cast<uint32_t *>(xs), wsum);
     for (uint32_t k = tid * 16u; k < a.xstride; k += kThreads * 16u)
         *reinterpret_cast<uint4 *>(xs + a.cap * a.xstride + k) = make_uint4(0u, 0u, 0u, 0u);
     // this CTA's run of tasks
     const uint32_t ntask = r.groups * a.tiles;
-    const uint32_t t0 = (uint32_t)((uint64_t)ntask * blockIdx.x / gridDim.x);
-    const uint32_t t1 = (uint32_t)((uint64_t)ntask * (blockIdx.x + 1) / gridDim.x);
-    const uint32_t ks = a.ks, teams = kWarps / ks, team = warp / ks, q = warp - team * ks;
-    const uint32_t c0 = a.chunks * q / ks, c1 = a.chunks * (q + 1) / ks;
+    const uint32_t t0 = fastdiv(ntask * blockIdx.x, a.griddiv), t1 = fastdiv(ntask * (blockIdx.x + 1), a.griddiv);
+    const uint32_t lg = SPLIT ? a.kslog : 0u, ks = 1u << lg, teams = kWarps >> lg, team = warp >> lg, q = warp & (ks - 1u);
+    const uint32_t c0 = (a.chunks * q) >> lg, c1 = (a.chunks * (q + 1)) >> lg;
 
     const uint32_t half = GATE_UP ? a.nrows : 8u;    // distance of the second 8 rows from the first
     const uint32_t tile_rows = GATE_UP ? 8u : 16u;
@@ -602,7 +605,7 @@ moe_kernel(const MoeArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[i] += acc2[i];
-            if (ks > 1) {       // the team's partial sums, in warp order
+            if (SPLIT && ks > 1) {       // the team's partial sums, in warp order
                 *reinterpret_cast<float4 *>(part + warp * 128u + lane * 4u) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 named_barrier_sync(1 + (int)team, (int)(ks * 32u));
                 if (q == 0)
@@ -669,7 +672,7 @@ moe_combine_kernel(const float *__restrict__ z, const int32_t *__restrict__ ids,
 namespace {
 
 template <typename... P, typename... Q>
-cudaError_t launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, bool dependent, cudaStream_t s, Q... args)
+cudaError_t launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Q... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -680,20 +683,21 @@ cudaError_t launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, bool
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = dependent ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+constexpr size_t kSmemHalf = 113 * 1024 - 256;
 constexpr size_t kSmemMax = 227 * 1024 - 256;     // less the static words of the kernel
 
-template <int FMT, bool GATE_UP, int D>
-cudaError_t run(MoeArgs a, size_t smem, int ctas, cudaStream_t s)
+template <int FMT, bool GATE_UP, int D, int W, bool SPLIT>
+cudaError_t run(const MoeArgs &a, size_t smem, int ctas, cudaStream_t s)
 {
-    const auto k = moe_kernel<FMT, GATE_UP, D>;
+    const auto k = moe_kernel<FMT, GATE_UP, D, W, SPLIT>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    return launch(k, dim3((unsigned)ctas), kThreads, smem, !GATE_UP, s, a);
+    return launch(k, dim3((unsigned)ctas), 32 * W, smem, s, a);
 }
 
 template <int FMT, bool GATE_UP>
@@ -707,29 +711,42 @@ cudaError_t moe_gemm(MoeArgs a, int ctas, cudaStream_t s)
     a.tiles = a.nrows / (GATE_UP ? 8 : 16);
     a.tilesdiv = make_fastdiv(a.tiles);
     a.topkdiv = make_fastdiv(a.topk);
+    a.griddiv = make_fastdiv((uint32_t)ctas);
     a.chunks = (a.K + Fmt<FMT>::chunk_k - 1) / Fmt<FMT>::chunk_k;
-    // Warps that share a task: doubled while every warp of the grid still gets
-    // at most one and each has a chunk, were all assignments of different
-    // experts.  Not by the experts really chosen: a token's sums are then added
-    // in the same order whatever its company chose.
-    a.ks = 1;
-    while (a.ks < 8 && a.ks * 2 <= a.chunks && (uint64_t)a.A * a.tiles * a.ks * 2 <= (uint64_t)ctas * kWarps)
-        a.ks *= 2;
     a.xstride = a.K * 2 + 64;       // 64 mod 128: the rows of a fragment load fall on different banks
-    const size_t lists = (3 * (size_t)a.A + 2) * 2 + 64;
-    const size_t fixed = kWarps * 128 * 4 + lists, row = a.xstride + 4;
-    // Stage: 8 activation rows and one of zeros at least, beside rings of 2
-    // chunks a warp; in layers too wide for that 4 rows, and then 1 chunk.
-    const auto fits = [&](size_t rows, size_t depth) {
-        return kWarps * depth * kSlotBytes + fixed + (rows + 1) * row + 16 <= kSmemMax;
+    const uint64_t most_tasks = (uint64_t)a.A * a.tiles;    // were all assignments of different experts
+    // Shared memory of a CTA of `warps` whose rings are `depth` chunks and whose
+    // stage has `rows` activation rows, one of zeros and room to round them up.
+    const auto need = [&](size_t warps, size_t depth, size_t rows) {
+        return warps * (depth * kSlotBytes + 128 * 4) + (3 * (size_t)a.A + 2) * 2 + 64 +
+               (rows + 1) * ((size_t)a.xstride + 4) + 16;
     };
-    a.group = fits(8, 2) ? 8 : 4;
-    const size_t depth = fits(4, 2) ? 2 : 1;
-    const size_t ring = kWarps * depth * kSlotBytes;
-    const size_t cap = (kSmemMax - ring - fixed - 16) / row - 1;
-    a.cap = (uint32_t)(cap > 64 ? 64 : cap);      // at least 20 KB in all: ids and expert counts lie there first
-    const size_t smem = ring + fixed + (a.cap + 1) * (size_t)a.xstride + (((size_t)a.cap + 3) & ~3ull) * 4;
-    return depth == 2 ? run<FMT, GATE_UP, 2>(a, smem, ctas, s) : run<FMT, GATE_UP, 1>(a, smem, ctas, s);
+    // The stage takes what `all` bytes leave, up to 64 rows (with 16 warps at
+    // least 20 KB in all: ids and expert counts lie there first); an expert's
+    // assignments are taken 8 at a time, or 4 where 8 rows do not fit.  Warps
+    // that share a task: doubled while every warp of the grid still gets at most
+    // one and each has a chunk.  Not by the experts really chosen: a token's sums
+    // are then added in the same order whatever its company chose.
+    const auto plan = [&](size_t warps, size_t depth, size_t all) {
+        a.cap = (uint32_t)std::min<size_t>((all - need(warps, depth, 0)) / (a.xstride + 4), 64);
+        a.group = a.cap >= 8 ? 8 : 4;
+        a.kslog = 0;
+        while (a.kslog < 3 && (2u << a.kslog) <= a.chunks && (most_tasks * 2 << a.kslog) <= (uint64_t)ctas * warps)
+            ++a.kslog;
+        return need(warps, depth, a.cap);
+    };
+    // At most two tasks a warp of half the size: 8 warps and half the shared
+    // memory, so that the next launch fetches its first weights meanwhile
+    // (5 tokens of a tiny layer 7.9 us, with 16 warps 9.6).
+    if (a.A <= 32 && most_tasks <= (uint64_t)ctas * 16 && need(8, 2, 4) <= kSmemHalf)
+        return run<FMT, GATE_UP, 2, 8, true>(a, plan(8, 2, kSmemHalf), ctas, s);
+    // Rings of 2 chunks a warp; in layers too wide for that and 4 rows, of 1.
+    // Tasks of one warp each are a kernel of their own: without the limits of a
+    // share 16 MXFP4 tokens take 72.5 us, with them 77.8.
+    if (need(16, 2, 4) > kSmemMax)
+        return run<FMT, GATE_UP, 1, 16, true>(a, plan(16, 1, kSmemMax), ctas, s);
+    const size_t smem = plan(16, 2, kSmemMax);
+    return a.kslog ? run<FMT, GATE_UP, 2, 16, true>(a, smem, ctas, s) : run<FMT, GATE_UP, 2, 16, false>(a, smem, ctas, s);
 }
 
 template <int FMT>
@@ -762,7 +779,7 @@ cudaError_t moe_all(const MoeLayer &m, int sms, cudaStream_t s)
     e = moe_gemm<FMT, false>(a, sms, s);
     if (e != cudaSuccess)
         return e;
-    return launch(moe_combine_kernel, dim3((unsigned)((m.hidden + 511) / 512), (unsigned)m.T), 128, 0, true, s,
+    return launch(moe_combine_kernel, dim3((unsigned)((m.hidden + 511) / 512), (unsigned)m.T), 128, 0, s,
                   (const float *)m.z, m.ids, (uint32_t)m.T, a.topk, a.E, (uint32_t)m.hidden, m.y);
 }
 
