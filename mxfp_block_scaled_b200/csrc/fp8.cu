@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(256)
 fp8_row_kernel(const uint16_t *__restrict__ x, uint32_t nblk, uint32_t cols, const FastDiv nbc,
                uint8_t *__restrict__ codes, float *__restrict__ scales, uint32_t *__restrict__ status)
 {
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t half = (blockIdx.x * 256u + threadIdx.x) >> 4, l8 = (threadIdx.x & 15u) * 8u;
     const uint32_t nhalf = gridDim.x * 16u;
     uint32_t bad = 0;
@@ -109,6 +111,8 @@ fp8_block_kernel(const uint16_t *__restrict__ x, uint32_t rows, uint32_t cols, u
                  uint8_t *__restrict__ codes, float *__restrict__ scales, uint32_t *__restrict__ status)
 {
     __shared__ uint32_t part[8];
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t br = blockIdx.x / nbc, bc = blockIdx.x - br * nbc;
     const uint32_t c = bc * 128u + (threadIdx.x & 15u) * 8u, r0 = br * 128u + (threadIdx.x >> 4);
     uint4 v[8];
@@ -151,14 +155,12 @@ cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int64_t cols, i
         uint64_t grid = (nblk + 16 * kRowUnroll - 1) / (16 * kRowUnroll);
         if (nblk <= 148 * 16)   // few blocks: one each, no thread waits for four
             grid = (nblk + 15) / 16;
-        fp8_row_kernel<<<(unsigned)grid, 256, 0, s>>>(x, (uint32_t)nblk, (uint32_t)cols, make_fastdiv(nbc), codes,
-                                                      scales, status);
-    } else {
-        const uint64_t grid = (uint64_t)((rows + 127) / 128) * nbc;
-        fp8_block_kernel<<<(unsigned)grid, 256, 0, s>>>(x, (uint32_t)rows, (uint32_t)cols, nbc, codes, scales,
-                                                        status);
+        return launch_dependent(fp8_row_kernel, dim3((unsigned)grid), 256, 0, s, x, (uint32_t)nblk, (uint32_t)cols,
+                                make_fastdiv(nbc), codes, scales, status);
     }
-    return cudaGetLastError();
+    const uint64_t grid = (uint64_t)((rows + 127) / 128) * nbc;
+    return launch_dependent(fp8_block_kernel, dim3((unsigned)grid), 256, 0, s, x, (uint32_t)rows, (uint32_t)cols, nbc,
+                            codes, scales, status);
 }
 
 } // namespace mxq

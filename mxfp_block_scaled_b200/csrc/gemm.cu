@@ -79,6 +79,8 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
     __shared__ float red[8][NT * 8][17];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
     const uint32_t n0 = blockIdx.x * 16u, m0 = blockIdx.y * (8u * NT), KB = (K + 127u) / 128u;
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const bool r0 = n0 + g < N, r1 = n0 + g + 8u < N;
     const uint8_t *b0 = b + (uint64_t)(n0 + g) * K, *b1 = b0 + 8ull * K;
@@ -403,6 +405,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
     __syncthreads();
     fence_after();
     const uint32_t tmem = bars.tmem;
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
 
     if (warp >= kEpiWarps) {
         regs_down<kServiceRegs>();
@@ -627,17 +631,15 @@ cudaError_t run_tile(const GemmArgs &g, int sms, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     const uint64_t tiles = (uint64_t)p.mt * p.nt;
-    k<<<(unsigned)(tiles < (uint64_t)sms ? tiles : sms), kTileThreads, smem, s>>>(ma, mb, mc, p);
-    return cudaGetLastError();
+    return launch_dependent(k, dim3((unsigned)(tiles < (uint64_t)sms ? tiles : sms)), kTileThreads, smem, s, ma, mb, mc, p);
 }
 
 template <int NT, typename Out>
 cudaError_t run_small(const GemmArgs &g, cudaStream_t s)
 {
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.M + 8 * NT - 1) / (8 * NT)));
-    gemm_small_kernel<NT, Out><<<grid, 256, 0, s>>>(g.a, g.sa, g.b, g.sb, (uint32_t)g.M, (uint32_t)g.N,
-                                                    (uint32_t)g.K, static_cast<Out *>(g.c));
-    return cudaGetLastError();
+    return launch_dependent(gemm_small_kernel<NT, Out>, grid, 256, 0, s, g.a, g.sa, g.b, g.sb, (uint32_t)g.M,
+                            (uint32_t)g.N, (uint32_t)g.K, static_cast<Out *>(g.c));
 }
 
 template <typename Out>

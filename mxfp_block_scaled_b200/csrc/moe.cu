@@ -671,22 +671,6 @@ moe_combine_kernel(const float *__restrict__ z, const int32_t *__restrict__ ids,
 
 namespace {
 
-template <typename... P, typename... Q>
-cudaError_t launch(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Q... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 constexpr size_t kSmemHalf = 113 * 1024 - 256;
 constexpr size_t kSmemMax = 227 * 1024 - 256;     // less the static words of the kernel
 
@@ -697,7 +681,7 @@ cudaError_t run(const MoeArgs &a, size_t smem, int ctas, cudaStream_t s)
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    return launch(k, dim3((unsigned)ctas), 32 * W, smem, s, a);
+    return launch_dependent(k, dim3((unsigned)ctas), 32 * W, smem, s, a);
 }
 
 template <int FMT, bool GATE_UP>
@@ -779,7 +763,7 @@ cudaError_t moe_all(const MoeLayer &m, int sms, cudaStream_t s)
     e = moe_gemm<FMT, false>(a, sms, s);
     if (e != cudaSuccess)
         return e;
-    return launch(moe_combine_kernel, dim3((unsigned)((m.hidden + 511) / 512), (unsigned)m.T), 128, 0, s,
+    return launch_dependent(moe_combine_kernel, dim3((unsigned)((m.hidden + 511) / 512), (unsigned)m.T), 128, 0, s,
                   (const float *)m.z, m.ids, (uint32_t)m.T, a.topk, a.E, (uint32_t)m.hidden, m.y);
 }
 

@@ -338,4 +338,23 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
+// Launch that may start while the kernel before it in the stream drains: `k`
+// waits (cudaGridDependencySynchronize) before it reads what may have been
+// written there or writes anything.
+template <typename... P, typename... Q>
+inline cudaError_t launch_dependent(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Q... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 } // namespace mxq
