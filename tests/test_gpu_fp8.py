@@ -95,3 +95,8 @@ def test_large_tile_by_rows():
     w = mxq.quantize_fp8(x, brows=128)
     part = mxq.quantize_fp8(x[128 * 1093:].contiguous(), brows=128)
     assert torch.equal(w["codes"][128 * 1093:], part["codes"]) and torch.equal(w["scales"][1093:], part["scales"])
+
+
+@pytest.mark.parametrize("rows,cols", [(4097, 2048), (4201, 2000), (66001, 16), (40000, 144)])
+def test_quantize_many_blocks_bit_exact(rows, cols):
+    _check_quant(workloads.activation_tile(rows, seed=cols, device="cuda", hidden=cols), 1)
