@@ -448,7 +448,7 @@ MXQ_API mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t col
  *   status   required (MXQ_DEV_WAIT_TIMEOUT).
  * Products are exact; their sums and the scaled sums of the blocks are fp32,
  * in an order that does not depend on scheduling (repeated calls give the
- * same bits; the order differs between small and large M).  A NaN code makes
+ * same bits; the order follows from M, N and K).  A NaN code makes
  * its row or column NaN.  No workspace. */
 MXQ_API mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b,
                                 const float *b_scales, int64_t M, int64_t N, int64_t K, mxq_out out,

@@ -8,7 +8,7 @@
 // cannot take them: every block's P (exact products, fp32 sums) is scaled and
 // added to fp32 sums in registers.
 //
-// gemm_tile_kernel (many rows).  One persistent CTA per SM, tiles of 128
+// gemm_tile_kernel (more rows).  One persistent CTA per SM, tiles of 128
 // rows by BN columns.  A producer warp fetches the 128-byte-wide K blocks of a
 // and b by TMA (128-byte swizzle; rows, columns and a last K block past the ends
 // arrive as zeros), another issues tcgen05.mma kind::f8f6f4 (four of K = 32 a
@@ -18,14 +18,15 @@
 // scale.  Two more warps bring the scales of each block into shared memory, four
 // blocks ahead: loaded by the summing warps themselves, 32 lines a load, they
 // took 17 % more time.  The service warps hand most of their registers to the
-// summing ones
-// (setmaxnreg), whose 128 sums a thread leave room to read one part of a buffer
-// while the part before is added.
+// summing ones (setmaxnreg), whose 128 sums a thread leave room to read one part
+// of a buffer while the part before is added.  What bounds it: the sums.  At
+// 65536 x 2560 x 2048 (bf16) it takes 320 us (2.15 PFLOP/s), about 360 under the
+// power limit; the same products and copies without sums and stores take 224.
 //
 // gemm_small_kernel (few rows: decoding).  The read of b is the bound.  A
 // warp multiplies 16 rows of b by up to 8 NT rows of a with mma.sync
 // m16n8k32; 8 warps of a CTA split K by blocks and add their sums in a fixed
-// order.  Both operands come straight from global memory: a lane's 16-byte
+// order (1 x 2560 x 2048 2.8 us).  Both operands come straight from global memory: a lane's 16-byte
 // pieces of a row of b and of a row of a hold the same k, and the order of k
 // inside a block is free.
 //
@@ -35,8 +36,8 @@
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq.h"
-#include <algorithm>
 #include "mxq_tma.cuh"
+#include <algorithm>
 
 namespace mxq {
 
@@ -47,11 +48,11 @@ namespace {
 // second or two.
 constexpr uint32_t kGemmSpin = 1u << 20;
 // Rows that stream b through mma.sync: up to 16, and more while the whole product
-// is small.  Measured, tiles against streaming: 16 x 2560 x 2048 7.1 against
-// 3.8 us, 24 rows of it 7.2 against 7.8; 32 x 1536 x 2048 (0.1 G) 7.2 against
-// 5.7, 48 x 2048 x 1280 (0.13 G) 5.7 against 7.9; 128 x 512 x 512 4.2 against 2.9.
+// is small.  Measured, tiles against streaming: 16 x 2560 x 2048 6.5 against
+// 3.4 us, 20 rows of it (0.1 G) 6.5 against 8.5; 20 x 1999 x 1552 (62 M) 7.5 against
+// 4.6, 33 x 2048 x 1280 (87 M) 5.0 against 7.2; 128 x 512 x 512 4.2 against 2.9.
 // (At most 1024 rows of it, far inside the grid's second dimension.)
-constexpr int64_t kSmallM = 16, kSmallMaxM = 1024, kSmallWork = 100 << 20;
+constexpr int64_t kSmallM = 16, kSmallMaxM = 1024, kSmallWork = 64 << 20;
 
 template <typename T>
 __device__ __forceinline__ T to_out(float v);
@@ -338,9 +339,8 @@ __device__ __forceinline__ void store_tma(const float2 *acc, char *buf, const CU
 }
 
 // The same by plain stores, for rows that are no multiple of 16 bytes and for
-// warps of less than 128 bytes a row: 64
-// bytes of each row at a time, their 16-byte pieces permuted against bank
-// conflicts, written out along the rows.
+// warps of less than 128 bytes a row: 64 bytes of each row at a time, their
+// 16-byte pieces permuted against bank conflicts, written out along the rows.
 template <int COLS, typename Out>
 __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c, uint32_t m0, uint32_t n0,
                                            const TileArgs &p, uint32_t lane)
@@ -378,23 +378,22 @@ __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c,
     }
 }
 
-// A summing warp's part of an item of W columns: its 32 rows and W / 2 columns,
-// whose products come through the TMEM buffers d, d + 1, ... of BN columns.
-template <int W, int BN, typename Out>
-__device__ __forceinline__ bool sum_item(const TileArgs &p, const CUtensorMap *mc, TileBars &bars,
-                                         const float (*srow)[128], const float (*scol)[2], uint32_t tmem, char *buf,
-                                         uint32_t m0, uint32_t n0, uint32_t warp, uint32_t lane, uint32_t &d,
-                                         uint32_t &dph)
+// A summing warp's part of an item of W columns, its 32 rows and W / 2 columns:
+// the scaled sum of `steps` products that come through the TMEM buffers d,
+// d + 1, ... of BN columns.
+template <int W, int BN>
+__device__ __forceinline__ bool sum_steps(const TileArgs &p, TileBars &bars, const float (*srow)[128],
+                                          const float (*scol)[2], uint32_t tmem, uint32_t steps, uint32_t warp,
+                                          uint32_t lane, uint32_t &d, uint32_t &dph, float2 (&acc)[W / 4])
 {
     constexpr int cols = W / 2;
     const uint32_t quad = warp & 3u, part = warp >> 2;
     const uint32_t taddr = tmem + ((quad * 32u) << 16) + part * cols;
     const float *const rows = &srow[0][quad * 32u + lane], *const col = &scol[0][part];
-    float2 acc[cols / 2];
 #pragma unroll
     for (int j = 0; j < cols / 2; ++j)
         acc[j] = make_float2(0.0f, 0.0f);
-    for (uint32_t kb = 0; kb < p.KB; ++kb) {
+    for (uint32_t kb = 0; kb < steps; ++kb) {
         if (!__all_sync(0xFFFFFFFFu, wait_bar(&bars.tfull[d], dph, bars, p.status)))
             return false;
         fence_after();
@@ -427,21 +426,61 @@ __device__ __forceinline__ bool sum_item(const TileArgs &p, const CUtensorMap *m
             dph ^= 1u;
         }
     }
-    m0 += quad * 32u;
-    n0 += part * cols;
-    if (p.tma_out && cols * sizeof(Out) >= 128)
-        store_tma<cols, Out>(acc, buf, mc, m0, n0, p, lane);
+    return true;
+}
+
+// COLS columns of this warp's 32 rows from (m0, n0) on -> c.
+template <int COLS, typename Out>
+__device__ __forceinline__ void store_sums(const float2 *acc, char *buf, const CUtensorMap *mc, uint32_t m0,
+                                           uint32_t n0, const TileArgs &p, uint32_t lane)
+{
+    if (p.tma_out && COLS * sizeof(Out) >= 128)
+        store_tma<COLS, Out>(acc, buf, mc, m0, n0, p, lane);
     else {
         // a copy of an item before may still read the buffer
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        store_rows<cols, Out>(acc, buf, static_cast<Out *>(p.c), m0, n0, p, lane);
+        store_rows<COLS, Out>(acc, buf, static_cast<Out *>(p.c), m0, n0, p, lane);
     }
+}
+
+template <int W, int BN, typename Out>
+__device__ __forceinline__ bool sum_item(const TileArgs &p, const CUtensorMap *mc, TileBars &bars,
+                                         const float (*srow)[128], const float (*scol)[2], uint32_t tmem, char *buf,
+                                         uint32_t m0, uint32_t n0, uint32_t warp, uint32_t lane, uint32_t &d,
+                                         uint32_t &dph)
+{
+    float2 acc[W / 4];
+    if (!sum_steps<W, BN>(p, bars, srow, scol, tmem, p.KB, warp, lane, d, dph, acc))
+        return false;
+    store_sums<W / 2, Out>(acc, buf, mc, m0 + (warp & 3u) * 32u, n0 + (warp >> 2) * (W / 2), p, lane);
     return true;
+}
+
+// All threads of the cluster; shared memory written before is seen behind it.
+__device__ __forceinline__ void cluster_sync_all()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's address `p`.
+__device__ __forceinline__ float4 peer_f4(const float4 *p, uint32_t rank)
+{
+    uint32_t at;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
 }
 
 } // namespace
 
-template <int BN, typename Out>
+// S > 1: a cluster of S CTAs shares an item (the grid holds S CTAs an item), each
+// over its part of K; their sums meet in shared memory, where each CTA adds up a
+// part of the columns in the order of the CTAs.
+template <int BN, typename Out, int S>
 __global__ void __launch_bounds__(kTileThreads, 1)
 gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ CUtensorMap mc, const TileArgs p)
@@ -455,6 +494,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     // the same value in every lane, and known to be
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
+    const uint32_t rank = blockIdx.x % S, item0 = blockIdx.x / S, items_on = gridDim.x / S;
+    const uint32_t k0 = p.KB * rank / S, k1 = p.KB * (rank + 1u) / S;      // this CTA's K blocks
     if (threadIdx.x == 0) {
         for (int i = 0; i < T::stages; ++i) {
             mbar_init(&bars.full[i], 1);
@@ -486,10 +527,10 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             const uint32_t one = elect_one();
             uint32_t s = 0, ph = 1;                  // a fresh barrier passes the wait for its odd phase
             bool ok = true;
-            for (uint32_t i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            for (uint32_t i = item0; i < p.items && ok; i += items_on) {
                 uint32_t m0, n0, w;
                 item_at<BN>(p, i, m0, n0, w);
-                for (uint32_t kb = 0; kb < p.KB; ++kb) {
+                for (uint32_t kb = k0; kb < k1; ++kb) {
                     if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.empty[s], ph, bars, p.status))))
                         break;
                     char *dst = smem + s * T::bytes;
@@ -519,10 +560,10 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             const uint32_t one = elect_one();
             uint32_t s = 0, ph = 0, d = 0, dph = 1;
             bool ok = true;
-            for (uint32_t i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            for (uint32_t i = item0; i < p.items && ok; i += items_on) {
                 const uint32_t w = BN == 256 && i >= p.whole ? BN >> p.cut : BN;
                 const uint32_t idesc = (1u << 4) | ((w / 8u) << 17) | ((128u / 16u) << 24);
-                for (uint32_t kb = 0; kb < p.KB; ++kb) {
+                for (uint32_t kb = k0; kb < k1; ++kb) {
                     ok = wait_bar(&bars.tempty[d], dph, bars, p.status) && wait_bar(&bars.full[s], ph, bars, p.status);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
@@ -555,7 +596,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             constexpr uint32_t kAhead = 4;
             const uint32_t sw = warp - (kEpiWarps + 2), r0 = sw * 64u + lane;
             float now[3][kAhead], next[3][kAhead];       // this lane's two rows, and (lanes 0, 1 of the first warp) its columns
-            uint32_t d = 0, dph = 1, ni = blockIdx.x, nkb = 0;    // the chunk to load next
+            uint32_t d = 0, dph = 1, ni = item0, nkb = k0;    // the chunk to load next
             bool ok = true;
             auto load = [&]() {
                 if (ni >= p.items)
@@ -567,20 +608,20 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 const bool in0 = row < p.M, in1 = row + 32u < p.M, inc = sw == 0 && lane < 2u && c0 < p.N;
     #pragma unroll
                 for (uint32_t j = 0; j < kAhead; ++j) {
-                    const bool in = nkb + j < p.KB;
+                    const bool in = nkb + j < k1;
                     next[0][j] = in && in0 ? __ldg(sa + j) : 0.0f;
                     next[1][j] = in && in1 ? __ldg(sa + 32ull * p.KB + j) : 0.0f;
                     next[2][j] = in && inc ? __ldg(sb + j) : 0.0f;
                 }
                 nkb += kAhead;
-                if (nkb >= p.KB) {
-                    nkb = 0;
-                    ni += gridDim.x;
+                if (nkb >= k1) {
+                    nkb = k0;
+                    ni += items_on;
                 }
             };
             load();
-            for (uint32_t i = blockIdx.x; i < p.items && ok; i += gridDim.x)
-                for (uint32_t kb = 0; kb < p.KB && ok; kb += kAhead) {
+            for (uint32_t i = item0; i < p.items && ok; i += items_on)
+                for (uint32_t kb = k0; kb < k1 && ok; kb += kAhead) {
     #pragma unroll
                     for (uint32_t j = 0; j < kAhead; ++j) {
                         now[0][j] = next[0][j];
@@ -590,7 +631,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     load();
     #pragma unroll
                     for (uint32_t j = 0; j < kAhead; ++j) {
-                        if (kb + j >= p.KB || !ok)
+                        if (kb + j >= k1 || !ok)
                             break;
                         ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tempty[d], dph, bars, p.status));
                         if (!ok)
@@ -614,7 +655,35 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
         char *buf = smem + T::stages * T::bytes + warp * kStageOut;
         uint32_t d = 0, dph = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        if constexpr (S > 1) {
+            constexpr int cols = BN / 2, mine = cols / S;
+            const uint32_t quad = warp & 3u, part = warp >> 2, row = quad * 32u + lane;
+            uint32_t m0, n0, w;
+            item_at<BN>(p, item0, m0, n0, w);
+            // [part][column / 4][row], in the ring of stages, which is empty now
+            float4 *xs = reinterpret_cast<float4 *>(smem) + part * (cols / 4) * 128u + row;
+            float2 acc[cols / 2];
+            ok = sum_steps<BN, BN>(p, bars, srow, scol, tmem, k1 - k0, warp, lane, d, dph, acc);
+#pragma unroll
+            for (int q = 0; q < cols / 4; ++q)
+                xs[q * 128] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
+            cluster_sync_all();
+            float2 sum[mine / 2];
+#pragma unroll
+            for (int q = 0; q < mine / 4; ++q) {
+                float4 v[S];
+#pragma unroll
+                for (int r = 0; r < S; ++r)
+                    v[r] = peer_f4(xs + (rank * (mine / 4) + q) * 128u, r);
+#pragma unroll
+                for (int r = 1; r < S; ++r)
+                    v[0] = make_float4(v[0].x + v[r].x, v[0].y + v[r].y, v[0].z + v[r].z, v[0].w + v[r].w);
+                sum[2 * q] = make_float2(v[0].x, v[0].y);
+                sum[2 * q + 1] = make_float2(v[0].z, v[0].w);
+            }
+            if (ok)
+                store_sums<mine, Out>(sum, buf, &mc, m0 + quad * 32u, n0 + part * cols + rank * mine, p, lane);
+        } else for (uint32_t i = item0; i < p.items && ok; i += items_on) {
             uint32_t m0, n0, w;
             item_at<BN>(p, i, m0, n0, w);
             if (BN < 256 || w == BN)
@@ -625,6 +694,11 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 ok = sum_item<64, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    if constexpr (S > 1) {
+        if (warp >= kEpiWarps)
+            cluster_sync_all();             // the sums are there (also after a wait that ran out)
+        cluster_sync_all();                 // and read
     }
     __syncwarp();
     fence_before();
@@ -637,7 +711,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
 
 namespace {
 
-template <int BN, typename Out>
+template <int BN, typename Out, int S>
 cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
 {
     using T = Tile<BN>;
@@ -663,7 +737,7 @@ cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
     if (p.tma_out && !make_out_map(&mc, g.c, (uint64_t)g.M, (uint64_t)g.N, sizeof(Out) == 4, 32))
         return cudaErrorInvalidValue;
     const size_t smem = (size_t)T::stages * T::bytes + kEpiWarps * kStageOut + 1024;
-    const auto k = gemm_tile_kernel<BN, Out>;
+    const auto k = gemm_tile_kernel<BN, Out, S>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
@@ -671,7 +745,8 @@ cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
     p.cut = cut;
     p.whole = cut ? tiles - tiles % (uint32_t)sms : tiles;
     p.items = p.whole + ((tiles - p.whole) << cut);
-    return launch_dependent(k, dim3(std::min(p.items, (uint32_t)sms)), kTileThreads, smem, s, ma, mb, mc, p);
+    return launch_dependent<S>(k, dim3(S > 1 ? p.items * S : std::min(p.items, (uint32_t)sms)), kTileThreads, smem, s, ma,
+                               mb, mc, p);
 }
 
 template <int NT, typename Out>
@@ -721,8 +796,21 @@ cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
             cut = 0;
         }
     }
-    return bn == 256 ? run_tile<256, Out>(g, sms, cut, s)
-                     : bn == 128 ? run_tile<128, Out>(g, sms, 0, s) : run_tile<64, Out>(g, sms, 0, s);
+    // Few tiles: clusters of 2 or 4 CTAs share the steps of a tile of 64 columns,
+    // at about 1.5 and 2.3 us for the join (64 x 2560 x 2048 6.6 us alone, 6.0 in
+    // pairs; 64 x 1536 x 2048 6.9, 6.0 and 5.4; 64 x 512 x 8192 18.9, 12.0 and 8.3;
+    // 64 x 2048 x 1280 5.0 and 5.3).  32 clusters of 4 are on the SMs at a time, 36
+    // are not.
+    const int64_t kb = (g.K + 127) / 128, items = mt * ((g.N + 63) / 64);
+    const double alone = best * (double)kb, pairs = 1.5 + step[2] * (double)((kb + 1) / 2),
+                 fours = 2.3 + step[2] * (double)((kb + 3) / 4);
+    if (items <= 32 && fours < alone && fours < pairs)
+        return run_tile<64, Out, 4>(g, sms, 0, s);
+    if (items * 2 <= sms && pairs < alone)
+        return run_tile<64, Out, 2>(g, sms, 0, s);
+    if (bn == 256)
+        return run_tile<256, Out, 1>(g, sms, cut, s);
+    return bn == 128 ? run_tile<128, Out, 1>(g, sms, 0, s) : run_tile<64, Out, 1>(g, sms, 0, s);
 }
 
 } // namespace

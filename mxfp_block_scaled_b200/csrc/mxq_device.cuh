@@ -340,8 +340,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
 
 // Launch that may start while the kernel before it in the stream drains: `k`
 // waits (cudaGridDependencySynchronize) before it reads what may have been
-// written there or writes anything.
-template <typename... P, typename... Q>
+// written there or writes anything.  CLUSTER CTAs to a cluster.
+template <unsigned CLUSTER = 1, typename... P, typename... Q>
 inline cudaError_t launch_dependent(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Q... args)
 {
     cudaLaunchConfig_t cfg = {};
@@ -349,11 +349,14 @@ inline cudaError_t launch_dependent(void (*k)(P...), dim3 grid, unsigned block, 
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CLUSTER;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, args...);
 }
 

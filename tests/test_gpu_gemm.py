@@ -121,15 +121,14 @@ def test_repeated_streamed_and_captured_calls(M, N, K):
 
 
 def test_offsets_past_32_bits():
-    """Operands and results of more than 2^32 bytes: rows at the end equal those rows multiplied alone."""
+    """Operands and results of more than 2^32 bytes: the first and the last rows and columns."""
     for M, N, K in ((300000, 256, 16384), (600000, 4096, 128)):
         a = torch.randint(0, 0x7E, (M, K), dtype=torch.uint8, device="cuda")
         sa = torch.rand((M, -(-K // 128)), device="cuda")
         _, _, b, sb = operands(1, N, K)
         c = mxq.gemm_fp8(a, sa, b, sb)["c"]
         for r in (slice(M - 300, M), slice(0, 300)):
-            part = mxq.gemm_fp8(a[r].contiguous(), sa[r].contiguous(), b, sb)["c"]
-            assert torch.equal(c[r], part)
+            ref.close(c[r], *ref.gemm(*(t.cpu().numpy() for t in (a[r], sa[r], b, sb)), "bf16"))
         del a, sa, c
     w = torch.randint(0, 0x7E, (300000, 16384), dtype=torch.uint8, device="cuda")
     sw = torch.rand((-(-300000 // 128), 128), device="cuda")
@@ -137,3 +136,13 @@ def test_offsets_past_32_bits():
     c = mxq.gemm_fp8(a, sa, w, sw)["c"]
     cut = 128 * 2340
     assert torch.equal(c[:, cut:], mxq.gemm_fp8(a, sa, w[cut:].contiguous(), sw[2340:].contiguous())["c"])
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 1536, 2048), (40, 2560, 2064), (120, 2000, 1296), (129, 640, 2192), (64, 512, 8192),
+                                   (300, 700, 4112), (1100, 200, 1552), (2000, 2100, 400), (4096, 2560, 272), (2500, 2300, 144)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_shared_steps_and_cut_last_rounds(M, N, K, out):
+    """Sizes whose tiles are shared by clusters, and whose last round of tiles is cut; the same bits twice."""
+    ops = operands(M, N, K, seed=N)
+    c = check(ops, out)
+    assert all(torch.equal(mxq.gemm_fp8(*ops, out=out)["c"], c) for _ in range(10))
