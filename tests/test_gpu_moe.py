@@ -224,3 +224,23 @@ def test_outputs_stay_inside_their_buffers():
     assert torch.equal(yf[pad:-pad].view(T, H), mxq.moe_forward(x, ids, w, gu, dn, "nvfp4")["y"])
     assert bool((yf[:pad] == 3).all()) and bool((yf[-pad:] == 3).all())
     assert bool((ws[:256] == 0xA5).all()) and bool((ws[-256:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 8, 256, 128), (1, 8, 8, 1024, 512), (4, 2, 8, 2560, 128), (8, 1, 1, 2048, 1280),
+                                       (16, 2, 2, 256, 256), (3, 10, 4, 128, 640), (32, 1, 3, 4096, 128), (6, 5, 4, 4864, 384)])
+def test_small_layers(fmt, T, k, E, H, I):
+    """Few tasks: warps that share a row, tiles summed inside a CTA, several tiles to a CTA; rows without an expert."""
+    gu, dn = stacks(fmt, E, H, I, seed=T)
+    x = workloads.activation_tile(T, seed=T, device="cuda", hidden=H)
+    g = torch.Generator(device="cuda").manual_seed(H)
+    ids = torch.randint(-1, E, (T, k), dtype=torch.int32, generator=g, device="cuda")
+    ids[T // 2, k // 2:] = -1
+    if T > 2:
+        ids[0] = E - 1
+    out = check(x, ids, torch.rand((T, k), generator=g, device="cuda"), gu, dn, fmt)
+    assert int(out["status"].item()) == 0
+    ids[0, 0] = E
+    assert int(check(x, ids, torch.ones((T, k), device="cuda"), gu, dn, fmt)["status"].item()) == mxq.DEV_INVALID_EXPERT
+    ids[:] = -7
+    assert bool((mxq.moe_forward(x, ids, torch.ones((T, k), device="cuda"), gu, dn, fmt)["y"] == 0).all())
