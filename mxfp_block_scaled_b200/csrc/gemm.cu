@@ -25,8 +25,8 @@
 //
 // gemm_small_kernel (few rows: decoding).  The read of b is the bound.  A
 // warp multiplies 16 rows of b by up to 8 NT rows of a with mma.sync
-// m16n8k32; 8 warps of a CTA split K by blocks and add their sums in a fixed
-// order (1 x 2560 x 2048 2.8 us).  Both operands come straight from global memory: a lane's 16-byte
+// m16n8k32; 8 or 16 warps of a CTA split K by blocks and add their sums in a fixed
+// order (1 x 2560 x 2048 2.5 us).  Both operands come straight from global memory: a lane's 16-byte
 // pieces of a row of b and of a row of a hold the same k, and the order of k
 // inside a block is free.
 //
@@ -48,9 +48,10 @@ namespace {
 // second or two.
 constexpr uint32_t kGemmSpin = 1u << 20;
 // Rows that stream b through mma.sync: up to 16, and more while the whole product
-// is small.  Measured, tiles against streaming: 16 x 2560 x 2048 6.5 against
+// (with K counted as 1024 at least, a block a warp) is small.  Measured, tiles against streaming: 16 x 2560 x 2048 6.5 against
 // 3.4 us, 20 rows of it (0.1 G) 6.5 against 8.5; 20 x 1999 x 1552 (62 M) 7.5 against
-// 4.6, 33 x 2048 x 1280 (87 M) 5.0 against 7.2; 128 x 512 x 512 4.2 against 2.9.
+// 4.6, 33 x 2048 x 1280 (87 M) 5.0 against 7.2; 128 x 512 x 512 4.2 against 2.9; of
+// short rows 496 x 4567 x 16 5.6 against 47.6.
 // (At most 1024 rows of it, far inside the grid's second dimension.)
 constexpr int64_t kSmallM = 16, kSmallMaxM = 1024, kSmallWork = 64 << 20;
 
@@ -73,12 +74,12 @@ __device__ __forceinline__ void mma16832(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int NT, typename Out>
-__global__ void __launch_bounds__(256)
+template <int NT, int W, typename Out>
+__global__ void __launch_bounds__(32 * W)
 gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, const uint8_t *__restrict__ b,
                   const float *__restrict__ sb, uint32_t M, uint32_t N, uint32_t K, Out *__restrict__ c)
 {
-    __shared__ float red[8][NT * 8][17];
+    __shared__ float red[W][NT * 8][17];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
     const uint32_t n0 = blockIdx.x * 16u, m0 = blockIdx.y * (8u * NT), KB = (K + 127u) / 128u;
     cudaGridDependencySynchronize();
@@ -91,7 +92,7 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
     for (int i = 0; i < NT; ++i)
         acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
 #pragma unroll 2
-    for (uint32_t kb = warp; kb < KB; kb += 8u) {
+    for (uint32_t kb = warp; kb < KB; kb += W) {
         const uint32_t k0 = kb * 128u + t * 16u, k1 = k0 + 64u;
         const bool p0 = k0 < K, p1 = k1 < K;
         const uint4 x0 = r0 && p0 ? __ldg(reinterpret_cast<const uint4 *>(b0 + k0)) : zero;
@@ -124,11 +125,11 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
         for (int j = 0; j < 4; ++j)
             red[warp][i * 8 + t * 2 + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < NT * 128u; i += 256u) {
+    for (uint32_t i = threadIdx.x; i < NT * 128u; i += 32u * W) {
         const uint32_t m = i >> 4, n = i & 15u;
         float s = red[0][m][n];
 #pragma unroll
-        for (int w = 1; w < 8; ++w)
+        for (int w = 1; w < W; ++w)
             s += red[w][m][n];
         if (m0 + m < M && n0 + n < N)
             c[(uint64_t)(m0 + m) * N + n0 + n] = to_out<Out>(s);
@@ -365,6 +366,19 @@ __device__ __forceinline__ void store_rows(const float2 *acc, char *buf, Out *c,
                 if (m0 + row < p.M && n < p.N)
                     *reinterpret_cast<uint4 *>(c + (uint64_t)(m0 + row) * p.N + n) =
                         *reinterpret_cast<const uint4 *>(buf + row * 128u + ((q ^ (row & 7u)) << 4));
+            }
+            continue;
+        }
+        if (sizeof(Out) == 2 && (p.N & 1u) == 0) {      // two at a time
+            constexpr int lanes = used / 2, rows = 32 / lanes;
+            const uint32_t col = (lane % lanes) * 2u, sub = lane / lanes;
+            Out *o = c + (uint64_t)(m0 + sub) * p.N + nr + col;
+#pragma unroll 16
+            for (int i = 0; i < 32 / rows; ++i, o += (uint64_t)rows * p.N) {
+                const uint32_t row = i * rows + sub, at = col * 2u;
+                if (m0 + row < p.M && nr + col < p.N)
+                    *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(
+                        buf + row * 128u + (((at >> 4) ^ (row & 7u)) << 4) + (at & 15u));
             }
             continue;
         }
@@ -758,29 +772,36 @@ cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
 }
 
 template <int NT, typename Out>
-cudaError_t run_small(const GemmArgs &g, cudaStream_t s)
+cudaError_t run_small(const GemmArgs &g, int sms, cudaStream_t s)
 {
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.M + 8 * NT - 1) / (8 * NT)));
-    return launch_dependent(gemm_small_kernel<NT, Out>, grid, 256, 0, s, g.a, g.sa, g.b, g.sb, (uint32_t)g.M,
+    // More than one block of K a warp: twice the warps, where all CTAs are on the
+    // SMs at once (16 x 2048 x 1280 2.4 against 2.7 us, 31 x 53 x 4224 6.4 against
+    // 8.9; 16 x 8192 x 8192 23.5 against 17.6) or small (8 x 8192 x 8192 12.0 against
+    // 12.8).
+    if (g.K > 8 * 128 && (NT == 1 || grid.x * grid.y <= (unsigned)sms))
+        return launch_dependent(gemm_small_kernel<NT, 16, Out>, grid, 512, 0, s, g.a, g.sa, g.b, g.sb, (uint32_t)g.M,
+                                (uint32_t)g.N, (uint32_t)g.K, static_cast<Out *>(g.c));
+    return launch_dependent(gemm_small_kernel<NT, 8, Out>, grid, 256, 0, s, g.a, g.sa, g.b, g.sb, (uint32_t)g.M,
                             (uint32_t)g.N, (uint32_t)g.K, static_cast<Out *>(g.c));
 }
 
 template <typename Out>
 cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
 {
-    if (g.M <= kSmallM || (g.M <= kSmallMaxM && g.M * g.N <= kSmallWork / g.K)) {
-        if (g.M <= 8)
-            return run_small<1, Out>(g, s);
-        if (g.M <= 16)
-            return run_small<2, Out>(g, s);
-        return run_small<4, Out>(g, s);
-    }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
+    if (g.M <= kSmallM || (g.M <= kSmallMaxM && g.M * g.N <= kSmallWork / std::max<int64_t>(g.K, 1024))) {
+        if (g.M <= 8)
+            return run_small<1, Out>(g, sms, s);
+        if (g.M <= 16)
+            return run_small<2, Out>(g, sms, s);
+        return run_small<4, Out>(g, sms, s);
+    }
     // Tile width: the fewest rounds of tiles on the SMs, each at what a step of
     // that width took (0.57, 0.38 and 0.28 us).  A last round of few tiles of 256
     // columns is cut into halves or quarters of their columns.
@@ -804,18 +825,32 @@ cudaError_t gemm(const GemmArgs &g, cudaStream_t s)
             cut = 0;
         }
     }
-    // Few tiles: clusters of 2 or 4 CTAs share the steps of a tile of 64 columns,
+    // Few tiles: clusters of 2 or 4 CTAs share the steps of a tile,
     // at about 1.5 and 2.3 us for the join (64 x 2560 x 2048 6.6 us alone, 6.0 in
     // pairs; 64 x 1536 x 2048 6.9, 6.0 and 5.4; 64 x 512 x 8192 18.9, 12.0 and 8.3;
     // 64 x 2048 x 1280 5.0 and 5.3).  32 clusters of 4 are on the SMs at a time, 36
     // are not.
-    const int64_t kb = (g.K + 127) / 128, items = mt * ((g.N + 63) / 64);
-    const double alone = best * (double)kb, pairs = 1.5 + step[2] * (double)((kb + 1) / 2),
-                 fours = 2.3 + step[2] * (double)((kb + 3) / 4);
-    if (items <= 32 && fours < alone && fours < pairs)
-        return run_tile<64, Out, 4>(g, sms, 0, s);
-    if (items * 2 <= sms && pairs < alone)
-        return run_tile<64, Out, 2>(g, sms, 0, s);
+    const int64_t kb = (g.K + 127) / 128;
+    best *= (double)kb;
+    int share = 1;
+    for (uint32_t i = 1; i <= 2; ++i) {
+        const int64_t items = mt * ((g.N + (256 >> i) - 1) / (256 >> i));
+        const double pairs = 1.5 + step[i] * (double)((kb + 1) / 2), fours = 2.3 + step[i] * (double)((kb + 3) / 4);
+        if (items * 2 <= sms && pairs < best) {
+            best = pairs;
+            bn = 256 >> i;
+            share = 2;
+        }
+        if (items <= 32 && fours < best) {
+            best = fours;
+            bn = 256 >> i;
+            share = 4;
+        }
+    }
+    if (share == 2)
+        return bn == 128 ? run_tile<128, Out, 2>(g, sms, 0, s) : run_tile<64, Out, 2>(g, sms, 0, s);
+    if (share == 4)
+        return bn == 128 ? run_tile<128, Out, 4>(g, sms, 0, s) : run_tile<64, Out, 4>(g, sms, 0, s);
     if (bn == 256)
         return run_tile<256, Out, 1>(g, sms, cut, s);
     return bn == 128 ? run_tile<128, Out, 1>(g, sms, 0, s) : run_tile<64, Out, 1>(g, sms, 0, s);

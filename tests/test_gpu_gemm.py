@@ -146,3 +146,11 @@ def test_shared_steps_and_cut_last_rounds(M, N, K, out):
     ops = operands(M, N, K, seed=N)
     c = check(ops, out)
     assert all(torch.equal(mxq.gemm_fp8(*ops, out=out)["c"], c) for _ in range(10))
+
+
+@pytest.mark.parametrize("M,N,K", [(496, 1001, 16), (388, 700, 48), (77, 98, 5072), (31, 53, 4224), (620, 529, 2064), (416, 1100, 4112),
+                                   (9, 33, 1040), (16, 2600, 1168), (700, 310, 272), (260, 1002, 400), (1025, 66, 144)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_short_rows_long_rows_and_even_rows(M, N, K, out):
+    """Short and long K with few columns, rows of an even but not 16-byte length, tiles of 128 columns shared by pairs."""
+    check(operands(M, N, K, seed=K), out)
