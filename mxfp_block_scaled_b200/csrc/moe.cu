@@ -226,6 +226,63 @@ __device__ __forceinline__ uint32_t route_warp(const MoeArgs &a, const Route &r,
     return total >> 16;
 }
 
+// Up to 128: several lanes an assignment count the keys (expert, number) below its
+// own, which is its place in the list, and those of lower experts; the places
+// where groups begin are numbered by votes.  A layer of 84 assignments takes
+// 9.9 us with it and 12.0 with route_block, one of 216 16.0 and 15.2.
+template <int kWarps>
+__device__ __forceinline__ uint32_t route_ranks(const MoeArgs &a, const Route &r, uint32_t *buf, uint32_t *wsum)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    constexpr uint32_t none = 0xFFFFu, most = 128;
+    static_assert(kWarps * 32 >= 4 * most, "four lanes an assignment");
+    uint16_t *first = reinterpret_cast<uint16_t *>(buf + most);     // by place: the expert where a group begins
+    const uint32_t lg = a.A <= 64u ? 3u : 2u, i = tid >> lg, part = tid & ((1u << lg) - 1u);
+    bool valid = false;
+    if (tid < most) {
+        const int id = tid < a.A ? a.ids[tid] : -1;
+        valid = id >= 0 && id < (int)a.E;
+        if (id >= (int)a.E)
+            atomicOr(a.status, MXQ_DEV_INVALID_EXPERT);
+        buf[tid] = ((valid ? (uint32_t)id : none) << 16) | tid;
+    }
+    const uint32_t n = (uint32_t)__syncthreads_count(valid);
+    const uint32_t key = buf[i & (most - 1u)], expert = key >> 16, low = expert << 16;
+    uint32_t pos = 0, below = 0;
+    for (uint32_t q = part; q < (a.A + 3u) / 4u; q += 1u << lg) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(buf + q * 4u);
+        pos += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+        below += (k.x < low) + (k.y < low) + (k.z < low) + (k.w < low);
+    }
+    for (uint32_t o = 1; o < 1u << lg; o <<= 1) {
+        pos += __shfl_xor_sync(0xFFFFFFFFu, pos, o);
+        below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
+    }
+    if (part == 0 && i < a.A && expert != none) {
+        r.list[pos] = (uint16_t)i;
+        first[pos] = (uint16_t)((pos - below) % a.group == 0 ? expert : none);
+    }
+    __syncthreads();
+    const uint32_t e = tid < n ? first[tid] : none, vote = __ballot_sync(0xFFFFFFFFu, e != none);
+    if (lane == 0)
+        wsum[warp] = __popc(vote);
+    __syncthreads();
+    uint32_t at = __popc(vote & ((1u << lane) - 1u)), total = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < most / 32; ++w) {
+        at += w < warp ? wsum[w] : 0u;
+        total += wsum[w];
+    }
+    if (e != none) {
+        r.start[at] = (uint16_t)tid;
+        r.expert[at] = (uint16_t)e;
+    }
+    if (tid == 0)
+        r.start[total] = (uint16_t)n;
+    __syncthreads();
+    return total;
+}
+
 // More: ids, then counts and places of the experts in shared memory (E words
 // at `cnt`), a scan, and a scatter.  The order of a group's assignments is
 // free (each is a column of its own), but an expert's groups have to be the
@@ -440,7 +497,9 @@ moe_kernel(const MoeArgs a)
         }
         __syncthreads();
         r.groups = groups_s;
-    } else
+    } else if (a.A <= 128u)
+        r.groups = route_ranks<16>(a, r, reinterpret_cast<uint32_t *>(xs), wsum);
+    else
         r.groups = route_block<kWarps>(a, r, reinterpret_cast<uint32_t *>(xs), wsum);
     for (uint32_t k = tid * 16u; k < a.xstride; k += kThreads * 16u)
         *reinterpret_cast<uint4 *>(xs + a.cap * a.xstride + k) = make_uint4(0u, 0u, 0u, 0u);

@@ -244,3 +244,19 @@ def test_small_layers(fmt, T, k, E, H, I):
     assert int(check(x, ids, torch.ones((T, k), device="cuda"), gu, dn, fmt)["status"].item()) == mxq.DEV_INVALID_EXPERT
     ids[:] = -7
     assert bool((mxq.moe_forward(x, ids, torch.ones((T, k), device="cuda"), gu, dn, fmt)["y"] == 0).all())
+
+
+@pytest.mark.parametrize("T,k,E", [(33, 1, 4), (16, 4, 3), (13, 5, 70), (64, 2, 5), (43, 3, 11), (128, 2, 7), (32, 8, 4000), (51, 5, 2), (257, 1, 9)])
+def test_every_way_the_experts_are_listed(T, k, E):
+    """33 to 257 assignments with few, many and repeated experts, empty and invalid places."""
+    gu, dn = stacks("mxfp4", E, 128, 128, seed=E)
+    x = workloads.activation_tile(T, seed=T, device="cuda", hidden=128)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.randint(-1, E, (T, k), dtype=torch.int32, generator=g, device="cuda")
+    ids[T // 3: T // 2] = E - 1
+    w = torch.rand((T, k), generator=g, device="cuda")
+    out = check(x, ids, w, gu, dn, "mxfp4")
+    assert int(out["status"].item()) == 0
+    assert torch.equal(out["y"], mxq.moe_forward(x, ids, w, gu, dn, "mxfp4")["y"])
+    ids[T - 1, k - 1] = E + 5
+    assert int(check(x, ids, w, gu, dn, "mxfp4")["status"].item()) == mxq.DEV_INVALID_EXPERT
