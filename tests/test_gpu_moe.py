@@ -260,3 +260,21 @@ def test_every_way_the_experts_are_listed(T, k, E):
     assert torch.equal(out["y"], mxq.moe_forward(x, ids, w, gu, dn, "mxfp4")["y"])
     ids[T - 1, k - 1] = E + 5
     assert int(check(x, ids, w, gu, dn, "mxfp4")["status"].item()) == mxq.DEV_INVALID_EXPERT
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I", [(60, 1, 5, 256, 128), (33, 3, 4, 640, 384), (64, 4, 6, 2048, 128), (90, 1, 1, 384, 256),
+                                       (30, 1, 2, 128, 896), (47, 5, 13, 128, 128), (52, 2, 3, 1920, 256)])
+def test_many_assignments_to_an_expert(fmt, T, k, E, H, I):
+    """Many groups to an expert, the last of any size; some experts without any."""
+    gu, dn = stacks(fmt, E, H, I, seed=T)
+    x = workloads.activation_tile(T, seed=T, device="cuda", hidden=H)
+    g = torch.Generator(device="cuda").manual_seed(H)
+    ids = torch.randint(-1, E, (T, k), dtype=torch.int32, generator=g, device="cuda")
+    ids[ids == E // 2] = 0
+    ids[:9] = E - 1
+    w = torch.rand((T, k), generator=g, device="cuda")
+    out = check(x, ids, w, gu, dn, fmt)
+    assert int(out["status"].item()) == 0
+    for _ in range(5):
+        assert torch.equal(out["y"], mxq.moe_forward(x, ids, w, gu, dn, fmt)["y"])
