@@ -50,7 +50,7 @@
 //
 // Measured (512 experts, hidden 2048, inter 768, 10 experts a token): 64 tokens in
 // NVFP4 235 us for the 952 MB of the experts chosen (4.0 TB/s), in MXFP8 315 us for
-// 1.74 GB (5.5 TB/s); 16 in MXFP4 73 us; one in NVFP4 15.8 us.  What bounds it: of
+// 1.74 GB (5.5 TB/s); 16 in MXFP4 73 us; one in NVFP4 15.4 us.  What bounds it: of
 // the 235 us the copies alone take 177 and the arithmetic alone 155 to 173, most of
 // it conversions and scaling at two cycles an instruction; a token alone waits
 // through the chain of dependent steps (list, first weights, rows, sums, twice).
@@ -827,10 +827,11 @@ cudaError_t moe_gemm(MoeArgs a, int ctas, cudaStream_t s, bool &summed)
             ++a.kslog;
         return need(warps, depth, a.cap);
     };
-    // At most two tasks a warp of half the size: 8 warps and half the shared
-    // memory, so that the next launch fetches its first weights meanwhile
-    // (5 tokens of a tiny layer 7.9 us, with 16 warps 9.6).
-    const bool few = a.A <= 32 && most_tasks <= (uint64_t)ctas * 16;
+    // At most a task a warp: CTAs of 8 warps and half the shared memory, so that the
+    // next launch fetches its first weights meanwhile (5 tokens of a tiny layer
+    // 7.9 us, with 16 warps 9.6; up to two tasks a warp a token of 10 experts takes
+    // 15.8 us, so 15.4).
+    const bool few = a.A <= 32 && most_tasks <= (uint64_t)ctas * 8;
     // And, where a CTA's tiles of the down product make about a task a warp (as
     // many groups as assignments or experts) and the rows are short, it takes them
     // for all groups and adds up y itself: two launches instead of three, which
