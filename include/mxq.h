@@ -448,8 +448,12 @@ MXQ_API mxq_status mxq_quantize_fp8(const uint16_t *x, int64_t rows, int64_t col
  *   status   required (MXQ_DEV_WAIT_TIMEOUT).
  * Products are exact; their sums and the scaled sums of the blocks are fp32,
  * in an order that does not depend on scheduling (repeated calls give the
- * same bits; the order follows from M, N and K).  A NaN code makes
- * its row or column NaN.  No workspace. */
+ * same bits; the order follows from M, N, K, the number of SMs and whether
+ * scales far out are among those of the rows and columns computed together).
+ * Scales may have any value: where the product of two leaves fp32's normal
+ * numbers (below 2^-126, above 2^128), they are applied one after the other,
+ * and a result in fp32's range is right; such products are slower, up to 25
+ * times.  A NaN code makes its row or column NaN.  No workspace. */
 MXQ_API mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *b,
                                 const float *b_scales, int64_t M, int64_t N, int64_t K, mxq_out out,
                                 void *c, uint32_t *status, cudaStream_t stream);

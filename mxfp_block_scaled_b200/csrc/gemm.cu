@@ -30,6 +30,13 @@
 // pieces of a row of b and of a row of a hold the same k, and the order of k
 // inside a block is free.
 //
+// Scales far out.  sa sb is formed in fp32 and may leave its range where sa sb P does
+// not.  No sum pays for that: the streamed ones are formed in a range of their own
+// (kLift), and for the tiles the warps that bring the scales keep the smallest and the
+// largest of an item; where a product may leave the range the item's sums are formed
+// again from global memory (sum_far).  A choice at every step, by the summing warps, took
+// 4 to 8 % more time at 65536 x 2560 x 2048, by either way that was tried.
+//
 // Every wait is bounded: a wait that runs into its limit sets
 // MXQ_DEV_WAIT_TIMEOUT, all roles leave their loops, copies and products in
 // flight are awaited (bounded) and TMEM is freed.
@@ -62,6 +69,51 @@ __device__ __forceinline__ float to_out<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Factor f of a block's sum P from its two scales: f = a b.  Where that leaves the
+// normal numbers although neither scale is 0, Inf or NaN, the scaled sum may still be
+// in range (|P| is 0 or from 2^-18 to below 2^25); (P pre) f is formed instead.  Of
+// scales whose product underflows pre is the larger one (P pre overflows only if the
+// smaller were 0), of scales whose product overflows the smaller one, which is above
+// 1 (P pre overflows only if P a b does).
+__device__ __forceinline__ void split_scales(float a, float b, float &f, float &pre)
+{
+    f = a * b;
+    pre = 1.0f;
+    const uint32_t e = __float_as_uint(f) & 0x7F800000u;
+    if ((e == 0u || e == 0x7F800000u) && a != 0.0f && b != 0.0f && fabsf(a) < INFINITY && fabsf(b) < INFINITY) {
+        const bool a_first = (fabsf(a) > fabsf(b)) == (e == 0u);
+        pre = a_first ? a : b;
+        f = a_first ? b : a;
+    }
+}
+
+// Smallest magnitude that is not 0 and largest magnitude of some scales, as twice
+// their bits (less 1 for the smallest: zeros are then above everything).
+struct Extremes {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+    __device__ __forceinline__ void add(float s)
+    {
+        const uint32_t u = __float_as_uint(s) * 2u;
+        lo = min(lo, u - 1u);
+        hi = max(hi, u);
+    }
+    // Of the whole warp's.
+    __device__ __forceinline__ void reduce()
+    {
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    }
+    __device__ __forceinline__ float low() const { return __uint_as_float((lo >> 1) + (lo & 1u)); }
+    __device__ __forceinline__ float high() const { return __uint_as_float(hi >> 1); }
+};
+
+// Whether a product of a scale of each set may leave the normal numbers.
+__device__ __forceinline__ bool far_apart(const Extremes &a, const Extremes &b)
+{
+    const bool none = a.lo == 0xFFFFFFFFu || b.lo == 0xFFFFFFFFu;       // zeros only
+    return (!none && a.low() * b.low() < 0x1p-126f) || !(a.high() * b.high() < INFINITY);
+}
+
 // ------------------------------------------------------------- few rows --
 
 // c += A B: A 16 rows x 32 k, B 32 k x 8 columns, E4M3.
@@ -74,8 +126,101 @@ __device__ __forceinline__ void mma16832(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The blocks of K from `first` on, STEP apart and below `last`: 16 rows of b from n0 on times
+// 8 NT rows of a from m0 on, scaled and added up, the scales of a block kept apart where
+// their product would leave the range.  acc[i][j] is row m0 + 8 i + 2 (lane % 4) + (j & 1),
+// column n0 + lane / 4 + 8 (j >> 1).
+template <int NT, int STEP>
+__device__ __forceinline__ void split_blocks(const uint8_t *__restrict__ a, const float *__restrict__ sa,
+                                             const uint8_t *__restrict__ b, const float *__restrict__ sb, uint32_t M,
+                                             uint32_t N, uint32_t K, uint32_t m0, uint32_t n0, uint32_t first,
+                                             uint32_t last, uint32_t lane, float (&acc)[NT][4])
+{
+    const uint32_t g = lane >> 2, t = lane & 3u, KB = (K + 127u) / 128u;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool r0 = n0 + g < N, r1 = n0 + g + 8u < N;
+    const uint8_t *b0 = b + (uint64_t)(n0 + g) * K, *b1 = b0 + 8ull * K;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+#pragma unroll 1
+    for (uint32_t kb = first; kb < last; kb += STEP) {
+        const uint32_t k0 = kb * 128u + t * 16u, k1 = k0 + 64u;
+        const bool p0 = k0 < K, p1 = k1 < K;
+        const uint4 x0 = r0 && p0 ? __ldg(reinterpret_cast<const uint4 *>(b0 + k0)) : zero;
+        const uint4 x1 = r0 && p1 ? __ldg(reinterpret_cast<const uint4 *>(b0 + k1)) : zero;
+        const uint4 y0 = r1 && p0 ? __ldg(reinterpret_cast<const uint4 *>(b1 + k0)) : zero;
+        const uint4 y1 = r1 && p1 ? __ldg(reinterpret_cast<const uint4 *>(b1 + k1)) : zero;
+        const float wb = __ldg(sb + (uint64_t)(n0 >> 7) * KB + kb);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const uint32_t m = m0 + i * 8u + g, mc = m0 + i * 8u + t * 2u;
+            const uint8_t *ar = a + (uint64_t)m * K;
+            const uint4 v0 = m < M && p0 ? __ldg(reinterpret_cast<const uint4 *>(ar + k0)) : zero;
+            const uint4 v1 = m < M && p1 ? __ldg(reinterpret_cast<const uint4 *>(ar + k1)) : zero;
+            float f0, f1, pre0, pre1;
+            split_scales(mc < M ? __ldg(sa + (uint64_t)mc * KB + kb) : 0.0f, wb, f0, pre0);
+            split_scales(mc + 1u < M ? __ldg(sa + (uint64_t)(mc + 1u) * KB + kb) : 0.0f, wb, f1, pre1);
+            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16832(p, x0.x, y0.x, x0.y, y0.y, v0.x, v0.y);
+            mma16832(p, x0.z, y0.z, x0.w, y0.w, v0.z, v0.w);
+            mma16832(p, x1.x, y1.x, x1.y, y1.y, v1.x, v1.y);
+            mma16832(p, x1.z, y1.z, x1.w, y1.w, v1.z, v1.w);
+            acc[i][0] = fmaf(p[0] * pre0, f0, acc[i][0]);
+            acc[i][1] = fmaf(p[1] * pre1, f1, acc[i][1]);
+            acc[i][2] = fmaf(p[2] * pre0, f0, acc[i][2]);
+            acc[i][3] = fmaf(p[3] * pre1, f1, acc[i][3]);
+        }
+    }
+}
+
+// The streamed sums are formed times 2^64 and brought back at the end: a product of
+// two scales that underflows all the same (below 2^-190) adds less than 2^-165, nothing in
+// fp32.  One that overflows leaves Inf or NaN in a sum, and the CTA's sums are formed again.
+constexpr float kLift = 0x1p64f;
+
+// The warps' parts of the CTA's sums, added up in their order and brought back by `unit`, to
+// c.  True in threads that met one which is not finite.
 template <int NT, int W, typename Out>
-__global__ void __launch_bounds__(32 * W)
+__device__ __forceinline__ bool store_streamed(const float (*red)[NT * 8][17], float unit, uint32_t M, uint32_t N,
+                                               uint32_t m0, uint32_t n0, Out *c)
+{
+    bool far = false;
+    for (uint32_t i = threadIdx.x; i < NT * 128u; i += 32u * W) {
+        const uint32_t m = i >> 4, n = i & 15u;
+        float s = red[0][m][n];
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+            s += red[w][m][n];
+        if (m0 + m < M && n0 + n < N)
+            c[(uint64_t)(m0 + m) * N + n0 + n] = to_out<Out>(s * unit);
+        far |= !(fabsf(s) < INFINITY);
+    }
+    return far;
+}
+
+// The CTA's sums once more, with the scales kept apart.  Out of line: a call that is hardly
+// ever made costs the kernel no registers.
+template <int NT, int W, typename Out>
+__device__ __noinline__ void stream_again(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, uint32_t M,
+                                          uint32_t N, uint32_t K, float (*red)[NT * 8][17], Out *c)
+{
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
+    const uint32_t n0 = blockIdx.x * 16u, m0 = blockIdx.y * (8u * NT);
+    float acc[NT][4];
+    split_blocks<NT, W>(a, sa, b, sb, M, N, K, m0, n0, warp, (K + 127u) / 128u, lane, acc);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            red[warp][i * 8 + t * 2 + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
+    __syncthreads();
+    store_streamed<NT, W>(red, 1.0f, M, N, m0, n0, c);
+}
+
+// Up to 8 rows: 1024 threads an SM (with fewer, 1 x 2560 x 2048 takes a second round of CTAs).
+template <int NT, int W, typename Out>
+__global__ void __launch_bounds__(32 * W, NT == 1 ? 32 / W : 0)
 gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, const uint8_t *__restrict__ b,
                   const float *__restrict__ sb, uint32_t M, uint32_t N, uint32_t K, Out *__restrict__ c)
 {
@@ -99,7 +244,7 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
         const uint4 x1 = r0 && p1 ? __ldg(reinterpret_cast<const uint4 *>(b0 + k1)) : zero;
         const uint4 y0 = r1 && p0 ? __ldg(reinterpret_cast<const uint4 *>(b1 + k0)) : zero;
         const uint4 y1 = r1 && p1 ? __ldg(reinterpret_cast<const uint4 *>(b1 + k1)) : zero;
-        const float wb = __ldg(sb + (uint64_t)(n0 >> 7) * KB + kb);
+        const float wb = __ldg(sb + (uint64_t)(n0 >> 7) * KB + kb) * kLift;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const uint32_t m = m0 + i * 8u + g, mc = m0 + i * 8u + t * 2u;
@@ -125,15 +270,8 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
         for (int j = 0; j < 4; ++j)
             red[warp][i * 8 + t * 2 + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < NT * 128u; i += 32u * W) {
-        const uint32_t m = i >> 4, n = i & 15u;
-        float s = red[0][m][n];
-#pragma unroll
-        for (int w = 1; w < W; ++w)
-            s += red[w][m][n];
-        if (m0 + m < M && n0 + n < N)
-            c[(uint64_t)(m0 + m) * N + n0 + n] = to_out<Out>(s);
-    }
+    if (__syncthreads_or(store_streamed<NT, W>(red, 1.0f / kLift, M, N, m0, n0, c)))
+        stream_again<NT, W>(a, sa, b, sb, M, N, K, red, c);
 }
 
 // ------------------------------------------------------------ many rows --
@@ -156,6 +294,7 @@ struct Tile {
 };
 
 struct TileArgs {
+    const uint8_t *a, *b;
     const float *sa, *sb;
     void *c;
     uint32_t *status;
@@ -167,9 +306,14 @@ struct TileArgs {
     uint32_t tma_out;           // c is stored by TMA (rows of a multiple of 16 bytes)
 };
 
+// Items whose flags of far scales are kept: more than the scale warps run ahead, which
+// is by one step a buffer.
+constexpr uint32_t kFarRing = 8;
+
 struct TileBars {
     uint64_t full[8], empty[8], tfull[4], tempty[4], drain;
     uint32_t tmem, abort;
+    uint32_t far[2][kFarRing];      // by half of the rows and item: scales whose products may leave the range
 };
 
 // Item number -> its first row and column and its width, a whole tile of BN
@@ -465,16 +609,51 @@ __device__ __forceinline__ void store_sums(const float2 *acc, char *buf, const C
     }
 }
 
+// Whether a summing warp's item (the CTA's `item`-th, all of its steps read) has scales far out.
+__device__ __forceinline__ bool far_item(const TileBars &bars, uint32_t warp, uint32_t item)
+{
+    return __any_sync(0xFFFFFFFFu, bars.far[(warp & 3u) >> 1][item % kFarRing] != 0u);
+}
+
+// The sums of a warp's 32 rows and `cols` columns from (m0, n0) on over the K blocks
+// [k0, k1) once more, from global memory, with the scales of a block kept apart: for
+// items with scales far out, which take about ten times as long.  To c, or
+// (SHARE) to the partial sums [column / 4][row] of a cluster.
+template <typename Out, bool SHARE>
+__device__ __forceinline__ void sum_far(const TileArgs &p, void *dst, uint32_t m0, uint32_t n0, uint32_t cols, uint32_t k0,
+                                     uint32_t k1, uint32_t lane)
+{
+    for (uint32_t n = 0; n < cols; n += 16u) {
+        float acc[4][4];
+        split_blocks<4, 1>(p.a, p.sa, p.b, p.sb, p.M, p.N, p.K, m0, n0 + n, k0, n0 + n < p.N ? k1 : k0, lane, acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t row = i * 8u + (lane & 3u) * 2u + (j & 1), col = n + (lane >> 2) + (j >> 1) * 8u;
+                if (SHARE)
+                    static_cast<float *>(dst)[(col >> 2) * 512u + row * 4u + (col & 3u)] = acc[i][j];
+                else if (m0 + row < p.M && n0 + col < p.N)
+                    static_cast<Out *>(dst)[(uint64_t)(m0 + row) * p.N + n0 + col] = to_out<Out>(acc[i][j]);
+            }
+    }
+}
+
 template <int W, int BN, typename Out>
 __device__ __forceinline__ bool sum_item(const TileArgs &p, const CUtensorMap *mc, TileBars &bars,
                                          const float (*srow)[128], const float (*scol)[2], uint32_t tmem, char *buf,
                                          uint32_t m0, uint32_t n0, uint32_t warp, uint32_t lane, uint32_t &d,
-                                         uint32_t &dph)
+                                         uint32_t &dph, uint32_t item)
 {
     float2 acc[W / 4];
     if (!sum_steps<W, BN>(p, bars, srow, scol, tmem, p.KB, warp, lane, d, dph, acc))
         return false;
-    store_sums<W / 2, Out>(acc, buf, mc, m0 + (warp & 3u) * 32u, n0 + (warp >> 2) * (W / 2), p, lane);
+    m0 += (warp & 3u) * 32u;
+    n0 += (warp >> 2) * (W / 2);
+    if (far_item(bars, warp, item))
+        sum_far<Out, false>(p, p.c, m0, n0, W / 2, 0, p.KB, lane);
+    else
+        store_sums<W / 2, Out>(acc, buf, mc, m0, n0, p, lane);
     return true;
 }
 
@@ -617,7 +796,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             // the way: a load takes longer than a step.
             constexpr uint32_t kAhead = 4;
             const uint32_t sw = warp - (kEpiWarps + 2), r0 = sw * 64u + lane;
-            float now[3][kAhead], next[3][kAhead];       // this lane's two rows, and (lanes 0, 1 of the first warp) its columns
+            float now[3][kAhead], next[3][kAhead];       // this lane's two rows, and (lanes 0, 1) the columns
             uint32_t d = 0, dph = 1, ni = item0, nkb = k0;    // the chunk to load next
             bool ok = true;
             auto load = [&]() {
@@ -627,7 +806,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 item_at<BN>(p, ni, m0, n0, w);
                 const uint32_t row = m0 + r0, c0 = n0 + lane * (w / 2u);
                 const float *sa = p.sa + (uint64_t)row * p.KB + nkb, *sb = p.sb + (uint64_t)(c0 >> 7) * p.KB + nkb;
-                const bool in0 = row < p.M, in1 = row + 32u < p.M, inc = sw == 0 && lane < 2u && c0 < p.N;
+                const bool in0 = row < p.M, in1 = row + 32u < p.M, inc = lane < 2u && c0 < p.N;
     #pragma unroll
                 for (uint32_t j = 0; j < kAhead; ++j) {
                     const bool in = nkb + j < k1;
@@ -642,7 +821,9 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 }
             };
             load();
-            for (uint32_t i = item0; i < p.items && ok; i += items_on)
+            uint32_t item = 0;
+            for (uint32_t i = item0; i < p.items && ok; i += items_on, ++item) {
+                Extremes er, ec;                     // of the item's row and column scales
                 for (uint32_t kb = k0; kb < k1 && ok; kb += kAhead) {
     #pragma unroll
                     for (uint32_t j = 0; j < kAhead; ++j) {
@@ -662,6 +843,15 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                         srow[d][r0 + 32u] = now[1][j];
                         if (sw == 0 && lane < 2u)
                             scol[d][lane] = now[2][j];
+                        er.add(now[0][j]);
+                        er.add(now[1][j]);
+                        ec.add(now[2][j]);
+                        if (kb + j + 1u == k1) {
+                            er.reduce();
+                            ec.reduce();
+                            if (lane == 0)
+                                bars.far[sw][item % kFarRing] = far_apart(er, ec);
+                        }
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive(&bars.tfull[d]);
@@ -671,6 +861,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                         }
                     }
                 }
+            }
         }
     } else {                                         // sums
         regs_up<kSumRegs>();
@@ -686,6 +877,9 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             float4 *xs = reinterpret_cast<float4 *>(smem) + part * (cols / 4) * 128u + row;
             float2 acc[cols / 2];
             ok = sum_steps<BN, BN>(p, bars, srow, scol, tmem, k1 - k0, warp, lane, d, dph, acc);
+            if (ok && far_item(bars, warp, 0))
+                sum_far<Out, true>(p, xs - lane, m0 + quad * 32u, n0 + part * cols, cols, k0, k1, lane);
+            else
 #pragma unroll
             for (int q = 0; q < cols / 4; ++q)
                 xs[q * 128] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
@@ -705,15 +899,15 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             }
             if (ok)
                 store_sums<mine, Out>(sum, buf, &mc, m0 + quad * 32u, n0 + part * cols + rank * mine, p, lane);
-        } else for (uint32_t i = item0; i < p.items && ok; i += items_on) {
+        } else for (uint32_t i = item0, item = 0; i < p.items && ok; i += items_on, ++item) {
             uint32_t m0, n0, w;
             item_at<BN>(p, i, m0, n0, w);
             if (BN < 256 || w == BN)
-                ok = sum_item<BN, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph);
+                ok = sum_item<BN, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph, item);
             else if (w == 128)
-                ok = sum_item<128, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph);
+                ok = sum_item<128, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph, item);
             else
-                ok = sum_item<64, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph);
+                ok = sum_item<64, BN, Out>(p, &mc, bars, srow, scol, tmem, buf, m0, n0, warp, lane, d, dph, item);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -738,6 +932,8 @@ cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
 {
     using T = Tile<BN>;
     TileArgs p;
+    p.a = g.a;
+    p.b = g.b;
     p.sa = g.sa;
     p.sb = g.sb;
     p.c = g.c;
