@@ -32,7 +32,7 @@
  *     the device address of the fixed scratch array of
  *     mxq_dequant_relerr_noalloc (per device and context, see there), the
  *     host address of the driver's tensor-map encoder (mxq_gemm_fp8, looked
- *     up once) and the one-shot request flag of the test hook in mxq_test.h;
+ *     up once) and the one-shot request flags of the test hooks in mxq_test.h;
  *     nothing else.
  *   - All work is enqueued asynchronously on `stream` (0 = legacy default
  *     stream).  The call returns after enqueueing; results are valid once

@@ -24,6 +24,17 @@ extern "C" {
  * process); it is ignored by the other kernels. */
 MXQ_API void mxq_test_stall_next_single_pass(int on);
 
+/* Make the next mxq_gemm_fp8 launch that works on tiles (more than a few
+ * rows; the streamed product of few rows has no waits and ignores the
+ * request) stall on purpose: the scales of its first CTA's first step
+ * (`on` = 1) or last step (`on` = 2) are never reported as there, so the
+ * summing warps' wait for them runs into a limit, a shorter one than usual.
+ * The launch then ORs MXQ_DEV_WAIT_TIMEOUT into *status, waits for its copies
+ * and products in flight and returns; the result of that call is undefined
+ * and the device stays usable.  `on` = 0 withdraws a pending request.  Taken
+ * by exactly one launch, of any thread of the process. */
+MXQ_API void mxq_test_stall_next_product(int on);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,22 +38,30 @@
 // 4 to 8 % more time at 65536 x 2560 x 2048, by either way that was tried.
 //
 // Every wait is bounded: a wait that runs into its limit sets
-// MXQ_DEV_WAIT_TIMEOUT, all roles leave their loops, copies and products in
-// flight are awaited (bounded) and TMEM is freed.
+// MXQ_DEV_WAIT_TIMEOUT and all roles leave their loops.  The producer and the product
+// warp leave theirs, on that way and on the ordinary one, behind the last of what
+// they have started (bounded waits too): whichever role gives up, and when, no
+// copy or product is in flight where TMEM is freed and the CTA ends.
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq.h"
+#include "mxq_test.h"
 #include "mxq_tma.cuh"
 #include <algorithm>
+#include <atomic>
 
 namespace mxq {
 
 namespace {
 
-// Waits give up after this many tests; a test may suspend for a while in
-// hardware, so this is well above any wait that makes progress and below a
-// second or two.
-constexpr uint32_t kGemmSpin = 1u << 20;
+// Waits give up after this many tests; a test suspends for 4 us at most (measured),
+// so after a second (65 ms in a launch that was told to stall).  A wait that makes
+// progress takes up to some ms, where the sums of an item are formed again.
+constexpr uint32_t kGemmSpin = 1u << 18, kStalledSpin = 1u << 14;
+
+// Test hook (include/mxq_test.h): the next launch of tiles stalls on purpose.
+std::atomic<int> g_stall_product{0};
+
 // Rows that stream b through mma.sync: up to 16, and more while the whole product
 // (with K counted as 1024 at least, a block a warp) is small.  Measured, tiles against streaming: 16 x 2560 x 2048 6.5 against
 // 3.4 us, 20 rows of it (0.1 G) 6.5 against 8.5; 20 x 1999 x 1552 (62 M) 7.5 against
@@ -304,6 +312,8 @@ struct TileArgs {
     uint32_t whole, cut;        // tiles after the first `whole` are cut into 2^cut parts of their columns
     uint32_t items;             // whole tiles and parts
     uint32_t tma_out;           // c is stored by TMA (rows of a multiple of 16 bytes)
+    uint32_t spin;              // tests of a barrier before a wait gives up
+    uint32_t stall;             // test hook: 1, 2: the scales of CTA 0's first, last step are never reported
 };
 
 // Items whose flags of far scales are kept: more than the scale warps run ahead, which
@@ -336,17 +346,24 @@ __device__ __forceinline__ void item_at(const TileArgs &p, uint32_t i, uint32_t 
     n0 = (grp * p.group + (in - m * w)) * BN + part * width;
 }
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, TileBars &s, uint32_t *status)
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, TileBars &s, const TileArgs &p)
 {
-    for (uint32_t i = 0; i < kGemmSpin; ++i) {
+    for (uint32_t i = 0; i < p.spin; ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
         if ((i & 63u) == 63u && *reinterpret_cast<volatile uint32_t *>(&s.abort))
             return false;
     }
     *reinterpret_cast<volatile uint32_t *>(&s.abort) = 1u;
-    atomicOr(status, MXQ_DEV_WAIT_TIMEOUT);
+    atomicOr(p.status, MXQ_DEV_WAIT_TIMEOUT);
     return false;
+}
+
+// The same for a role that leaves: it waits whether or not another one gave up.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < kGemmSpin && !mbar_try_wait(bar, parity); ++i)
+        ;
 }
 
 // Shared-memory descriptor of a K-major operand tile, rows of 128 bytes with
@@ -560,7 +577,7 @@ __device__ __forceinline__ bool sum_steps(const TileArgs &p, TileBars &bars, con
     for (int j = 0; j < cols / 2; ++j)
         acc[j] = make_float2(0.0f, 0.0f);
     for (uint32_t kb = 0; kb < steps; ++kb) {
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(&bars.tfull[d], dph, bars, p.status)))
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(&bars.tfull[d], dph, bars, p)))
             return false;
         fence_after();
         const float f = rows[d * 128u] * col[d * 2u];
@@ -732,7 +749,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 uint32_t m0, n0, w;
                 item_at<BN>(p, i, m0, n0, w);
                 for (uint32_t kb = k0; kb < k1; ++kb) {
-                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.empty[s], ph, bars, p.status))))
+                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.empty[s], ph, bars, p))))
                         break;
                     char *dst = smem + s * T::bytes;
                     expect_tx(&bars.full[s], (128u + w) * 128u, one);
@@ -747,16 +764,11 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     }
                 }
             }
-            if (!ok) {
-                // copies in flight: the last fill of every stage.  Stages before
-                // s were filled in the current pass over the ring (phase ph ^ 1),
-                // the others in the pass before.
-                for (uint32_t k = 0; k < (uint32_t)T::stages; ++k) {
-                    const uint32_t par = k < s ? ph ^ 1u : ph;
-                    for (uint32_t n = 0; n < kGemmSpin && !mbar_try_wait(&bars.full[k], par); ++n)
-                        ;
-                }
-            }
+            // The last fill of every stage has landed.  Stages before s were filled in the
+            // current pass over the ring (phase ph ^ 1), the others in the pass before
+            // (a stage never filled passes the wait for its odd phase).
+            for (uint32_t k = 0; k < (uint32_t)T::stages; ++k)
+                wait_out(&bars.full[k], k < s ? ph ^ 1u : ph);
         } else if (warp == kEpiWarps + 1) {          // product
             const uint32_t one = elect_one();
             uint32_t s = 0, ph = 0, d = 0, dph = 1;
@@ -765,7 +777,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                 const uint32_t w = BN == 256 && i >= p.whole ? BN >> p.cut : BN;
                 const uint32_t idesc = (1u << 4) | ((w / 8u) << 17) | ((128u / 16u) << 24);
                 for (uint32_t kb = k0; kb < k1; ++kb) {
-                    ok = wait_bar(&bars.tempty[d], dph, bars, p.status) && wait_bar(&bars.full[s], ph, bars, p.status);
+                    ok = wait_bar(&bars.tempty[d], dph, bars, p) && wait_bar(&bars.full[s], ph, bars, p);
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
                         break;
                     fence_after();
@@ -786,11 +798,8 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     }
                 }
             }
-            if (!ok) {                               // products in flight
-                umma_commit(&bars.drain, one);
-                for (uint32_t n = 0; n < kGemmSpin && !mbar_try_wait(&bars.drain, 0); ++n)
-                    ;
-            }
+            umma_commit(&bars.drain, one);           // every product is done
+            wait_out(&bars.drain, 0);
         } else {                                         // scales: two warps, 64 rows each
             // kAhead steps' scales at a time, and those of the steps after them on
             // the way: a load takes longer than a step.
@@ -836,7 +845,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                     for (uint32_t j = 0; j < kAhead; ++j) {
                         if (kb + j >= k1 || !ok)
                             break;
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tempty[d], dph, bars, p.status));
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars.tempty[d], dph, bars, p));
                         if (!ok)
                             break;
                         srow[d][r0] = now[0][j];
@@ -853,7 +862,10 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
                                 bars.far[sw][item % kFarRing] = far_apart(er, ec);
                         }
                         __syncwarp();
-                        if (lane == 0)
+                        const bool held = p.stall != 0u && blockIdx.x == 0 && sw == 0 &&
+                                          (p.stall == 1u ? i == item0 && kb + j == k0
+                                                         : i + items_on >= p.items && kb + j + 1u == k1);
+                        if (lane == 0 && !held)
                             mbar_arrive(&bars.tfull[d]);
                         if (++d == T::bufs) {
                             d = 0;
@@ -873,16 +885,18 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__
             const uint32_t quad = warp & 3u, part = warp >> 2, row = quad * 32u + lane;
             uint32_t m0, n0, w;
             item_at<BN>(p, item0, m0, n0, w);
-            // [part][column / 4][row], in the ring of stages, which is empty now
+            // [part][column / 4][row], in the ring of stages
             float4 *xs = reinterpret_cast<float4 *>(smem) + part * (cols / 4) * 128u + row;
             float2 acc[cols / 2];
             ok = sum_steps<BN, BN>(p, bars, srow, scol, tmem, k1 - k0, warp, lane, d, dph, acc);
+            // All steps read: the ring is empty.  After a wait that ran out it may not be, and
+            // is left alone (the cluster's result is undefined then).
             if (ok && far_item(bars, warp, 0))
                 sum_far<Out, true>(p, xs - lane, m0 + quad * 32u, n0 + part * cols, cols, k0, k1, lane);
-            else
+            else if (ok)
 #pragma unroll
-            for (int q = 0; q < cols / 4; ++q)
-                xs[q * 128] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
+                for (int q = 0; q < cols / 4; ++q)
+                    xs[q * 128] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
             cluster_sync_all();
             float2 sum[mine / 2];
 #pragma unroll
@@ -959,6 +973,8 @@ cudaError_t run_tile(const GemmArgs &g, int sms, uint32_t cut, cudaStream_t s)
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
+    p.stall = g_stall_product.load() ? (uint32_t)g_stall_product.exchange(0) : 0u;
+    p.spin = p.stall ? kStalledSpin : kGemmSpin;
     const uint32_t tiles = p.mt * p.nt;
     p.cut = cut;
     p.whole = cut ? tiles - tiles % (uint32_t)sms : tiles;
@@ -1060,3 +1076,8 @@ cudaError_t launch_gemm_fp8(const GemmArgs &g, int out_f32, cudaStream_t s)
 }
 
 } // namespace mxq
+
+extern "C" MXQ_API void mxq_test_stall_next_product(int on)
+{
+    mxq::g_stall_product.store(on == 1 || on == 2 ? on : 0);
+}

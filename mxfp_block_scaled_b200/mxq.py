@@ -108,6 +108,8 @@ def load(path=LIB_PATH):
                                   vp, sz, vp]
     L.mxq_test_stall_next_single_pass.restype = None
     L.mxq_test_stall_next_single_pass.argtypes = [i32]
+    L.mxq_test_stall_next_product.restype = None
+    L.mxq_test_stall_next_product.argtypes = [i32]
     if path == LIB_PATH:
         _lib = L
     return L
