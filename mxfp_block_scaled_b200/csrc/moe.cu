@@ -785,7 +785,10 @@ template <int FMT, bool GATE_UP, int D, int W, bool SPLIT, bool WHOLE = false>
 cudaError_t run(const MoeArgs &a, size_t smem, int ctas, cudaStream_t s)
 {
     const auto k = moe_kernel<FMT, GATE_UP, D, W, SPLIT, WHOLE>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The limit belongs to the kernel, not to the launch: always the largest, so that
+    // calls of other sizes from other threads set the same.
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(W == 8 ? kSmemHalf : kSmemMax));
     if (e != cudaSuccess)
         return e;
     return launch_dependent(k, dim3((unsigned)ctas), 32 * W, smem, s, a);
