@@ -578,6 +578,14 @@ cudaError_t launch_group_amax(const uint16_t *x, int64_t n_groups, int64_t nb,
 // purpose and must end with MXQ_DEV_WAIT_TIMEOUT.
 static std::atomic<int> g_test_stall{0};
 
+// The limit of a kernel's dynamic shared memory belongs to the kernel, not to a
+// launch: always the largest that its launches ask for on the device, so that
+// calls of other sizes from other threads set the same.
+static cudaError_t set_smem_limit(const void *fn, int bytes)
+{
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 static int sm_count()
 {
     int dev = 0, n = 0;
@@ -645,7 +653,7 @@ cudaError_t launch_nvfp4_fused(const uint16_t *x, int64_t n_groups, int64_t nb, 
                                         : (const void *)nvfp4_fused_kernel<true, false>)
                               : (sl.swz ? (const void *)nvfp4_fused_kernel<false, true>
                                         : (const void *)nvfp4_fused_kernel<false, false>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+    cudaError_t e = set_smem_limit(fn, max_optin - 2048);
     if (e != cudaSuccess)
         return e;
     int per_sm = 0;
@@ -834,7 +842,7 @@ cudaError_t launch_nvfp4_small(const uint16_t *x, int64_t nb, int four_six, uint
                                         : (const void *)nvfp4_small_kernel<true, false>)
                               : (sl.swz ? (const void *)nvfp4_small_kernel<false, true>
                                         : (const void *)nvfp4_small_kernel<false, false>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+    cudaError_t e = set_smem_limit(fn, max_optin - 4096);
     if (e == cudaSuccess && P > 8)
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
@@ -1071,7 +1079,7 @@ cudaError_t launch_nvfp4_grid(const uint16_t *x, int64_t nb, int four_six, uint8
                                         : (const void *)nvfp4_grid_kernel<true, false>)
                               : (sl.swz ? (const void *)nvfp4_grid_kernel<false, true>
                                         : (const void *)nvfp4_grid_kernel<false, false>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+    cudaError_t e = set_smem_limit(fn, max_optin - 2048);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return cudaErrorNotSupported;

@@ -59,3 +59,27 @@ def test_layers_of_different_sizes_at_once():
     _together(jobs, 1500)
     for y, want, st in results:
         assert torch.equal(y, want) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("shapes", [[(1, T, 2048) for T in (300, 400, 500, 640)],        # a cluster
+                                    [(8, 256, 2048), (8, 768, 512), (24, 128, 512), (50, 96, 512)],
+                                    [(1, T, 2048) for T in (1024, 3000, 4096, 5000)]])   # a grid    # one pass over several groups
+def test_quantizers_of_different_sizes_at_once(shapes):
+    jobs, results = [], []
+    for i, (G, R, C) in enumerate(shapes):
+        x = torch.randn((G, R, C), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda").to(torch.bfloat16)
+        want, stream = mxq.quantize_nvfp4(x), torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = {k: torch.zeros_like(v) for k, v in want.items() if torch.is_tensor(v)}
+            ws, _ = mxq._workspace("quantize_nvfp4", G, R, C, x.device)
+        torch.cuda.synchronize()
+
+        def job(x=x, G=G, R=R, C=C, o=got, ws=ws, stream=stream):
+            mxq.mxq_quantize_nvfp4(x, G, R, C, "four_six", "linear", o["codes"], o["scales"], o["s2"], o["mbits"], o["m4_count"],
+                                   o["status"], ws, stream=stream)
+        jobs.append(job)
+        results.append((got, want))
+    _together(jobs, 3000)
+    for got, want in results:
+        assert int(got["status"].item()) == 0
+        assert all(torch.equal(got[k], want[k]) for k in ("codes", "scales", "s2"))
