@@ -34,9 +34,12 @@ __device__ __forceinline__ uint32_t fold_halves(uint32_t m) { return max(m & 0x7
 // ---- packed conversions (PTX ISA: cvt with .e2m1x2 / .e4m3x2) ------------
 // Two fp32 values -> one byte of two E2M1 codes (lo in the low nibble),
 // round to nearest even, saturating at +-6, sign kept; zero-extended.
-// Bytes move between .b8 and 32-bit registers only with cvt.u8.u32 /
-// cvt.u32.u8: vector moves of .b8 registers ({b0, b1, ...}) corrupted
-// bytes when a packed word was unpacked again in the same kernel.
+// A byte moves from a .b8 register into a 32-bit one, and back out of a word that
+// the same kernel has packed, only with cvt.u32.u8 / cvt.u8.u32: where a vector move
+// of .b8 registers ({b0, b1, ...}) had packed the word, a vector move that unpacked it
+// again gave other bytes.  Words that come from memory are not concerned; the layer's
+// decoder (moe.cu) takes them apart that way, and tests/test_gpu_decode.py sees every
+// byte value at every place of a word through each of its kernels.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi)
 {
     uint32_t out;
