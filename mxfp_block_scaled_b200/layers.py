@@ -51,12 +51,20 @@ def quantize_routed_layer(gate_up, down, fmt="nvfp4", mode="four_six", stream=No
 
 def block_fp8_layer(gate_up, down, stream=None):
     """A stacked routed-expert layer in block FP8 (E4M3, one fp32 scale per
-    128 x 128 block), the format of the layers a mixed model retains; 2I and H
-    multiples of 128.  {"gate_up": q, "down": q} for routed_forward."""
+    128 x 128 block), the format of the layers a mixed model retains.  gate_up
+    [E, 2I, H] and down [E, H, I] with I and H multiples of 128: no block then
+    holds rows of both gate and up, and routed_forward can run the layer (up to
+    its own limits).  {"gate_up": q, "down": q} for routed_forward."""
+    for name, x in (("gate_up", gate_up), ("down", down)):
+        if x.dim() != 3:
+            raise ValueError("%s: a stack of matrices [E, R, C]" % name)
+    E, H, I = down.shape
+    if tuple(gate_up.shape) != (E, 2 * I, H):
+        raise ValueError("gate_up %s does not go with down %s" % (list(gate_up.shape), list(down.shape)))
+    if H % 128 or I % 128:
+        raise ValueError("stacks of hidden %d and inter %d: both must be multiples of 128" % (H, I))
     out = {}
     for name, x in (("gate_up", gate_up), ("down", down)):
-        if x.dim() != 3 or x.shape[1] % 128:
-            raise ValueError("%s: a stack [E, R, C] with R a multiple of 128" % name)
         out[name] = dict(mxq.quantize_fp8(x, 128, stream=stream), fmt="fp8_block")
     return out
 
@@ -64,8 +72,9 @@ def block_fp8_layer(gate_up, down, stream=None):
 def routed_forward(layer_q, x, topk_ids, topk_weights, workspace=None, stream=None):
     """y[t] = sum_j w[t, j] down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j],
     of a converted layer (a quantize_routed_layer or block_fp8_layer result)
-    for a few tokens.  x: bf16 [T, H]; topk_ids int32, topk_weights fp32
-    [T, k].  Returns dict y bf16 [T, H], status."""
+    for a few tokens: T and T * k at most 2048, H and inter multiples of 128 up
+    to 8192, at most 4096 experts, linear scales.  x: bf16 [T, H]; topk_ids
+    int32, topk_weights fp32 [T, k].  Returns dict y bf16 [T, H], status."""
     gu, dn = layer_q["gate_up"], layer_q["down"]
     if gu["fmt"] != dn["fmt"]:
         raise ValueError("gate_up is %s, down is %s" % (gu["fmt"], dn["fmt"]))
