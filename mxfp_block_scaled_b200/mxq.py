@@ -331,8 +331,16 @@ def mxq_dequant_relerr_noalloc(x, codes, scales, s2, fmt, n_tensors, rows, cols,
 
 
 # The layer operators are called once per layer and token, so their checks are
-# kept light.  They run on the device of their first tensor, whichever is
-# current, and refuse buffers that lie on different ones.
+# kept light.  They run on the device of their first buffer that is not None
+# (data of zero bytes may be), whichever device is current, and refuse buffers
+# that lie on different ones.
+def _first(*bufs):
+    for t in bufs:
+        if t is not None:
+            return t
+    raise ValueError("no buffer given")
+
+
 def _device(t):
     dev = t.get_device()
     if dev < 0:
@@ -360,7 +368,7 @@ def _enqueue(fn, args, dev, stream):
 
 
 def mxq_quantize_fp8(x, rows, cols, brows, bcols, codes, scales, status, stream=None):
-    dev, n = _device(x), rows * cols
+    dev, n = _device(_first(x, status)), rows * cols
     nblk = -(-rows // brows) * -(-cols // bcols) if brows > 0 and bcols > 0 else 0
     rc = _enqueue(load().mxq_quantize_fp8,
                   (_buf("x", x, 2 * n, dev), rows, cols, brows, bcols, _buf("codes", codes, n, dev),
@@ -369,7 +377,7 @@ def mxq_quantize_fp8(x, rows, cols, brows, bcols, codes, scales, status, stream=
 
 
 def mxq_gemm_fp8(a, a_scales, b, b_scales, M, N, K, out, c, status, stream=None):
-    dev, kb = _device(a), -(-K // 128)
+    dev, kb = _device(_first(a, status)), -(-K // 128)
     rc = _enqueue(load().mxq_gemm_fp8,
                   (_buf("a", a, M * K, dev), _buf("a_scales", a_scales, 4 * M * kb, dev), _buf("b", b, N * K, dev),
                    _buf("b_scales", b_scales, 4 * -(-N // 128) * kb, dev), M, N, K, OUT[out],
@@ -389,7 +397,7 @@ def moe_weight_bytes(fmt, experts, rows, cols):
 def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, inter, gate_up_codes,
                     gate_up_scales, gate_up_s2, down_codes, down_scales, down_s2, y, status, workspace,
                     stream=None):
-    dev = _device(x)
+    dev = _device(_first(x, status))
     gc, gs = moe_weight_bytes(fmt, experts, 2 * inter, hidden)
     dc, ds = moe_weight_bytes(fmt, experts, hidden, inter)
     s2 = 4 * experts if fmt == "nvfp4" else 0
