@@ -565,7 +565,7 @@ mxq_status mxq_gemm_fp8(const uint8_t *a, const float *a_scales, const uint8_t *
     const int64_t kMax = 0x7FFFFF00ll;      // rows, columns and values are indexed in 32 bits
     int64_t mn, mk, nk;
     if (M > kMax || N > kMax || K > kMax || !mul_ok(M, N, &mn) || !mul_ok(M, K, &mk) || !mul_ok(N, K, &nk) ||
-        ((M + 127) / 128) * ((N + 63) / 64) > kMax || (M + 7) / 8 > kMax)
+        ((M + 127) / 128) * ((N + 63) / 64) > kMax)
         return MXQ_ERR_SHAPE;
     if (mn == 0)
         return MXQ_OK;

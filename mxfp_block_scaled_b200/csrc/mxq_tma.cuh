@@ -1,22 +1,11 @@
-// mxq_tma.cuh -- tensor maps of byte matrices and the TMA load that uses them
-// (sm_100a; PTX ISA, cp.async.bulk.tensor).
+// mxq_tma.cuh -- tensor maps of matrices, for cp.async.bulk.tensor (sm_100a).
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "mxq_device.cuh"
-
 namespace mxq {
-
-// Box at byte column x (a multiple of 16) and row y of the map's matrix ->
-// shared memory, counted in bytes on `bar`; what lies past the matrix is 0.
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint32_t x, uint32_t y, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-                 ::"r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y) : "memory");
-}
 
 // The driver's encoder of tensor maps (the library links the runtime only);
 // its address, the same for every device, is looked up once.
