@@ -497,10 +497,11 @@ MXQ_API size_t mxq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t hidden, 
  * T * topk and T at most 2048, experts at most 4096 (MXQ_ERR_UNSUPPORTED) and
  * at least 1 (MXQ_ERR_INVALID_ARG).  T or hidden 0 leaves everything as it is;
  * topk or inter 0 gives rows of zeros.
- * Sums are fp32 in a fixed order: repeated calls give the same bits.  They are
- * formed over the token's row scaled so that its largest element is about 2^15,
- * and h is rounded to 11 bits in the same way; block scales above about 2^80
- * may overflow. */
+ * Sums are fp32 in a fixed order (it follows from the sizes and the number of
+ * SMs): repeated calls give the same bits.  They are formed over the token's
+ * row scaled so that its largest element is about 2^15, and h is rounded to 11
+ * bits in the same way; block scales (NVFP4: s2) above about 2^80 may overflow,
+ * and below about 2^-100 sums lose bits. */
 MXQ_API mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden,
                                    const int32_t *topk_ids, const float *topk_weights, int64_t topk,
                                    mxq_fmt fmt, int64_t experts, int64_t inter,

@@ -20,13 +20,14 @@
 // took 17 % more time.  The service warps hand most of their registers to the
 // summing ones (setmaxnreg), whose 128 sums a thread leave room to read one part
 // of a buffer while the part before is added.  What bounds it: the sums.  At
-// 65536 x 2560 x 2048 (bf16) it takes 320 us (2.15 PFLOP/s), about 360 under the
-// power limit; the same products and copies without sums and stores take 224.
+// 65536 x 2560 x 2048 (bf16) it takes 328 us in a burst (2.1 PFLOP/s), 370 to 390
+// under the power limit; the same products and copies without sums and stores take
+// 224.
 //
 // gemm_small_kernel (few rows: decoding).  The read of b is the bound.  A
 // warp multiplies 16 rows of b by up to 8 NT rows of a with mma.sync
 // m16n8k32; 8 or 16 warps of a CTA split K by blocks and add their sums in a fixed
-// order (1 x 2560 x 2048 2.5 us).  Both operands come straight from global memory: a lane's 16-byte
+// order (1 x 2560 x 2048 2.6 us).  Both operands come straight from global memory: a lane's 16-byte
 // pieces of a row of b and of a row of a hold the same k, and the order of k
 // inside a block is free.
 //
@@ -384,7 +385,7 @@ __device__ __forceinline__ uint32_t elect_one()
 // The instructions below are issued by the lane whose `one` is 1, inside code
 // that the whole warp runs: their descriptors and addresses then stay in
 // uniform registers.  In a branch of one thread each product took 85 cycles to
-// issue, and a step of four with its commits 710 instead of 512.
+// issue, and a step of four with its commits 710 cycles instead of 512.
 __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one)
 {
     asm volatile("{\n\t.reg .pred p, q;\n\t"

@@ -49,8 +49,8 @@
 // 2^-11 a value, an eighth of the bf16 output's own rounding).
 //
 // Measured (512 experts, hidden 2048, inter 768, 10 experts a token): 64 tokens in
-// NVFP4 235 us for the 952 MB of the experts chosen (4.0 TB/s), in MXFP8 315 us for
-// 1.74 GB (5.5 TB/s); 16 in MXFP4 73 us; one in NVFP4 15.4 us.  What bounds it: of
+// NVFP4 235 us for the 952 MB of the experts chosen (4.0 TB/s), in MXFP8 294 us for
+// 1.74 GB (5.9 TB/s); 16 in MXFP4 73 us; one in NVFP4 15.3 us.  What bounds it: of
 // the 235 us the copies alone take 177 and the arithmetic alone 155 to 173, most of
 // it conversions and scaling at two cycles an instruction; a token alone waits
 // through the chain of dependent steps (list, first weights, rows, sums, twice).
