@@ -27,7 +27,7 @@
 // gemm_small_kernel (few rows: decoding).  The read of b is the bound.  A
 // warp multiplies 16 rows of b by up to 8 NT rows of a with mma.sync
 // m16n8k32; 8 or 16 warps of a CTA split K by blocks and add their sums in a fixed
-// order (1 x 2560 x 2048 2.6 us).  Both operands come straight from global memory: a lane's 16-byte
+// order (1 x 2560 x 2048 2.4 us).  Both operands come straight from global memory: a lane's 16-byte
 // pieces of a row of b and of a row of a hold the same k, and the order of k
 // inside a block is free.
 //
@@ -185,16 +185,15 @@ __device__ __forceinline__ void split_blocks(const uint8_t *__restrict__ a, cons
 
 // The streamed sums are formed times 2^64 and brought back at the end: a product of
 // two scales that underflows all the same (below 2^-190) adds less than 2^-165, nothing in
-// fp32.  One that overflows leaves Inf or NaN in a sum, and the CTA's sums are formed again.
-constexpr float kLift = 0x1p64f;
+// fp32.  One that overflows leaves Inf or NaN in a warp's part of a sum, and the CTA's sums
+// are formed again; so they are where a part reaches kFar, since up to 16 of them are added.
+constexpr float kLift = 0x1p64f, kFar = 0x1p120f;
 
-// The warps' parts of the CTA's sums, added up in their order and brought back by `unit`, to
-// c.  True in threads that met one which is not finite.
+// The warps' parts of the CTA's sums, added up in their order and brought back by `unit`, to c.
 template <int NT, int W, typename Out>
-__device__ __forceinline__ bool store_streamed(const float (*red)[NT * 8][17], float unit, uint32_t M, uint32_t N,
+__device__ __forceinline__ void store_streamed(const float (*red)[NT * 8][17], float unit, uint32_t M, uint32_t N,
                                                uint32_t m0, uint32_t n0, Out *c)
 {
-    bool far = false;
     for (uint32_t i = threadIdx.x; i < NT * 128u; i += 32u * W) {
         const uint32_t m = i >> 4, n = i & 15u;
         float s = red[0][m][n];
@@ -203,9 +202,7 @@ __device__ __forceinline__ bool store_streamed(const float (*red)[NT * 8][17], f
             s += red[w][m][n];
         if (m0 + m < M && n0 + n < N)
             c[(uint64_t)(m0 + m) * N + n0 + n] = to_out<Out>(s * unit);
-        far |= !(fabsf(s) < INFINITY);
     }
-    return far;
 }
 
 // The CTA's sums once more, with the scales kept apart.  Out of line: a call that is hardly
@@ -278,9 +275,16 @@ gemm_small_kernel(const uint8_t *__restrict__ a, const float *__restrict__ sa, c
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             red[warp][i * 8 + t * 2 + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
-    __syncthreads();
-    if (__syncthreads_or(store_streamed<NT, W>(red, 1.0f / kLift, M, N, m0, n0, c)))
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            far |= !(fabsf(acc[i][j]) < kFar);
+    if (__syncthreads_or(far))
         stream_again<NT, W>(a, sa, b, sb, M, N, K, red, c);
+    else
+        store_streamed<NT, W>(red, 1.0f / kLift, M, N, m0, n0, c);
 }
 
 // ------------------------------------------------------------ many rows --
