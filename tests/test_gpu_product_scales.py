@@ -106,3 +106,44 @@ def test_tiny_tokens_against_ordinary_weights(M):
     t = mxq.quantize_fp8(x)
     c, _ = _close(t["codes"], t["scales"], w["codes"], w["scales"])
     assert torch.equal(layers.fp8_linear(x, w, out="f32")["c"], c)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES + [(700, 311, 400), (9, 77, 272), (129, 642, 2192)])       # rows of odd and even lengths too
+def test_bf16_results_are_the_fp32_ones_rounded(M, N, K):
+    """Far scales and ordinary ones, some of the blocks 0: the same sums, rounded once; memory beside the result is left alone."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    a, b, kb, pad = _codes(g, M, K, 0, 0x50), _codes(g, N, K, 0, 0x50), -(-K // 128), 512
+    for la, lb in ((-100, -40), (60, 50), (-3, -3)):
+        sa, sb = _scales(g, (M, kb), la, la + 4), _scales(g, (-(-N // 128), kb), lb, lb + 4)
+        sa[M // 2, kb // 2], sb[0, 0] = 0, 0
+        full = torch.full((M * N + 2 * pad,), 3.0, dtype=torch.bfloat16, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        mxq.mxq_gemm_fp8(a, sa, b, sb, M, N, K, "bf16", full[pad:pad + M * N], st)
+        c = mxq.gemm_fp8(a, sa, b, sb, out="f32")["c"]
+        assert int(st.item()) == 0 and bool(torch.isfinite(c).all())
+        assert torch.equal(full[pad:pad + M * N].view(M, N), c.to(torch.bfloat16))
+        assert bool((full[:pad] == 3).all()) and bool((full[pad + M * N:] == 3).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(6, 300, 1296), (700, 310, 2064), (64, 512, 4112)])
+def test_far_scales_captured_and_side_by_side(M, N, K):
+    """The scales that a replayed graph finds decide, not those of the capture; streams at once.  The largest scales
+    overflow some results, so bits are compared."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, b, kb = _codes(g, M, K, 0, 0x50), _codes(g, N, K, 0, 0x50), -(-K // 128)
+    sets = [(_scales(g, (M, kb), la, la + 3), _scales(g, (-(-N // 128), kb), lb, lb + 3)) for la, lb in ((-2, -3), (-95, -50), (58, 62))]
+    want = [mxq.gemm_fp8(a, *s[:1], b, s[1], out="f32")["c"] for s in sets]
+    sa, sb = (t.clone() for t in sets[0])
+    c, st = torch.empty_like(want[0]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxq.mxq_gemm_fp8(a, sa, b, sb, M, N, K, "f32", c, st)
+    for i in (1, 0, 2, 1, 0):
+        sa.copy_(sets[i][0]), sb.copy_(sets[i][1])
+        graph.replay()
+        assert torch.equal(c.view(torch.int32), want[i].view(torch.int32))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    outs = [[mxq.gemm_fp8(a, s[0], b, s[1], out="f32", stream=t)["c"] for s, t in zip(sets, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.view(torch.int32), w.view(torch.int32)) for row in outs for o, w in zip(row, want)) and int(st.item()) == 0
