@@ -47,7 +47,8 @@
  *     are then undefined), MXQ_DEV_INVALID_SCALE when a caller-given global
  *     scale is negative or not finite (that group's outputs are undefined),
  *     MXQ_DEV_INVALID_EXPERT when an expert id is not below the number of
- *     experts (it is left out).  `status` may be NULL on the MX entry point
+ *     experts (it is left out), MXQ_DEV_INVALID_PAGE when a token's page is
+ *     not one of the cache's (see mxq_cache).  `status` may be NULL on the MX entry point
  *     only (the check is then skipped); elsewhere it is required.
  *   - Input bf16 data must be 16-byte aligned; code and scale outputs
  *     must be 16-byte aligned; fp32 / fp64 arrays naturally aligned.
@@ -109,6 +110,7 @@ typedef enum mxq_status {
 #define MXQ_DEV_WAIT_TIMEOUT 0x2u
 #define MXQ_DEV_INVALID_SCALE 0x4u
 #define MXQ_DEV_INVALID_EXPERT 0x8u
+#define MXQ_DEV_INVALID_PAGE 0x10u
 
 typedef enum mxq_fmt {
     MXQ_FMT_NVFP4 = 0,
@@ -510,6 +512,145 @@ MXQ_API mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden,
                                    const void *down_scales, const float *down_s2, uint16_t *y,
                                    uint32_t *status, void *workspace, size_t workspace_bytes,
                                    cudaStream_t stream);
+
+/* Bytes of device workspace of mxq_linear (0 for sizes it refuses).  Nothing
+ * in it needs to start at zero. */
+MXQ_API size_t mxq_linear_workspace_bytes(int64_t T, int64_t K);
+
+/* Product of a few tokens with a quantized weight matrix (weight-only: the
+ * tokens are not quantized),
+ *   y[t, n] = sum_k x[t, k] w[n, k],
+ * w dequantized on the fly from the codes that the quantizers write: the
+ * projections of a layer whose matrices are kept in these formats.
+ * Source: azampatti/Qwen3.8-Flash-Next-FP4-Local-AZ, "The shared expert"
+ * (MXFP8 matrices outside the routed experts); MJPansa/Qwen3.8-Flash-Next-
+ * MXFP4-FP8-R12, "Quantization format" (MXFP4 weights with UE8M0 scales).
+ *   x        bf16 [T, K], K a multiple of 32 (MXQ_ERR_SHAPE).
+ *   fmt      MXQ_FMT_NVFP4, MXQ_FMT_MXFP4 or MXQ_FMT_MXFP8.
+ *   codes, scales, s2   the matrix [N, K]: codes (16-byte aligned) and linear
+ *            scales as mxq_quantize_nvfp4 (one group, s2 [1]) or
+ *            mxq_quantize_mx writes them; s2 is read for NVFP4 only.
+ *   out, y   MXQ_OUT_BF16 or MXQ_OUT_F32, out, [T, N].
+ *   status   required.  MXQ_DEV_NONFINITE_INPUT when a token holds Inf or NaN
+ *            (its row of y is then undefined, the others are not touched by
+ *            it).  NaN codes or scales make their column NaN.
+ *   workspace at least mxq_linear_workspace_bytes(T, K), 256-byte aligned.  Two
+ *            calls that overlap in time need one each.
+ * T at most 2048, K at most 65536 (MXQ_ERR_UNSUPPORTED).  T or N 0 does nothing,
+ * K 0 gives zeros.  Sums are fp32 in a fixed order (it follows from the sizes and
+ * the number of SMs): repeated calls give the same bits, and a token's row does not
+ * depend on the others' values.  They are formed over the token's row scaled so
+ * that its largest element is about 2^15; block scales (NVFP4: s2) above about 2^80
+ * may overflow, and below about 2^-100 sums lose bits. */
+MXQ_API mxq_status mxq_linear(const uint16_t *x, int64_t T, int64_t K, mxq_fmt fmt, const uint8_t *codes,
+                              const uint8_t *scales, const float *s2, int64_t N, mxq_out out, void *y,
+                              uint32_t *status, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/* A key/value cache in pages, quantized (a host struct of device pointers; the
+ * caller owns it and the buffers).
+ * Source: MJPansa/Qwen3.8-Flash-Next-MXFP4-FP8-R12, "Quantization format"
+ * (activations dynamically quantized to MXFP8); josch15366/Qwen3.8-Flash-Next-
+ * NVFP4-LocalHessian-Experts, introduction (global scales held apart).  The
+ * pages do not describe a cache; the layout is a reading.
+ *   k_codes, v_codes    [pages, kv_heads, page_tokens, head_dim] values: a byte
+ *            each (MXFP8) or two codes a byte (NVFP4).  16-byte aligned.
+ *   k_scales, v_scales  [pages, kv_heads, page_tokens, head_dim / block]: a
+ *            UE8M0 byte per 32 values or an E4M3 byte per 16.  16-byte aligned.
+ *   k_s2, v_s2   NVFP4: fp32 [kv_heads], the global scale of each head (from a
+ *            calibration: amax / 2688); else not read.
+ *   fmt      MXQ_FMT_MXFP8 or MXQ_FMT_NVFP4 (others MXQ_ERR_UNSUPPORTED).
+ *   head_dim 64, 128 or 256; page_tokens 16, 32, 64, 128 or 256 (others
+ *            MXQ_ERR_UNSUPPORTED).
+ *   pages at least 0 and below 2^31, kv_heads from 1 to 1024.
+ * A batch of sequences is described to the calls below by
+ *   cu       int32 [seqs + 1], ascending: rows cu[b] .. cu[b + 1] - 1 of the
+ *            call's tensors are sequence b's.  Rows before cu[0] and from
+ *            cu[seqs] on belong to none: nothing is read or written for them.
+ *   lens     int32 [seqs]: tokens the sequence has in the cache once its rows
+ *            are in it.  Row i of a sequence of n rows stands for position
+ *            lens[b] - n + i; a row whose position is negative has no place.
+ *   table    int32 [seqs, width]: table[b, i] is the page that holds the
+ *            sequence's positions i page_tokens and on.  Entries behind its last
+ *            position are not read.
+ *   seqs     0 to 4096, width 0 to 2^31 - 1.
+ * A needed entry of the table that is not a page of the cache (negative, not
+ * below `pages`, or behind `width`) sets MXQ_DEV_INVALID_PAGE; what that means for
+ * the row is said at each call.  No index from these arrays is used unchecked. */
+typedef struct mxq_cache {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    const float *k_s2, *v_s2;
+    int64_t pages, kv_heads, page_tokens, head_dim;
+    mxq_fmt fmt;
+} mxq_cache;
+
+/* Quantize the keys and values of the batch's rows into their places.
+ *   k, v     bf16, row t at k + t k_stride (values): kv_heads * head_dim values,
+ *            so columns of a wider tensor will do.  16-byte aligned, strides
+ *            multiples of 8 and at least kv_heads * head_dim.
+ *   T        rows of k and v.
+ *   mode     NVFP4: MXQ_SCALE_RTN or MXQ_SCALE_FOUR_SIX block scales; MXFP8:
+ *            not read.
+ * Codes and scales are those that mxq_quantize_mx and mxq_quantize_nvfp4_s2 give
+ * for the same values (one group a head).  Rows without a place, or on an invalid
+ * page, are left out; nothing else of the cache is touched.
+ * MXQ_DEV_NONFINITE_INPUT: a value is Inf or NaN (its block is undefined);
+ * MXQ_DEV_INVALID_SCALE: an s2 is negative or not finite (that head's rows are left
+ * out).  No two rows may have the same place (a page that two sequences share is
+ * for reading): which row's codes and which one's scales stay is then undefined. */
+MXQ_API mxq_status mxq_cache_write(const mxq_cache *cache, const uint16_t *k, int64_t k_stride,
+                                   const uint16_t *v, int64_t v_stride, int64_t T, const int32_t *cu,
+                                   const int32_t *lens, const int32_t *table, int64_t seqs, int64_t width,
+                                   mxq_scale_mode mode, uint32_t *status, cudaStream_t stream);
+
+/* Read the batch's rows back: k and v are out, bf16 [T, kv_heads, head_dim],
+ * contiguous, 16-byte aligned.  (With cu the running sum of lens: whole
+ * sequences.)  MXFP8: code 2^e, exact in bf16's normal numbers; NVFP4: the fp32
+ * product (code D) s2, rounded to bf16.  Rows without a place, or on an invalid
+ * page, are left as they were. */
+MXQ_API mxq_status mxq_cache_read(const mxq_cache *cache, const int32_t *cu, const int32_t *lens,
+                                  const int32_t *table, int64_t seqs, int64_t width, int64_t T,
+                                  uint16_t *k, uint16_t *v, uint32_t *status, cudaStream_t stream);
+
+/* Bytes of device workspace of mxq_cache_attention (0 for sizes it refuses).
+ * Nothing in it needs to start at zero. */
+MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64_t T, int64_t heads,
+                                                   int64_t seqs, int64_t max_new);
+
+/* Attention of the batch's rows (the sequences' last tokens: a step of decoding,
+ * several guessed tokens, or a chunk of a prompt) over the cache, causal:
+ *   s_j = scale (q . k_j) for positions j <= the row's own,
+ *   o = sum_j softmax(s)_j v_j,   lse = ln sum_j exp(s_j),
+ * with k_j, v_j as the cache holds them (the rows' own tokens among them: write
+ * them first).  heads / kv_heads query heads share a key/value head.
+ *   q        bf16, row t at q + t q_stride (values): [heads, head_dim].  16-byte
+ *            aligned, q_stride a multiple of 8 and at least heads * head_dim.
+ *   heads    a multiple of kv_heads (MXQ_ERR_SHAPE), at most 256 of them to one
+ *            (MXQ_ERR_UNSUPPORTED).
+ *   max_new  at least the rows of every sequence (a bound known to the host); a
+ *            sequence with more is left out and sets MXQ_DEV_INVALID_PAGE.
+ *   scale    any finite number.
+ *   o        out, bf16 [T, heads, head_dim], 16-byte aligned.
+ *   lse      out, fp32 [T, heads], or NULL.
+ *   status   required.  MXQ_DEV_INVALID_PAGE as above (the sequence's rows are
+ *            then undefined); MXQ_DEV_WAIT_TIMEOUT.
+ *   workspace at least mxq_cache_attention_workspace_bytes(...), 256-byte aligned.
+ *            Two calls that overlap in time need one each.
+ * A row without a key (its position is negative) gives zeros and -Inf.  Rows of no
+ * sequence are left as they were.  What pages hold behind a sequence's last
+ * position does not matter, NaN patterns included.  Codes and scales of the
+ * positions read are taken to be finite, as mxq_cache_write leaves them.
+ * Scores, maxima, sums and outputs are fp32, weights are rounded to 11 bits;
+ * repeated calls give the same bits (the order of the sums follows from the sizes,
+ * the lengths of the batch's sequences and the number of SMs).  MXFP8: exact
+ * while the block maxima of neighbouring tokens lie within 2^22 of one another (what
+ * is smaller is off by at most 2^-41 of the largest); values (v) below 2^-100 count
+ * as zeros. */
+MXQ_API mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride,
+                                       int64_t T, int64_t heads, const int32_t *cu, const int32_t *lens,
+                                       const int32_t *table, int64_t seqs, int64_t width, int64_t max_new,
+                                       float scale, uint16_t *o, float *lse, uint32_t *status,
+                                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Zero a census (enqueued on `stream`).  census: device mxq_census. */
 MXQ_API mxq_status mxq_census_reset(mxq_census *census, cudaStream_t stream);

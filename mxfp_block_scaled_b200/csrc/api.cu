@@ -3,7 +3,9 @@
 // synchronisation; no state (the no-alloc verifier keeps its own, in noalloc.cu).
 #include "mxq.h"
 #include "mxq_internal.h"
+#include "mxq_layer.h"
 
+#include <algorithm>
 #include <limits.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -80,7 +82,7 @@ using namespace mxq;
 
 extern "C" {
 
-int mxq_version(void) { return 10300; }
+int mxq_version(void) { return 10400; }
 
 const char *mxq_status_string(mxq_status s)
 {
@@ -675,6 +677,236 @@ mxq_status mxq_moe_forward(const uint16_t *x, int64_t T, int64_t hidden, const i
     m.h = reinterpret_cast<float *>(ws);
     m.z = reinterpret_cast<float *>(ws + h_bytes);
     return launched(launch_moe(m, (int)fmt, stream));
+}
+
+static bool linear_sizes_ok(int64_t T, int64_t K) { return T <= kLinearMaxTokens && K <= kLinearMaxWidth; }
+
+size_t mxq_linear_workspace_bytes(int64_t T, int64_t K)
+{
+    if (T < 0 || K < 0 || K % 32 != 0 || !linear_sizes_ok(T, K))
+        return 0;
+    return linear_workspace_bytes(T, K);
+}
+
+mxq_status mxq_linear(const uint16_t *x, int64_t T, int64_t K, mxq_fmt fmt, const uint8_t *codes,
+                      const uint8_t *scales, const float *s2, int64_t N, mxq_out out, void *y,
+                      uint32_t *status, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const ApiRange range_("mxq_linear");
+    if (T < 0 || K < 0 || N < 0 || (out != MXQ_OUT_BF16 && out != MXQ_OUT_F32))
+        return MXQ_ERR_INVALID_ARG;
+    if (fmt != MXQ_FMT_NVFP4 && fmt != MXQ_FMT_MXFP4 && fmt != MXQ_FMT_MXFP8)
+        return MXQ_ERR_INVALID_ARG;
+    if (K % 32 != 0 || N > 0x7FFFFF00ll)    // rows of w are numbered in 32 bits
+        return MXQ_ERR_SHAPE;
+    if (!linear_sizes_ok(T, K))
+        return MXQ_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0)
+        return MXQ_OK;
+    if (!y || !status)
+        return MXQ_ERR_INVALID_ARG;
+    const size_t width = out == MXQ_OUT_F32 ? 4 : 2;
+    if (!aligned(y, width) || !aligned(status, 4))
+        return MXQ_ERR_ALIGN;
+    if (K == 0)                             // an empty sum
+        return launched(cudaMemsetAsync(y, 0, (size_t)(T * N) * width, stream));
+    if (!x || !codes || !scales || (fmt == MXQ_FMT_NVFP4 && !s2))
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16) || (fmt == MXQ_FMT_NVFP4 && !aligned(s2, 4)))
+        return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < linear_workspace_bytes(T, K))
+        return MXQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return MXQ_ERR_ALIGN;
+    LinearArgs a;
+    a.x = x;
+    a.T = T;
+    a.K = K;
+    a.N = N;
+    a.codes = codes;
+    a.scales = scales;
+    a.s2 = s2;
+    a.y = y;
+    a.status = status;
+    a.xh = static_cast<uint32_t *>(workspace);
+    a.xf = reinterpret_cast<float *>(static_cast<char *>(workspace) + linear_rows_bytes(T, K));
+    return launched(launch_linear(a, (int)fmt, out == MXQ_OUT_F32, stream));
+}
+
+// What is wrong with a cache's sizes, apart from its pointers.
+static mxq_status cache_sizes(const mxq_cache *c)
+{
+    if (!c || c->pages < 0 || c->kv_heads < 1 || c->page_tokens < 1 || c->head_dim < 1)
+        return MXQ_ERR_INVALID_ARG;
+    if (c->fmt != MXQ_FMT_NVFP4 && c->fmt != MXQ_FMT_MXFP4 && c->fmt != MXQ_FMT_MXFP8 && c->fmt != MXQ_FMT_FP8_BLOCK)
+        return MXQ_ERR_INVALID_ARG;
+    if (c->fmt != MXQ_FMT_NVFP4 && c->fmt != MXQ_FMT_MXFP8)
+        return MXQ_ERR_UNSUPPORTED;
+    const int64_t d = c->head_dim, p = c->page_tokens;
+    if ((d != 64 && d != 128 && d != 256) || (p != 16 && p != 32 && p != 64 && p != 128 && p != 256))
+        return MXQ_ERR_UNSUPPORTED;
+    if (c->pages > 0x7FFFFFFFll || c->kv_heads > 1024)
+        return MXQ_ERR_SHAPE;
+    return MXQ_OK;
+}
+
+// The checks that the calls on a cache share; `out` is filled where they pass.
+static mxq_status cache_view(const mxq_cache *c, const int32_t *cu, const int32_t *lens, const int32_t *table,
+                             int64_t T, int64_t seqs, int64_t width, uint32_t *status, CacheView *out)
+{
+    const mxq_status st = cache_sizes(c);
+    if (st != MXQ_OK)
+        return st;
+    if (T < 0 || seqs < 0 || width < 0)
+        return MXQ_ERR_INVALID_ARG;
+    if (seqs > kMaxSeqs)
+        return MXQ_ERR_UNSUPPORTED;
+    if (T > 0x7FFFFFFFll || width > 0x7FFFFFFFll)
+        return MXQ_ERR_SHAPE;
+    if (T == 0 || seqs == 0)
+        return MXQ_OK;
+    if (!cu || !lens || !status || (width > 0 && !table))
+        return MXQ_ERR_INVALID_ARG;
+    if (c->pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+        return MXQ_ERR_INVALID_ARG;
+    if (c->fmt == MXQ_FMT_NVFP4 && (!c->k_s2 || !c->v_s2))
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(cu, 4) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(status, 4) || !aligned(c->k_codes, 16) ||
+        !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16) ||
+        (c->fmt == MXQ_FMT_NVFP4 && (!aligned(c->k_s2, 4) || !aligned(c->v_s2, 4))))
+        return MXQ_ERR_ALIGN;
+    out->k_codes = c->k_codes;
+    out->k_scales = c->k_scales;
+    out->v_codes = c->v_codes;
+    out->v_scales = c->v_scales;
+    out->k_s2 = c->fmt == MXQ_FMT_NVFP4 ? c->k_s2 : nullptr;
+    out->v_s2 = c->fmt == MXQ_FMT_NVFP4 ? c->v_s2 : nullptr;
+    out->pages = (uint32_t)c->pages;
+    out->heads = (uint32_t)c->kv_heads;
+    out->page_log = 4;
+    while ((16ll << (out->page_log - 4)) < c->page_tokens)
+        ++out->page_log;
+    out->cu = cu;
+    out->lens = lens;
+    out->table = table;
+    out->seqs = (uint32_t)seqs;
+    out->width = (uint32_t)width;
+    out->status = status;
+    return MXQ_OK;
+}
+
+mxq_status mxq_cache_write(const mxq_cache *cache, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                           int64_t v_stride, int64_t T, const int32_t *cu, const int32_t *lens,
+                           const int32_t *table, int64_t seqs, int64_t width, mxq_scale_mode mode,
+                           uint32_t *status, cudaStream_t stream)
+{
+    const ApiRange range_("mxq_cache_write");
+    CacheView c;
+    const mxq_status st = cache_view(cache, cu, lens, table, T, seqs, width, status, &c);
+    if (st != MXQ_OK)
+        return st;
+    if (mode != MXQ_SCALE_RTN && mode != MXQ_SCALE_FOUR_SIX)
+        return MXQ_ERR_INVALID_ARG;
+    const int64_t values = cache->kv_heads * cache->head_dim;
+    if (k_stride < values || v_stride < values || k_stride > INT64_MAX / 0x80000000ll ||
+        v_stride > INT64_MAX / 0x80000000ll)
+        return MXQ_ERR_SHAPE;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0)
+        return MXQ_ERR_ALIGN;
+    if (T * (2 * values / 16) > 0x7FFFFFFFll * 256)
+        return MXQ_ERR_SHAPE;
+    if (T == 0 || seqs == 0)
+        return MXQ_OK;
+    if (!k || !v)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return MXQ_ERR_ALIGN;
+    return launched(launch_cache_write(c, (int)cache->fmt, (int)cache->head_dim, mode == MXQ_SCALE_FOUR_SIX, k, k_stride,
+                                       v, v_stride, (uint32_t)T, stream));
+}
+
+mxq_status mxq_cache_read(const mxq_cache *cache, const int32_t *cu, const int32_t *lens, const int32_t *table,
+                          int64_t seqs, int64_t width, int64_t T, uint16_t *k, uint16_t *v, uint32_t *status,
+                          cudaStream_t stream)
+{
+    const ApiRange range_("mxq_cache_read");
+    CacheView c;
+    const mxq_status st = cache_view(cache, cu, lens, table, T, seqs, width, status, &c);
+    if (st != MXQ_OK)
+        return st;
+    if (T * (2 * cache->kv_heads * cache->head_dim / 16) > 0x7FFFFFFFll * 256)
+        return MXQ_ERR_SHAPE;
+    if (T == 0 || seqs == 0)
+        return MXQ_OK;
+    if (!k || !v)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return MXQ_ERR_ALIGN;
+    return launched(launch_cache_read(c, (int)cache->fmt, (int)cache->head_dim, (uint32_t)T, k, v, stream));
+}
+
+// Sizes of a call of the attention, beside those of the cache and the batch.
+static mxq_status attention_sizes(const mxq_cache *c, int64_t T, int64_t heads, int64_t max_new)
+{
+    if (T < 0 || heads < 1 || max_new < 0)
+        return MXQ_ERR_INVALID_ARG;
+    if (heads % c->kv_heads != 0)
+        return MXQ_ERR_SHAPE;
+    if (heads / c->kv_heads > 256)
+        return MXQ_ERR_UNSUPPORTED;
+    int64_t rows;
+    if (!mul_ok(T, heads, &rows) || rows > 0x7FFFFFFFll)
+        return MXQ_ERR_SHAPE;               // rows are numbered in 32 bits
+    return MXQ_OK;
+}
+
+size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64_t T, int64_t heads, int64_t seqs,
+                                           int64_t max_new)
+{
+    if (cache_sizes(cache) != MXQ_OK || attention_sizes(cache, T, heads, max_new) != MXQ_OK || seqs < 0 ||
+        seqs > kMaxSeqs)
+        return 0;
+    return attention_workspace_bytes(seqs, cache->head_dim);
+}
+
+mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride, int64_t T, int64_t heads,
+                               const int32_t *cu, const int32_t *lens, const int32_t *table, int64_t seqs,
+                               int64_t width, int64_t max_new, float scale, uint16_t *o, float *lse,
+                               uint32_t *status, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const ApiRange range_("mxq_cache_attention");
+    AttentionCall a;
+    mxq_status st = cache_view(cache, cu, lens, table, T, seqs, width, status, &a.c);
+    if (st == MXQ_OK)
+        st = attention_sizes(cache, T, heads, max_new);
+    if (st != MXQ_OK)
+        return st;
+    if (!(scale - scale == 0.0f))
+        return MXQ_ERR_INVALID_ARG;
+    if (q_stride < heads * cache->head_dim || q_stride > INT64_MAX / 0x80000000ll)
+        return MXQ_ERR_SHAPE;
+    if (q_stride % 8 != 0)
+        return MXQ_ERR_ALIGN;
+    if (T == 0 || seqs == 0)
+        return MXQ_OK;
+    if (!q || !o)
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 4)))
+        return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < attention_workspace_bytes(seqs, cache->head_dim))
+        return MXQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return MXQ_ERR_ALIGN;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = (uint32_t)T;
+    a.heads = (uint32_t)heads;
+    a.max_new = (uint32_t)std::min<int64_t>(max_new, T);
+    a.scale = scale;
+    a.o = o;
+    a.lse = lse;
+    a.workspace = workspace;
+    return launched(launch_attention(a, (int)cache->fmt, (int)cache->head_dim, stream));
 }
 
 mxq_status mxq_census_reset(mxq_census *census, cudaStream_t stream)

@@ -1,0 +1,66 @@
+// mxq_cache.cuh -- where the tokens of a paged cache lie (sm_100a).
+//
+// A batch of sequences: cu[b] .. cu[b + 1] are the rows of sequence b's new
+// tokens, lens[b] the tokens it has in the cache, those among them, and
+// table[b, i] the page that holds its tokens i 2^page_log and on.  All of it
+// is device data and nothing of it is trusted: every index is compared with
+// its bound before it is used.
+#pragma once
+
+#include "mxq_device.cuh"
+#include "mxq_layer.h"
+
+namespace mxq {
+
+// Number of the sequence that row `row` belongs to, by bisection of cu (which
+// ascends; of any other the result is some number below seqs, or seqs).
+__device__ __forceinline__ uint32_t find_sequence(const CacheView &c, uint32_t row)
+{
+    uint32_t lo = 0, hi = c.seqs;       // the last b with cu[b] <= row is in [lo, hi)
+    while (hi - lo > 1u) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (__ldg(c.cu + mid) <= (int64_t)row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return __ldg(c.cu + lo) <= (int64_t)row && (int64_t)row < __ldg(c.cu + lo + 1) ? lo : c.seqs;
+}
+
+// New tokens of sequence b: at most `T`, none where cu descends.
+__device__ __forceinline__ uint32_t new_tokens(const CacheView &c, uint32_t b, uint32_t T, uint32_t &first)
+{
+    const int64_t r0 = __ldg(c.cu + b), r1 = __ldg(c.cu + b + 1);
+    first = (uint32_t)r0;
+    return r0 >= 0 && r1 > r0 && r1 <= (int64_t)T ? (uint32_t)(r1 - r0) : 0u;
+}
+
+// Page of position `pos` (at least 0) of sequence b; c.pages where the table
+// has none, and the status bit set.
+__device__ __forceinline__ uint32_t find_page(const CacheView &c, uint32_t b, uint32_t pos)
+{
+    const uint32_t i = pos >> c.page_log;
+    const uint32_t page = i < c.width ? (uint32_t)__ldg(c.table + (uint64_t)b * c.width + i) : c.pages;
+    if (page < c.pages)
+        return page;
+    atomicOr(c.status, MXQ_DEV_INVALID_PAGE);
+    return c.pages;
+}
+
+// Number of the (page, head, token) row of codes that holds row `row`'s token;
+// false where the row has no place: behind the last sequence, before the
+// sequence's first position, or on an invalid page.
+__device__ __forceinline__ bool find_place(const CacheView &c, uint32_t row, uint64_t &at)
+{
+    const uint32_t b = find_sequence(c, row);
+    if (b == c.seqs)
+        return false;
+    const int64_t pos = (int64_t)__ldg(c.lens + b) - __ldg(c.cu + b + 1) + row;
+    if (pos < 0)
+        return false;
+    const uint32_t page = find_page(c, b, (uint32_t)pos);
+    at = (((uint64_t)page * c.heads) << c.page_log) + ((uint32_t)pos & ((1u << c.page_log) - 1u));
+    return page < c.pages;
+}
+
+} // namespace mxq

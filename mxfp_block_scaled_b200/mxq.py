@@ -26,6 +26,7 @@ DEV_NONFINITE_INPUT = 0x1
 DEV_WAIT_TIMEOUT = 0x2
 DEV_INVALID_SCALE = 0x4
 DEV_INVALID_EXPERT = 0x8
+DEV_INVALID_PAGE = 0x10
 
 FMT = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2, "fp8_block": 3}
 SCALE_MODE = {"rtn": 0, "four_six": 1}
@@ -37,13 +38,21 @@ EXPORTED = ("mxq_version", "mxq_status_string", "mxq_scale_bytes", "mxq_workspac
             "mxq_quantize_nvfp4", "mxq_global_scale_nvfp4", "mxq_quantize_nvfp4_s2", "mxq_quantize_nvfp4_weighted",
             "mxq_quantize_mx", "mxq_requant_fp8_mx", "mxq_quantize_act", "mxq_dequant_relerr",
             "mxq_dequant_relerr_noalloc", "mxq_census_reset", "mxq_census_add", "mxq_quantize_fp8",
-            "mxq_gemm_fp8", "mxq_moe_workspace_bytes", "mxq_moe_forward")
+            "mxq_gemm_fp8", "mxq_moe_workspace_bytes", "mxq_moe_forward", "mxq_linear_workspace_bytes", "mxq_linear",
+            "mxq_cache_write", "mxq_cache_read", "mxq_cache_attention_workspace_bytes", "mxq_cache_attention")
 
 # Fields of struct mxq_census (include/mxq.h), in order, each 8 bytes.
 CENSUS_FIELDS = ("sum_relerr", "max_relerr", "sum_sq_err", "sum_sq_ref", "sum_sq_err_rtn",
                  "n_tensors", "n_tensors_rtn", "blocks", "blocks_m4",
                  "mean_relerr", "sse_vs_rtn", "m4_fraction", "reserved")
 _CENSUS_INTS = ("n_tensors", "n_tensors_rtn", "blocks", "blocks_m4")
+
+
+class _CacheStruct(ctypes.Structure):
+    """struct mxq_cache (include/mxq.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "k_s2", "v_s2")]
+                + [(n, ctypes.c_int64) for n in ("pages", "kv_heads", "page_tokens", "head_dim")]
+                + [("fmt", ctypes.c_int)])
 
 
 class MxqError(RuntimeError):
@@ -106,6 +115,20 @@ def load(path=LIB_PATH):
     L.mxq_moe_forward.restype = i32
     L.mxq_moe_forward.argtypes = [vp, i64, i64, vp, vp, i64, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp,
                                   vp, sz, vp]
+    cp = ctypes.POINTER(_CacheStruct)
+    L.mxq_linear_workspace_bytes.restype = sz
+    L.mxq_linear_workspace_bytes.argtypes = [i64, i64]
+    L.mxq_linear.restype = i32
+    L.mxq_linear.argtypes = [vp, i64, i64, i32, vp, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+    L.mxq_cache_write.restype = i32
+    L.mxq_cache_write.argtypes = [cp, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i32, vp, vp]
+    L.mxq_cache_read.restype = i32
+    L.mxq_cache_read.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp]
+    L.mxq_cache_attention_workspace_bytes.restype = sz
+    L.mxq_cache_attention_workspace_bytes.argtypes = [cp, i64, i64, i64, i64]
+    L.mxq_cache_attention.restype = i32
+    L.mxq_cache_attention.argtypes = [cp, vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, vp, vp,
+                                      sz, vp]
     L.mxq_test_stall_next_single_pass.restype = None
     L.mxq_test_stall_next_single_pass.argtypes = [i32]
     L.mxq_test_stall_next_product.restype = None
@@ -412,6 +435,108 @@ def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, in
     _check("mxq_moe_forward", rc)
 
 
+def mxq_linear(x, T, K, fmt, codes, scales, s2, N, out, y, status, workspace, stream=None):
+    dev = _device(_first(x, status))
+    nb = N * K // (16 if fmt == "nvfp4" else 32)
+    rc = _enqueue(load().mxq_linear,
+                  (_buf("x", x, 2 * T * K, dev), T, K, FMT[fmt], _buf("codes", codes, _code_bytes(fmt, N * K), dev),
+                   _buf("scales", scales, nb, dev), _buf("s2", s2, 4 if fmt == "nvfp4" else 0, dev), N, OUT[out],
+                   _buf("y", y, T * N * (4 if out == "f32" else 2), dev), _buf("status", status, 4, dev),
+                   _buf("workspace", workspace, 0, dev), _nbytes(workspace)), dev, stream)
+    _check("mxq_linear", rc)
+
+
+class Cache:
+    """A paged, quantized key/value cache: the tensors of struct mxq_cache and the
+    struct itself.  k_codes, v_codes: uint8 [pages, kv_heads, page_tokens, head_dim]
+    ("mxfp8") or [..., head_dim / 2] ("nvfp4"); k_scales, v_scales: uint8 [...,
+    head_dim / 32] or [..., head_dim / 16]; k_s2, v_s2: fp32 [kv_heads], the heads'
+    global scales ("nvfp4" only).  Contiguous, on one device."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, fmt="mxfp8", k_s2=None, v_s2=None):
+        if fmt not in ("mxfp8", "nvfp4"):
+            raise ValueError("a cache is mxfp8 or nvfp4, not %r" % (fmt,))
+        if k_codes.dim() != 4:
+            raise ValueError("codes [pages, kv_heads, page_tokens, ...]")
+        pages, heads, tokens, width = k_codes.shape
+        dim, block = (width, 32) if fmt == "mxfp8" else (2 * width, 16)
+        if dim not in (64, 128, 256) or tokens not in (16, 32, 64, 128, 256):
+            raise ValueError("heads of 64, 128 or 256 values on pages of 16, 32, 64, 128 or 256 tokens, not of %d on %d"
+                             % (dim, tokens))
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            _typed(name, t, torch.uint8, (pages, heads, tokens, width))
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _typed(name, t, torch.uint8, (pages, heads, tokens, dim // block))
+        if fmt == "nvfp4":
+            for name, t in (("k_s2", k_s2), ("v_s2", v_s2)):
+                _typed(name, t, torch.float32, (heads,))
+        else:
+            k_s2 = v_s2 = None
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, k_s2, v_s2)
+        self.device = k_codes.device
+        if any(t is not None and t.device != self.device for t in self.tensors):
+            raise ValueError("the cache's tensors lie on different devices")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.k_s2, self.v_s2 = self.tensors
+        self.fmt, self.pages, self.kv_heads, self.page_tokens, self.head_dim = fmt, pages, heads, tokens, dim
+        self.struct = _CacheStruct(*[None if t is None else t.data_ptr() for t in self.tensors], pages, heads, tokens,
+                                   dim, FMT[fmt])
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_tokens, head_dim, fmt="mxfp8", k_s2=None, v_s2=None, device="cuda"):
+        """A cache of zeros."""
+        width, block = (head_dim, 32) if fmt == "mxfp8" else (head_dim // 2, 16)
+        make = lambda w: torch.zeros((pages, kv_heads, page_tokens, w), dtype=torch.uint8, device=device)  # noqa: E731
+        return cls(make(width), make(head_dim // block), make(width), make(head_dim // block), fmt, k_s2, v_s2)
+
+
+def _batch(cu, lens, table, seqs, width, dev):
+    return (_buf("cu", cu, 4 * (seqs + 1), dev), _buf("lens", lens, 4 * seqs, dev),
+            _buf("table", table, 4 * seqs * width, dev), seqs, width)
+
+
+def _rows(name, t, stride, T, values, dev):
+    """Address of T rows of `values` values, `stride` values apart (the last dimensions contiguous)."""
+    if t is None:
+        return None
+    if T > 0 and (t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+                  < ((T - 1) * stride + values) * t.element_size()):
+        raise ValueError("%s does not hold %d rows of %d values, %d apart" % (name, T, values, stride))
+    if t.get_device() != dev:
+        raise ValueError("%s is not on the device of the first tensor" % name)
+    return t.data_ptr()
+
+
+def mxq_cache_write(cache, k, k_stride, v, v_stride, T, cu, lens, table, seqs, width, mode, status, stream=None):
+    """k and v: bf16 tensors whose row t starts t * stride values behind their first
+    value and holds kv_heads * head_dim contiguous ones."""
+    dev, n = _device(cache.k_codes), cache.kv_heads * cache.head_dim
+    rc = _enqueue(load().mxq_cache_write,
+                  (cache.struct, _rows("k", k, k_stride, T, n, dev), k_stride, _rows("v", v, v_stride, T, n, dev), v_stride,
+                   T, *_batch(cu, lens, table, seqs, width, dev), SCALE_MODE[mode], _buf("status", status, 4, dev)),
+                  dev, stream)
+    _check("mxq_cache_write", rc)
+
+
+def mxq_cache_read(cache, cu, lens, table, seqs, width, T, k, v, status, stream=None):
+    dev, n = _device(cache.k_codes), 2 * T * cache.kv_heads * cache.head_dim
+    rc = _enqueue(load().mxq_cache_read,
+                  (cache.struct, *_batch(cu, lens, table, seqs, width, dev), T, _buf("k", k, n, dev),
+                   _buf("v", v, n, dev), _buf("status", status, 4, dev)), dev, stream)
+    _check("mxq_cache_read", rc)
+
+
+def mxq_cache_attention(cache, q, q_stride, T, heads, cu, lens, table, seqs, width, max_new, scale, o, lse, status,
+                        workspace, stream=None):
+    """q: bf16, row t `t * q_stride` values behind the first, heads * head_dim contiguous ones each."""
+    dev, n = _device(cache.k_codes), heads * cache.head_dim
+    rc = _enqueue(load().mxq_cache_attention,
+                  (cache.struct, _rows("q", q, q_stride, T, n, dev), q_stride, T, heads,
+                   *_batch(cu, lens, table, seqs, width, dev), max_new, scale, _buf("o", o, 2 * T * n, dev),
+                   _buf("lse", lse, 4 * T * heads, dev), _buf("status", status, 4, dev),
+                   _buf("workspace", workspace, 0, dev), _nbytes(workspace)), dev, stream)
+    _check("mxq_cache_attention", rc)
+
+
 # ------------------------------------------------------------ allocating --
 def _on(stream):
     """Results and workspaces made on the stream that the call runs on: what is
@@ -659,6 +784,119 @@ def moe_forward(x, topk_ids, topk_weights, gate_up, down, fmt, workspace=None, s
                         gate_up["s2"] if fmt == "nvfp4" else None, down["codes"], down["scales"],
                         down["s2"] if fmt == "nvfp4" else None, out["y"], out["status"],
                         moe_workspace(T, k, H, I, dev) if workspace is None else workspace, stream)
+    return out
+
+
+def linear_workspace(T, K, device="cuda"):
+    """A workspace for mxq_linear at these sizes, to keep from call to call."""
+    return torch.empty(max(load().mxq_linear_workspace_bytes(T, K), 256), dtype=torch.uint8, device=device)
+
+
+def linear(x, w, fmt, out="bf16", workspace=None, stream=None):
+    """x w^T for a few tokens over a quantized matrix.  x: bf16 [T, K]; w: a dict with
+    codes, scales (and s2 [1] for "nvfp4") of the matrix [N, K] as quantize_nvfp4 (of
+    [1, N, K]) or quantize_mx return it with linear scales; workspace: a
+    linear_workspace to use again, not by two calls at once.  Returns dict y [T, N]
+    (bf16, or fp32 for out="f32"), status."""
+    _bf16(x)
+    per = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32}.get(fmt)
+    if per is None:
+        raise ValueError("unknown format %r" % (fmt,))
+    if out not in OUT:
+        raise ValueError("out is one of %s" % sorted(OUT))
+    T, K = x.shape
+    codes = w["codes"][0] if w["codes"].dim() == 3 and w["codes"].shape[0] == 1 else w["codes"]
+    scales = w["scales"][0] if w["scales"].dim() == 3 and w["scales"].shape[0] == 1 else w["scales"]
+    N = codes.shape[0]
+    _typed("codes", codes, torch.uint8, (N, K if fmt == "mxfp8" else K // 2))
+    _typed("scales", scales, torch.uint8, (N, K // per))
+    if fmt == "nvfp4":
+        _typed("s2", w["s2"], torch.float32, (1,))
+    dev = x.device
+    with _on(stream):
+        res = {"y": torch.empty((T, N), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=dev),
+               "status": torch.zeros(1, dtype=torch.int32, device=dev)}
+        mxq_linear(x, T, K, fmt, codes, scales, w["s2"] if fmt == "nvfp4" else None, N, out, res["y"], res["status"],
+                   linear_workspace(T, K, dev) if workspace is None else workspace, stream)
+    return res
+
+
+def _token_rows(name, t, heads, dim):
+    """(rows, stride) of a bf16 [T, heads, dim] tensor whose tokens may lie apart."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError("expected %s as bf16 [T, %d, %d]" % (name, heads, dim))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError("a token's heads must be contiguous in %s" % name)
+    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else heads * dim)
+
+
+def _batch_of(cu, lens, table):
+    """(sequences, width of the table) of a batch."""
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    _typed("cu", cu, torch.int32, (B + 1,))
+    _typed("lens", lens, torch.int32, (B,))
+    if table.dim() != 2:
+        raise ValueError("table is [sequences, pages of the longest]")
+    _typed("table", table, torch.int32, (B, table.shape[1]))
+    return B, table.shape[1]
+
+
+def cache_write(cache, k, v, cu, lens, table, mode="rtn", status=None, stream=None):
+    """Quantize the keys and values of the batch's new tokens into the cache.  k, v:
+    bf16 [T, kv_heads, head_dim], a token's heads contiguous; cu int32 [B + 1], lens
+    int32 [B], table int32 [B, width]: see include/mxq.h.  mode: block scales of
+    "nvfp4", "rtn" or "four_six".  Returns the status (a given one is added to)."""
+    T, ks = _token_rows("k", k, cache.kv_heads, cache.head_dim)
+    Tv, vs = _token_rows("v", v, cache.kv_heads, cache.head_dim)
+    if T != Tv:
+        raise ValueError("%d keys and %d values" % (T, Tv))
+    B, width = _batch_of(cu, lens, table)
+    with _on(stream):
+        status = torch.zeros(1, dtype=torch.int32, device=cache.device) if status is None else status
+        mxq_cache_write(cache, k, ks, v, vs, T, cu, lens, table, B, width, mode, status, stream)
+    return status
+
+
+def cache_read(cache, cu, lens, table, T, stream=None):
+    """The last tokens of the batch's sequences back from the cache: dict k, v bf16
+    [T, kv_heads, head_dim] (rows of no sequence, or without a place, are zeros),
+    status.  With cu the running sum of lens: whole sequences."""
+    B, width = _batch_of(cu, lens, table)
+    with _on(stream):
+        out = {n: torch.zeros((T, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device) for n in "kv"}
+        out["status"] = torch.zeros(1, dtype=torch.int32, device=cache.device)
+        mxq_cache_read(cache, cu, lens, table, B, width, T, out["k"], out["v"], out["status"], stream)
+    return out
+
+
+def cache_attention_workspace(cache, T, heads, seqs, max_new):
+    """A workspace for mxq_cache_attention at these sizes, to keep from call to call."""
+    n = load().mxq_cache_attention_workspace_bytes(cache.struct, T, heads, seqs, max_new)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.device)
+
+
+def cache_attention(cache, q, cu, lens, table, max_new, scale=None, workspace=None, status=None, stream=None):
+    """Causal attention of the batch's new tokens over the cache, which holds their
+    own keys and values already.  q: bf16 [T, heads, head_dim], a token's heads
+    contiguous; max_new: no sequence has more new tokens; scale: 1 / sqrt(head_dim)
+    where None; workspace: a cache_attention_workspace to use again, not by two calls
+    at once.  Returns dict o bf16 [T, heads, head_dim], lse fp32 [T, heads] (rows of
+    no sequence: zeros), status (a given one is added to)."""
+    if q.dim() != 3:
+        raise ValueError("expected q as bf16 [T, heads, head_dim]")
+    heads = q.shape[1]
+    T, qs = _token_rows("q", q, heads, cache.head_dim)
+    B, width = _batch_of(cu, lens, table)
+    dev = cache.device
+    with _on(stream):
+        out = {"o": torch.zeros((T, heads, cache.head_dim), dtype=torch.bfloat16, device=dev),
+               "lse": torch.zeros((T, heads), dtype=torch.float32, device=dev),
+               "status": torch.zeros(1, dtype=torch.int32, device=dev) if status is None else status}
+        if workspace is None:
+            workspace = cache_attention_workspace(cache, T, heads, B, max_new)
+        mxq_cache_attention(cache, q, qs, T, heads, cu, lens, table, B, width, max_new,
+                            cache.head_dim ** -0.5 if scale is None else scale, out["o"], out["lse"], out["status"],
+                            workspace, stream)
     return out
 
 
