@@ -866,7 +866,7 @@ size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64_t T, in
     if (cache_sizes(cache) != MXQ_OK || attention_sizes(cache, T, heads, max_new) != MXQ_OK || seqs < 0 ||
         seqs > kMaxSeqs)
         return 0;
-    return attention_workspace_bytes(seqs, cache->head_dim);
+    return attention_workspace_bytes(heads / cache->kv_heads, cache->head_dim, std::min(max_new, T));
 }
 
 mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride, int64_t T, int64_t heads,
@@ -893,7 +893,8 @@ mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_
         return MXQ_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 4)))
         return MXQ_ERR_ALIGN;
-    if (!workspace || workspace_bytes < attention_workspace_bytes(seqs, cache->head_dim))
+    if (!workspace ||
+        workspace_bytes < attention_workspace_bytes(heads / cache->kv_heads, cache->head_dim, std::min(max_new, T)))
         return MXQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256))
         return MXQ_ERR_ALIGN;

@@ -1,743 +1,95 @@
-// attention.cu -- attention of new tokens over a paged, quantized cache
-// (sm_100a):
+// attention.cu -- attention of new tokens over a paged, quantized cache: which
+// kernel takes which sequences, and the join of unfinished tiles (sm_100a).
 //
 //   s[j] = scale q . k_j (j <= the row's position),  p = softmax(s),
 //   o = sum_j p_j v_j,  lse = ln sum_j exp(s[j]),
 //
 // for every row (a new token and a query head); the heads of a group share a
 // key/value head.  k_j and v_j are the cache's codes times their block scales.
-//
-// Rows of few tokens (decoding: the read of the cache is the work).  A tile is
-// up to 16 rows of one sequence and key/value head: its new tokens times the
-// heads of the group.  The tiles' keys are cut into items of about equal length,
-// so that the items of all sequences fill the card once; a CTA of 4 warps takes
-// an item, its warps take turns of 32 keys, each with its own running maximum,
-// sum and output, joined at the end (in the order of the warps).  Items of a
-// tile that was cut leave their maximum, sum and output in the workspace, and
-// attention_join_kernel adds them up in their order: no atomics, and the cut
-// follows from the lengths, the sizes and the number of SMs alone.  Each CTA works
-// the cut out for itself; the first also writes it down for the join.
-//
-// Codes go from global memory to a warp's own two stages of shared memory by
-// cp.async and from there, decoded, into the operands of mma.sync m16n8k16 (f16,
-// fp32 sums).  The order of a head's dimension inside a product is free, so a
-// lane takes a contiguous run of every key's codes, and a contiguous run of the
-// values' columns; pairs of keys are put together a byte (or nibble) at a time
-// before they are decoded, so the values need no transposition.
-//
-// Precision.  E2M1 times its E4M3 scale is exact in f16.  E4M3 codes (MXFP8) are
-// multiplied in f16 by their block's power of two relative to the largest of the
-// warp's 32 keys, 2^7 at most: exact while the blocks' maxima lie within 2^22 of one
-// another, below that off by 2^-25 / 57344 of the largest.  The largest one's power
-// itself multiplies the scores in fp32, and for the values it enters the running
-// maximum, m = max(s + E): weights are w = 2^(s + E - m), so an output needs no
-// second factor.  Queries are held in f16 times a power of two of the row (as the
-// layer's tokens, moe.cu); weights are rounded to f16's 11 bits, an eighth of the bf16
-// result's own step; scores, maxima, sums and outputs are fp32.
-#include "mxq_cache.cuh"
-#include "mxq_mma.cuh"
-#include "mxq.h"
+#include "attention.cuh"
 #include <algorithm>
 
 namespace mxq {
 
+cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint32_t &ctas, cudaStream_t s);
+cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t ctas, cudaStream_t s);
+
 namespace {
 
-constexpr uint32_t kRows = 16;          // rows of a tile
-constexpr uint32_t kKeys = 32;          // keys of a warp's turn
-constexpr uint32_t kWarps = 4;
-constexpr uint32_t kMaxItems = 640;     // the items the keys are cut into, where nothing else cuts them
-constexpr uint32_t kMaxCut = 2 * kMaxItems;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLowest = -1e30f;       // the running maximum before the first key
+// Sequences of up to this many rows are attention_rows.cu's.
+constexpr uint32_t kFewRows = 64;
+constexpr uint32_t kMaxSms = 160;           // the division uses no more (workspace)
+constexpr uint32_t kFewCtas = 4 * kMaxSms;  // of attention_rows.cu
+constexpr uint32_t kFewTile = 16, kTile = 256;
 
-// The cut, in the workspace: turns of an item, then for each sequence the first
-// of its items and the first of its parts (items of tiles that are cut).
-struct Plan {
-    uint32_t len;
-    uint32_t pad[3];
-};
-
-struct AttArgs {
-    CacheView c;
-    const uint16_t *q;
-    int64_t q_stride;
-    uint32_t T, group, max_new;
-    float scale;                // softmax scale times log2(e)
-    uint16_t *o;
-    float *lse;
-    uint32_t target;            // items wanted
-    uint32_t *plan;             // Plan, items [seqs + 1], parts [seqs + 1]
-    float *part;                // [kMaxCut][kRows][dim + 2]
-    FastDiv groupdiv;
-};
-
-template <int FMT, int D>
-struct Shape {
-    static constexpr bool fp4 = FMT == MXQ_FMT_NVFP4;
-    static constexpr uint32_t row = fp4 ? D / 2 : D;            // bytes of a key's codes
-    static constexpr uint32_t blocks = fp4 ? D / 16 : D / 32;   // and of its scales
-    static constexpr uint32_t codes = kKeys * row, scales = kKeys * blocks;
-    static constexpr uint32_t stage = 2 * (codes + scales);     // k codes, v codes, k scales, v scales
-    static constexpr uint32_t ring = 2 * stage;                 // of a warp
-    static constexpr bool q_regs = D <= 128;                    // queries in registers
-    static constexpr uint32_t q_pitch = D * 2 + 16;             // bytes of a query row in shared memory
-    static constexpr uint32_t outs = kRows * (D + 4) * 4;       // a warp's outputs, when they are joined
-    static constexpr uint32_t smem = kWarps * ring + kRows * q_pitch;
-};
-
-// Byte `off` of a stage's codes in shared memory: 16-byte pieces are permuted in
-// their 128-byte line so that the reads of 8 lanes (keys: pieces of neighbouring rows;
-// values: the same piece of every other row) touch every bank once.
-template <uint32_t ROW>
-__device__ __forceinline__ uint32_t swizzle(uint32_t off)
-{
-    const uint32_t line = off >> 7;
-    uint32_t m;
-    if (ROW == 256)
-        m = ((line >> 1) & 7u) ^ ((line & 1u) << 1);
-    else if (ROW == 128)
-        m = line & 7u;
-    else if (ROW == 64)
-        m = (line & 3u) << 1;
-    else
-        m = (line & 1u) << 1;
-    return off ^ (m << 4);
-}
-
-// 16 bytes (zeros where `ok` is 0) into shared memory.
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// New tokens and tokens in the cache of sequence b that the kernels go by.
-__device__ __forceinline__ uint32_t sequence(const AttArgs &a, uint32_t b, uint32_t &first, uint32_t &len)
-{
-    uint32_t n = new_tokens(a.c, b, a.T, first);
-    if (n > a.max_new) {
-        atomicOr(a.c.status, MXQ_DEV_INVALID_PAGE);
-        n = 0;
-    }
-    len = (uint32_t)max(__ldg(a.c.lens + b), 0);
-    return n;
-}
-
-__device__ __forceinline__ uint32_t tiles_of(uint32_t n, uint32_t group) { return (n * group + kRows - 1) / kRows; }
-__device__ __forceinline__ uint32_t turns_of(uint32_t len) { return (len + kKeys - 1) / kKeys; }
-
-// Sum of v over the CTA, the same in every thread; and the exclusive sum before this thread.
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t *ws, uint32_t &before)
-{
-    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    uint32_t s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        s += lane >= (uint32_t)o ? u : 0u;
-    }
-    __syncthreads();
-    if (lane == 31u)
-        ws[warp] = s;
-    __syncthreads();
-    uint32_t total = 0;
-    before = s - v;
-    for (uint32_t w = 0; w < blockDim.x >> 5; ++w) {
-        before += w < warp ? ws[w] : 0u;
-        total += ws[w];
-    }
-    return total;
-}
+size_t left_bytes() { return kFewCtas * sizeof(Unfinished); }
+size_t rows_part_bytes(int64_t dim) { return (size_t)kFewCtas * 2 * kFewTile * (size_t)(dim + 2) * 4; }
+size_t tiles_part_bytes(int64_t dim) { return (size_t)kMaxSms * 2 * (dim == 256 ? 128 : kTile) * (size_t)(dim + 2) * 4; }
+bool few(int64_t group, int64_t max_new) { return group * max_new <= (int64_t)kFewRows; }
 
 } // namespace
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kWarps, D == 64 ? 4 : D == 128 ? 3 : 2)
-attention_rows_kernel(const AttArgs a)
-{
-    using S = Shape<FMT, D>;
-    constexpr uint32_t kThreads = 32 * kWarps;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ uint32_t ws[kWarps];
-    __shared__ float stat[2][kWarps][kRows];        // the warps' maxima and sums
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3u;
-    uint32_t *items = reinterpret_cast<uint32_t *>(smem + std::max<uint32_t>(S::smem, kWarps * S::outs));   // [seqs + 1]
-    uint32_t *parts = items + a.c.seqs + 1;
-    cudaGridDependencySynchronize();
-    cudaTriggerProgrammaticLaunchCompletion();
-
-    // The cut: as many turns to an item as give about `target` items.
-    uint32_t mine = 0, before;
-    for (uint32_t b = tid; b < a.c.seqs; b += kThreads) {
-        uint32_t first, len;
-        const uint32_t n = sequence(a, b, first, len);
-        mine += tiles_of(n, a.group) * a.c.heads * turns_of(len);
-    }
-    const uint32_t total = block_sum(mine, ws, before);
-    const uint32_t len_items = max((total + a.target - 1) / a.target, kWarps);
-    uint32_t base_items = 0, base_parts = 0;
-    for (uint32_t b0 = 0; b0 < a.c.seqs; b0 += kThreads) {
-        const uint32_t b = b0 + tid;
-        uint32_t ni = 0, np = 0;
-        if (b < a.c.seqs) {
-            uint32_t first, len;
-            const uint32_t n = sequence(a, b, first, len);
-            const uint32_t cut = max((turns_of(len) + len_items - 1) / len_items, 1u);
-            ni = tiles_of(n, a.group) * a.c.heads * cut;
-            np = cut > 1u ? ni : 0u;
-        }
-        uint32_t bi, bp;
-        const uint32_t ti = block_sum(ni, ws, bi), tp = block_sum(np, ws, bp);
-        if (b < a.c.seqs) {
-            items[b] = base_items + bi;
-            parts[b] = base_parts + bp;
-        }
-        base_items += ti;
-        base_parts += tp;
-    }
-    if (tid == 0) {
-        items[a.c.seqs] = base_items;
-        parts[a.c.seqs] = base_parts;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0) {
-        for (uint32_t i = tid; i <= a.c.seqs; i += kThreads) {
-            a.plan[4 + i] = items[i];
-            a.plan[4 + a.c.seqs + 1 + i] = parts[i];
-        }
-        if (tid == 0)
-            a.plan[0] = len_items;
-    }
-
-    char *ring = smem + warp * S::ring;
-    const uint32_t ring_s = smem_addr(ring);
-    char *qs = smem + kWarps * S::ring;
-    for (uint32_t item = blockIdx.x; item < base_items; item += gridDim.x) {
-        // Sequence of the item: the last b with items[b] <= item.
-        uint32_t lo = 0, hi = a.c.seqs;
-        while (hi - lo > 1u) {
-            const uint32_t mid = (lo + hi) >> 1;
-            if (items[mid] <= item)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const uint32_t b = lo;
-        uint32_t first, len;
-        const uint32_t n = sequence(a, b, first, len), rows = n * a.group, tiles = tiles_of(n, a.group);
-        const uint32_t cut = max((turns_of(len) + len_items - 1) / len_items, 1u);
-        const uint32_t in = item - items[b], split = in % cut, tile = (in / cut) % tiles, head = in / (cut * tiles);
-        // Keys of the tile: those its last row sees.
-        const uint32_t row_end = min((tile + 1) * kRows, rows);
-        const int64_t last = (int64_t)len - n + fastdiv(row_end - 1u, a.groupdiv);      // the last row's position
-        const uint32_t seen = last < 0 ? 0u : (uint32_t)last + 1u;
-        const uint32_t k0 = min(split * len_items * kKeys, seen), k1 = min(k0 + len_items * kKeys, seen);
-
-        // Queries: f16 rows times their factors, one warp a row.
-        __syncthreads();
-        float *factor = &stat[0][0][0];
-        for (uint32_t r = warp; r < kRows; r += kWarps) {
-            const uint32_t row = tile * kRows + r, i = fastdiv(row, a.groupdiv), h = row - i * a.group;
-            constexpr uint32_t per = D / 32;        // values of a lane
-            uint32_t w[per < 2 ? 1 : per / 2], m = 0;
-            const uint16_t *src = a.q + (int64_t)(first + i) * a.q_stride + ((uint64_t)head * a.group + h) * D + lane * per;
-#pragma unroll
-            for (uint32_t j = 0; j < per / 2; ++j) {
-                w[j] = row < rows ? __ldg(reinterpret_cast<const uint32_t *>(src) + j) : 0u;
-                m = absmax_bf16x2(m, w[j]);
-            }
-            m = __reduce_max_sync(0xFFFFFFFFu, fold_halves(m)) << 16;
-            const float f = row_factor(m);
-#pragma unroll
-            for (uint32_t j = 0; j < per / 2; ++j)
-                *reinterpret_cast<uint32_t *>(qs + r * S::q_pitch + (lane * per + 2 * j) * 2) =
-                    half2_bits(bf16_lo(w[j]) * f, bf16_hi(w[j]) * f);
-            if (lane == 0)
-                factor[r] = 1.0f / f;
-        }
-        __syncthreads();
-        // Of this lane's two rows: log2-scale factor and last key.
-        float fq[2];
-        int64_t pos[2];         // rows past the sequence's see every key, and are not stored
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t row = tile * kRows + g8 + 8 * i;
-            fq[i] = factor[g8 + 8 * i] * a.scale;
-            pos[i] = row < rows ? (int64_t)len - n + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
-        }
-        // This lane's run of a query: values [t4 D / 4, + D / 4) of rows g8 and g8 + 8.
-        uint2 q0[S::q_regs ? D / 16 : 1], q1[S::q_regs ? D / 16 : 1];
-        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2), *qb = qa + 8 * S::q_pitch;
-        if (S::q_regs) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                q0[i] = lds64(qa + i * 8);
-                q1[i] = lds64(qb + i * 8);
-            }
-        }
-        float kfac = 1.0f;
-        if (FMT == MXQ_FMT_NVFP4)
-            kfac = __ldg(a.c.k_s2 + head);
-
-        float acc[D / 8][4];
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-        float mx[2] = {kLowest, kLowest}, sum[2] = {0.0f, 0.0f};
-
-        // One turn's copies.  32 keys lie on one page, or on two of 16 tokens.
-        auto issue = [&](uint32_t key, uint32_t slot) {
-            if (key < k1) {
-                const uint32_t half = a.c.page_log == 4u ? 16u : 32u;
-                uint32_t page0 = find_page(a.c, b, key), page1 = page0;
-                if (half == 16u)
-                    page1 = key + 16u < k1 ? find_page(a.c, b, key + 16u) : a.c.pages;
-                const uint32_t mask = (1u << a.c.page_log) - 1u;
-                const uint32_t st = ring_s + slot * S::stage;
-                auto place = [&](uint32_t r, bool &ok) -> uint64_t {        // row of codes of the turn's key r
-                    const uint32_t page = r < half ? page0 : page1;
-                    ok = page < a.c.pages && key + r < k1;
-                    return ok ? (((uint64_t)page * a.c.heads + head) << a.c.page_log) + ((key + r) & mask) : 0ull;
-                };
-                constexpr uint32_t pieces = S::row / 16;        // of a key's codes
-#pragma unroll
-                for (uint32_t i = 0; i < pieces; ++i) {
-                    const uint32_t p = i * 32u + lane, r = p / pieces;
-                    bool ok;
-                    const uint64_t src = place(r, ok) * S::row + (p % pieces) * 16u;
-                    const uint32_t dst = st + swizzle<S::row>(p * 16u);
-                    cp16_or_zero(dst, a.c.k_codes + src, ok);
-                    cp16_or_zero(dst + S::codes, a.c.v_codes + src, ok);
-                }
-                // Scales: 16 bytes are 16 / blocks keys of one page.
-#pragma unroll
-                for (uint32_t i = 0; i < (S::scales / 16 + 31) / 32; ++i) {
-                    const uint32_t p = i * 32u + lane;
-                    if (p < S::scales / 16) {
-                        bool ok;
-                        const uint64_t src = place(p * 16u / S::blocks, ok) * S::blocks + p * 16u % S::blocks;
-                        cp16_or_zero(st + 2 * S::codes + p * 16u, a.c.k_scales + src, ok);
-                        cp16_or_zero(st + 2 * S::codes + S::scales + p * 16u, a.c.v_scales + src, ok);
-                    }
-                }
-            }
-            cp_commit();
-        };
-
-        uint32_t key = k0 + warp * kKeys, slot = 0;
-        issue(key, 0);
-        for (; key < k1; key += kWarps * kKeys, slot ^= 1u) {
-            issue(key + kWarps * kKeys, slot ^ 1u);
-            cp_wait<1>();
-            __syncwarp();
-            const char *st = ring + slot * S::stage;
-            const char *ksc = st + 2 * S::codes, *vsc = ksc + S::scales;
-            const uint32_t left = k1 - key;             // keys of the turn
-
-            // Scores of 32 keys: columns nt * 8 + ..., this lane decodes key g8 of each.
-            float s[4][4];
-            uint32_t kscale[4][S::fp4 ? D / 64 : (D + 127) / 128];      // f16x2, of the blocks of the lane's run
-            float kf = kfac;
-            if (S::fp4) {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const char *p = ksc + (nt * 8 + g8) * S::blocks + t4 * (D / 64);
-                    uint32_t w = 0;
-                    if (D == 64)
-                        w = *reinterpret_cast<const uint8_t *>(p);
-                    else if (D == 128)
-                        w = *reinterpret_cast<const uint16_t *>(p);
-                    else
-                        w = lds32(p);
-                    if (nt * 8 + g8 >= left)
-                        w = 0u;
-                    uint32_t h0, h1;
-                    e4m3x4_unpack(w, h0, h1);
-                    kscale[nt][0] = __byte_perm(h0, 0, 0x1010);
-                    if (D >= 128)
-                        kscale[nt][D >= 128 ? 1 : 0] = __byte_perm(h0, 0, 0x3232);
-                    if (D == 256) {
-                        kscale[nt][D == 256 ? 2 : 0] = __byte_perm(h1, 0, 0x1010);
-                        kscale[nt][D == 256 ? 3 : 0] = __byte_perm(h1, 0, 0x3232);
-                    }
-                }
-            } else {
-                uint32_t e[4][(D + 127) / 128], top = 0;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < (D + 127) / 128; ++j) {
-                        const uint32_t blk = D == 64 ? t4 >> 1 : D == 128 ? t4 : t4 * 2 + j;
-                        e[nt][j] = *reinterpret_cast<const uint8_t *>(ksc + (nt * 8 + g8) * S::blocks + blk);
-                        if (nt * 8 + g8 >= left)
-                            e[nt][j] = 0u;
-                        top = max(top, e[nt][j]);
-                    }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < (D + 127) / 128; ++j) {
-                        const float f = __uint_as_float((uint32_t)max((int)(e[nt][j] + 134u) - (int)top, 0) << 23);
-                        kscale[nt][j] = half2_bits(f, f);
-                    }
-                // 2^(top - 134), in two steps: it may be subnormal
-                kf = __uint_as_float(top << 23) * 0x1p-7f;
-                if (top == 0u)
-                    kf = 0x1p-134f;
-            }
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-                const uint32_t row = (nt * 8 + g8) * S::row;
-                constexpr int run = S::row / 4;          // bytes of a lane's run
-#pragma unroll
-                for (int p = 0; p < (run + 15) / 16; ++p) {
-                    uint32_t w[4];
-                    if (run >= 16) {
-                        const uint4 v = lds128(st + swizzle<S::row>(row + t4 * run + p * 16));
-                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                    } else {
-                        const uint2 v = lds64(st + swizzle<S::row>(row + t4 * run));
-                        w[0] = v.x, w[1] = v.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < (run >= 16 ? 4 : 2); ++i) {
-                        uint32_t h[4];
-                        constexpr int per = S::fp4 ? 2 : 1;         // products of a word
-                        if (S::fp4)
-                            e2m1x8_unpack(w[i], h);
-                        else
-                            e4m3x4_unpack(w[i], h[0], h[1]);
-#pragma unroll
-                        for (int u = 0; u < per; ++u) {
-                            const int step = (p * 4 + i) * per + u;       // of 4 values of each lane
-                            const uint32_t sc = kscale[nt][S::fp4 ? step / 4 : step / 8];
-                            uint2 x0, x1;
-                            if (S::q_regs) {
-                                x0 = q0[step % (D / 16)];
-                                x1 = q1[step % (D / 16)];
-                            } else {
-                                x0 = lds64(qa + step * 8);
-                                x1 = lds64(qb + step * 8);
-                            }
-                            mma16816(s[nt], x0.x, x1.x, x0.y, x1.y, hmul2_bits(h[2 * u], sc), hmul2_bits(h[2 * u + 1], sc));
-                        }
-                    }
-                }
-            }
-
-            // The values' scales; E: their largest power.
-            constexpr int vblocks = S::fp4 && D == 256 ? 2 : 1;      // of a lane's run of D / 8
-            uint32_t vscale[4][vblocks];        // of key pairs (2 t4, + 1) + 8 i
-            float E = 0.0f, inv = 1.0f;
-            if (S::fp4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < vblocks; ++j) {
-                        const uint32_t r = i * 8 + 2 * t4, blk = D == 64 ? g8 >> 1 : D == 128 ? g8 : g8 * 2 + j;
-                        uint32_t w0 = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
-                        uint32_t w1 = *reinterpret_cast<const uint8_t *>(vsc + (r + 1) * S::blocks + blk);
-                        w0 = r < left ? w0 : 0u;
-                        w1 = r + 1 < left ? w1 : 0u;
-                        vscale[i][j] = e4m3x2_to_f16x2(w0 | (w1 << 8));
-                    }
-            } else {
-                uint32_t e[4][2], top = 27u;       // 2^-100 at least: what is below is nothing beside a sum
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t r = i * 8 + 2 * t4 + j, blk = D == 64 ? g8 >> 2 : D == 128 ? g8 >> 1 : g8;
-                        e[i][j] = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
-                        if (r >= left)
-                            e[i][j] = 0u;
-                        top = max(top, e[i][j]);
-                    }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    vscale[i][0] = half2_bits(__uint_as_float((uint32_t)max((int)(e[i][0] + 134u) - (int)top, 0) << 23),
-                                              __uint_as_float((uint32_t)max((int)(e[i][1] + 134u) - (int)top, 0) << 23));
-                E = (float)((int)top - 134);
-                inv = __uint_as_float((uint32_t)(261 - (int)top) << 23);       // 2^-E, top at least 27 (and at most 254)
-            }
-
-            // Running maximum, weights.
-            float f[2] = {fq[0] * kf, fq[1] * kf};
-            int lim[2];                                 // last key of the turn that a row sees
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                lim[i] = (int)max(min(pos[i] - (int64_t)key, (int64_t)min(left, kKeys) - 1), (int64_t)-1);
-            if (__any_sync(0xFFFFFFFFu, min(lim[0], lim[1]) < (int)kKeys - 1)) {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[nt][j] = (int)(nt * 8 + 2 * t4 + (j & 1)) <= lim[j >> 1] ? fmaf(s[nt][j], f[j >> 1], E) : -INFINITY;
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[nt][j] = fmaf(s[nt][j], f[j >> 1], E);
-            }
-            float alpha[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float m = mx[i];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-                    m = fmaxf(m, fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                alpha[i] = ex2(mx[i] - m);
-                mx[i] = m;
-                float part = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    s[nt][2 * i] = ex2(s[nt][2 * i] - m);
-                    s[nt][2 * i + 1] = ex2(s[nt][2 * i + 1] - m);
-                    part += s[nt][2 * i] + s[nt][2 * i + 1];
-                }
-                sum[i] = fmaf(sum[i], alpha[i], part * inv);
-            }
-            if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    acc[j][0] *= alpha[0];
-                    acc[j][1] *= alpha[0];
-                    acc[j][2] *= alpha[1];
-                    acc[j][3] *= alpha[1];
-                }
-            }
-
-            // Outputs: 16 keys at a time, columns d = run of this lane.
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const uint32_t p0 = half2_bits(s[2 * kk][0], s[2 * kk][1]), p1 = half2_bits(s[2 * kk][2], s[2 * kk][3]);
-                const uint32_t p2 = half2_bits(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                               p3 = half2_bits(s[2 * kk + 1][2], s[2 * kk + 1][3]);
-                constexpr int run = S::row / 8;          // bytes of a lane's run of columns
-                constexpr int words = run < 16 ? run / 4 : 4;
-                const char *vs = st + S::codes;
-#pragma unroll
-                for (int p = 0; p < (run + 15) / 16; ++p) {
-                    uint32_t w[4][words];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t r = kk * 16 + (i >> 1) * 8 + 2 * t4 + (i & 1);
-                        // of two pieces the lanes of odd g8 take the second first (banks)
-                        const uint32_t off = r * S::row + g8 * run + (run == 32 ? (p ^ (g8 & 1u)) * 16u : 0u);
-                        const char *q = vs + swizzle<S::row>(off);
-                        if (words == 4) {
-                            const uint4 v = lds128(q);
-                            w[i][0] = v.x, w[i][words > 1 ? 1 : 0] = v.y, w[i][words > 2 ? 2 : 0] = v.z, w[i][words > 2 ? 3 : 0] = v.w;
-                        } else if (words == 2) {
-                            const uint2 v = lds64(q);
-                            w[i][0] = v.x, w[i][words > 1 ? 1 : 0] = v.y;
-                        } else
-                            w[i][0] = lds32(q);
-                    }
-#pragma unroll
-                    for (int i = 0; i < words; ++i) {
-                        if (S::fp4) {
-                            // nibbles of two keys side by side: codes 0, 2, 4, 6 and 1, 3, 5, 7 of the word
-                            const uint32_t lm = 0x0F0F0F0Fu;
-                            uint32_t b0[2][4], b1[2][4];
-                            e2m1x8_unpack((w[0][i] & lm) | ((w[1][i] << 4) & ~lm), b0[0]);
-                            e2m1x8_unpack(((w[0][i] >> 4) & lm) | (w[1][i] & ~lm), b0[1]);
-                            e2m1x8_unpack((w[2][i] & lm) | ((w[3][i] << 4) & ~lm), b1[0]);
-                            e2m1x8_unpack(((w[2][i] >> 4) & lm) | (w[3][i] & ~lm), b1[1]);
-                            const int blk = vblocks == 2 ? i / 2 : 0;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                mma16816(acc[(p * words + i) * 8 + j], p0, p1, p2, p3,
-                                         hmul2_bits(b0[j & 1][j >> 1], vscale[2 * kk][blk]),
-                                         hmul2_bits(b1[j & 1][j >> 1], vscale[2 * kk + 1][blk]));
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                uint32_t x0, x1, y0, y1;
-                                e4m3x4_unpack(__byte_perm(w[0][i], w[1][i], u ? 0x7362 : 0x5140), x0, x1);
-                                e4m3x4_unpack(__byte_perm(w[2][i], w[3][i], u ? 0x7362 : 0x5140), y0, y1);
-                                const int j = (p * words + i) * 4 + u * 2;
-                                mma16816(acc[j], p0, p1, p2, p3, hmul2_bits(x0, vscale[2 * kk][0]),
-                                         hmul2_bits(y0, vscale[2 * kk + 1][0]));
-                                mma16816(acc[j + 1], p0, p1, p2, p3, hmul2_bits(x1, vscale[2 * kk][0]),
-                                         hmul2_bits(y1, vscale[2 * kk + 1][0]));
-                            }
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-        }
-        cp_wait<0>();
-
-        // Join the warps: sums over the lanes of a row first.
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-        }
-        __syncthreads();
-        if (t4 == 0) {
-            stat[0][warp][g8] = mx[0];
-            stat[0][warp][g8 + 8] = mx[1];
-            stat[1][warp][g8] = sum[0];
-            stat[1][warp][g8 + 8] = sum[1];
-        }
-        __syncthreads();
-        float *outs = reinterpret_cast<float *>(smem) + warp * (S::outs / 4);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t r = g8 + 8 * i;
-            float m = stat[0][0][r];
-#pragma unroll
-            for (uint32_t w = 1; w < kWarps; ++w)
-                m = fmaxf(m, stat[0][w][r]);
-            const float f = ex2(mx[i] - m);
-            // columns 2 t4 and 2 t4 + 1 of each product: the runs of lanes g8 = 2 t4 and 2 t4 + 1
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    const uint32_t jj = S::row == 256 && c ? j ^ 16 : j;
-                    outs[r * (D + 4) + (2 * t4 + c) * (D / 8) + jj] = acc[j][2 * i + c] * f;
-                }
-        }
-        __syncthreads();
-        const float vfac = FMT == MXQ_FMT_NVFP4 ? __ldg(a.c.v_s2 + head) : 1.0f;
-        const uint32_t slot_part = parts[b] + in;
-        for (uint32_t i = tid; i < kRows * (D / 4); i += kThreads) {
-            const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, row = tile * kRows + r;
-            if (row >= rows)
-                continue;
-            float m = stat[0][0][r];
-#pragma unroll
-            for (uint32_t w = 1; w < kWarps; ++w)
-                m = fmaxf(m, stat[0][w][r]);
-            float l = 0.0f;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (uint32_t w = 0; w < kWarps; ++w) {
-                l = fmaf(stat[1][w][r], ex2(stat[0][w][r] - m), l);
-                const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + w * (S::outs / 4) + r * (D + 4) + d);
-                v.x += x.x;
-                v.y += x.y;
-                v.z += x.z;
-                v.w += x.w;
-            }
-            if (cut > 1u) {
-                float *p = a.part + (uint64_t)slot_part * (kRows * (D + 2)) + r * D + d;
-                *reinterpret_cast<float4 *>(p) = v;
-                if (d == 0) {
-                    float *q = a.part + (uint64_t)slot_part * (kRows * (D + 2)) + kRows * D + r * 2;
-                    q[0] = m;
-                    q[1] = l;
-                }
-                continue;
-            }
-            const uint32_t it = fastdiv(row, a.groupdiv), h = head * a.group + row - it * a.group;
-            const uint64_t out = (uint64_t)(first + it) * (a.c.heads * a.group) + h;
-            const float f = l == 0.0f ? 0.0f : vfac / l;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi2 = __floats2bfloat162_rn(v.z * f, v.w * f);
-            *reinterpret_cast<uint2 *>(a.o + out * D + d) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi2));
-            if (d == 0 && a.lse)
-                a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        }
-        __syncthreads();
-    }
-}
-
-// Rows of tiles that were cut: their parts, in order.  A warp takes a row.
-template <int D>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttArgs a)
+// The parts of a tile that CTA blockIdx.x of the kernel before began, added up in
+// their order.  A warp takes a row, lanes its columns.
+template <uint32_t R, int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttArgs a)
 {
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    const uint32_t lane = threadIdx.x & 31u, heads = a.c.heads * a.group;
-    const uint64_t w = (uint64_t)blockIdx.x * 4u + (threadIdx.x >> 5);
-    if (w >= (uint64_t)a.T * heads)
-        return;
-    const uint32_t t = (uint32_t)(w / heads), hq = (uint32_t)(w - (uint64_t)t * heads);
-    const uint32_t b = find_sequence(a.c, t);
-    if (b == a.c.seqs)
-        return;
-    uint32_t first, len;
-    const uint32_t n = sequence(a, b, first, len), len_items = a.plan[0];
-    const uint32_t cut = (turns_of(len) + len_items - 1) / len_items;
-    if (n == 0 || cut < 2u)
-        return;
-    const uint32_t head = fastdiv(hq, a.groupdiv), row = (t - first) * a.group + hq - head * a.group;
-    const uint32_t tile = row / kRows, r = row % kRows;
-    const uint32_t p0 = a.plan[4 + a.c.seqs + 1 + b] + (head * tiles_of(n, a.group) + tile) * cut;
-    const float *part = a.part + (uint64_t)p0 * (kRows * (D + 2));
-    float m = kLowest;
-    for (uint32_t i = lane; i < cut; i += 32u)
-        m = fmaxf(m, part[(uint64_t)i * (kRows * (D + 2)) + kRows * D + r * 2]);
+    const uint32_t lane = threadIdx.x & 31u, cta = blockIdx.x;
+    const Unfinished u = a.left[cta];
+    const uint32_t end = min(u.rows - u.row0, R);
+    for (uint32_t r = blockIdx.y * 8u + (threadIdx.x >> 5); u.parts > 0u && r < end; r += gridDim.y * 8u) {
+        // maximum over the parts: the first is the CTA's second, the others their CTAs' first
+        float m = kLowest;
+        for (uint32_t i = lane; i < u.parts; i += 32u)
+            m = fmaxf(m, part_of<R, D>(a, cta + i, i == 0u)[R * D + r * 2u]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    constexpr int per = D / 32;
-    float v[per], l = 0.0f;
-#pragma unroll
-    for (int j = 0; j < per; ++j)
-        v[j] = 0.0f;
-    for (uint32_t i = 0; i < cut; ++i) {
-        const float *p = part + (uint64_t)i * (kRows * (D + 2));
-        const float f = ex2(p[kRows * D + r * 2] - m);
-        l = fmaf(p[kRows * D + r * 2 + 1], f, l);
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        constexpr int per = D / 32;
+        float v[per], l = 0.0f;
 #pragma unroll
         for (int j = 0; j < per; ++j)
-            v[j] = fmaf(p[r * D + j * 32 + lane], f, v[j]);
-    }
-    const float vfac = a.c.v_s2 ? __ldg(a.c.v_s2 + head) : 1.0f, f = l == 0.0f ? 0.0f : vfac / l;
+            v[j] = 0.0f;
+#pragma unroll 4
+        for (uint32_t i = 0; i < u.parts; ++i) {
+            const float *p = part_of<R, D>(a, cta + i, i == 0u);
+            const float2 st = *reinterpret_cast<const float2 *>(p + R * D + r * 2u);
+            const float f = ex2(st.x - m);
+            l = fmaf(st.y, f, l);
 #pragma unroll
-    for (int j = 0; j < per; ++j)
-        reinterpret_cast<__nv_bfloat16 *>(a.o)[w * D + j * 32 + lane] = __float2bfloat16_rn(v[j] * f);
-    if (lane == 0 && a.lse)
-        a.lse[w] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            for (int j = 0; j < per; ++j)
+                v[j] = fmaf(p[r * D + j * 32 + lane], f, v[j]);
+        }
+        const uint32_t row = u.row0 + r, i = fastdiv(row, a.groupdiv), h = u.head * a.group + row - i * a.group;
+        const uint64_t out = (uint64_t)(u.first + i) * (a.c.heads * a.group) + h;
+        const float f = l == 0.0f ? 0.0f : (a.c.v_s2 ? __ldg(a.c.v_s2 + u.head) : 1.0f) / l;
+#pragma unroll
+        for (int j = 0; j < per; ++j)
+            reinterpret_cast<__nv_bfloat16 *>(a.o)[out * D + j * 32 + lane] = __float2bfloat16_rn(v[j] * f);
+        if (lane == 0 && a.lse)
+            a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
 }
 
 namespace {
 
-template <int FMT, int D>
-cudaError_t run(AttArgs a, int sms, cudaStream_t s)
+template <uint32_t R>
+cudaError_t join(const AttArgs &a, int dim, uint32_t ctas, cudaStream_t s)
 {
-    using S = Shape<FMT, D>;
-    const auto k = attention_rows_kernel<FMT, D>;
-    constexpr size_t most = 227 * 1024 - 2048;
-    const size_t smem = std::max<size_t>(S::smem, kWarps * S::outs) + 8 * ((size_t)a.c.seqs + 1);
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    if (e != cudaSuccess)
-        return e;
-    const uint32_t fit = (uint32_t)std::min<size_t>(most / smem, D == 64 ? 4 : D == 128 ? 3 : 2);
-    a.target = std::min<uint32_t>((uint32_t)sms * fit, kMaxItems);
-    const cudaError_t r = launch_dependent(k, dim3(a.target), 32 * kWarps, smem, s, a);
-    if (r != cudaSuccess)
-        return r;
-    const uint64_t rows = (uint64_t)a.T * a.c.heads * a.group;
-    return launch_dependent(attention_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a);
+    const dim3 grid(ctas, R == 16 ? 2 : 8);
+    return dim == 64    ? launch_dependent(attention_join_kernel<R, 64>, grid, 256, 0, s, a)
+           : dim == 128 ? launch_dependent(attention_join_kernel<R, 128>, grid, 256, 0, s, a)
+                        : launch_dependent(attention_join_kernel<R == 256 ? 128 : R, 256>, grid, 256, 0, s, a);
 }
-
-size_t plan_bytes(int64_t seqs) { return (size_t)((4 + 2 * (seqs + 1)) * 4 + 255) / 256 * 256; }
 
 } // namespace
 
-size_t attention_workspace_bytes(int64_t seqs, int64_t head_dim)
+// Both kernels' parts lie in the same place: one joins before the other begins.
+size_t attention_workspace_bytes(int64_t group, int64_t head_dim, int64_t max_new)
 {
-    return plan_bytes(seqs) + (size_t)kMaxCut * kRows * (size_t)(head_dim + 2) * 4;
+    return left_bytes() + std::max(rows_part_bytes(head_dim), few(group, max_new) ? 0 : tiles_part_bytes(head_dim));
 }
 
 cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStream_t s)
@@ -758,17 +110,31 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     a.scale = c.scale * kLog2e;
     a.o = c.o;
     a.lse = c.lse;
-    a.target = 0;
-    a.plan = static_cast<uint32_t *>(c.workspace);
-    a.part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + plan_bytes(c.c.seqs));
+    a.left = static_cast<Unfinished *>(c.workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + left_bytes());
     a.groupdiv = make_fastdiv(a.group);
-    if (fmt == MXQ_FMT_NVFP4)
-        return dim == 64    ? run<MXQ_FMT_NVFP4, 64>(a, sms, s)
-               : dim == 128 ? run<MXQ_FMT_NVFP4, 128>(a, sms, s)
-                            : run<MXQ_FMT_NVFP4, 256>(a, sms, s);
-    return dim == 64    ? run<MXQ_FMT_MXFP8, 64>(a, sms, s)
-           : dim == 128 ? run<MXQ_FMT_MXFP8, 128>(a, sms, s)
-                        : run<MXQ_FMT_MXFP8, 256>(a, sms, s);
+    const uint32_t ctas = std::min<uint32_t>((uint32_t)sms, kMaxSms);
+    const bool many = !few(a.group, c.max_new);
+    // A lone sequence is one kernel's, whatever it has.
+    const bool rows = !many || c.c.seqs > 1u;
+    if (many) {
+        a.over = rows ? kFewRows : 0u;
+        a.upto = 0xFFFFFFFFu;
+        a.min_steps = 4;
+        e = launch_attention_tiles(a, fmt, dim, ctas, s);
+        if (e == cudaSuccess)
+            e = join<kTile>(a, dim, ctas, s);
+    }
+    if (rows && e == cudaSuccess) {
+        a.over = 0;
+        a.upto = many ? kFewRows : 0xFFFFFFFFu;
+        a.min_steps = 8;
+        uint32_t n = 0;         // at most kFewCtas
+        e = launch_attention_rows(a, fmt, dim, ctas, n, s);
+        if (e == cudaSuccess)
+            e = join<kFewTile>(a, dim, n, s);
+    }
+    return e;
 }
 
 } // namespace mxq

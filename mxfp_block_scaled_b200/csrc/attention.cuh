@@ -1,0 +1,286 @@
+// attention.cuh -- how the attention kernels divide their work (sm_100a).
+//
+// A tile is up to R rows (a new token and a query head each) of one sequence and
+// key/value head: row r is new token r / group and head r % group of the group.  A
+// step is a tile and 2^LOG keys from a multiple of 2^LOG on; a tile has those of
+// the keys that its last row sees, and one at least.  All steps in a row, by
+// sequence, head, tile and key, are divided evenly among the CTAs, whatever tile
+// boundaries lie between: no CTA has more than another by more than one step, and
+// each leaves at most two tiles unfinished, the one it begins with and the one it
+// ends with.  Unfinished tiles are left in the workspace (`part`), and
+// attention_join_kernel adds up the parts of each in the order of the keys: no
+// atomics, and the division follows from the lengths, the sizes and the number of
+// SMs alone.  Every warp works its CTA's range out for itself, in the same way.
+#pragma once
+
+#include "mxq_cache.cuh"
+#include "mxq.h"
+
+namespace mxq {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e30f;       // a running maximum before the first key
+
+// What a CTA leaves of the tile that it begins and does not finish (parts 0: none).
+struct Unfinished {
+    uint32_t first;             // the sequence's first row
+    uint32_t row0, rows;        // the tile's first row, and the sequence's rows
+    uint32_t head;
+    uint32_t parts;             // the CTAs from this one on that have a part
+    uint32_t pad[3];
+};
+
+struct AttArgs {
+    CacheView c;
+    const uint16_t *q;
+    int64_t q_stride;
+    uint32_t T, group, max_new;
+    uint32_t over, upto;        // the sequences of this launch: those of over < rows <= upto
+    uint32_t min_steps;         // of a CTA, where there are few
+    float scale;                // softmax scale times log2(e)
+    uint16_t *o;
+    float *lse;
+    Unfinished *left;           // [CTA]
+    float *part;                // [CTA][2][R][dim] outputs, [R][2] maxima and sums
+    FastDiv groupdiv;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Sequence b as this launch sees it: rows 0 where it is another launch's, or invalid.
+struct Sequence {
+    uint32_t first, n, rows;
+    int64_t len;
+};
+__device__ __forceinline__ Sequence sequence(const AttArgs &a, uint32_t b)
+{
+    Sequence s;
+    s.n = new_tokens(a.c, b, a.T, s.first);
+    if (s.n > a.max_new) {
+        atomicOr(a.c.status, MXQ_DEV_INVALID_PAGE);
+        s.n = 0;
+    }
+    s.rows = s.n * a.group;
+    if (s.rows <= a.over || s.rows > a.upto)
+        s.n = s.rows = 0;
+    s.len = max(__ldg(a.c.lens + b), 0);
+    return s;
+}
+
+template <uint32_t R, uint32_t LOG>
+struct Division {
+    // Keys that tile `rt` sees, and its steps.
+    static __device__ __forceinline__ uint32_t keys(const AttArgs &a, const Sequence &s, uint32_t rt)
+    {
+        const uint32_t last = min((rt + 1u) * R, s.rows) - 1u;
+        return (uint32_t)max(s.len - s.n + fastdiv(last, a.groupdiv) + 1, (int64_t)0);
+    }
+    static __device__ __forceinline__ uint32_t steps(const AttArgs &a, const Sequence &s, uint32_t rt)
+    {
+        return max((keys(a, s, rt) + (1u << LOG) - 1u) >> LOG, 1u);
+    }
+    static __device__ __forceinline__ uint32_t tiles(const Sequence &s) { return (s.rows + R - 1u) / R; }
+
+    // Steps of a key/value head of sequence s, all lanes of the warp together.
+    static __device__ __forceinline__ uint64_t head_steps(const AttArgs &a, const Sequence &s)
+    {
+        uint64_t v = 0;
+        for (uint32_t rt = threadIdx.x & 31u; rt < tiles(s); rt += 32u)
+            v += steps(a, s, rt);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    }
+
+    // A sequence a lane: steps of all heads of sequence b (0 past the last).
+    static __device__ __forceinline__ uint64_t lane_steps(const AttArgs &a, uint32_t b)
+    {
+        Sequence s = {};
+        if (b < a.c.seqs)
+            s = sequence(a, b);
+        const uint32_t nt = tiles(s);
+        uint64_t v = 0;
+        if (nt <= 4u)
+            for (uint32_t rt = 0; rt < nt; ++rt)
+                v += steps(a, s, rt);
+        for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nt > 4u); many; many &= many - 1u) {
+            const uint32_t lane = __ffs(many) - 1;
+            Sequence w;
+            w.first = 0;
+            w.n = __shfl_sync(0xFFFFFFFFu, s.n, lane);
+            w.rows = __shfl_sync(0xFFFFFFFFu, s.rows, lane);
+            w.len = __shfl_sync(0xFFFFFFFFu, s.len, lane);
+            const uint64_t u = head_steps(a, w);
+            if ((threadIdx.x & 31u) == lane)
+                v = u;
+        }
+        return v * a.c.heads;
+    }
+};
+
+// Where a CTA's range of steps begins and ends; in shared memory.
+struct Range {
+    uint64_t sums[32];
+    uint64_t begin, end;        // steps of this CTA
+    uint64_t total;
+    uint32_t ctas;              // that have steps
+    uint32_t b;                 // sequence of the first step, and its place there
+    uint64_t at;
+};
+
+// Sum of v over the CTA, the same in every thread; `before`: over the threads before this one.
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, Range &r, uint64_t &before)
+{
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    uint64_t s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        s += lane >= (uint32_t)o ? u : 0ull;
+    }
+    __syncthreads();
+    if (lane == 31u)
+        r.sums[warp] = s;
+    __syncthreads();
+    uint64_t total = 0;
+    before = s - v;
+    for (uint32_t w = 0; w < blockDim.x >> 5; ++w) {
+        before += w < warp ? r.sums[w] : 0ull;
+        total += r.sums[w];
+    }
+    return total;
+}
+
+// All threads: this CTA's range.
+template <typename Div>
+__device__ __forceinline__ void find_range(const AttArgs &a, Range &r)
+{
+    uint64_t own = 0, before, v = 0;
+    for (uint32_t b0 = 0; b0 < a.c.seqs; b0 += blockDim.x)
+        own += v = Div::lane_steps(a, b0 + threadIdx.x);
+    const uint64_t total = block_sum(own, r, before);
+    const uint32_t ctas = (uint32_t)max(min((uint64_t)gridDim.x, total / a.min_steps), (uint64_t)1);
+    const uint64_t begin = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    const uint64_t end = blockIdx.x < ctas ? total * (blockIdx.x + 1u) / ctas : total;
+    if (threadIdx.x == 0) {
+        r.begin = begin;
+        r.end = end;
+        r.total = total;
+        r.ctas = ctas;
+    }
+    if (begin < end) {
+        uint64_t base = 0;
+        for (uint32_t b0 = 0; b0 < a.c.seqs && base <= begin; b0 += blockDim.x) {
+            if (a.c.seqs > blockDim.x)
+                v = Div::lane_steps(a, b0 + threadIdx.x);
+            const uint64_t sum = block_sum(v, r, before);
+            if (begin >= base + before && begin < base + before + v) {
+                r.b = b0 + threadIdx.x;
+                r.at = begin - base - before;
+            }
+            base += sum;
+        }
+    }
+    __syncthreads();
+}
+
+// A warp's walk over the pieces of its CTA's range: a tile, or the part of it in
+// the range.  All lanes call and hold the same values.
+template <uint32_t R, uint32_t LOG>
+struct Walk {
+    using Div = Division<R, LOG>;
+    uint64_t left;              // steps of the range after this piece
+    Sequence s;
+    uint32_t b, head, rt;
+    uint32_t k0, k1, steps;     // the piece's steps of the tile's
+    uint32_t keys;              // the tile's keys
+
+    __device__ __forceinline__ bool whole() const { return k1 - k0 == steps; }
+
+    __device__ __forceinline__ void take()
+    {
+        steps = Div::steps(*a, s, rt);
+        keys = Div::keys(*a, s, rt);
+        k1 = (uint32_t)min((uint64_t)steps, k0 + left);
+        left -= k1 - k0;
+    }
+    __device__ __forceinline__ bool begin(const AttArgs &args, const Range &r)
+    {
+        a = &args;
+        left = r.end - r.begin;
+        if (left == 0)
+            return false;
+        b = r.b;
+        s = sequence(args, b);
+        const uint64_t per = Div::head_steps(args, s);
+        head = (uint32_t)(r.at / per);
+        uint64_t at = r.at - head * per;
+        // the tile: 32 at a time
+        const uint32_t lane = threadIdx.x & 31u, nt = Div::tiles(s);
+        for (rt = 0;; rt += 32u) {
+            uint64_t v = rt + lane < nt ? Div::steps(args, s, rt + lane) : 0u;
+            const uint64_t own = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                v += lane >= (uint32_t)o ? u : 0ull;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, v > at);
+            if (past) {
+                const uint32_t l = __ffs(past) - 1;
+                at -= __shfl_sync(0xFFFFFFFFu, v - own, l);
+                rt += l;
+                break;
+            }
+            at -= __shfl_sync(0xFFFFFFFFu, v, 31);
+            if (rt + 32u >= nt)         // cannot be: the range lies in the sequence
+                return false;
+        }
+        k0 = (uint32_t)at;
+        take();
+        return true;
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (left == 0)
+            return false;
+        k0 = 0;
+        if (++rt == Div::tiles(s)) {
+            rt = 0;
+            if (++head == a->c.heads) {
+                head = 0;
+                do {
+                    if (++b >= a->c.seqs)
+                        return false;
+                    s = sequence(*a, b);
+                } while (s.rows == 0);
+            }
+        }
+        take();
+        return true;
+    }
+    const AttArgs *a;
+};
+
+// CTAs from this one on that have a part of the tile that the range's last piece
+// (of k steps so far) begins.
+__device__ __forceinline__ uint32_t parts_of(const Range &r, uint32_t steps, uint32_t done)
+{
+    const uint64_t last = r.end - done + steps - 1u;            // the tile's last step
+    // the CTA of a step x: the largest c with total c / ctas <= x
+    return (uint32_t)(((last + 1u) * r.ctas + r.total - 1u) / r.total) - blockIdx.x;
+}
+
+template <uint32_t R, int D>
+__device__ __forceinline__ float *part_of(const AttArgs &a, uint32_t cta, uint32_t second)
+{
+    return a.part + (uint64_t)(cta * 2u + second) * (R * (D + 2));
+}
+
+} // namespace mxq

@@ -47,6 +47,7 @@
 #include "mxq_internal.h"
 #include "mxq.h"
 #include "mxq_test.h"
+#include "mxq_tcgen05.cuh"
 #include "mxq_tma.cuh"
 #include <algorithm>
 #include <atomic>
@@ -371,21 +372,6 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
         ;
 }
 
-// Shared-memory descriptor of a K-major operand tile, rows of 128 bytes with
-// the 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// 1 in one lane of the (whole) warp.
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
 // The instructions below are issued by the lane whose `one` is 1, inside code
 // that the whole warp runs: their descriptors and addresses then stay in
 // uniform registers.  In a branch of one thread each product took 85 cycles to
@@ -397,15 +383,6 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
                  "setp.ne.u32 q, %5, 0;\n\t"
                  "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(one) : "memory");
-}
-
-// The products so far arrive on `bar` when done.
-__device__ __forceinline__ void umma_commit(uint64_t *bar, uint32_t one)
-{
-    asm volatile("{\n\t.reg .pred q;\n\t"
-                 "setp.ne.u32 q, %1, 0;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-                 ::"r"(smem_addr(bar)), "r"(one) : "memory");
 }
 
 __device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes, uint32_t one)
@@ -425,39 +402,6 @@ __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, uint
                  "[%0], [%1, {%3, %4}], [%2];\n\t}"
                  ::"r"(smem_addr(dst)), "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(one) : "memory");
 }
-
-// 32 columns of this warp's 32 TMEM lanes, one lane a thread.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
-                   "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
-                   "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
-                   "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-                 : "r"(addr));
-}
-
-// The loads so far are done; v is named so that no use of it moves above.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
-                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
-                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
-                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-                 :: "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
 // Sums of 16 bytes' worth of results -> their bits.
 template <typename Out>

@@ -53,7 +53,7 @@ struct AttentionCall {
     float *lse;
     void *workspace;
 };
-size_t attention_workspace_bytes(int64_t seqs, int64_t head_dim);
+size_t attention_workspace_bytes(int64_t group, int64_t head_dim, int64_t max_new);
 cudaError_t launch_attention(const AttentionCall &a, int fmt, int dim, cudaStream_t s);
 
 } // namespace mxq
