@@ -35,10 +35,14 @@ namespace mxq {
 namespace {
 
 constexpr uint32_t kSpin = 1u << 18;        // tests of a barrier before a wait gives up
-constexpr int kThreads = 512;               // two softmax groups, decoding, issue (one warp of four)
-// Registers of a thread: 128 at launch; the sum of the shares must not pass that.
-constexpr int kSoftRegs = 184, kCodeRegs = 112, kIssueRegs = 32;
-static_assert(2 * kSoftRegs + kCodeRegs + kIssueRegs <= 4 * 128, "register shares");
+// Warps 0-3 and 4-7: softmax groups, whose first warps issue; 8-11 decode keys,
+// 12-15 values.
+constexpr uint32_t kCodeWarp = 8;
+constexpr int kThreads = 512;
+// Registers of a thread: 128 at launch, of which the decoding warps give up what the
+// softmax ones take.
+constexpr int kLaunchRegs = 128, kSoftRegs = 192, kCodeRegs = 64;
+static_assert(kLaunchRegs * kThreads <= 65536 && kSoftRegs + kCodeRegs <= 2 * kLaunchRegs, "register shares");
 
 template <int FMT, int D>
 struct Shape {
@@ -57,7 +61,7 @@ struct Shape {
 };
 
 struct Bars {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pv[2], qfull[2], ffull[4], meet, drain;
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pv[2], qfull[2], ffull[4], meet, drain[2];
     uint32_t tmem, abort;
     float kfac[4][4], vexp[4][4], vinv[4][4];   // by step % 4 and decoding warp: powers of keys, values
 };
@@ -163,22 +167,22 @@ attention_tiles_kernel(const AttArgs a)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.kfull[i], 4);
-            mbar_init(&bars.kempty[i], 1);
+            mbar_init(&bars.kempty[i], 2);
             mbar_init(&bars.vfull[i], 4);
-            mbar_init(&bars.vempty[i], 1);
+            mbar_init(&bars.vempty[i], 2);
             mbar_init(&bars.sfull[i], 1);
             mbar_init(&bars.pfull[i], 4);
             mbar_init(&bars.pv[i], 1);
             mbar_init(&bars.qfull[i], 4);
+            mbar_init(&bars.drain[i], 1);
         }
         for (int i = 0; i < 4; ++i)
-            mbar_init(&bars.ffull[i], 4);
+            mbar_init(&bars.ffull[i], 8);
         mbar_init(&bars.meet, 8);
-        mbar_init(&bars.drain, 1);
         bars.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_addr(&bars.tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -199,104 +203,61 @@ attention_tiles_kernel(const AttArgs a)
     static_assert(D == 128 || kP + S::keys <= 512, "TMEM");
 
     W w;
-    if (warp >= 12) {
-        regs_down<kIssueRegs>();
-        if (warp == 12) {
-            const uint32_t one = elect_one();
-            uint32_t t0 = 0, buf0[2] = {0, 0}, q0[2] = {0, 0};
-            bool ok = true;
-            constexpr uint32_t sdesc = (1u << 4) | ((S::keys / 8u) << 17) | (8u << 24);
-            constexpr uint32_t odesc = (1u << 4) | (1u << 16) | ((D / 8u) << 17) | (8u << 24);
-            for (bool more = w.begin(a, range); more && ok; more = w.next()) {
-                const Units<S> un(w);
-                const uint32_t units = un.two ? 2u * un.steps : un.steps;
-                ok = wait_all(&bars.qfull[0], q0[0], bars, a.c.status) &&
-                     (!un.two || wait_all(&bars.qfull[1], q0[1], bars, a.c.status));
-                ++q0[0];
-                q0[1] += un.two;
-                auto scores = [&](uint32_t u) {
-                    const uint32_t j = un.two ? u >> 1 : u, sub = un.two ? u & 1u : 0u, t = t0 + j;
-                    if (!(ok = ok && wait_all(&bars.kfull[t & 1u], t >> 1, bars, a.c.status)))
-                        return;
-                    fence_after();
-                    const uint32_t qa = smem_addr(smem + sub * S::qbytes), ka = smem_addr(kt + (t & 1u) * S::tile);
-#pragma unroll
-                    for (uint32_t k = 0; k < D / 16; ++k)
-                        umma_ss(tmem + (u & 1u) * S::keys, operand_desc(qa + (k >> 2) * S::qpanel) + (k & 3u) * 2u,
-                                operand_desc(ka + (k >> 2) * S::panel) + (k & 3u) * 2u, sdesc, k > 0, one);
-                    umma_commit(&bars.sfull[u & 1u], one);
-                    if (!un.two || sub == 1u)
-                        umma_commit(&bars.kempty[t & 1u], one);
-                };
-                scores(0);
-                if (units > 1u)
-                    scores(1);
-                for (uint32_t u = 0; u < units && ok; ++u) {
-                    const uint32_t j = un.two ? u >> 1 : u, sub = un.two ? u & 1u : 0u, t = t0 + j;
-                    ok = wait_all(&bars.vfull[t & 1u], t >> 1, bars, a.c.status) &&
-                         wait_all(&bars.pfull[u & 1u], buf0[u & 1u] + (u >> 1), bars, a.c.status);
-                    if (!ok)
-                        break;
-                    fence_after();
-                    const uint32_t va = smem_addr(vt + (t & 1u) * S::tile);
-#pragma unroll
-                    for (uint32_t k = 0; k < S::keys / 16; ++k)
-                        umma_ts(tmem + kOut + sub * D, tmem + kP + (u & 1u) * kPStride + k * 8u,
-                                columns_desc(va + k * 2048u, S::panel), odesc, j > 0 || k > 0, one);
-                    umma_commit(&bars.pv[sub], one);
-                    if (!un.two || sub == 1u)
-                        umma_commit(&bars.vempty[t & 1u], one);
-                    if (u + 2u < units)
-                        scores(u + 2u);
-                }
-                t0 += un.steps;
-                buf0[0] += un.uses(0);
-                buf0[1] += un.uses(1);
-            }
-            umma_commit(&bars.drain, one);           // every product is done
-            for (uint32_t i = 0; i < kSpin && !mbar_try_wait(&bars.drain, 0); ++i)
-                ;
-        }
-    } else if (warp >= 8) {                          // decoding
+    if (warp >= kCodeWarp) {                         // decoding
         regs_down<kCodeRegs>();
-        const uint32_t dw = warp - 8u;
-        Raw<FMT, D> rk, rv;
+        const bool values = warp >= kCodeWarp + 4u;
+        const uint32_t dw = warp & 3u;
+        const uint8_t *codes = values ? a.c.v_codes : a.c.k_codes, *scales = values ? a.c.v_scales : a.c.k_scales;
+        uint64_t *full = values ? bars.vfull : bars.kfull, *empty = values ? bars.vempty : bars.kempty;
+        char *tiles = values ? vt : kt;
+        Raw<FMT, D> raw;
         bool more = w.begin(a, range);
         uint32_t step = w.k0;
+        const uint32_t row0 = lane / S::pieces, piece0 = lane % S::pieces;      // of the lane's first load
+        constexpr uint32_t rows_a_load = 32 / S::pieces;
         // Pages of this warp's keys of the step to load; c.pages: none.
         uint32_t page[2] = {0, 0};
         auto pages = [&]() {
             const uint32_t key = (step << S::log) + dw * S::mine;
-#pragma unroll
-            for (uint32_t i = 0; i < (S::mine + 15) / 16; ++i)
-                page[i] = key + 16u * i < w.keys && (i == 0 || a.c.page_log == 4u) ? find_page(a.c, w.b, key + 16u * i)
-                                                                                  : a.c.pages;
-            if (S::mine > 16 && a.c.page_log > 4u)
-                page[1] = page[0];
+            page[0] = key < w.keys ? find_page(a.c, w.b, key) : a.c.pages;
+            page[1] = page[0];
+            if (S::mine > 16 && a.c.page_log == 4u)
+                page[1] = key + 16u < w.keys ? find_page(a.c, w.b, key + 16u) : a.c.pages;
         };
-        auto load = [&](Raw<FMT, D> &r, const uint8_t *codes, const uint8_t *scales) {
+        auto load = [&]() {
             const uint32_t key = (step << S::log) + dw * S::mine, mask = (1u << a.c.page_log) - 1u;
+            if (key + S::mine <= w.keys && page[0] < a.c.pages && (S::mine <= 16 || a.c.page_log > 4u)) {
+                // all of them, one behind the other
+                const uint64_t at = (((uint64_t)page[0] * a.c.heads + w.head) << a.c.page_log) + (key & mask) + row0;
+                const uint8_t *c = codes + at * S::row + piece0 * 16u, *sc = scales + at * S::blocks;
+#pragma unroll
+                for (uint32_t i = 0; i < S::loads; ++i)
+                    raw.c[i] = __ldg(reinterpret_cast<const uint4 *>(c + i * 512u));
+#pragma unroll
+                for (uint32_t i = 0; i < S::loads; ++i)
+                    raw.s[i] = S::fp4 ? __ldg(reinterpret_cast<const uint16_t *>(sc + i * rows_a_load * S::blocks) + piece0)
+                                      : __ldg(sc + i * rows_a_load * S::blocks + (piece0 >> 1));
+                return;
+            }
 #pragma unroll
             for (uint32_t i = 0; i < S::loads; ++i) {
-                const uint32_t p = i * 32u + lane, row = p / S::pieces, piece = p % S::pieces;
-                const uint32_t pg = page[S::mine > 16 ? row >> 4 : 0];
+                const uint32_t row = row0 + i * rows_a_load, pg = page[S::mine > 16 ? row >> 4 : 0];
                 const bool in = key + row < w.keys && pg < a.c.pages;
                 const uint64_t at = in ? (((uint64_t)pg * a.c.heads + w.head) << a.c.page_log) + ((key + row) & mask) : 0ull;
-                r.c[i] = in ? __ldg(reinterpret_cast<const uint4 *>(codes + at * S::row) + piece) : make_uint4(0u, 0u, 0u, 0u);
-                if (S::fp4)
-                    r.s[i] = in ? __ldg(reinterpret_cast<const uint16_t *>(scales + at * S::blocks) + piece) : 0u;
-                else
-                    r.s[i] = in ? __ldg(scales + at * S::blocks + (piece >> 1)) : 0u;
+                raw.c[i] = in ? __ldg(reinterpret_cast<const uint4 *>(codes + at * S::row) + piece0) : make_uint4(0u, 0u, 0u, 0u);
+                raw.s[i] = !in      ? 0u
+                           : S::fp4 ? __ldg(reinterpret_cast<const uint16_t *>(scales + at * S::blocks) + piece0)
+                                    : __ldg(scales + at * S::blocks + (piece0 >> 1));
             }
         };
         // One tensor's part of a step into its f16 tile.  top: see attention_rows.cu.
-        auto store = [&](const Raw<FMT, D> &r, uint32_t top, char *tile) {
+        auto store = [&](uint32_t top, char *tile) {
 #pragma unroll
             for (uint32_t i = 0; i < S::loads; ++i) {
-                const uint32_t p = i * 32u + lane, row = dw * S::mine + p / S::pieces, piece = p % S::pieces;
-                const uint32_t cw[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
+                const uint32_t row = dw * S::mine + row0 + i * rows_a_load, piece = piece0;
+                const uint32_t cw[4] = {raw.c[i].x, raw.c[i].y, raw.c[i].z, raw.c[i].w};
                 if (S::fp4) {
-                    uint32_t sc0 = e4m3x2_to_f16x2(r.s[i]), sc1 = __byte_perm(sc0, 0, 0x3232);
+                    uint32_t sc0 = e4m3x2_to_f16x2(raw.s[i]), sc1 = __byte_perm(sc0, 0, 0x3232);
                     sc0 = __byte_perm(sc0, 0, 0x1010);
                     uint32_t h[4][4];
 #pragma unroll
@@ -321,7 +282,7 @@ attention_tiles_kernel(const AttArgs a)
                         *reinterpret_cast<uint4 *>(line + at * 16u) = v;
                     }
                 } else {
-                    const float f = __uint_as_float((uint32_t)max((int)(r.s[i] + 134u) - (int)top, 0) << 23);
+                    const float f = __uint_as_float((uint32_t)max((int)(raw.s[i] + 134u) - (int)top, 0) << 23);
                     const uint32_t sc = half2_bits(f, f);
                     uint32_t h[8];
 #pragma unroll
@@ -339,24 +300,24 @@ attention_tiles_kernel(const AttArgs a)
                 }
             }
         };
-        auto largest = [&](const Raw<FMT, D> &r) {
-            uint32_t top = 27u;     // 2^-100 at least: values below count as zeros
-#pragma unroll
-            for (uint32_t i = 0; i < S::loads; ++i)
-                top = max(top, r.s[i]);
-            return __reduce_max_sync(0xFFFFFFFFu, top);
-        };
         if (more) {
             pages();
-            load(rk, a.c.k_codes, a.c.k_scales);
-            load(rv, a.c.v_codes, a.c.v_scales);
+            load();
         }
-        bool ok = true;
         for (uint32_t t = 0; more; ++t) {
-            uint32_t ktop = 0, vtop = 0;
+            uint32_t top = 27u;     // 2^-100 at least: values below count as zeros
             if (!S::fp4) {
-                ktop = largest(rk);
-                vtop = largest(rv);
+#pragma unroll
+                for (uint32_t i = 0; i < S::loads; ++i)
+                    top = max(top, raw.s[i]);
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+            }
+            // The powers: a slot was read four steps ago, which a product with the values of
+            // the step after that says (waited for below), and scores two steps on.
+            if (!S::fp4 && values && lane == 0) {
+                bars.vexp[t & 3u][dw] = (float)((int)top - 134);
+                bars.vinv[t & 3u][dw] = __uint_as_float((uint32_t)(261 - (int)top) << 23);
+                mbar_arrive(&bars.ffull[t & 3u]);
             }
             // the step after this one
             if (++step == w.k1) {
@@ -366,36 +327,29 @@ attention_tiles_kernel(const AttArgs a)
             if (more)
                 pages();
             // a fresh barrier passes the wait for its odd phase
-            if (!(ok = wait_all(&bars.kempty[t & 1u], (t >> 1) + 1u, bars, a.c.status)))
+            if (!wait_all(&empty[t & 1u], (t >> 1) + 1u, bars, a.c.status))
                 break;
-            if (lane == 0) {
-                bars.kfac[t & 3u][dw] = S::fp4 ? 1.0f : __uint_as_float(ktop << 23) * 0x1p-7f;
-                bars.vexp[t & 3u][dw] = S::fp4 ? 0.0f : (float)((int)vtop - 134);
-                bars.vinv[t & 3u][dw] = S::fp4 ? 1.0f : __uint_as_float((uint32_t)(261 - (int)vtop) << 23);
+            if (!S::fp4 && !values && lane == 0) {
+                bars.kfac[t & 3u][dw] = __uint_as_float(top << 23) * 0x1p-7f;
                 mbar_arrive(&bars.ffull[t & 3u]);
             }
-            store(rk, ktop, kt + (t & 1u) * S::tile);
+            store(top, tiles + (t & 1u) * S::tile);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&bars.kfull[t & 1u]);
+                mbar_arrive(&full[t & 1u]);
             if (more)
-                load(rk, a.c.k_codes, a.c.k_scales);
-            if (!(ok = wait_all(&bars.vempty[t & 1u], (t >> 1) + 1u, bars, a.c.status)))
-                break;
-            store(rv, vtop, vt + (t & 1u) * S::tile);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.vfull[t & 1u]);
-            if (more)
-                load(rv, a.c.v_codes, a.c.v_scales);
+                load();
         }
     } else {                                         // softmax: a row a thread
         regs_up<kSoftRegs>();
         const uint32_t wg = warp >> 2, r = (warp & 3u) * 32u + lane, lanes = ((warp & 3u) * 32u) << 16;
         char *qs = smem + wg * S::qbytes;
-        uint32_t t0 = 0, buf0[2] = {0, 0}, pv0 = 0, met = 0;
+        const bool issuer = (warp & 3u) == 0u;
+        const uint32_t one = elect_one();
+        constexpr uint32_t sdesc = (1u << 4) | ((S::keys / 8u) << 17) | (8u << 24);
+        constexpr uint32_t odesc = (1u << 4) | (1u << 16) | ((D / 8u) << 17) | (8u << 24);
+        uint32_t t0 = 0, buf0[2] = {0, 0}, pv0 = 0, met = 0, pieces = 0;
         bool ok = wg < S::subs;
         // Both groups, before and after a piece that one of them has to itself: a wait for
         // a barrier's phase is one only for those who have seen the phase before it.
@@ -406,6 +360,39 @@ attention_tiles_kernel(const AttArgs a)
                     mbar_arrive(&bars.meet);
                 ok = wait_all(&bars.meet, met++, bars, a.c.status);
             }
+        };
+        // The issuing warp: scores of step j of the piece; then weights times values.
+        // A group alone makes up for the other's arrivals.
+        auto scores = [&](uint32_t j, uint32_t buf, bool two) {
+            const uint32_t t = t0 + j;
+            if (!(ok = ok && wait_all(&bars.kfull[t & 1u], t >> 1, bars, a.c.status)))
+                return;
+            fence_after();
+            const uint64_t qd = operand_desc(smem_addr(qs)), kd = operand_desc(smem_addr(kt + (t & 1u) * S::tile));
+#pragma unroll
+            for (uint32_t k = 0; k < D / 16; ++k)
+                umma_ss(tmem + buf * S::keys, qd + (k >> 2) * (S::qpanel >> 4) + (k & 3u) * 2u,
+                        kd + (k >> 2) * (S::panel >> 4) + (k & 3u) * 2u, sdesc, k > 0, one);
+            umma_commit(&bars.sfull[buf], one);
+            umma_commit(&bars.kempty[t & 1u], one);
+            if (!two)
+                umma_commit(&bars.kempty[t & 1u], one);
+        };
+        auto products = [&](uint32_t j, uint32_t buf, uint32_t phase, bool two) {
+            const uint32_t t = t0 + j;
+            ok = ok && wait_all(&bars.vfull[t & 1u], t >> 1, bars, a.c.status) &&
+                 wait_all(&bars.pfull[buf], phase, bars, a.c.status);
+            if (!ok)
+                return;
+            fence_after();
+            const uint64_t vd = columns_desc(smem_addr(vt + (t & 1u) * S::tile), S::panel);
+#pragma unroll
+            for (uint32_t k = 0; k < S::keys / 16; ++k)
+                umma_ts(tmem + kOut + wg * D, tmem + kP + buf * kPStride + k * 8u, vd + k * 128u, odesc, j > 0 || k > 0, one);
+            umma_commit(&bars.pv[wg], one);
+            umma_commit(&bars.vempty[t & 1u], one);
+            if (!two)
+                umma_commit(&bars.vempty[t & 1u], one);
         };
         for (bool more = w.begin(a, range); more && ok; more = w.next()) {
             const Units<S> un(w);
@@ -442,6 +429,13 @@ attention_tiles_kernel(const AttArgs a)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.qfull[wg]);
+                if (issuer) {
+                    ok = wait_all(&bars.qfull[wg], pieces, bars, a.c.status);
+                    scores(0, un.two ? wg : 0u, un.two);
+                    if (!un.two && un.steps > 1u)
+                        scores(1, 1, false);
+                }
+                ++pieces;
 
                 // rows past the sequence's see every key, and are not stored
                 const int64_t pos = in ? w.s.len - w.s.n + i : 0x7FFFFFFFll;
@@ -450,7 +444,7 @@ attention_tiles_kernel(const AttArgs a)
                 for (uint32_t j = 0; j < un.steps; ++j) {
                     const uint32_t buf = un.two ? wg : j & 1u, t = t0 + j;
                     const uint32_t at = tmem + buf * S::keys + lanes, to_p = tmem + kP + buf * kPStride + lanes;
-                    ok = wait_all(&bars.ffull[t & 3u], t >> 2, bars, a.c.status) &&
+                    ok = ok && (S::fp4 || wait_all(&bars.ffull[t & 3u], t >> 2, bars, a.c.status)) &&
                          wait_all(&bars.sfull[buf], buf0[buf] + (un.two ? j : j >> 1), bars, a.c.status);
                     if (!ok)
                         break;
@@ -467,8 +461,8 @@ attention_tiles_kernel(const AttArgs a)
                     float fac[4], e[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        fac[c] = fq * bars.kfac[t & 3u][c];
-                        e[c] = bars.vexp[t & 3u][c];
+                        fac[c] = S::fp4 ? fq : fq * bars.kfac[t & 3u][c];
+                        e[c] = S::fp4 ? 0.0f : bars.vexp[t & 3u][c];
                     }
                     const uint32_t key = (w.k0 + j) << S::log;
                     const int lim = (int)max(min(pos, (int64_t)w.keys - 1) - (int64_t)key, (int64_t)-1);
@@ -523,7 +517,7 @@ attention_tiles_kernel(const AttArgs a)
                             part = __fadd2_rn(part, s);
                             p[x] = half2_bits(s.x, s.y);
                         }
-                        sum = fmaf(part.x + part.y, bars.vinv[t & 3u][g], sum);
+                        sum = S::fp4 ? sum + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t & 3u][g], sum);
                         if constexpr (S::mine == 32)
                             tmem_st16(to_p + g * 16, p);
                         else
@@ -555,6 +549,15 @@ attention_tiles_kernel(const AttArgs a)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bars.pfull[buf]);
+                    if (issuer) {
+                        products(j, buf, buf0[buf] + (un.two ? j : j >> 1), un.two);
+                        if (un.two && j + 1u < un.steps)
+                            scores(j + 1u, buf, true);
+                        if (!un.two && j + 2u < un.steps)
+                            scores(j + 2u, buf, false);
+                        if (!ok)
+                            break;
+                    }
                 }
                 if (!ok)
                     break;
@@ -615,11 +618,16 @@ attention_tiles_kernel(const AttArgs a)
             if (!un.two)
                 meet();
         }
+        if (issuer) {
+            umma_commit(&bars.drain[wg], one);       // every product of this warp is done
+            for (uint32_t i = 0; i < kSpin && !mbar_try_wait(&bars.drain[wg], 0); ++i)
+                ;
+        }
     }
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 0) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
     }
