@@ -29,19 +29,22 @@
 #include "mxq_mma.cuh"
 #include "mxq_tcgen05.cuh"
 #include <algorithm>
+#include <type_traits>
 
 namespace mxq {
 
 namespace {
 
 constexpr uint32_t kSpin = 1u << 18;        // tests of a barrier before a wait gives up
-// Warps 0-3 and 4-7: softmax groups, whose first warps issue; 8-11 decode keys,
-// 12-15 values.
+// Warps 0-3 and 4-7: softmax groups; 8-10 decode keys, 12-14 values; 11 and 15 issue
+// the groups' products.  (A warp is held while its products queue and at every wait
+// that it makes between them; with one for both groups the tensor cores were idle for
+// more than half of the time.)
 constexpr uint32_t kCodeWarp = 8;
 constexpr int kThreads = 512;
 // Registers of a thread: 128 at launch, of which the decoding warps give up what the
 // softmax ones take.
-constexpr int kLaunchRegs = 128, kSoftRegs = 192, kCodeRegs = 64;
+constexpr int kLaunchRegs = 128, kSoftRegs = 160, kCodeRegs = 96;
 static_assert(kLaunchRegs * kThreads <= 65536 && kSoftRegs + kCodeRegs <= 2 * kLaunchRegs, "register shares");
 
 template <int FMT, int D>
@@ -49,21 +52,25 @@ struct Shape {
     static constexpr bool fp4 = FMT == MXQ_FMT_NVFP4;
     static constexpr uint32_t row = fp4 ? D / 2 : D;            // bytes of a token's codes
     static constexpr uint32_t blocks = fp4 ? D / 16 : D / 32;   // and of its scales
-    static constexpr uint32_t log = D == 256 ? 6 : 7, keys = 1u << log;
-    static constexpr uint32_t mine = keys / 4;                  // keys of a decoding warp
+    static constexpr uint32_t log = 6, keys = 1u << log;        // of a step
+    static constexpr uint32_t mine = D == 256 ? 16 : 32;        // keys of a chunk, one turn of a decoding warp
+    static constexpr uint32_t chunks = keys / mine;
     static constexpr uint32_t subs = D == 256 ? 1 : 2, rows = 128 * subs;
     static constexpr uint32_t panel = keys * 128;               // 64 values of a step's tokens
     static constexpr uint32_t qpanel = 128 * 128;
     static constexpr uint32_t qbytes = 128 * D * 2, tile = keys * D * 2;
-    static constexpr uint32_t smem = subs * qbytes + 4 * tile + 1024;
+    static constexpr uint32_t stages = D == 256 ? 2 : 4;        // of keys, and of values
+    static constexpr uint32_t smem = subs * qbytes + 2 * stages * tile + 1024;
     static constexpr uint32_t pieces = row / 16;                // of a token's codes
     static constexpr uint32_t loads = mine * pieces / 32;       // pieces of a lane
 };
 
+constexpr uint32_t kBufs = 4;               // of scores, in TMEM
+constexpr uint32_t kRing = 16;              // steps whose powers are kept; decoding is fewer ahead
 struct Bars {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], pv[2], qfull[2], ffull[4], meet, drain[2];
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], qfull[2], ffull[kRing], meet, drain[2];
     uint32_t tmem, abort;
-    float kfac[4][4], vexp[4][4], vinv[4][4];   // by step % 4 and decoding warp: powers of keys, values
+    float kfac[kRing][4], vexp[kRing][4], vinv[kRing][4];       // by step and chunk: powers of keys, values
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
@@ -133,12 +140,15 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 template <typename S>
 struct Units {
     bool two;
-    uint32_t steps;
+    uint32_t steps, all;
     template <typename W>
     __device__ __forceinline__ Units(const W &w)
-        : two(S::subs == 2 && min(w.s.rows - w.rt * S::rows, S::rows) > 128u), steps(w.k1 - w.k0) {}
-    // Uses of TMEM buffer i.
-    __device__ __forceinline__ uint32_t uses(uint32_t i) const { return two ? steps : (steps + 1u - i) >> 1; }
+        : two(S::subs == 2 && min(w.s.rows - w.rt * S::rows, S::rows) > 128u), steps(w.k1 - w.k0),
+          all(two ? 2u * steps : steps) {}
+    // TMEM buffer of group g's step j, the number of that use, and the uses of buffer i in all.
+    __device__ __forceinline__ uint32_t buffer(uint32_t g, uint32_t j) const { return (two ? 2u * j + g : j) % kBufs; }
+    __device__ __forceinline__ uint32_t use(uint32_t j) const { return two ? j >> 1 : j >> 2; }
+    __device__ __forceinline__ uint32_t uses(uint32_t i) const { return (all + kBufs - 1u - i) / kBufs; }
     // Products with the values of group i.
     __device__ __forceinline__ uint32_t products(uint32_t i) const { return two || i == 0 ? steps : 0u; }
 };
@@ -146,8 +156,10 @@ struct Units {
 // A decoding warp's part of a step: pieces of codes and their scales, in registers.
 template <int FMT, int D>
 struct Raw {
-    uint4 c[Shape<FMT, D>::loads];
-    uint32_t s[Shape<FMT, D>::loads];       // MXFP8: a byte; NVFP4: two
+    using S = Shape<FMT, D>;
+    uint4 c[S::loads];
+    // NVFP4: the two scales of each piece.  MXFP8: the scales of key lane % mine.
+    uint32_t s[S::fp4 ? S::loads : (S::blocks + 3) / 4];
 };
 
 } // namespace
@@ -161,23 +173,26 @@ attention_tiles_kernel(const AttArgs a)
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ Bars bars;
     __shared__ Range range;
+    __shared__ W saved[8];      // a softmax warp's walk, while it is in a piece
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    char *kt = smem + S::subs * S::qbytes, *vt = kt + 2 * S::tile;
+    char *kt = smem + S::subs * S::qbytes, *vt = kt + S::stages * S::tile;
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.kfull[i], 4);
-            mbar_init(&bars.kempty[i], 2);
-            mbar_init(&bars.vfull[i], 4);
-            mbar_init(&bars.vempty[i], 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.kfull[i], S::chunks);
+            mbar_init(&bars.kempty[i], S::subs);
+            mbar_init(&bars.vfull[i], S::chunks);
+            mbar_init(&bars.vempty[i], S::subs);
             mbar_init(&bars.sfull[i], 1);
             mbar_init(&bars.pfull[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.pv[i], 1);
             mbar_init(&bars.qfull[i], 4);
             mbar_init(&bars.drain[i], 1);
         }
-        for (int i = 0; i < 4; ++i)
-            mbar_init(&bars.ffull[i], 8);
+        for (uint32_t i = 0; i < kRing; ++i)
+            mbar_init(&bars.ffull[i], 2 * S::chunks);
         mbar_init(&bars.meet, 8);
         bars.abort = 0;
         fence_mbar_init();
@@ -196,33 +211,121 @@ attention_tiles_kernel(const AttArgs a)
     const uint32_t tmem = bars.tmem;
     if (threadIdx.x == 0)
         a.left[blockIdx.x].parts = 0u;
-    // TMEM columns: scores in two buffers, outputs, weights.  With heads of 128 values
-    // there is no room for the weights but over the scores that they come from.
-    constexpr uint32_t kOut = 2 * S::keys;
-    constexpr uint32_t kP = D == 128 ? 0 : kOut + S::subs * D, kPStride = D == 128 ? S::keys : S::keys / 2;
-    static_assert(D == 128 || kP + S::keys <= 512, "TMEM");
+    // TMEM columns: scores in four buffers, whose first halves take the weights, and outputs.
+    constexpr uint32_t kOut = kBufs * S::keys;
+    static_assert(kOut + S::subs * D <= 512, "TMEM");
 
     W w;
-    if (warp >= kCodeWarp) {                         // decoding
+    if (warp >= kCodeWarp)
         regs_down<kCodeRegs>();
+    if (warp >= kCodeWarp && (warp & 3u) == 3u) {    // issue
+        const uint32_t one = elect_one(), wg = (warp - kCodeWarp) >> 2;
+        uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, q0 = 0, pv0 = 0;
+        bool ok = wg < S::subs;
+        constexpr uint32_t sdesc = (1u << 4) | ((S::keys / 8u) << 17) | (8u << 24);
+        constexpr uint32_t odesc = (1u << 4) | (1u << 16) | ((D / 8u) << 17) | (8u << 24);
+        const uint64_t qd = operand_desc(smem_addr(smem + wg * S::qbytes)), kd = operand_desc(smem_addr(kt));
+        const uint64_t vd = columns_desc(smem_addr(vt), S::panel);
+        const uint32_t out = tmem + kOut + wg * D;
+        for (bool more = w.begin(a, range); more && ok; more = w.next()) {
+            const Units<S> un(w);
+            if (wg == 0u || un.two) {
+                const uint32_t buffers = un.two ? kBufs / 2u : kBufs;       // of this group
+                ok = wait_all(&bars.qfull[wg], q0++, bars, a.c.status);
+                // Scores of step j; a group alone makes up for the other's arrivals.
+                auto scores = [&](uint32_t j) {
+                    const uint32_t t = t0 + j, stage = t % S::stages, buf = un.buffer(wg, j);
+                    if (!(ok = ok && wait_all(&bars.kfull[stage], t / S::stages, bars, a.c.status)))
+                        return;
+                    fence_after();
+                    const uint64_t k1 = kd + stage * (S::tile >> 4);
+#pragma unroll
+                    for (uint32_t k = 0; k < D / 16; ++k)
+                        umma_ss(tmem + buf * S::keys, qd + (k >> 2) * (S::qpanel >> 4) + (k & 3u) * 2u,
+                                k1 + (k >> 2) * (S::panel >> 4) + (k & 3u) * 2u, sdesc, k > 0, one);
+                    umma_commit(&bars.sfull[buf], one);
+                    umma_commit(&bars.kempty[stage], one);
+                    if (S::subs == 2 && !un.two)
+                        umma_commit(&bars.kempty[stage], one);
+                };
+                for (uint32_t j = 0; j < min(un.steps, buffers); ++j)
+                    scores(j);
+                for (uint32_t j = 0; j < un.steps && ok; ++j) {
+                    const uint32_t t = t0 + j, stage = t % S::stages, buf = un.buffer(wg, j);
+                    ok = wait_all(&bars.vfull[stage], t / S::stages, bars, a.c.status) &&
+                         wait_all(&bars.pfull[buf], buf0[buf] + un.use(j), bars, a.c.status);
+                    if (!ok)
+                        break;
+                    fence_after();
+                    const uint64_t v1 = vd + stage * (S::tile >> 4);
+#pragma unroll
+                    for (uint32_t k = 0; k < S::keys / 16; ++k)
+                        umma_ts(out, tmem + buf * S::keys + k * 8u, v1 + k * 128u, odesc, j > 0 || k > 0, one);
+                    umma_commit(&bars.pv[wg], one);
+                    umma_commit(&bars.vempty[stage], one);
+                    if (S::subs == 2 && !un.two)
+                        umma_commit(&bars.vempty[stage], one);
+                    // The weights have been read, and the next scores may take their place.
+                    ok = wait_all(&bars.pv[wg], pv0 + j, bars, a.c.status);
+                    if (j + buffers < un.steps)
+                        scores(j + buffers);
+                }
+            }
+            t0 += un.steps;
+#pragma unroll
+            for (uint32_t i = 0; i < kBufs; ++i)
+                buf0[i] += un.uses(i);
+            pv0 += un.products(wg);
+        }
+        umma_commit(&bars.drain[wg], one);           // every product of this warp is done
+        for (uint32_t i = 0; i < kSpin && !mbar_try_wait(&bars.drain[wg], 0); ++i)
+            ;
+    } else if (warp >= kCodeWarp) {                  // decoding
+        // Three warps take the chunks of keys in turn, three those of values.
         const bool values = warp >= kCodeWarp + 4u;
-        const uint32_t dw = warp & 3u;
+        constexpr uint32_t stride = 3;
+        uint32_t dw = warp & 3u;
         const uint8_t *codes = values ? a.c.v_codes : a.c.k_codes, *scales = values ? a.c.v_scales : a.c.k_scales;
         uint64_t *full = values ? bars.vfull : bars.kfull, *empty = values ? bars.vempty : bars.kempty;
         char *tiles = values ? vt : kt;
         Raw<FMT, D> raw;
         bool more = w.begin(a, range);
-        uint32_t step = w.k0;
-        const uint32_t row0 = lane / S::pieces, piece0 = lane % S::pieces;      // of the lane's first load
+        uint32_t step = w.k0, t = 0;
+        auto settle = [&]() {       // the chunk is number dw from step `step` on: its own step
+            while (dw >= S::chunks && more) {
+                dw -= S::chunks;
+                ++t;
+                if (++step == w.k1) {
+                    more = w.next();
+                    step = w.k0;
+                }
+            }
+        };
+        if (more)
+            settle();
+        // The lane's piece and row of a load, so that the 8 lanes of a store to shared memory
+        // have pieces of one panel: 4 of 2 rows (E2M1, whose pieces are twice as long in f16,
+        // 2 of 4), which the swizzle spreads over all banks.
+        constexpr uint32_t low = S::fp4 ? 1u : 2u, mid = 3u - low;       // bits of the piece, of the row
+        constexpr uint32_t bits = S::pieces == 2 ? 1u : S::pieces == 4 ? 2u : S::pieces == 8 ? 3u : 4u;
+        const uint32_t piece0 = (lane & ((1u << low) - 1u)) | (((lane >> 3) & ((1u << (bits - low)) - 1u)) << low);
+        const uint32_t row0 = ((lane >> low) & ((1u << mid) - 1u)) | ((lane >> (3u + bits - low)) << mid);
         constexpr uint32_t rows_a_load = 32 / S::pieces;
-        // Pages of this warp's keys of the step to load; c.pages: none.
+        // Pages of this warp's keys of the step to load, as the table has them.
         uint32_t page[2] = {0, 0};
         auto pages = [&]() {
             const uint32_t key = (step << S::log) + dw * S::mine;
-            page[0] = key < w.keys ? find_page(a.c, w.b, key) : a.c.pages;
-            page[1] = page[0];
-            if (S::mine > 16 && a.c.page_log == 4u)
-                page[1] = key + 16u < w.keys ? find_page(a.c, w.b, key + 16u) : a.c.pages;
+            page[0] = key < w.keys ? table_entry(a.c, w.b, key) : a.c.pages;
+            page[1] = S::mine > 16 && a.c.page_log == 4u && key + 16u < w.keys ? table_entry(a.c, w.b, key + 16u) : a.c.pages;
+        };
+        // MXFP8: a key's scales.
+        auto key_scales = [&](const uint8_t *p, bool in) {
+            if (S::blocks == 2)
+                raw.s[0] = in ? __ldg(reinterpret_cast<const uint16_t *>(p)) : 0u;
+            else
+#pragma unroll
+                for (uint32_t i = 0; i < sizeof(raw.s) / 4; ++i)
+                    raw.s[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
         };
         auto load = [&]() {
             const uint32_t key = (step << S::log) + dw * S::mine, mask = (1u << a.c.page_log) - 1u;
@@ -233,70 +336,72 @@ attention_tiles_kernel(const AttArgs a)
 #pragma unroll
                 for (uint32_t i = 0; i < S::loads; ++i)
                     raw.c[i] = __ldg(reinterpret_cast<const uint4 *>(c + i * 512u));
+                if constexpr (S::fp4) {
 #pragma unroll
-                for (uint32_t i = 0; i < S::loads; ++i)
-                    raw.s[i] = S::fp4 ? __ldg(reinterpret_cast<const uint16_t *>(sc + i * rows_a_load * S::blocks) + piece0)
-                                      : __ldg(sc + i * rows_a_load * S::blocks + (piece0 >> 1));
+                    for (uint32_t i = 0; i < S::loads; ++i)
+                        raw.s[i] = __ldg(reinterpret_cast<const uint16_t *>(sc + i * rows_a_load * S::blocks) + piece0);
+                } else
+                    key_scales(scales + (at - row0 + lane % S::mine) * S::blocks, true);
                 return;
             }
+            const bool short_pages = S::mine > 16 && a.c.page_log == 4u;
+            if ((key < w.keys && page[0] >= a.c.pages) || (short_pages && key + 16u < w.keys && page[1] >= a.c.pages))
+                atomicOr(a.c.status, MXQ_DEV_INVALID_PAGE);
 #pragma unroll
             for (uint32_t i = 0; i < S::loads; ++i) {
-                const uint32_t row = row0 + i * rows_a_load, pg = page[S::mine > 16 ? row >> 4 : 0];
+                const uint32_t row = row0 + i * rows_a_load, pg = short_pages && row >= 16u ? page[1] : page[0];
                 const bool in = key + row < w.keys && pg < a.c.pages;
                 const uint64_t at = in ? (((uint64_t)pg * a.c.heads + w.head) << a.c.page_log) + ((key + row) & mask) : 0ull;
                 raw.c[i] = in ? __ldg(reinterpret_cast<const uint4 *>(codes + at * S::row) + piece0) : make_uint4(0u, 0u, 0u, 0u);
-                raw.s[i] = !in      ? 0u
-                           : S::fp4 ? __ldg(reinterpret_cast<const uint16_t *>(scales + at * S::blocks) + piece0)
-                                    : __ldg(scales + at * S::blocks + (piece0 >> 1));
+                if constexpr (S::fp4)
+                    raw.s[i] = in ? __ldg(reinterpret_cast<const uint16_t *>(scales + at * S::blocks) + piece0) : 0u;
+            }
+            if constexpr (!S::fp4) {
+                const uint32_t row = lane % S::mine, pg = short_pages && row >= 16u ? page[1] : page[0];
+                const bool in = key + row < w.keys && pg < a.c.pages;
+                const uint64_t at = in ? (((uint64_t)pg * a.c.heads + w.head) << a.c.page_log) + ((key + row) & mask) : 0ull;
+                key_scales(scales + at * S::blocks, in);
             }
         };
-        // One tensor's part of a step into its f16 tile.  top: see attention_rows.cu.
-        auto store = [&](uint32_t top, char *tile) {
+        // The chunk into its f16 tile.  top: see attention_rows.cu.
+        auto store = [&](uint32_t top, uint32_t chunk, char *tile) {
+            char *line0 = tile + (piece0 >> low) * S::panel + (chunk * S::mine + row0) * 128u;
 #pragma unroll
             for (uint32_t i = 0; i < S::loads; ++i) {
-                const uint32_t row = dw * S::mine + row0 + i * rows_a_load, piece = piece0;
                 const uint32_t cw[4] = {raw.c[i].x, raw.c[i].y, raw.c[i].z, raw.c[i].w};
+                const uint32_t turn = (row0 + i * rows_a_load) & 7u, at = (piece0 & ((1u << low) - 1u)) * (8u >> low);
+                char *line = line0 + i * rows_a_load * 128u;
                 if (S::fp4) {
-                    uint32_t sc0 = e4m3x2_to_f16x2(raw.s[i]), sc1 = __byte_perm(sc0, 0, 0x3232);
-                    sc0 = __byte_perm(sc0, 0, 0x1010);
-                    uint32_t h[4][4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        e2m1x8_unpack(cw[j], h[j]);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            h[j][u] = hmul2_bits(h[j][u], j < 2 ? sc0 : sc1);
-                    }
-                    char *line = tile + (piece >> 1) * S::panel + row * 128u;
-                    // 4 pieces of 16 bytes; lanes whose pieces would meet on a bank take them in another order
-                    const uint32_t turn = D == 64 ? 0u : piece & 2u;
+                    const uint32_t sc = e4m3x2_to_f16x2(raw.s[i]);
+                    const uint32_t sc0 = __byte_perm(sc, 0, 0x1010), sc1 = __byte_perm(sc, 0, 0x3232);
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j) {
-                        const uint32_t at = ((piece & 1u) * 4u + (j ^ turn)) ^ (row & 7u);
-                        uint4 v = make_uint4(h[j][0], h[j][1], h[j][2], h[j][3]);
-                        if (D != 64) {
-                            const uint32_t o = j ^ 2u;
-                            if (turn)
-                                v = make_uint4(h[o][0], h[o][1], h[o][2], h[o][3]);
-                        }
-                        *reinterpret_cast<uint4 *>(line + at * 16u) = v;
+                        uint32_t h[4];
+                        e2m1x8_unpack(cw[j], h);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            h[u] = hmul2_bits(h[u], j < 2 ? sc0 : sc1);
+                        *reinterpret_cast<uint4 *>(line + (((at + j) ^ turn) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 } else {
-                    const float f = __uint_as_float((uint32_t)max((int)(raw.s[i] + 134u) - (int)top, 0) << 23);
+                    uint32_t b = __shfl_sync(0xFFFFFFFFu, raw.s[0], row0 + i * rows_a_load);
+                    if (S::blocks == 8) {
+                        const uint32_t hi = __shfl_sync(0xFFFFFFFFu, raw.s[sizeof(raw.s) / 4 - 1], row0 + i * rows_a_load);
+                        b = piece0 & 8u ? hi : b;
+                    }
+                    b = (b >> ((piece0 & 6u) * 4u)) & 0xFFu;       // of 32 values: two pieces
+                    const float f = __uint_as_float((uint32_t)max((int)(b + 134u) - (int)top, 0) << 23);
                     const uint32_t sc = half2_bits(f, f);
-                    uint32_t h[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        e4m3x4_unpack(cw[j], h[2 * j], h[2 * j + 1]);
+                    for (uint32_t j = 0; j < 2; ++j) {
+                        uint32_t h[4];
+                        e4m3x4_unpack(cw[2 * j], h[0], h[1]);
+                        e4m3x4_unpack(cw[2 * j + 1], h[2], h[3]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        h[j] = hmul2_bits(h[j], sc);
-                    char *line = tile + (piece >> 2) * S::panel + row * 128u;
-                    const bool turn = D != 64 && (piece & 4u);
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    const uint32_t at = (piece & 3u) * 2u;
-                    *reinterpret_cast<uint4 *>(line + (((at + turn) ^ (row & 7u)) << 4)) = turn ? hi : lo;
-                    *reinterpret_cast<uint4 *>(line + (((at + !turn) ^ (row & 7u)) << 4)) = turn ? lo : hi;
+                        for (int u = 0; u < 4; ++u)
+                            h[u] = hmul2_bits(h[u], sc);
+                        *reinterpret_cast<uint4 *>(line + (((at + j) ^ turn) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
                 }
             }
         };
@@ -304,40 +409,38 @@ attention_tiles_kernel(const AttArgs a)
             pages();
             load();
         }
-        for (uint32_t t = 0; more; ++t) {
-            uint32_t top = 27u;     // 2^-100 at least: values below count as zeros
+        while (more) {
+            uint32_t top = 27u;     // 2^-100 at least: what is below counts as zeros
             if (!S::fp4) {
+                uint32_t m = raw.s[0];
 #pragma unroll
-                for (uint32_t i = 0; i < S::loads; ++i)
-                    top = max(top, raw.s[i]);
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                for (uint32_t i = 1; i < sizeof(raw.s) / 4; ++i)
+                    m = __vmaxu4(m, raw.s[i]);
+                m = __vmaxu4(m, m >> 16);
+                top = __reduce_max_sync(0xFFFFFFFFu, max(top, max(m & 0xFFu, (m >> 8) & 0xFFu)));
             }
-            // The powers: a slot was read four steps ago, which a product with the values of
-            // the step after that says (waited for below), and scores two steps on.
-            if (!S::fp4 && values && lane == 0) {
-                bars.vexp[t & 3u][dw] = (float)((int)top - 134);
-                bars.vinv[t & 3u][dw] = __uint_as_float((uint32_t)(261 - (int)top) << 23);
-                mbar_arrive(&bars.ffull[t & 3u]);
-            }
-            // the step after this one
-            if (++step == w.k1) {
-                more = w.next();
-                step = w.k0;
-            }
+            // The next chunk's place; its pages are on the way while this one is stored.
+            const uint32_t now = t, chunk = dw;
+            dw += stride;
+            settle();
             if (more)
                 pages();
             // a fresh barrier passes the wait for its odd phase
-            if (!wait_all(&empty[t & 1u], (t >> 1) + 1u, bars, a.c.status))
+            if (!wait_all(&empty[now % S::stages], now / S::stages + 1u, bars, a.c.status))
                 break;
-            if (!S::fp4 && !values && lane == 0) {
-                bars.kfac[t & 3u][dw] = __uint_as_float(top << 23) * 0x1p-7f;
-                mbar_arrive(&bars.ffull[t & 3u]);
+            if (!S::fp4 && lane == 0) {         // the slot was read long ago (kRing)
+                if (values) {
+                    bars.vexp[now % kRing][chunk] = (float)((int)top - 134);
+                    bars.vinv[now % kRing][chunk] = __uint_as_float((uint32_t)(261 - (int)top) << 23);
+                } else
+                    bars.kfac[now % kRing][chunk] = __uint_as_float(top << 23) * 0x1p-7f;
+                mbar_arrive(&bars.ffull[now % kRing]);
             }
-            store(top, tiles + (t & 1u) * S::tile);
+            store(top, chunk, tiles + now % S::stages * S::tile);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&full[t & 1u]);
+                mbar_arrive(&full[now % S::stages]);
             if (more)
                 load();
         }
@@ -345,11 +448,7 @@ attention_tiles_kernel(const AttArgs a)
         regs_up<kSoftRegs>();
         const uint32_t wg = warp >> 2, r = (warp & 3u) * 32u + lane, lanes = ((warp & 3u) * 32u) << 16;
         char *qs = smem + wg * S::qbytes;
-        const bool issuer = (warp & 3u) == 0u;
-        const uint32_t one = elect_one();
-        constexpr uint32_t sdesc = (1u << 4) | ((S::keys / 8u) << 17) | (8u << 24);
-        constexpr uint32_t odesc = (1u << 4) | (1u << 16) | ((D / 8u) << 17) | (8u << 24);
-        uint32_t t0 = 0, buf0[2] = {0, 0}, pv0 = 0, met = 0, pieces = 0;
+        uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, pv0 = 0, met = 0;
         bool ok = wg < S::subs;
         // Both groups, before and after a piece that one of them has to itself: a wait for
         // a barrier's phase is one only for those who have seen the phase before it.
@@ -360,39 +459,6 @@ attention_tiles_kernel(const AttArgs a)
                     mbar_arrive(&bars.meet);
                 ok = wait_all(&bars.meet, met++, bars, a.c.status);
             }
-        };
-        // The issuing warp: scores of step j of the piece; then weights times values.
-        // A group alone makes up for the other's arrivals.
-        auto scores = [&](uint32_t j, uint32_t buf, bool two) {
-            const uint32_t t = t0 + j;
-            if (!(ok = ok && wait_all(&bars.kfull[t & 1u], t >> 1, bars, a.c.status)))
-                return;
-            fence_after();
-            const uint64_t qd = operand_desc(smem_addr(qs)), kd = operand_desc(smem_addr(kt + (t & 1u) * S::tile));
-#pragma unroll
-            for (uint32_t k = 0; k < D / 16; ++k)
-                umma_ss(tmem + buf * S::keys, qd + (k >> 2) * (S::qpanel >> 4) + (k & 3u) * 2u,
-                        kd + (k >> 2) * (S::panel >> 4) + (k & 3u) * 2u, sdesc, k > 0, one);
-            umma_commit(&bars.sfull[buf], one);
-            umma_commit(&bars.kempty[t & 1u], one);
-            if (!two)
-                umma_commit(&bars.kempty[t & 1u], one);
-        };
-        auto products = [&](uint32_t j, uint32_t buf, uint32_t phase, bool two) {
-            const uint32_t t = t0 + j;
-            ok = ok && wait_all(&bars.vfull[t & 1u], t >> 1, bars, a.c.status) &&
-                 wait_all(&bars.pfull[buf], phase, bars, a.c.status);
-            if (!ok)
-                return;
-            fence_after();
-            const uint64_t vd = columns_desc(smem_addr(vt + (t & 1u) * S::tile), S::panel);
-#pragma unroll
-            for (uint32_t k = 0; k < S::keys / 16; ++k)
-                umma_ts(tmem + kOut + wg * D, tmem + kP + buf * kPStride + k * 8u, vd + k * 128u, odesc, j > 0 || k > 0, one);
-            umma_commit(&bars.pv[wg], one);
-            umma_commit(&bars.vempty[t & 1u], one);
-            if (!two)
-                umma_commit(&bars.vempty[t & 1u], one);
         };
         for (bool more = w.begin(a, range); more && ok; more = w.next()) {
             const Units<S> un(w);
@@ -429,101 +495,118 @@ attention_tiles_kernel(const AttArgs a)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.qfull[wg]);
-                if (issuer) {
-                    ok = wait_all(&bars.qfull[wg], pieces, bars, a.c.status);
-                    scores(0, un.two ? wg : 0u, un.two);
-                    if (!un.two && un.steps > 1u)
-                        scores(1, 1, false);
-                }
-                ++pieces;
 
-                // rows past the sequence's see every key, and are not stored
-                const int64_t pos = in ? w.s.len - w.s.n + i : 0x7FFFFFFFll;
+                // The last key of the piece that the row sees; rows past the sequence's see
+                // every one, and are not stored.
+                const int64_t base = (int64_t)w.k0 << S::log, pos = in ? w.s.len - w.s.n + i : 0x7FFFFFFFll;
+                const int last = (int)max(min(pos, (int64_t)w.keys - 1) - base, (int64_t)-1);
                 float mx = kLowest, sum = 0.0f;
-                const uint32_t out = tmem + kOut + wg * D + lanes;
-                for (uint32_t j = 0; j < un.steps; ++j) {
-                    const uint32_t buf = un.two ? wg : j & 1u, t = t0 + j;
-                    const uint32_t at = tmem + buf * S::keys + lanes, to_p = tmem + kP + buf * kPStride + lanes;
-                    ok = ok && (S::fp4 || wait_all(&bars.ffull[t & 3u], t >> 2, bars, a.c.status)) &&
-                         wait_all(&bars.sfull[buf], buf0[buf] + (un.two ? j : j >> 1), bars, a.c.status);
+                // the walk is not needed meanwhile, and its registers are
+                __syncwarp();
+                if (lane == 0)
+                    saved[warp] = w;
+                const uint32_t steps = un.steps;
+                const bool two = un.two;
+                // phases of this group's buffers: of the even ones and the odd ones of its units
+                const uint32_t p0 = two ? (wg ? buf0[1] : buf0[0]) : 0u, p1 = two ? (wg ? buf0[3] : buf0[2]) : 0u;
+                for (uint32_t j = 0; j < steps; ++j) {
+                    const uint32_t u = two ? 2u * j + wg : j, buf = u % kBufs, t = t0 + j;
+                    const uint32_t phase = two ? (j & 1u ? p1 : p0) + (j >> 1)
+                                               : (buf & 2u ? (buf & 1u ? buf0[3] : buf0[2]) : (buf & 1u ? buf0[1] : buf0[0])) + (j >> 2);
+                    const uint32_t at = tmem + buf * S::keys + lanes;
+                    ok = (S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a.c.status)) &&
+                         wait_all(&bars.sfull[buf], phase, bars, a.c.status);
                     if (!ok)
                         break;
                     fence_after();
-                    constexpr int chunks = S::keys / 32;        // of 32 columns
-                    constexpr int per = 32 / S::mine < 1 ? 1 : 32 / S::mine;    // powers of a chunk: 1, or 2 of 16 columns
-                    uint32_t v[chunks][32];
+                    constexpr int parts = S::keys / 32;         // of 32 columns
+                    constexpr int groups = S::chunks;           // of columns whose powers are the same
+                    uint32_t v[parts][32];
 #pragma unroll
-                    for (int c = 0; c < chunks; ++c)
+                    for (int c = 0; c < parts; ++c)
                         tmem_ld32(at + c * 32, v[c]);
 #pragma unroll
-                    for (int c = 0; c < chunks; ++c)
+                    for (int c = 0; c < parts; ++c)
                         tmem_ld_wait(v[c]);
-                    float fac[4], e[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        fac[c] = S::fp4 ? fq : fq * bars.kfac[t & 3u][c];
-                        e[c] = S::fp4 ? 0.0f : bars.vexp[t & 3u][c];
-                    }
-                    const uint32_t key = (w.k0 + j) << S::log;
-                    const int lim = (int)max(min(pos, (int64_t)w.keys - 1) - (int64_t)key, (int64_t)-1);
+                    const int lim = last - (int)(j << S::log);
                     const bool cut = __any_sync(0xFFFFFFFFu, lim < (int)S::keys - 1);
-                    float top = -INFINITY;
-                    if (cut) {
+                    // Of a chunk's columns: powers of the keys (with the row's own factor), of the values.
+                    auto fac = [&](int g) { return S::fp4 ? fq : fq * bars.kfac[t % kRing][g]; };
+                    auto e = [&](int g) { return S::fp4 ? 0.0f : bars.vexp[t % kRing][g]; };
+                    // Weights against the maximum so far, which stays unless a row's grows by more
+                    // than 2^8; then (and at first) the maximum is found first, and the weights
+                    // from the scores again, which are still where they were.
+                    uint32_t p[groups][S::mine / 2];
+                    float alpha = 1.0f, total = 0.0f, high = -INFINITY;
+                    auto weights_of = [&](auto masked) {
+                        total = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < chunks; ++c)
+                        for (int g = 0; g < groups; ++g) {
+                            const float fg = fac(g), bg = e(g) - mx;
+                            const float2 f2 = make_float2(fg, fg), b2 = make_float2(bg, bg);
+                            float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const int g = c * per + x * per / 32;
-                                const float s = c * 32 + x <= lim ? fmaf(__uint_as_float(v[c][x]), fac[g], e[g]) : -INFINITY;
-                                v[c][x] = __float_as_uint(s);
-                                top = fmaxf(top, s);
+                            for (int x = 0; x < (int)S::mine / 2; ++x) {
+                                const int col = g * S::mine + 2 * x;
+                                float2 s = __ffma2_rn(make_float2(__uint_as_float(v[col / 32][col % 32]),
+                                                                  __uint_as_float(v[col / 32][col % 32 + 1])), f2, b2);
+                                if (masked.value) {
+                                    s.x = col <= lim ? s.x : -INFINITY;
+                                    s.y = col + 1 <= lim ? s.y : -INFINITY;
+                                }
+                                high = fmaxf(fmaxf(high, s.x), s.y);
+                                s.x = ex2(s.x);
+                                s.y = ex2(s.y);
+                                part = __fadd2_rn(part, s);
+                                p[g][x] = half2_bits(s.x, s.y);
                             }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            fac[c] = 1.0f;
-                            e[c] = 0.0f;
+                            total = S::fp4 ? total + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t % kRing][g], total);
                         }
-                    } else {
+                    };
+                    auto weights = [&]() {
+                        if (cut)
+                            weights_of(std::true_type());
+                        else
+                            weights_of(std::false_type());
+                    };
+                    if (j > 0)
+                        weights();
+                    if (j == 0 || __any_sync(0xFFFFFFFFu, high > 8.0f)) {
+                        if (j > 0) {
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            float m0 = -INFINITY, m1 = -INFINITY;
+                            for (int c = 0; c < parts; ++c)
+                                tmem_ld32(at + c * 32, v[c]);
 #pragma unroll
-                            for (int x = 0; x < (int)S::mine; x += 2) {
+                            for (int c = 0; c < parts; ++c)
+                                tmem_ld_wait(v[c]);
+                        }
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int g = 0; g < groups; ++g) {
+                            const float fg = fac(g), eg = e(g);
+#pragma unroll
+                            for (int x = 0; x < (int)S::mine; ++x) {
                                 const int col = g * S::mine + x;
-                                m0 = fmaxf(m0, __uint_as_float(v[col / 32][col % 32]));
-                                m1 = fmaxf(m1, __uint_as_float(v[col / 32][col % 32 + 1]));
+                                const float s = fmaf(__uint_as_float(v[col / 32][col % 32]), fg, eg);
+                                top = fmaxf(top, col <= lim ? s : -INFINITY);
                             }
-                            top = fmaxf(top, fmaf(fmaxf(m0, m1), fac[g], e[g]));
                         }
-                    }
-                    float alpha = 1.0f;
-                    if (top > mx + 8.0f) {
-                        alpha = ex2(mx - top);
-                        mx = top;
-                        sum *= alpha;
-                    }
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float2 f2 = make_float2(fac[g], fac[g]), b2 = make_float2(e[g] - mx, e[g] - mx);
-                        float2 part = make_float2(0.0f, 0.0f);
-                        uint32_t p[S::mine / 2];
-#pragma unroll
-                        for (int x = 0; x < (int)S::mine / 2; ++x) {
-                            const int col = g * S::mine + 2 * x;
-                            float2 s = __ffma2_rn(make_float2(__uint_as_float(v[col / 32][col % 32]),
-                                                              __uint_as_float(v[col / 32][col % 32 + 1])), f2, b2);
-                            s.x = ex2(s.x);
-                            s.y = ex2(s.y);
-                            part = __fadd2_rn(part, s);
-                            p[x] = half2_bits(s.x, s.y);
+                        if (top > mx + 8.0f) {
+                            alpha = ex2(mx - top);
+                            mx = top;
+                            sum *= alpha;
                         }
-                        sum = S::fp4 ? sum + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t & 3u][g], sum);
+                        weights();
+                    }
+                    sum += total;
+#pragma unroll
+                    for (int g = 0; g < groups; ++g) {
                         if constexpr (S::mine == 32)
-                            tmem_st16(to_p + g * 16, p);
+                            tmem_st16(at + g * 16, p[g]);
                         else
                             asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                                         ::"r"(to_p + g * 8), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]),
-                                           "r"(p[6]), "r"(p[7]) : "memory");
+                                         ::"r"(at + g * 8), "r"(p[g][0]), "r"(p[g][1]), "r"(p[g][2]), "r"(p[g][3]),
+                                           "r"(p[g][4]), "r"(p[g][5]), "r"(p[g][6]), "r"(p[g][7]) : "memory");
                     }
                     // The product before this one is done (every phase is waited for, since a wait
                     // is for the one that comes next): the output may be rescaled.
@@ -532,7 +615,8 @@ attention_tiles_kernel(const AttArgs a)
                             break;
                         if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
                             fence_after();
-#pragma unroll
+                            const uint32_t out = tmem + kOut + wg * D + lanes;
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o[32];
                                 tmem_ld32(out + c * 32, o);
@@ -549,24 +633,19 @@ attention_tiles_kernel(const AttArgs a)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bars.pfull[buf]);
-                    if (issuer) {
-                        products(j, buf, buf0[buf] + (un.two ? j : j >> 1), un.two);
-                        if (un.two && j + 1u < un.steps)
-                            scores(j + 1u, buf, true);
-                        if (!un.two && j + 2u < un.steps)
-                            scores(j + 2u, buf, false);
-                        if (!ok)
-                            break;
-                    }
                 }
                 if (!ok)
                     break;
                 // The tile's output, or this CTA's part of it.
-                if (!(ok = wait_all(&bars.pv[wg], pv0 + un.steps - 1u, bars, a.c.status)))
+                if (!(ok = wait_all(&bars.pv[wg], pv0 + steps - 1u, bars, a.c.status)))
                     break;
                 fence_after();
-                const bool whole = w.whole();
-                const uint64_t to = (uint64_t)(w.s.first + i) * (a.c.heads * a.group) + h;
+                __syncwarp();
+                w = saved[warp];
+                const uint32_t out = tmem + kOut + wg * D + lanes, row1 = w.rt * S::rows + wg * 128u + r;
+                const uint32_t i1 = fastdiv(row1, a.groupdiv), h1 = w.head * a.group + row1 - i1 * a.group;
+                const bool in1 = row1 < w.s.rows, whole = w.whole();
+                const uint64_t to = (uint64_t)(w.s.first + i1) * (a.c.heads * a.group) + h1;
                 float *part = part_of<S::rows, D>(a, blockIdx.x, w.k0 == 0u);
                 const float f2 = sum == 0.0f ? 0.0f : (S::fp4 ? __ldg(a.c.v_s2 + w.head) : 1.0f) / sum;
 #pragma unroll 1
@@ -574,7 +653,7 @@ attention_tiles_kernel(const AttArgs a)
                     uint32_t o[32];
                     tmem_ld32(out + c * 32, o);
                     tmem_ld_wait(o);
-                    if (!in)
+                    if (!in1)
                         continue;
                     if (whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.o + to * D + c * 32);
@@ -596,9 +675,9 @@ attention_tiles_kernel(const AttArgs a)
                             dst[x] = make_uint4(o[x * 4], o[x * 4 + 1], o[x * 4 + 2], o[x * 4 + 3]);
                     }
                 }
-                if (in && whole && a.lse)
+                if (in1 && whole && a.lse)
                     a.lse[to] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
-                if (in && !whole)
+                if (in1 && !whole)
                     *reinterpret_cast<float2 *>(part + S::rows * D + (wg * 128u + r) * 2u) = make_float2(mx, sum);
                 fence_before();     // the loads of the output, before the next tile's products
             }
@@ -612,16 +691,12 @@ attention_tiles_kernel(const AttArgs a)
                 a.left[blockIdx.x] = u;
             }
             t0 += un.steps;
-            buf0[0] += un.uses(0);
-            buf0[1] += un.uses(1);
+#pragma unroll
+            for (uint32_t i = 0; i < kBufs; ++i)
+                buf0[i] += un.uses(i);
             pv0 += un.products(wg);
             if (!un.two)
                 meet();
-        }
-        if (issuer) {
-            umma_commit(&bars.drain[wg], one);       // every product of this warp is done
-            for (uint32_t i = 0; i < kSpin && !mbar_try_wait(&bars.drain[wg], 0); ++i)
-                ;
         }
     }
     __syncwarp();

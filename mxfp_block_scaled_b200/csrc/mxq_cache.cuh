@@ -35,12 +35,19 @@ __device__ __forceinline__ uint32_t new_tokens(const CacheView &c, uint32_t b, u
     return r0 >= 0 && r1 > r0 && r1 <= (int64_t)T ? (uint32_t)(r1 - r0) : 0u;
 }
 
+// What the table says of position `pos` of sequence b: a page, or a number that is none
+// (c.pages where the table ends before).
+__device__ __forceinline__ uint32_t table_entry(const CacheView &c, uint32_t b, uint32_t pos)
+{
+    const uint32_t i = pos >> c.page_log;
+    return i < c.width ? (uint32_t)__ldg(c.table + (uint64_t)b * c.width + i) : c.pages;
+}
+
 // Page of position `pos` (at least 0) of sequence b; c.pages where the table
 // has none, and the status bit set.
 __device__ __forceinline__ uint32_t find_page(const CacheView &c, uint32_t b, uint32_t pos)
 {
-    const uint32_t i = pos >> c.page_log;
-    const uint32_t page = i < c.width ? (uint32_t)__ldg(c.table + (uint64_t)b * c.width + i) : c.pages;
+    const uint32_t page = table_entry(c, b, pos);
     if (page < c.pages)
         return page;
     atomicOr(c.status, MXQ_DEV_INVALID_PAGE);
