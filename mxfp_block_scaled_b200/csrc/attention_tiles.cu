@@ -68,7 +68,7 @@ struct Shape {
 constexpr uint32_t kBufs = 4;               // of scores, in TMEM
 constexpr uint32_t kRing = 16;              // steps whose powers are kept; decoding is fewer ahead
 struct Bars {
-    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], qfull[2], ffull[kRing], meet, drain[2];
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], odone[2], qfull[2], ffull[kRing], meet, drain[2];
     uint32_t tmem, abort;
     float kfac[kRing][4], vexp[kRing][4], vinv[kRing][4];       // by step and chunk: powers of keys, values
 };
@@ -188,6 +188,7 @@ attention_tiles_kernel(const AttArgs a)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.pv[i], 1);
+            mbar_init(&bars.odone[i], 1);
             mbar_init(&bars.qfull[i], 4);
             mbar_init(&bars.drain[i], 1);
         }
@@ -232,10 +233,14 @@ attention_tiles_kernel(const AttArgs a)
             if (wg == 0u || un.two) {
                 const uint32_t buffers = un.two ? kBufs / 2u : kBufs;       // of this group
                 ok = wait_all(&bars.qfull[wg], q0++, bars, a.c.status);
+                auto keys_there = [&](uint32_t j) {
+                    const uint32_t t = t0 + j;
+                    ok = ok && wait_all(&bars.kfull[t % S::stages], t / S::stages, bars, a.c.status);
+                };
                 // Scores of step j; a group alone makes up for the other's arrivals.
                 auto scores = [&](uint32_t j) {
                     const uint32_t t = t0 + j, stage = t % S::stages, buf = un.buffer(wg, j);
-                    if (!(ok = ok && wait_all(&bars.kfull[stage], t / S::stages, bars, a.c.status)))
+                    if (!ok)
                         return;
                     fence_after();
                     const uint64_t k1 = kd + stage * (S::tile >> 4);
@@ -248,11 +253,15 @@ attention_tiles_kernel(const AttArgs a)
                     if (S::subs == 2 && !un.two)
                         umma_commit(&bars.kempty[stage], one);
                 };
-                for (uint32_t j = 0; j < min(un.steps, buffers); ++j)
+                for (uint32_t j = 0; j < min(un.steps, buffers); ++j) {
+                    keys_there(j);
                     scores(j);
+                }
                 for (uint32_t j = 0; j < un.steps && ok; ++j) {
                     const uint32_t t = t0 + j, stage = t % S::stages, buf = un.buffer(wg, j);
-                    ok = wait_all(&bars.vfull[stage], t / S::stages, bars, a.c.status) &&
+                    if (j + buffers < un.steps)
+                        keys_there(j + buffers);
+                    ok = ok && wait_all(&bars.vfull[stage], t / S::stages, bars, a.c.status) &&
                          wait_all(&bars.pfull[buf], buf0[buf] + un.use(j), bars, a.c.status);
                     if (!ok)
                         break;
@@ -265,6 +274,8 @@ attention_tiles_kernel(const AttArgs a)
                     umma_commit(&bars.vempty[stage], one);
                     if (S::subs == 2 && !un.two)
                         umma_commit(&bars.vempty[stage], one);
+                    if (j + 1u == un.steps)
+                        umma_commit(&bars.odone[wg], one);
                     // The weights have been read, and the next scores may take their place.
                     ok = wait_all(&bars.pv[wg], pv0 + j, bars, a.c.status);
                     if (j + buffers < un.steps)
@@ -448,7 +459,7 @@ attention_tiles_kernel(const AttArgs a)
         regs_up<kSoftRegs>();
         const uint32_t wg = warp >> 2, r = (warp & 3u) * 32u + lane, lanes = ((warp & 3u) * 32u) << 16;
         char *qs = smem + wg * S::qbytes;
-        uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, pv0 = 0, met = 0;
+        uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, pv0 = 0, pieces = 0, met = 0;
         bool ok = wg < S::subs;
         // Both groups, before and after a piece that one of them has to itself: a wait for
         // a barrier's phase is one only for those who have seen the phase before it.
@@ -608,24 +619,27 @@ attention_tiles_kernel(const AttArgs a)
                                          ::"r"(at + g * 8), "r"(p[g][0]), "r"(p[g][1]), "r"(p[g][2]), "r"(p[g][3]),
                                            "r"(p[g][4]), "r"(p[g][5]), "r"(p[g][6]), "r"(p[g][7]) : "memory");
                     }
-                    // The product before this one is done (every phase is waited for, since a wait
-                    // is for the one that comes next): the output may be rescaled.
-                    if (j > 0) {
+                    // Where a row's maximum has grown the output is rescaled, once the product before
+                    // this one is done.  (A wait is for a barrier's next phase.  Of two groups each has
+                    // two buffers of scores, so with these scores the product before that one is done;
+                    // a group alone has four, and waits at every step.)
+                    const bool grown = j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
+                    if (j > 0 && (grown || !two)) {
                         if (!(ok = wait_all(&bars.pv[wg], pv0 + j - 1u, bars, a.c.status)))
                             break;
-                        if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-                            fence_after();
-                            const uint32_t out = tmem + kOut + wg * D + lanes;
+                    }
+                    if (grown) {
+                        fence_after();
+                        const uint32_t out = tmem + kOut + wg * D + lanes;
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(out + c * 32, o);
-                                tmem_ld_wait(o);
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(out + c * 32, o);
+                            tmem_ld_wait(o);
 #pragma unroll
-                                for (int x = 0; x < 32; ++x)
-                                    o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                                tmem_st32(out + c * 32, o);
-                            }
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                            tmem_st32(out + c * 32, o);
                         }
                     }
                     tmem_st_wait();
@@ -637,7 +651,7 @@ attention_tiles_kernel(const AttArgs a)
                 if (!ok)
                     break;
                 // The tile's output, or this CTA's part of it.
-                if (!(ok = wait_all(&bars.pv[wg], pv0 + steps - 1u, bars, a.c.status)))
+                if (!(ok = wait_all(&bars.odone[wg], pieces++, bars, a.c.status)))
                     break;
                 fence_after();
                 __syncwarp();
