@@ -10,7 +10,9 @@
 // ends with.  Unfinished tiles are left in the workspace (`part`), and
 // attention_join_kernel adds up the parts of each in the order of the keys: no
 // atomics, and the division follows from the lengths, the sizes and the number of
-// SMs alone.  Every warp works its CTA's range out for itself, in the same way.
+// SMs alone.  Every warp works its CTA's range out for itself, in the same way (out of
+// line: a launch begins with cold instruction caches, and inlined in every role the
+// division was most of a kernel's code).
 #pragma once
 
 #include "mxq_cache.cuh"
@@ -99,7 +101,7 @@ struct Division {
     }
 
     // A sequence a lane: steps of all heads of sequence b (0 past the last).
-    static __device__ __forceinline__ uint64_t lane_steps(const AttArgs &a, uint32_t b)
+    static __device__ __noinline__ uint64_t lane_steps(const AttArgs &a, uint32_t b)
     {
         Sequence s = {};
         if (b < a.c.seqs)
@@ -159,7 +161,7 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, Range &r, uint64_t &be
 
 // All threads: this CTA's range.
 template <typename Div>
-__device__ __forceinline__ void find_range(const AttArgs &a, Range &r)
+__device__ __noinline__ void find_range(const AttArgs &a, Range &r)
 {
     uint64_t own = 0, before, v = 0;
     for (uint32_t b0 = 0; b0 < a.c.seqs; b0 += blockDim.x)
@@ -191,7 +193,7 @@ __device__ __forceinline__ void find_range(const AttArgs &a, Range &r)
 }
 
 // A warp's walk over the pieces of its CTA's range: a tile, or the part of it in
-// the range.  All lanes call and hold the same values.
+// the range.  It lies in shared memory; all lanes call.
 template <uint32_t R, uint32_t LOG>
 struct Walk {
     using Div = Division<R, LOG>;
@@ -203,28 +205,34 @@ struct Walk {
 
     __device__ __forceinline__ bool whole() const { return k1 - k0 == steps; }
 
-    __device__ __forceinline__ void take()
+    // The piece at the walk's place, of as many steps as the range has left; back to `to`.
+    __device__ __forceinline__ void take(const AttArgs &a, Walk &to)
     {
-        steps = Div::steps(*a, s, rt);
-        keys = Div::keys(*a, s, rt);
+        steps = Div::steps(a, s, rt);
+        keys = Div::keys(a, s, rt);
         k1 = (uint32_t)min((uint64_t)steps, k0 + left);
         left -= k1 - k0;
+        __syncwarp();
+        if ((threadIdx.x & 31u) == 0u)
+            to = *this;
+        __syncwarp();
     }
-    __device__ __forceinline__ bool begin(const AttArgs &args, const Range &r)
+    static __device__ __noinline__ bool begin(Walk &to, const AttArgs &a, const Range &r)
     {
-        a = &args;
-        left = r.end - r.begin;
-        if (left == 0)
+        Walk w;
+        w.left = r.end - r.begin;
+        if (w.left == 0)
             return false;
-        b = r.b;
-        s = sequence(args, b);
-        const uint64_t per = Div::head_steps(args, s);
-        head = (uint32_t)(r.at / per);
-        uint64_t at = r.at - head * per;
+        w.b = r.b;
+        w.s = sequence(a, w.b);
+        const uint64_t per = Div::head_steps(a, w.s);
+        w.head = (uint32_t)(r.at / per);
+        uint64_t at = r.at - w.head * per;
         // the tile: 32 at a time
-        const uint32_t lane = threadIdx.x & 31u, nt = Div::tiles(s);
-        for (rt = 0;; rt += 32u) {
-            uint64_t v = rt + lane < nt ? Div::steps(args, s, rt + lane) : 0u;
+        const uint32_t lane = threadIdx.x & 31u, nt = Div::tiles(w.s);
+#pragma unroll 1
+        for (w.rt = 0;; w.rt += 32u) {
+            uint64_t v = w.rt + lane < nt ? Div::steps(a, w.s, w.rt + lane) : 0u;
             const uint64_t own = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -235,37 +243,37 @@ struct Walk {
             if (past) {
                 const uint32_t l = __ffs(past) - 1;
                 at -= __shfl_sync(0xFFFFFFFFu, v - own, l);
-                rt += l;
+                w.rt += l;
                 break;
             }
             at -= __shfl_sync(0xFFFFFFFFu, v, 31);
-            if (rt + 32u >= nt)         // cannot be: the range lies in the sequence
+            if (w.rt + 32u >= nt)       // cannot be: the range lies in the sequence
                 return false;
         }
-        k0 = (uint32_t)at;
-        take();
+        w.k0 = (uint32_t)at;
+        w.take(a, to);
         return true;
     }
-    __device__ __forceinline__ bool next()
+    static __device__ __noinline__ bool next(Walk &to, const AttArgs &a)
     {
-        if (left == 0)
+        Walk w = to;
+        if (w.left == 0)
             return false;
-        k0 = 0;
-        if (++rt == Div::tiles(s)) {
-            rt = 0;
-            if (++head == a->c.heads) {
-                head = 0;
+        w.k0 = 0;
+        if (++w.rt == Div::tiles(w.s)) {
+            w.rt = 0;
+            if (++w.head == a.c.heads) {
+                w.head = 0;
                 do {
-                    if (++b >= a->c.seqs)
+                    if (++w.b >= a.c.seqs)
                         return false;
-                    s = sequence(*a, b);
-                } while (s.rows == 0);
+                    w.s = sequence(a, w.b);
+                } while (w.s.rows == 0);
             }
         }
-        take();
+        w.take(a, to);
         return true;
     }
-    const AttArgs *a;
 };
 
 // CTAs from this one on that have a part of the tile that the range's last piece

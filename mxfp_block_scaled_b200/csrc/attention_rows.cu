@@ -81,12 +81,13 @@ __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * kWarps, Shape<FMT, D>::most)
-attention_rows_kernel(const AttArgs a)
+attention_rows_kernel(const __grid_constant__ AttArgs a)
 {
     using S = Shape<FMT, D>;
     constexpr uint32_t kThreads = 32 * kWarps;
     extern __shared__ __align__(128) char smem[];
     __shared__ Range range;
+    __shared__ Walk<kRows, kLog> walks[kWarps];
     __shared__ float stat[2][kWarps][kRows];        // the warps' maxima and sums
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3u;
     cudaGridDependencySynchronize();
@@ -98,8 +99,8 @@ attention_rows_kernel(const AttArgs a)
     char *ring = smem + warp * S::ring;
     const uint32_t ring_s = smem_addr(ring);
     char *qs = smem + kWarps * S::ring;
-    Walk<kRows, kLog> walk;
-    for (bool more = walk.begin(a, range); more; more = walk.next()) {
+    Walk<kRows, kLog> &walk = walks[warp];
+    for (bool more = Walk<kRows, kLog>::begin(walk, a, range); more; more = Walk<kRows, kLog>::next(walk, a)) {
         const uint32_t first = walk.s.first, rows = walk.s.rows, tile = walk.rt, head = walk.head, b = walk.b;
         const int64_t pos0 = walk.s.len - walk.s.n;           // position of the sequence's first new token
         const uint32_t k0 = walk.k0 << kLog, k1 = min(walk.k1 << kLog, walk.keys);

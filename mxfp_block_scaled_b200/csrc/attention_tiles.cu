@@ -29,7 +29,6 @@
 #include "mxq_mma.cuh"
 #include "mxq_tcgen05.cuh"
 #include <algorithm>
-#include <type_traits>
 
 namespace mxq {
 
@@ -42,10 +41,6 @@ constexpr uint32_t kSpin = 1u << 18;        // tests of a barrier before a wait 
 // more than half of the time.)
 constexpr uint32_t kCodeWarp = 8;
 constexpr int kThreads = 512;
-// Registers of a thread: 128 at launch, of which the decoding warps give up what the
-// softmax ones take.
-constexpr int kLaunchRegs = 128, kSoftRegs = 160, kCodeRegs = 96;
-static_assert(kLaunchRegs * kThreads <= 65536 && kSoftRegs + kCodeRegs <= 2 * kLaunchRegs, "register shares");
 
 template <int FMT, int D>
 struct Shape {
@@ -73,10 +68,11 @@ struct Bars {
     float kfac[kRing][4], vexp[kRing][4], vinv[kRing][4];       // by step and chunk: powers of keys, values
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
+// Further tests of a barrier whose first one failed.
+__device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
 {
     for (uint32_t i = 0; i < kSpin; ++i) {
-        if (mbar_try_wait(bar, parity & 1u))
+        if (mbar_try_wait(bar, parity))
             return true;
         if ((i & 63u) == 63u && *reinterpret_cast<volatile uint32_t *>(&s.abort))
             return false;
@@ -88,7 +84,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bars &s
 // The whole warp.
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
 {
-    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, s, status));
+    return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity & 1u)) ||
+           __all_sync(0xFFFFFFFFu, wait_more(bar, parity & 1u, s, status));
 }
 
 // 128 x N products of 16, f16 operands, from shared memory and from TMEM; issued
@@ -166,14 +163,14 @@ struct Raw {
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_tiles_kernel(const AttArgs a)
+attention_tiles_kernel(const __grid_constant__ AttArgs a)
 {
     using S = Shape<FMT, D>;
     using W = Walk<S::rows, S::log>;
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ Bars bars;
     __shared__ Range range;
-    __shared__ W saved[8];      // a softmax warp's walk, while it is in a piece
+    __shared__ W walks[16];     // of the warps
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     char *kt = smem + S::subs * S::qbytes, *vt = kt + S::stages * S::tile;
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
@@ -216,9 +213,7 @@ attention_tiles_kernel(const AttArgs a)
     constexpr uint32_t kOut = kBufs * S::keys;
     static_assert(kOut + S::subs * D <= 512, "TMEM");
 
-    W w;
-    if (warp >= kCodeWarp)
-        regs_down<kCodeRegs>();
+    W &w = walks[warp];
     if (warp >= kCodeWarp && (warp & 3u) == 3u) {    // issue
         const uint32_t one = elect_one(), wg = (warp - kCodeWarp) >> 2;
         uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, q0 = 0, pv0 = 0;
@@ -228,7 +223,7 @@ attention_tiles_kernel(const AttArgs a)
         const uint64_t qd = operand_desc(smem_addr(smem + wg * S::qbytes)), kd = operand_desc(smem_addr(kt));
         const uint64_t vd = columns_desc(smem_addr(vt), S::panel);
         const uint32_t out = tmem + kOut + wg * D;
-        for (bool more = w.begin(a, range); more && ok; more = w.next()) {
+        for (bool more = W::begin(w, a, range); more && ok; more = W::next(w, a)) {
             const Units<S> un(w);
             if (wg == 0u || un.two) {
                 const uint32_t buffers = un.two ? kBufs / 2u : kBufs;       // of this group
@@ -300,14 +295,14 @@ attention_tiles_kernel(const AttArgs a)
         uint64_t *full = values ? bars.vfull : bars.kfull, *empty = values ? bars.vempty : bars.kempty;
         char *tiles = values ? vt : kt;
         Raw<FMT, D> raw;
-        bool more = w.begin(a, range);
+        bool more = W::begin(w, a, range);
         uint32_t step = w.k0, t = 0;
         auto settle = [&]() {       // the chunk is number dw from step `step` on: its own step
             while (dw >= S::chunks && more) {
                 dw -= S::chunks;
                 ++t;
                 if (++step == w.k1) {
-                    more = w.next();
+                    more = W::next(w, a);
                     step = w.k0;
                 }
             }
@@ -456,7 +451,6 @@ attention_tiles_kernel(const AttArgs a)
                 load();
         }
     } else {                                         // softmax: a row a thread
-        regs_up<kSoftRegs>();
         const uint32_t wg = warp >> 2, r = (warp & 3u) * 32u + lane, lanes = ((warp & 3u) * 32u) << 16;
         char *qs = smem + wg * S::qbytes;
         uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, pv0 = 0, pieces = 0, met = 0;
@@ -471,7 +465,7 @@ attention_tiles_kernel(const AttArgs a)
                 ok = wait_all(&bars.meet, met++, bars, a.c.status);
             }
         };
-        for (bool more = w.begin(a, range); more && ok; more = w.next()) {
+        for (bool more = W::begin(w, a, range); more && ok; more = W::next(w, a)) {
             const Units<S> un(w);
             if (!un.two)
                 meet();
@@ -485,7 +479,7 @@ attention_tiles_kernel(const AttArgs a)
                 const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.first + (in ? i : 0u)) * a.q_stride +
                                                                    (uint64_t)(in ? h : 0u) * D);
                 uint32_t m = 0;
-#pragma unroll
+#pragma unroll 8
                 for (uint32_t k = 0; k < D / 8; ++k) {
                     const uint4 v = __ldg(src + k);
                     m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v.x), v.y), v.z), v.w);
@@ -493,9 +487,9 @@ attention_tiles_kernel(const AttArgs a)
                 float f = row_factor(fold_halves(m) << 16);
                 float fq = fabsf(a.scale) / f;
                 if (S::fp4)
-                    fq *= __ldg(a.c.k_s2 + w.head);
+                    fq = fmaxf(fq * __ldg(a.c.k_s2 + w.head), 0x1p-126f);
                 f = a.scale < 0.0f ? -f : f;
-#pragma unroll
+#pragma unroll 4
                 for (uint32_t k = 0; k < D / 8; ++k) {
                     const uint4 v = __ldg(src + k);
                     *reinterpret_cast<uint4 *>(qs + (k >> 3) * S::qpanel + r * 128u + (((k & 7u) ^ (r & 7u)) << 4)) =
@@ -512,10 +506,6 @@ attention_tiles_kernel(const AttArgs a)
                 const int64_t base = (int64_t)w.k0 << S::log, pos = in ? w.s.len - w.s.n + i : 0x7FFFFFFFll;
                 const int last = (int)max(min(pos, (int64_t)w.keys - 1) - base, (int64_t)-1);
                 float mx = kLowest, sum = 0.0f;
-                // the walk is not needed meanwhile, and its registers are
-                __syncwarp();
-                if (lane == 0)
-                    saved[warp] = w;
                 const uint32_t steps = un.steps;
                 const bool two = un.two;
                 // phases of this group's buffers: of the even ones and the odd ones of its units
@@ -532,25 +522,53 @@ attention_tiles_kernel(const AttArgs a)
                     fence_after();
                     constexpr int parts = S::keys / 32;         // of 32 columns
                     constexpr int groups = S::chunks;           // of columns whose powers are the same
-                    uint32_t v[parts][32];
-#pragma unroll
-                    for (int c = 0; c < parts; ++c)
-                        tmem_ld32(at + c * 32, v[c]);
-#pragma unroll
-                    for (int c = 0; c < parts; ++c)
-                        tmem_ld_wait(v[c]);
+                    // Keys from `lim` + 1 on the row does not see.
                     const int lim = last - (int)(j << S::log);
                     const bool cut = __any_sync(0xFFFFFFFFu, lim < (int)S::keys - 1);
-                    // Of a chunk's columns: powers of the keys (with the row's own factor), of the values.
-                    auto fac = [&](int g) { return S::fp4 ? fq : fq * bars.kfac[t % kRing][g]; };
+                    // Of a chunk's columns: powers of the keys (with the row's own factor, kept above
+                    // 0, which times -Inf would be NaN), of the values.
+                    auto fac = [&](int g) { return S::fp4 ? fq : fmaxf(fq * bars.kfac[t % kRing][g], 0x1p-126f); };
                     auto e = [&](int g) { return S::fp4 ? 0.0f : bars.vexp[t % kRing][g]; };
                     // Weights against the maximum so far, which stays unless a row's grows by more
                     // than 2^8; then (and at first) the maximum is found first, and the weights
-                    // from the scores again, which are still where they were.
+                    // from the scores again.  (One copy of each loop: cold instruction caches are
+                    // what a short call waits for.)
                     uint32_t p[groups][S::mine / 2];
-                    float alpha = 1.0f, total = 0.0f, high = -INFINITY;
-                    auto weights_of = [&](auto masked) {
+                    float alpha = 1.0f, total, high;
+#pragma unroll 1
+                    for (bool find = j == 0;;) {
+                        uint32_t v[parts][32];
+#pragma unroll
+                        for (int c = 0; c < parts; ++c)
+                            tmem_ld32(at + c * 32, v[c]);
+#pragma unroll
+                        for (int c = 0; c < parts; ++c)
+                            tmem_ld_wait(v[c]);
+                        if (cut) {
+#pragma unroll
+                            for (int x = 0; x < (int)S::keys; ++x)
+                                v[x / 32][x % 32] = x <= lim ? v[x / 32][x % 32] : 0xFF800000u;        // -Inf
+                        }
+                        if (find) {
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int g = 0; g < groups; ++g) {
+                                float m = -INFINITY;
+#pragma unroll
+                                for (int x = 0; x < (int)S::mine; ++x) {
+                                    const int col = g * S::mine + x;
+                                    m = fmaxf(m, __uint_as_float(v[col / 32][col % 32]));
+                                }
+                                top = fmaxf(top, fmaf(m, fac(g), e(g)));
+                            }
+                            if (top > mx + 8.0f) {
+                                alpha = ex2(mx - top);
+                                mx = top;
+                                sum *= alpha;
+                            }
+                        }
                         total = 0.0f;
+                        high = -INFINITY;
 #pragma unroll
                         for (int g = 0; g < groups; ++g) {
                             const float fg = fac(g), bg = e(g) - mx;
@@ -561,10 +579,6 @@ attention_tiles_kernel(const AttArgs a)
                                 const int col = g * S::mine + 2 * x;
                                 float2 s = __ffma2_rn(make_float2(__uint_as_float(v[col / 32][col % 32]),
                                                                   __uint_as_float(v[col / 32][col % 32 + 1])), f2, b2);
-                                if (masked.value) {
-                                    s.x = col <= lim ? s.x : -INFINITY;
-                                    s.y = col + 1 <= lim ? s.y : -INFINITY;
-                                }
                                 high = fmaxf(fmaxf(high, s.x), s.y);
                                 s.x = ex2(s.x);
                                 s.y = ex2(s.y);
@@ -573,41 +587,9 @@ attention_tiles_kernel(const AttArgs a)
                             }
                             total = S::fp4 ? total + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t % kRing][g], total);
                         }
-                    };
-                    auto weights = [&]() {
-                        if (cut)
-                            weights_of(std::true_type());
-                        else
-                            weights_of(std::false_type());
-                    };
-                    if (j > 0)
-                        weights();
-                    if (j == 0 || __any_sync(0xFFFFFFFFu, high > 8.0f)) {
-                        if (j > 0) {
-#pragma unroll
-                            for (int c = 0; c < parts; ++c)
-                                tmem_ld32(at + c * 32, v[c]);
-#pragma unroll
-                            for (int c = 0; c < parts; ++c)
-                                tmem_ld_wait(v[c]);
-                        }
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int g = 0; g < groups; ++g) {
-                            const float fg = fac(g), eg = e(g);
-#pragma unroll
-                            for (int x = 0; x < (int)S::mine; ++x) {
-                                const int col = g * S::mine + x;
-                                const float s = fmaf(__uint_as_float(v[col / 32][col % 32]), fg, eg);
-                                top = fmaxf(top, col <= lim ? s : -INFINITY);
-                            }
-                        }
-                        if (top > mx + 8.0f) {
-                            alpha = ex2(mx - top);
-                            mx = top;
-                            sum *= alpha;
-                        }
-                        weights();
+                        if (find || !__any_sync(0xFFFFFFFFu, high > 8.0f))
+                            break;
+                        find = true;
                     }
                     sum += total;
 #pragma unroll
@@ -654,8 +636,6 @@ attention_tiles_kernel(const AttArgs a)
                 if (!(ok = wait_all(&bars.odone[wg], pieces++, bars, a.c.status)))
                     break;
                 fence_after();
-                __syncwarp();
-                w = saved[warp];
                 const uint32_t out = tmem + kOut + wg * D + lanes, row1 = w.rt * S::rows + wg * 128u + r;
                 const uint32_t i1 = fastdiv(row1, a.groupdiv), h1 = w.head * a.group + row1 - i1 * a.group;
                 const bool in1 = row1 < w.s.rows, whole = w.whole();
