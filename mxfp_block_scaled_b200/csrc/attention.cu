@@ -29,59 +29,126 @@ bool few(int64_t group, int64_t max_new) { return group * max_new <= (int64_t)kF
 
 } // namespace
 
-// The parts of a tile that CTA blockIdx.x of the kernel before began, added up in
-// their order.  A warp takes a row, lanes its columns.
-template <uint32_t R, int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttArgs a)
+// Parts of unfinished tiles, added up in their order.  Of the `ctas` CTAs of the kernel
+// before, blockIdx.x counts those that began one; blockIdx.y its rows, 8 / WPR to a CTA.
+// WPR warps share a row's parts, and their sums are added in the order of the warps;
+// lanes have its columns.
+template <uint32_t R, int D, uint32_t WPR>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttArgs a, uint32_t ctas)
 {
+    __shared__ uint32_t found, count[8];
+    __shared__ float sums[8][D + 1];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    const uint32_t lane = threadIdx.x & 31u, cta = blockIdx.x;
+    if (tid == 0)
+        found = ctas;
+    uint32_t before = 0;
+#pragma unroll 1
+    for (uint32_t c0 = 0; c0 < ctas; c0 += 256u) {
+        const bool has = c0 + tid < ctas && a.left[c0 + tid].parts > 0u;
+        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, has);
+        __syncthreads();
+        if (lane == 0)
+            count[warp] = __popc(vote);
+        __syncthreads();
+        uint32_t at = before + __popc(vote & ((1u << lane) - 1u));
+#pragma unroll
+        for (uint32_t w = 0; w < 8u; ++w) {
+            at += w < warp ? count[w] : 0u;
+            before += count[w];
+        }
+        if (has && at == blockIdx.x)
+            found = c0 + tid;
+    }
+    __syncthreads();
+    const uint32_t cta = found;
+    if (cta == ctas)
+        return;
     const Unfinished u = a.left[cta];
-    const uint32_t end = min(u.rows - u.row0, R);
-    for (uint32_t r = blockIdx.y * 8u + (threadIdx.x >> 5); u.parts > 0u && r < end; r += gridDim.y * 8u) {
+    const uint32_t r = blockIdx.y * (8u / WPR) + warp / WPR, q = warp % WPR;
+    const bool in = r < min(u.rows - u.row0, R);
+    constexpr int per = D / 32;                 // neighbouring columns of a lane
+    float v[per], l = 0.0f, m = kLowest;
+#pragma unroll
+    for (int j = 0; j < per; ++j)
+        v[j] = 0.0f;
+    if (in) {
         // maximum over the parts: the first is the CTA's second, the others their CTAs' first
-        float m = kLowest;
         for (uint32_t i = lane; i < u.parts; i += 32u)
             m = fmaxf(m, part_of<R, D>(a, cta + i, i == 0u)[R * D + r * 2u]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        constexpr int per = D / 32;
-        float v[per], l = 0.0f;
-#pragma unroll
-        for (int j = 0; j < per; ++j)
-            v[j] = 0.0f;
-#pragma unroll 4
-        for (uint32_t i = 0; i < u.parts; ++i) {
+#pragma unroll 8
+        for (uint32_t i = q; i < u.parts; i += WPR) {
             const float *p = part_of<R, D>(a, cta + i, i == 0u);
             const float2 st = *reinterpret_cast<const float2 *>(p + R * D + r * 2u);
+            float x[per];
+            if constexpr (per == 2)
+                *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(p + r * D + lane * per);
+            else
+#pragma unroll
+                for (int j = 0; j < per; j += 4)
+                    *reinterpret_cast<float4 *>(x + j) = *reinterpret_cast<const float4 *>(p + r * D + lane * per + j);
             const float f = ex2(st.x - m);
             l = fmaf(st.y, f, l);
 #pragma unroll
             for (int j = 0; j < per; ++j)
-                v[j] = fmaf(p[r * D + j * 32 + lane], f, v[j]);
+                v[j] = fmaf(x[j], f, v[j]);
         }
-        const uint32_t row = u.row0 + r, i = fastdiv(row, a.groupdiv), h = u.head * a.group + row - i * a.group;
-        const uint64_t out = (uint64_t)(u.first + i) * (a.c.heads * a.group) + h;
-        const float f = l == 0.0f ? 0.0f : (a.c.v_s2 ? __ldg(a.c.v_s2 + u.head) : 1.0f) / l;
+    }
+    if (WPR > 1u) {
 #pragma unroll
         for (int j = 0; j < per; ++j)
-            reinterpret_cast<__nv_bfloat16 *>(a.o)[out * D + j * 32 + lane] = __float2bfloat16_rn(v[j] * f);
-        if (lane == 0 && a.lse)
-            a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            sums[warp][lane * per + j] = v[j];
+        if (lane == 0)
+            sums[warp][D] = l;
+        __syncthreads();
+        if (q != 0u)
+            return;
+#pragma unroll
+        for (uint32_t w = 1; w < WPR; ++w) {
+            l += sums[warp + w][D];
+#pragma unroll
+            for (int j = 0; j < per; ++j)
+                v[j] += sums[warp + w][lane * per + j];
+        }
     }
+    if (!in)
+        return;
+    const uint32_t row = u.row0 + r, i = fastdiv(row, a.groupdiv), h = u.head * a.group + row - i * a.group;
+    const uint64_t out = (uint64_t)(u.first + i) * (a.c.heads * a.group) + h;
+    const float f = l == 0.0f ? 0.0f : (a.c.v_s2 ? __ldg(a.c.v_s2 + u.head) : 1.0f) / l;
+#pragma unroll
+    for (int j = 0; j < per; j += 2)
+        *reinterpret_cast<__nv_bfloat162 *>(a.o + out * D + lane * per + j) = __floats2bfloat162_rn(v[j] * f, v[j + 1] * f);
+    if (lane == 0 && a.lse)
+        a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 namespace {
 
+template <uint32_t R, int D>
+cudaError_t join_of(const AttArgs &a, uint32_t ctas, uint32_t tiles, cudaStream_t s)
+{
+    // Few tiles have many parts: eight warps a row (a decoding step over 65536 tokens, 222
+    // parts of each of two tiles, with one 50 us more).
+    if ((uint64_t)tiles * R <= 4096u)
+        return launch_dependent(attention_join_kernel<R, D, 8>, dim3(tiles, R), 256, 0, s, a, ctas);
+    return launch_dependent(attention_join_kernel<R, D, 1>, dim3(tiles, R / 8), 256, 0, s, a, ctas);
+}
+
+// Tiles there can be at most, and a CTA begins one unfinished at most.
 template <uint32_t R>
 cudaError_t join(const AttArgs &a, int dim, uint32_t ctas, cudaStream_t s)
 {
-    const dim3 grid(ctas, R == 16 ? 2 : 8);
-    return dim == 64    ? launch_dependent(attention_join_kernel<R, 64>, grid, 256, 0, s, a)
-           : dim == 128 ? launch_dependent(attention_join_kernel<R, 128>, grid, 256, 0, s, a)
-                        : launch_dependent(attention_join_kernel<R == 256 ? 128 : R, 256>, grid, 256, 0, s, a);
+    const uint32_t rows = dim == 256 && R == 256 ? 128 : R;
+    const uint64_t tiles = a.c.heads * ((uint64_t)a.T * a.group / rows + a.c.seqs);
+    const uint32_t n = (uint32_t)std::min<uint64_t>(tiles, ctas);
+    return dim == 64    ? join_of<R, 64>(a, ctas, n, s)
+           : dim == 128 ? join_of<R, 128>(a, ctas, n, s)
+                        : join_of<R == 256 ? 128 : R, 256>(a, ctas, n, s);
 }
 
 } // namespace

@@ -157,225 +157,229 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
         float mx[2] = {kLowest, kLowest}, sum[2] = {0.0f, 0.0f};
 
-        // One turn's copies.  32 keys lie on one page, or on two of 16 tokens.
-        auto issue = [&](uint32_t key, uint32_t slot) {
+        // Pages of a turn's keys, as the table has them: 32 keys lie on one page, or on two of 16
+        // tokens.  Looked up a turn before the copies are made, which are a turn ahead themselves.
+        const bool short_pages = a.c.page_log == 4u;
+        auto look = [&](uint32_t key, uint32_t (&page)[2]) {
+            page[0] = key < k1 ? table_entry(a.c, b, key) : 0u;
+            page[1] = short_pages && key + 16u < k1 ? table_entry(a.c, b, key + 16u) : page[0];
+        };
+        // One turn's copies: two runs of 16 keys, each contiguous.
+        auto issue = [&](uint32_t key, uint32_t slot, const uint32_t (&page)[2]) {
             if (key < k1) {
-                const uint32_t half = a.c.page_log == 4u ? 16u : 32u;
-                uint32_t page0 = find_page(a.c, b, key), page1 = page0;
-                if (half == 16u)
-                    page1 = key + 16u < k1 ? find_page(a.c, b, key + 16u) : a.c.pages;
-                const uint32_t mask = (1u << a.c.page_log) - 1u;
-                const uint32_t st = ring_s + slot * S::stage;
-                auto place = [&](uint32_t r, bool &ok) -> uint64_t {        // row of codes of the turn's key r
-                    const uint32_t page = r < half ? page0 : page1;
-                    ok = page < a.c.pages && key + r < k1;
-                    return ok ? (((uint64_t)page * a.c.heads + head) << a.c.page_log) + ((key + r) & mask) : 0ull;
-                };
+                if (page[0] >= a.c.pages || page[1] >= a.c.pages)
+                    atomicOr(a.c.status, MXQ_DEV_INVALID_PAGE);
+                const uint32_t mask = (1u << a.c.page_log) - 1u, st = ring_s + slot * S::stage;
+                const uint32_t keys0 = page[0] < a.c.pages ? k1 - key : 0u, keys1 = page[1] < a.c.pages ? k1 - key : 0u;
+                uint64_t at[2];         // rows of codes of keys 0 and 16 (0 where they are not read)
+                at[0] = keys0 ? (((uint64_t)page[0] * a.c.heads + head) << a.c.page_log) + (key & mask) : 0ull;
+                at[1] = keys1 > 16u ? (((uint64_t)page[1] * a.c.heads + head) << a.c.page_log) + ((key + 16u) & mask) : 0ull;
                 constexpr uint32_t pieces = S::row / 16;        // of a key's codes
+                static_assert(pieces * 16 % 32 == 0, "a copy of the warp stays in a run");
 #pragma unroll
                 for (uint32_t i = 0; i < pieces; ++i) {
-                    const uint32_t p = i * 32u + lane, r = p / pieces;
-                    bool ok;
-                    const uint64_t src = place(r, ok) * S::row + (p % pieces) * 16u;
-                    const uint32_t dst = st + swizzle<S::row>(p * 16u);
-                    cp16_or_zero(dst, a.c.k_codes + src, ok);
-                    cp16_or_zero(dst + S::codes, a.c.v_codes + src, ok);
+                    const uint32_t run = i * 32u / (16u * pieces), p = i * 32u + lane - run * 16u * pieces;
+                    const uint32_t r = run * 16u + p / pieces;
+                    const uint64_t src = at[run] * S::row + p * 16u;
+                    const uint32_t dst = st + swizzle<S::row>((i * 32u + lane) * 16u);
+                    const bool ok = r < (run ? keys1 : keys0);
+                    cp16_or_zero(dst, a.c.k_codes + (ok ? src : 0ull), ok);
+                    cp16_or_zero(dst + S::codes, a.c.v_codes + (ok ? src : 0ull), ok);
                 }
-                // Scales: 16 bytes are 16 / blocks keys of one page.
+                // Scales: 16 bytes are 16 / blocks keys.
 #pragma unroll
                 for (uint32_t i = 0; i < (S::scales / 16 + 31) / 32; ++i) {
                     const uint32_t p = i * 32u + lane;
                     if (p < S::scales / 16) {
-                        bool ok;
-                        const uint64_t src = place(p * 16u / S::blocks, ok) * S::blocks + p * 16u % S::blocks;
-                        cp16_or_zero(st + 2 * S::codes + p * 16u, a.c.k_scales + src, ok);
-                        cp16_or_zero(st + 2 * S::codes + S::scales + p * 16u, a.c.v_scales + src, ok);
+                        const uint32_t r = p * 16u / S::blocks, run = r >> 4;
+                        const uint64_t src = (run ? at[1] : at[0]) * S::blocks + p * 16u - run * 16u * S::blocks;
+                        const bool ok = r < (run ? keys1 : keys0);
+                        cp16_or_zero(st + 2 * S::codes + p * 16u, a.c.k_scales + (ok ? src : 0ull), ok);
+                        cp16_or_zero(st + 2 * S::codes + S::scales + p * 16u, a.c.v_scales + (ok ? src : 0ull), ok);
                     }
                 }
             }
             cp_commit();
         };
 
-        uint32_t key = k0 + warp * kKeys, slot = 0;
-        issue(key, 0);
-        for (; key < k1; key += kWarps * kKeys, slot ^= 1u) {
-            issue(key + kWarps * kKeys, slot ^ 1u);
+        // The loops over parts of a turn are rolled: cold instruction caches are what a short
+        // call waits for, and the code of a whole turn would not stay in them.
+        constexpr uint32_t stride = kWarps * kKeys;
+        uint32_t key = k0 + warp * kKeys, slot = 0, page[2], ahead[2];
+        look(key, page);
+        look(key + stride, ahead);
+        bool first_turn = true;
+        if (key < k1)
+            issue(key, 0, page);
+#pragma unroll 1
+        for (; key < k1; key += stride, slot ^= 1u) {
+            page[0] = ahead[0];
+            page[1] = ahead[1];
+            look(key + 2u * stride, ahead);
+            issue(key + stride, slot ^ 1u, page);
             cp_wait<1>();
             __syncwarp();
             const char *st = ring + slot * S::stage;
             const char *ksc = st + 2 * S::codes, *vsc = ksc + S::scales;
             const uint32_t left = k1 - key;             // keys of the turn
 
-            // Scores of 32 keys: columns nt * 8 + ..., this lane decodes key g8 of each.
+            // Scores: 16 keys at a time, columns nt * 8 + ... of which this lane decodes key g8.
             float s[4][4];
-            uint32_t kscale[4][S::fp4 ? D / 64 : (D + 127) / 128];      // f16x2, of the blocks of the lane's run
-            float kf = kfac;
-            if (S::fp4) {
+#pragma unroll 1
+            for (uint32_t half = 0; half < 2u; ++half) {
+                constexpr int nblk = S::fp4 ? D / 64 : (D + 127) / 128;         // blocks of the lane's run
+                uint32_t kscale[2][nblk];               // f16x2
+                float kf = kfac;
+                const uint32_t kr = half * 16u + g8;
+                if (S::fp4) {
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const char *p = ksc + (nt * 8 + g8) * S::blocks + t4 * (D / 64);
-                    uint32_t w = 0;
-                    if (D == 64)
-                        w = *reinterpret_cast<const uint8_t *>(p);
-                    else if (D == 128)
-                        w = *reinterpret_cast<const uint16_t *>(p);
-                    else
-                        w = lds32(p);
-                    if (nt * 8 + g8 >= left)
-                        w = 0u;
-                    uint32_t h0, h1;
-                    e4m3x4_unpack(w, h0, h1);
-                    kscale[nt][0] = __byte_perm(h0, 0, 0x1010);
-                    if (D >= 128)
-                        kscale[nt][D >= 128 ? 1 : 0] = __byte_perm(h0, 0, 0x3232);
-                    if (D == 256) {
-                        kscale[nt][D == 256 ? 2 : 0] = __byte_perm(h1, 0, 0x1010);
-                        kscale[nt][D == 256 ? 3 : 0] = __byte_perm(h1, 0, 0x3232);
-                    }
-                }
-            } else {
-                uint32_t e[4][(D + 127) / 128], top = 0;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < (D + 127) / 128; ++j) {
-                        const uint32_t blk = D == 64 ? t4 >> 1 : D == 128 ? t4 : t4 * 2 + j;
-                        e[nt][j] = *reinterpret_cast<const uint8_t *>(ksc + (nt * 8 + g8) * S::blocks + blk);
-                        if (nt * 8 + g8 >= left)
-                            e[nt][j] = 0u;
-                        top = max(top, e[nt][j]);
-                    }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < (D + 127) / 128; ++j) {
-                        const float f = __uint_as_float((uint32_t)max((int)(e[nt][j] + 134u) - (int)top, 0) << 23);
-                        kscale[nt][j] = half2_bits(f, f);
-                    }
-                // 2^(top - 134), in two steps: it may be subnormal
-                kf = __uint_as_float(top << 23) * 0x1p-7f;
-                if (top == 0u)
-                    kf = 0x1p-134f;
-            }
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-                const uint32_t row = (nt * 8 + g8) * S::row;
-                constexpr int run = S::row / 4;          // bytes of a lane's run
-#pragma unroll
-                for (int p = 0; p < (run + 15) / 16; ++p) {
-                    uint32_t w[4];
-                    if (run >= 16) {
-                        const uint4 v = lds128(st + swizzle<S::row>(row + t4 * run + p * 16));
-                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                    } else {
-                        const uint2 v = lds64(st + swizzle<S::row>(row + t4 * run));
-                        w[0] = v.x, w[1] = v.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < (run >= 16 ? 4 : 2); ++i) {
-                        uint32_t h[4];
-                        constexpr int per = S::fp4 ? 2 : 1;         // products of a word
-                        if (S::fp4)
-                            e2m1x8_unpack(w[i], h);
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const char *p = ksc + (kr + nt * 8) * S::blocks + t4 * (D / 64);
+                        uint32_t w = 0;
+                        if (D == 64)
+                            w = *reinterpret_cast<const uint8_t *>(p);
+                        else if (D == 128)
+                            w = *reinterpret_cast<const uint16_t *>(p);
                         else
-                            e4m3x4_unpack(w[i], h[0], h[1]);
+                            w = lds32(p);
+                        if (kr + nt * 8 >= left)
+                            w = 0u;
+                        uint32_t h0, h1;
+                        e4m3x4_unpack(w, h0, h1);
+                        kscale[nt][0] = __byte_perm(h0, 0, 0x1010);
+                        if (D >= 128)
+                            kscale[nt][D >= 128 ? 1 : 0] = __byte_perm(h0, 0, 0x3232);
+                        if (D == 256) {
+                            kscale[nt][D == 256 ? 2 : 0] = __byte_perm(h1, 0, 0x1010);
+                            kscale[nt][D == 256 ? 3 : 0] = __byte_perm(h1, 0, 0x3232);
+                        }
+                    }
+                } else {
+                    uint32_t e[2][nblk], top = 27u;     // 2^-100 at least: what is below counts as zeros
 #pragma unroll
-                        for (int u = 0; u < per; ++u) {
-                            const int step = (p * 4 + i) * per + u;       // of 4 values of each lane
-                            const uint32_t sc = kscale[nt][S::fp4 ? step / 4 : step / 8];
-                            uint2 x0, x1;
-                            if (S::q_regs) {
-                                x0 = q0[step % (D / 16)];
-                                x1 = q1[step % (D / 16)];
-                            } else {
-                                x0 = lds64(qa + step * 8);
-                                x1 = lds64(qb + step * 8);
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int j = 0; j < nblk; ++j) {
+                            const uint32_t blk = D == 64 ? t4 >> 1 : D == 128 ? t4 : t4 * 2 + j;
+                            e[nt][j] = *reinterpret_cast<const uint8_t *>(ksc + (kr + nt * 8) * S::blocks + blk);
+                            if (kr + nt * 8 >= left)
+                                e[nt][j] = 0u;
+                            top = max(top, e[nt][j]);
+                        }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int j = 0; j < nblk; ++j) {
+                            const float f = __uint_as_float((uint32_t)max((int)(e[nt][j] + 134u) - (int)top, 0) << 23);
+                            kscale[nt][j] = half2_bits(f, f);
+                        }
+                    kf = __uint_as_float(top << 23) * 0x1p-7f;
+                }
+                float c[2][4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
+                    const uint32_t row = (kr + nt * 8) * S::row;
+                    constexpr int run = S::row / 4;          // bytes of a lane's run
+#pragma unroll
+                    for (int p = 0; p < (run + 15) / 16; ++p) {
+                        uint32_t w[4];
+                        if (run >= 16) {
+                            const uint4 v = lds128(st + swizzle<S::row>(row + t4 * run + p * 16));
+                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                        } else {
+                            const uint2 v = lds64(st + swizzle<S::row>(row + t4 * run));
+                            w[0] = v.x, w[1] = v.y;
+                        }
+#pragma unroll
+                        for (int i = 0; i < (run >= 16 ? 4 : 2); ++i) {
+                            uint32_t h[4];
+                            constexpr int per = S::fp4 ? 2 : 1;         // products of a word
+                            if (S::fp4)
+                                e2m1x8_unpack(w[i], h);
+                            else
+                                e4m3x4_unpack(w[i], h[0], h[1]);
+#pragma unroll
+                            for (int u = 0; u < per; ++u) {
+                                const int step = (p * 4 + i) * per + u;       // of 4 values of each lane
+                                const uint32_t sc = kscale[nt][S::fp4 ? step / 4 : step / 8];
+                                uint2 x0, x1;
+                                if (S::q_regs) {
+                                    x0 = q0[step % (D / 16)];
+                                    x1 = q1[step % (D / 16)];
+                                } else {
+                                    x0 = lds64(qa + step * 8);
+                                    x1 = lds64(qb + step * 8);
+                                }
+                                mma16816(c[nt], x0.x, x1.x, x0.y, x1.y, hmul2_bits(h[2 * u], sc),
+                                         hmul2_bits(h[2 * u + 1], sc));
                             }
-                            mma16816(s[nt], x0.x, x1.x, x0.y, x1.y, hmul2_bits(h[2 * u], sc), hmul2_bits(h[2 * u + 1], sc));
                         }
                     }
                 }
+                const float f[2] = {fq[0] * kf, fq[1] * kf};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[nt][j] = half ? s[nt][j] : c[nt][j] * f[j >> 1];
+                        s[nt + 2][j] = c[nt][j] * f[j >> 1];
+                    }
             }
 
-            // The values' scales; E: their largest power.
-            constexpr int vblocks = S::fp4 && D == 256 ? 2 : 1;      // of a lane's run of D / 8
-            uint32_t vscale[4][vblocks];        // of key pairs (2 t4, + 1) + 8 i
+            // E: the largest power of the values' scales.
             float E = 0.0f, inv = 1.0f;
-            if (S::fp4) {
+            uint32_t vtop = 27u;
+            if (!S::fp4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < vblocks; ++j) {
-                        const uint32_t r = i * 8 + 2 * t4, blk = D == 64 ? g8 >> 1 : D == 128 ? g8 : g8 * 2 + j;
-                        uint32_t w0 = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
-                        uint32_t w1 = *reinterpret_cast<const uint8_t *>(vsc + (r + 1) * S::blocks + blk);
-                        w0 = r < left ? w0 : 0u;
-                        w1 = r + 1 < left ? w1 : 0u;
-                        vscale[i][j] = e4m3x2_to_f16x2(w0 | (w1 << 8));
-                    }
-            } else {
-                uint32_t e[4][2], top = 27u;       // 2^-100 at least: what is below is nothing beside a sum
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t r = i * 8 + 2 * t4 + j, blk = D == 64 ? g8 >> 2 : D == 128 ? g8 >> 1 : g8;
-                        e[i][j] = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
-                        if (r >= left)
-                            e[i][j] = 0u;
-                        top = max(top, e[i][j]);
-                    }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    vscale[i][0] = half2_bits(__uint_as_float((uint32_t)max((int)(e[i][0] + 134u) - (int)top, 0) << 23),
-                                              __uint_as_float((uint32_t)max((int)(e[i][1] + 134u) - (int)top, 0) << 23));
-                E = (float)((int)top - 134);
-                inv = __uint_as_float((uint32_t)(261 - (int)top) << 23);       // 2^-E, top at least 27 (and at most 254)
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t r = (i >> 1) * 8 + 2 * t4 + (i & 1), blk = D == 64 ? g8 >> 2 : D == 128 ? g8 >> 1 : g8;
+                    const uint32_t e = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
+                    vtop = max(vtop, r < left ? e : 0u);
+                }
+                vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+                E = (float)((int)vtop - 134);
+                inv = __uint_as_float((uint32_t)(261 - (int)vtop) << 23);      // 2^-E, vtop at least 27 (and at most 254)
             }
 
-            // Running maximum, weights.
-            float f[2] = {fq[0] * kf, fq[1] * kf};
+            // Running maximum, which stays unless it grows by more than 2^8; weights.
             int lim[2];                                 // last key of the turn that a row sees
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 lim[i] = (int)max(min(pos[i] - (int64_t)key, (int64_t)min(left, kKeys) - 1), (int64_t)-1);
-            if (__any_sync(0xFFFFFFFFu, min(lim[0], lim[1]) < (int)kKeys - 1)) {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[nt][j] = (int)(nt * 8 + 2 * t4 + (j & 1)) <= lim[j >> 1] ? fmaf(s[nt][j], f[j >> 1], E) : -INFINITY;
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[nt][j] = fmaf(s[nt][j], f[j >> 1], E);
-            }
+            const bool cut = __any_sync(0xFFFFFFFFu, min(lim[0], lim[1]) < (int)kKeys - 1);
             float alpha[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float m = mx[i];
+                float m = -INFINITY;
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt)
-                    m = fmaxf(m, fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
+#pragma unroll
+                    for (int j = 2 * i; j < 2 * i + 2; ++j) {
+                        if (cut)
+                            s[nt][j] = (int)(nt * 8 + 2 * t4 + (j & 1)) <= lim[i] ? s[nt][j] : -INFINITY;
+                        m = fmaxf(m, s[nt][j]);
+                    }
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                alpha[i] = ex2(mx[i] - m);
-                mx[i] = m;
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) + E;
+                alpha[i] = 1.0f;
+                if (m > mx[i] + 8.0f) {
+                    alpha[i] = ex2(mx[i] - m);
+                    mx[i] = m;
+                }
+                const float off = E - mx[i];
                 float part = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    s[nt][2 * i] = ex2(s[nt][2 * i] - m);
-                    s[nt][2 * i + 1] = ex2(s[nt][2 * i + 1] - m);
-                    part += s[nt][2 * i] + s[nt][2 * i + 1];
-                }
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int j = 2 * i; j < 2 * i + 2; ++j) {
+                        s[nt][j] = ex2(s[nt][j] + off);
+                        part += s[nt][j];
+                    }
                 sum[i] = fmaf(sum[i], alpha[i], part * inv);
             }
-            if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+            if (!first_turn && __any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
                     acc[j][0] *= alpha[0];
@@ -384,13 +388,40 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                     acc[j][3] *= alpha[1];
                 }
             }
-
-            // Outputs: 16 keys at a time, columns d = run of this lane.
+            first_turn = false;
+            uint32_t pw[2][4];
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                const uint32_t p0 = half2_bits(s[2 * kk][0], s[2 * kk][1]), p1 = half2_bits(s[2 * kk][2], s[2 * kk][3]);
-                const uint32_t p2 = half2_bits(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                               p3 = half2_bits(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+                pw[kk][0] = half2_bits(s[2 * kk][0], s[2 * kk][1]);
+                pw[kk][1] = half2_bits(s[2 * kk][2], s[2 * kk][3]);
+                pw[kk][2] = half2_bits(s[2 * kk + 1][0], s[2 * kk + 1][1]);
+                pw[kk][3] = half2_bits(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+            }
+
+            // Outputs: 16 keys at a time, columns d = run of this lane.
+#pragma unroll 1
+            for (uint32_t kk = 0; kk < 2u; ++kk) {
+                const uint32_t p0 = kk ? pw[1][0] : pw[0][0], p1 = kk ? pw[1][1] : pw[0][1];
+                const uint32_t p2 = kk ? pw[1][2] : pw[0][2], p3 = kk ? pw[1][3] : pw[0][3];
+                constexpr int vblocks = S::fp4 && D == 256 ? 2 : 1;      // of a lane's run of D / 8
+                uint32_t vscale[2][vblocks];        // of the key pairs 2 t4, + 1 and 8 further
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < vblocks; ++j) {
+                        const uint32_t r = kk * 16u + i * 8 + 2 * t4;
+                        const uint32_t blk = S::fp4 ? (D == 64 ? g8 >> 1 : D == 128 ? g8 : g8 * 2 + j)
+                                                    : (D == 64 ? g8 >> 2 : D == 128 ? g8 >> 1 : g8);
+                        uint32_t w0 = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
+                        uint32_t w1 = *reinterpret_cast<const uint8_t *>(vsc + (r + 1) * S::blocks + blk);
+                        w0 = r < left ? w0 : 0u;
+                        w1 = r + 1 < left ? w1 : 0u;
+                        if (S::fp4)
+                            vscale[i][j] = e4m3x2_to_f16x2(w0 | (w1 << 8));
+                        else
+                            vscale[i][j] = half2_bits(__uint_as_float((uint32_t)max((int)(w0 + 134u) - (int)vtop, 0) << 23),
+                                                      __uint_as_float((uint32_t)max((int)(w1 + 134u) - (int)vtop, 0) << 23));
+                    }
                 constexpr int run = S::row / 8;          // bytes of a lane's run of columns
                 constexpr int words = run < 16 ? run / 4 : 4;
                 const char *vs = st + S::codes;
@@ -399,7 +430,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                     uint32_t w[4][words];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t r = kk * 16 + (i >> 1) * 8 + 2 * t4 + (i & 1);
+                        const uint32_t r = kk * 16u + (i >> 1) * 8 + 2 * t4 + (i & 1);
                         // of two pieces the lanes of odd g8 take the second first (banks)
                         const uint32_t off = r * S::row + g8 * run + (run == 32 ? (p ^ (g8 & 1u)) * 16u : 0u);
                         const char *q = vs + swizzle<S::row>(off);
@@ -426,8 +457,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 mma16816(acc[(p * words + i) * 8 + j], p0, p1, p2, p3,
-                                         hmul2_bits(b0[j & 1][j >> 1], vscale[2 * kk][blk]),
-                                         hmul2_bits(b1[j & 1][j >> 1], vscale[2 * kk + 1][blk]));
+                                         hmul2_bits(b0[j & 1][j >> 1], vscale[0][blk]),
+                                         hmul2_bits(b1[j & 1][j >> 1], vscale[1][blk]));
                         } else {
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
@@ -435,10 +466,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                                 e4m3x4_unpack(__byte_perm(w[0][i], w[1][i], u ? 0x7362 : 0x5140), x0, x1);
                                 e4m3x4_unpack(__byte_perm(w[2][i], w[3][i], u ? 0x7362 : 0x5140), y0, y1);
                                 const int j = (p * words + i) * 4 + u * 2;
-                                mma16816(acc[j], p0, p1, p2, p3, hmul2_bits(x0, vscale[2 * kk][0]),
-                                         hmul2_bits(y0, vscale[2 * kk + 1][0]));
-                                mma16816(acc[j + 1], p0, p1, p2, p3, hmul2_bits(x1, vscale[2 * kk][0]),
-                                         hmul2_bits(y1, vscale[2 * kk + 1][0]));
+                                mma16816(acc[j], p0, p1, p2, p3, hmul2_bits(x0, vscale[0][0]), hmul2_bits(y0, vscale[1][0]));
+                                mma16816(acc[j + 1], p0, p1, p2, p3, hmul2_bits(x1, vscale[0][0]), hmul2_bits(y1, vscale[1][0]));
                             }
                         }
                     }
