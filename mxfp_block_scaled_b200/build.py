@@ -15,7 +15,7 @@ SOURCES = ["api.cu", "nvfp4.cu", "weighted.cu", "mx.cu", "verify.cu", "noalloc.c
            "fp8.cu", "gemm.cu", "moe.cu", "linear.cu", "cache.cu", "attention.cu",
            "attention_rows.cu", "attention_tiles.cu"]
 HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_layer.h", "mxq_tma.cuh", "mxq_tcgen05.cuh", "mxq_mma.cuh",
-           "mxq_cache.cuh", "attention.cuh",
+           "mxq_cache.cuh", "mxq_cluster.cuh", "attention.cuh",
            "nvfp4_block.cuh", "mx_block.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -11,7 +11,8 @@
 
 namespace mxq {
 
-cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint32_t &ctas, cudaStream_t s);
+cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint64_t most_keys, uint32_t &ctas,
+                                  cudaStream_t s);
 cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t ctas, cudaStream_t s);
 
 namespace {
@@ -181,6 +182,7 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     a.part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + left_bytes());
     a.groupdiv = make_fastdiv(a.group);
     const uint32_t ctas = std::min<uint32_t>((uint32_t)sms, kMaxSms);
+    a.tiles = 0;
     const bool many = !few(a.group, c.max_new);
     // A lone sequence is one kernel's, whatever it has.
     const bool rows = !many || c.c.seqs > 1u;
@@ -196,9 +198,10 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
         a.over = 0;
         a.upto = many ? kFewRows : 0xFFFFFFFFu;
         a.min_steps = 8;
+        a.tiles = std::max(((many ? kFewRows : a.max_new * a.group) + kFewTile - 1) / kFewTile, 1u);
         uint32_t n = 0;         // at most kFewCtas
-        e = launch_attention_rows(a, fmt, dim, ctas, n, s);
-        if (e == cudaSuccess)
+        e = launch_attention_rows(a, fmt, dim, ctas, (uint64_t)c.c.width << c.c.page_log, n, s);
+        if (e == cudaSuccess && n > 0u)
             e = join<kFewTile>(a, dim, n, s);
     }
     return e;

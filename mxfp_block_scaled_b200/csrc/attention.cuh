@@ -39,6 +39,7 @@ struct AttArgs {
     uint32_t T, group, max_new;
     uint32_t over, upto;        // the sequences of this launch: those of over < rows <= upto
     uint32_t min_steps;         // of a CTA, where there are few
+    uint32_t tiles;             // of a sequence and head, at most
     float scale;                // softmax scale times log2(e)
     uint16_t *o;
     float *lse;

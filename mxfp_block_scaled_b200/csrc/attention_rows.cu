@@ -4,7 +4,10 @@
 // A tile is up to 16 rows of one sequence and key/value head, a step 32 keys;
 // attention.cuh divides them.  A CTA has 4 warps, which take turns of the steps of a
 // tile, each with its own running maximum, sum and output, joined at the end (in the
-// order of the warps).
+// order of the warps).  Where there are few tiles, a cluster of CTAs takes each instead
+// (CLUSTER), a run of its steps a CTA, and the parts are joined through the CTAs' shared
+// memory: nothing is divided and no second launch is needed, which is most of a short
+// call's time.
 //
 // Codes go from global memory to a warp's own two stages of shared memory by
 // cp.async and from there, decoded, into the operands of mma.sync m16n8k16 (f16,
@@ -23,6 +26,7 @@
 // layer's tokens, moe.cu); weights are rounded to f16's 11 bits, an eighth of the bf16
 // result's own step; scores, maxima, sums and outputs are fp32.
 #include "attention.cuh"
+#include "mxq_cluster.cuh"
 #include "mxq_mma.cuh"
 #include <algorithm>
 
@@ -33,6 +37,7 @@ namespace {
 constexpr uint32_t kRows = 16;          // rows of a tile
 constexpr uint32_t kKeys = 32, kLog = 5;    // keys of a step
 constexpr uint32_t kWarps = 4;
+constexpr uint32_t kClusterTurns = 8;       // of a warp, of a tile that a cluster takes
 
 template <int FMT, int D>
 struct Shape {
@@ -79,84 +84,60 @@ __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool
 
 } // namespace
 
-template <int FMT, int D>
+template <int FMT, int D, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kWarps, Shape<FMT, D>::most)
 attention_rows_kernel(const __grid_constant__ AttArgs a)
 {
     using S = Shape<FMT, D>;
+    using W = Walk<kRows, kLog>;
     constexpr uint32_t kThreads = 32 * kWarps;
     extern __shared__ __align__(128) char smem[];
     __shared__ Range range;
-    __shared__ Walk<kRows, kLog> walks[kWarps];
-    __shared__ float stat[2][kWarps][kRows];        // the warps' maxima and sums
+    __shared__ W walks[kWarps];
+    __shared__ __align__(16) float stat[2][kWarps][kRows];        // the warps' maxima and sums
+    __shared__ __align__(16) float joint[2][kRows];               // the CTA's
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3u;
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    find_range<Division<kRows, kLog>>(a, range);
-    if (tid == 0)
-        a.left[blockIdx.x].parts = 0u;
+    W &walk = walks[warp];
+    uint32_t rank = 0, ranks = 1;
+    bool more;
+    if (CLUSTER) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+        const uint32_t c = blockIdx.x / ranks, tile = c % a.tiles, ch = c / a.tiles;
+        W w;
+        w.b = ch / a.c.heads;
+        w.head = ch - w.b * a.c.heads;
+        w.rt = tile;
+        w.s = sequence(a, w.b);
+        if (tile >= W::Div::tiles(w.s))
+            return;             // all of the cluster
+        w.steps = W::Div::steps(a, w.s, tile);
+        w.keys = W::Div::keys(a, w.s, tile);
+        w.k0 = (uint32_t)((uint64_t)w.steps * rank / ranks);
+        w.k1 = (uint32_t)((uint64_t)w.steps * (rank + 1u) / ranks);
+        w.left = 0;
+        __syncwarp();
+        if (lane == 0)
+            walk = w;
+        __syncwarp();
+        more = true;
+    } else {
+        find_range<W::Div>(a, range);
+        if (tid == 0)
+            a.left[blockIdx.x].parts = 0u;
+        more = W::begin(walk, a, range);
+    }
 
     char *ring = smem + warp * S::ring;
     const uint32_t ring_s = smem_addr(ring);
     char *qs = smem + kWarps * S::ring;
-    Walk<kRows, kLog> &walk = walks[warp];
-    for (bool more = Walk<kRows, kLog>::begin(walk, a, range); more; more = Walk<kRows, kLog>::next(walk, a)) {
+    for (; more; more = !CLUSTER && W::next(walk, a)) {
         const uint32_t first = walk.s.first, rows = walk.s.rows, tile = walk.rt, head = walk.head, b = walk.b;
         const int64_t pos0 = walk.s.len - walk.s.n;           // position of the sequence's first new token
         const uint32_t k0 = walk.k0 << kLog, k1 = min(walk.k1 << kLog, walk.keys);
-
-        // Queries: f16 rows times their factors, one warp a row.
         __syncthreads();
-        float *factor = &stat[0][0][0];
-        for (uint32_t r = warp; r < kRows; r += kWarps) {
-            const uint32_t row = tile * kRows + r, i = fastdiv(row, a.groupdiv), h = row - i * a.group;
-            constexpr uint32_t per = D / 32;        // values of a lane
-            uint32_t x[per / 2], m = 0;
-            const uint16_t *src = a.q + (int64_t)(first + i) * a.q_stride + ((uint64_t)head * a.group + h) * D + lane * per;
-#pragma unroll
-            for (uint32_t j = 0; j < per / 2; ++j) {
-                x[j] = row < rows ? __ldg(reinterpret_cast<const uint32_t *>(src) + j) : 0u;
-                m = absmax_bf16x2(m, x[j]);
-            }
-            m = __reduce_max_sync(0xFFFFFFFFu, fold_halves(m)) << 16;
-            const float f = row_factor(m);
-#pragma unroll
-            for (uint32_t j = 0; j < per / 2; ++j)
-                *reinterpret_cast<uint32_t *>(qs + r * S::q_pitch + (lane * per + 2 * j) * 2) =
-                    half2_bits(bf16_lo(x[j]) * f, bf16_hi(x[j]) * f);
-            if (lane == 0)
-                factor[r] = 1.0f / f;
-        }
-        __syncthreads();
-        // Of this lane's two rows: log2-scale factor and last key.
-        float fq[2];
-        int64_t pos[2];         // rows past the sequence's see every key, and are not stored
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t row = tile * kRows + g8 + 8 * i;
-            fq[i] = factor[g8 + 8 * i] * a.scale;
-            pos[i] = row < rows ? pos0 + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
-        }
-        // This lane's run of a query: values [t4 D / 4, + D / 4) of rows g8 and g8 + 8.
-        uint2 q0[S::q_regs ? D / 16 : 1], q1[S::q_regs ? D / 16 : 1];
-        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2), *qb = qa + 8 * S::q_pitch;
-        if (S::q_regs) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                q0[i] = lds64(qa + i * 8);
-                q1[i] = lds64(qb + i * 8);
-            }
-        }
-        float kfac = 1.0f;
-        if (FMT == MXQ_FMT_NVFP4)
-            kfac = __ldg(a.c.k_s2 + head);
-
-        float acc[D / 8][4];
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-        float mx[2] = {kLowest, kLowest}, sum[2] = {0.0f, 0.0f};
-
         // Pages of a turn's keys, as the table has them: 32 keys lie on one page, or on two of 16
         // tokens.  Looked up a turn before the copies are made, which are a turn ahead themselves.
         const bool short_pages = a.c.page_log == 4u;
@@ -202,8 +183,6 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             cp_commit();
         };
 
-        // The loops over parts of a turn are rolled: cold instruction caches are what a short
-        // call waits for, and the code of a whole turn would not stay in them.
         constexpr uint32_t stride = kWarps * kKeys;
         uint32_t key = k0 + warp * kKeys, slot = 0, page[2], ahead[2];
         look(key, page);
@@ -211,6 +190,69 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         bool first_turn = true;
         if (key < k1)
             issue(key, 0, page);
+
+        // Queries: f16 rows times their factors, a warp's rows at the same time.
+        float *factor = &stat[0][0][0];
+        {
+            constexpr uint32_t per = D / 32, mine = kRows / kWarps;     // values of a lane, rows of a warp
+            uint32_t x[mine][per / 2];
+#pragma unroll
+            for (uint32_t n = 0; n < mine; ++n) {
+                const uint32_t row = tile * kRows + warp + n * kWarps, i = fastdiv(row, a.groupdiv), h = row - i * a.group;
+                const uint16_t *src = a.q + (int64_t)(first + i) * a.q_stride + ((uint64_t)head * a.group + h) * D + lane * per;
+#pragma unroll
+                for (uint32_t j = 0; j < per / 2; ++j)
+                    x[n][j] = row < rows ? __ldg(reinterpret_cast<const uint32_t *>(src) + j) : 0u;
+            }
+#pragma unroll
+            for (uint32_t n = 0; n < mine; ++n) {
+                const uint32_t r = warp + n * kWarps;
+                uint32_t m = 0;
+#pragma unroll
+                for (uint32_t j = 0; j < per / 2; ++j)
+                    m = absmax_bf16x2(m, x[n][j]);
+                m = __reduce_max_sync(0xFFFFFFFFu, fold_halves(m)) << 16;
+                const float f = row_factor(m);
+#pragma unroll
+                for (uint32_t j = 0; j < per / 2; ++j)
+                    *reinterpret_cast<uint32_t *>(qs + r * S::q_pitch + (lane * per + 2 * j) * 2) =
+                        half2_bits(bf16_lo(x[n][j]) * f, bf16_hi(x[n][j]) * f);
+                if (lane == 0)
+                    factor[r] = 1.0f / f;
+            }
+        }
+        __syncthreads();
+        // Of this lane's two rows: log2-scale factor and last key.
+        float fq[2];
+        int64_t pos[2];         // rows past the sequence's see every key, and are not stored
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t row = tile * kRows + g8 + 8 * i;
+            fq[i] = factor[g8 + 8 * i] * a.scale;
+            pos[i] = row < rows ? pos0 + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
+        }
+        // This lane's run of a query: values [t4 D / 4, + D / 4) of rows g8 and g8 + 8.
+        uint2 q0[S::q_regs ? D / 16 : 1], q1[S::q_regs ? D / 16 : 1];
+        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2), *qb = qa + 8 * S::q_pitch;
+        if (S::q_regs) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                q0[i] = lds64(qa + i * 8);
+                q1[i] = lds64(qb + i * 8);
+            }
+        }
+        float kfac = 1.0f;
+        if (FMT == MXQ_FMT_NVFP4)
+            kfac = __ldg(a.c.k_s2 + head);
+
+        float acc[D / 8][4];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+        float mx[2] = {kLowest, kLowest}, sum[2] = {0.0f, 0.0f};
+
+        // The loops over parts of a turn are rolled: cold instruction caches are what a short
+        // call waits for, and the code of a whole turn would not stay in them.
 #pragma unroll 1
         for (; key < k1; key += stride, slot ^= 1u) {
             page[0] = ahead[0];
@@ -513,9 +555,22 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         const float vfac = FMT == MXQ_FMT_NVFP4 ? __ldg(a.c.v_s2 + head) : 1.0f;
         const bool whole = walk.whole();
         float *part = part_of<kRows, D>(a, blockIdx.x, walk.k0 == 0u);
+        auto put = [&](uint32_t r, uint32_t d, float m, float l, float4 v) {        // 4 columns of a finished row
+            const uint32_t row = tile * kRows + r, it = fastdiv(row, a.groupdiv), h = head * a.group + row - it * a.group;
+            const uint64_t out = (uint64_t)(first + it) * (a.c.heads * a.group) + h;
+            const float f = l == 0.0f ? 0.0f : vfac / l;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+            *reinterpret_cast<uint2 *>(a.o + out * D + d) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            if (d == 0 && a.lse)
+                a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        };
+        const float *all = reinterpret_cast<const float *>(smem);
+        float *sum4 = reinterpret_cast<float *>(smem);      // CLUSTER: the CTA's outputs, over the first warp's
+#pragma unroll 1
         for (uint32_t i = tid; i < kRows * (D / 4); i += kThreads) {
-            const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, row = tile * kRows + r;
-            if (row >= rows)
+            const uint32_t r = i / (D / 4), d = i % (D / 4) * 4;
+            if (tile * kRows + r >= rows)
                 continue;
             float m = stat[0][0][r];
 #pragma unroll
@@ -526,28 +581,54 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
             for (uint32_t w = 0; w < kWarps; ++w) {
                 l = fmaf(stat[1][w][r], ex2(stat[0][w][r] - m), l);
-                const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + w * (S::outs / 4) + r * (D + 4) + d);
+                const float4 x = *reinterpret_cast<const float4 *>(all + w * (S::outs / 4) + r * (D + 4) + d);
                 v.x += x.x;
                 v.y += x.y;
                 v.z += x.z;
                 v.w += x.w;
             }
-            if (!whole) {
+            if (CLUSTER && ranks > 1u) {
+                *reinterpret_cast<float4 *>(sum4 + r * (D + 4) + d) = v;        // read by this thread alone
+                if (d == 0) {
+                    joint[0][r] = m;
+                    joint[1][r] = l;
+                }
+            } else if (CLUSTER || whole)
+                put(r, d, m, l, v);
+            else {
                 *reinterpret_cast<float4 *>(part + r * D + d) = v;
                 if (d == 0)
                     *reinterpret_cast<float2 *>(part + kRows * D + r * 2) = make_float2(m, l);
-                continue;
             }
-            const uint32_t it = fastdiv(row, a.groupdiv), h = head * a.group + row - it * a.group;
-            const uint64_t out = (uint64_t)(first + it) * (a.c.heads * a.group) + h;
-            const float f = l == 0.0f ? 0.0f : vfac / l;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi2 = __floats2bfloat162_rn(v.z * f, v.w * f);
-            *reinterpret_cast<uint2 *>(a.o + out * D + d) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi2));
-            if (d == 0 && a.lse)
-                a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        if (tid == 0 && walk.k0 == 0u && !whole) {
+        if (CLUSTER && ranks > 1u) {
+            cluster_sync_all();
+            // Each CTA joins its share of the columns, in the order of the CTAs.
+#pragma unroll 1
+            for (uint32_t i = rank * kThreads + tid; i < kRows * (D / 4); i += ranks * kThreads) {
+                const uint32_t r = i / (D / 4), d = i % (D / 4) * 4;
+                if (tile * kRows + r >= rows)
+                    continue;
+                float m = kLowest;
+                for (uint32_t c = 0; c < ranks; ++c)
+                    m = fmaxf(m, peer_f(&joint[0][r], c));
+                float l = 0.0f;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (uint32_t c = 0; c < ranks; ++c) {
+                    const float f = ex2(peer_f(&joint[0][r], c) - m);
+                    const float4 x = peer_f4(reinterpret_cast<const float4 *>(sum4 + r * (D + 4) + d), c);
+                    l = fmaf(peer_f(&joint[1][r], c), f, l);
+                    v.x = fmaf(x.x, f, v.x);
+                    v.y = fmaf(x.y, f, v.y);
+                    v.z = fmaf(x.z, f, v.z);
+                    v.w = fmaf(x.w, f, v.w);
+                }
+                put(r, d, m, l, v);
+            }
+            cluster_sync_all();         // every CTA's sums have been read
+        }
+        if (!CLUSTER && tid == 0 && walk.k0 == 0u && !whole) {
             Unfinished u = {};
             u.first = first;
             u.row0 = tile * kRows;
@@ -566,24 +647,60 @@ template <int FMT, int D>
 cudaError_t run(const AttArgs &a, uint32_t sms, uint32_t &ctas, cudaStream_t s)
 {
     using S = Shape<FMT, D>;
-    const auto k = attention_rows_kernel<FMT, D>;
+    const auto k = attention_rows_kernel<FMT, D, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::all);
     ctas = sms * S::fit;
     return e != cudaSuccess ? e : launch_dependent(k, dim3(ctas), 32 * kWarps, S::all, s, a);
 }
 
+// Clusters of 1 to 8 CTAs, one a tile, where they fit the card at once.  most_keys: what a
+// sequence can have.
+template <int FMT, int D>
+cudaError_t run_clusters(const AttArgs &a, uint32_t sms, uint64_t most_keys, bool &taken, cudaStream_t s)
+{
+    using S = Shape<FMT, D>;
+    const uint64_t clusters = (uint64_t)a.c.seqs * a.c.heads * a.tiles, room = (uint64_t)sms * S::fit;
+    uint32_t size = 1;
+    while (size < 8u && clusters * size * 2u <= room && (uint64_t)size * kWarps * kKeys < most_keys)
+        size *= 2u;
+    // turns of a warp, at most: beyond these the work is divided evenly
+    taken = clusters <= room && most_keys <= (uint64_t)size * kWarps * kKeys * kClusterTurns;
+    if (!taken)
+        return cudaSuccess;
+    const auto k = attention_rows_kernel<FMT, D, true>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::all);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid((unsigned)(clusters * size));
+    return size == 1   ? launch_dependent<1>(k, grid, 32 * kWarps, S::all, s, a)
+           : size == 2 ? launch_dependent<2>(k, grid, 32 * kWarps, S::all, s, a)
+           : size == 4 ? launch_dependent<4>(k, grid, 32 * kWarps, S::all, s, a)
+                       : launch_dependent<8>(k, grid, 32 * kWarps, S::all, s, a);
+}
+
+template <int FMT, int D>
+cudaError_t either(const AttArgs &a, uint32_t sms, uint64_t most_keys, uint32_t &ctas, cudaStream_t s)
+{
+    bool taken = false;
+    ctas = 0;
+    const cudaError_t e = run_clusters<FMT, D>(a, sms, most_keys, taken, s);
+    return taken || e != cudaSuccess ? e : run<FMT, D>(a, sms, ctas, s);
+}
+
 } // namespace
 
-// `ctas`: of the launch, each with its entry in `left`.
-cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint32_t &ctas, cudaStream_t s)
+// `ctas`: of a launch that leaves unfinished tiles, each with its entry in `left`; 0 of
+// one that does not.
+cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint64_t most_keys, uint32_t &ctas,
+                                  cudaStream_t s)
 {
     if (fmt == MXQ_FMT_NVFP4)
-        return dim == 64    ? run<MXQ_FMT_NVFP4, 64>(a, sms, ctas, s)
-               : dim == 128 ? run<MXQ_FMT_NVFP4, 128>(a, sms, ctas, s)
-                            : run<MXQ_FMT_NVFP4, 256>(a, sms, ctas, s);
-    return dim == 64    ? run<MXQ_FMT_MXFP8, 64>(a, sms, ctas, s)
-           : dim == 128 ? run<MXQ_FMT_MXFP8, 128>(a, sms, ctas, s)
-                        : run<MXQ_FMT_MXFP8, 256>(a, sms, ctas, s);
+        return dim == 64    ? either<MXQ_FMT_NVFP4, 64>(a, sms, most_keys, ctas, s)
+               : dim == 128 ? either<MXQ_FMT_NVFP4, 128>(a, sms, most_keys, ctas, s)
+                            : either<MXQ_FMT_NVFP4, 256>(a, sms, most_keys, ctas, s);
+    return dim == 64    ? either<MXQ_FMT_MXFP8, 64>(a, sms, most_keys, ctas, s)
+           : dim == 128 ? either<MXQ_FMT_MXFP8, 128>(a, sms, most_keys, ctas, s)
+                        : either<MXQ_FMT_MXFP8, 256>(a, sms, most_keys, ctas, s);
 }
 
 } // namespace mxq

@@ -43,6 +43,7 @@
 // warp leave theirs, on that way and on the ordinary one, behind the last of what
 // they have started (bounded waits too): whichever role gives up, and when, no
 // copy or product is in flight where TMEM is freed and the CTA ends.
+#include "mxq_cluster.cuh"
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
 #include "mxq.h"
@@ -621,25 +622,6 @@ __device__ __forceinline__ bool sum_item(const TileArgs &p, const CUtensorMap *m
     else
         store_sums<W / 2, Out>(acc, buf, mc, m0, n0, p, lane);
     return true;
-}
-
-// All threads of the cluster; shared memory written before is seen behind it.
-__device__ __forceinline__ void cluster_sync_all()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// 16 bytes of the shared memory of CTA `rank` of the cluster, at this CTA's address `p`.
-__device__ __forceinline__ float4 peer_f4(const float4 *p, uint32_t rank)
-{
-    uint32_t at;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
 }
 
 } // namespace
