@@ -50,4 +50,28 @@ __device__ __forceinline__ uint32_t mx_quantize_block(const uint32_t (&w)[16], u
     return (uint32_t)(e + 127);
 }
 
+// The same of an MXFP8 block that two neighbouring lanes hold, 8 words each, both of them
+// together: each has its 16 codes, and both the scale byte and `amax`.
+__device__ __forceinline__ uint32_t mx_quantize_half(uint4 v0, uint4 v1, uint32_t &amax, uint4 &o)
+{
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = absmax_bf16x2(m, w[j]);
+    m = fold_halves(m);
+    amax = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    const int e = mx_exponent<MXQ_FMT_MXFP8>(amax);
+    const float sc = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e, normal
+    const float2 sc2 = make_float2(sc, sc);
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 y = __fmul2_rn(make_float2(bf16_lo(w[j]), bf16_hi(w[j])), sc2);
+        c[j] = e4m3x2(y.x, y.y);
+    }
+    o = make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+    return (uint32_t)(e + 127);
+}
+
 } // namespace mxq

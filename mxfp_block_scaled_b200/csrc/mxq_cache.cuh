@@ -12,18 +12,33 @@
 
 namespace mxq {
 
-// Number of the sequence that row `row` belongs to, by bisection of cu (which
-// ascends; of any other the result is some number below seqs, or seqs).
+// Number of the sequence that row `row` belongs to (cu ascends; of any other the
+// result is some number below seqs, or seqs).  All lanes of a warp call, with rows of
+// their own that do not descend.  The warp looks for the first lane's row together, 32
+// places of cu at a time, since a bisection is a chain of as many loads as log2(seqs);
+// rows of sequences further on are looked for by bisection, from there.
 __device__ __forceinline__ uint32_t find_sequence(const CacheView &c, uint32_t row)
 {
-    uint32_t lo = 0, hi = c.seqs;       // the last b with cu[b] <= row is in [lo, hi)
-    while (hi - lo > 1u) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (__ldg(c.cu + mid) <= (int64_t)row)
-            lo = mid;
-        else
-            hi = mid;
+    const uint32_t lane = threadIdx.x & 31u;
+    const int64_t want = __shfl_sync(0xFFFFFFFFu, row, 0);
+    uint32_t lo = 0, n = c.seqs;        // the last b with cu[b] <= want is in [lo, lo + n)
+    while (n > 1u) {
+        const uint32_t step = (n + 31u) / 32u, at = lo + lane * step;
+        const bool below = lane * step < n && __ldg(c.cu + at) <= want;
+        const uint32_t k = __popc(__ballot_sync(0xFFFFFFFFu, below));
+        const uint32_t skip = k ? (k - 1u) * step : 0u;
+        lo += skip;
+        n = min(step, n - skip);
     }
+    uint32_t hi = c.seqs;
+    if (__ldg(c.cu + lo + 1) <= (int64_t)row)
+        while (hi - lo > 1u) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (__ldg(c.cu + mid) <= (int64_t)row)
+                lo = mid;
+            else
+                hi = mid;
+        }
     return __ldg(c.cu + lo) <= (int64_t)row && (int64_t)row < __ldg(c.cu + lo + 1) ? lo : c.seqs;
 }
 
@@ -56,7 +71,7 @@ __device__ __forceinline__ uint32_t find_page(const CacheView &c, uint32_t b, ui
 
 // Number of the (page, head, token) row of codes that holds row `row`'s token;
 // false where the row has no place: behind the last sequence, before the
-// sequence's first position, or on an invalid page.
+// sequence's first position, or on an invalid page.  All lanes of a warp call, as above.
 __device__ __forceinline__ bool find_place(const CacheView &c, uint32_t row, uint64_t &at)
 {
     const uint32_t b = find_sequence(c, row);
