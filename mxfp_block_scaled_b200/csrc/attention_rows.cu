@@ -76,12 +76,6 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t off)
     return off ^ (m << 4);
 }
 
-// 16 bytes (zeros where `ok` is 0) into shared memory.
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
-}
-
 } // namespace
 
 template <int FMT, int D, bool CLUSTER>

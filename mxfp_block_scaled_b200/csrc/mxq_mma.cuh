@@ -27,6 +27,12 @@ __device__ __forceinline__ uint32_t lds32(const char *p) { return *reinterpret_c
 __device__ __forceinline__ uint2 lds64(const char *p) { return *reinterpret_cast<const uint2 *>(p); }
 __device__ __forceinline__ uint4 lds128(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
 
+// 16 bytes (zeros where `ok` is 0) into shared memory.
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
+
 // c += A B: A 16 rows x 16 k (f16), B 16 k x 8 columns (f16).
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
@@ -83,6 +89,22 @@ __device__ __forceinline__ uint32_t low2(uint32_t h)
 {
     const __half2 r = __low2half2(*reinterpret_cast<const __half2 *>(&h));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t high2(uint32_t h)
+{
+    const __half2 r = __high2half2(*reinterpret_cast<const __half2 *>(&h));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// c = A B of the same.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Power of two that brings a magnitude of these fp32 bits into [2^14, 2^15),
