@@ -29,6 +29,7 @@ namespace mxq {
 
 namespace {
 
+constexpr uint32_t kOwnTurns = 6;       // pieces of 8 values of a thread, of tokens that every CTA brings into f16 itself
 constexpr uint32_t kMostWarps = 16, kMostSlots = 3, kMostCap = 32;
 // One chunk in shared memory: 16 rows of 128 bytes of codes, and the rows' scales, 16 apart.
 // The fragment loads touch every bank once: of 4 bytes (MX) with rows 144 apart, of 16
@@ -197,30 +198,34 @@ linear_kernel(const Args a)
         issue();
     if (a.x) {
         const uint32_t pieces = ntok * (a.width / 8u);
-        auto load = [&](uint32_t i, uint32_t &r, uint32_t &k) {
-            r = fastdiv(i, a.rowdiv);
-            k = (i - r * (a.width / 8u)) * 8u;
-            const uint16_t *src = a.x + (uint64_t)(tok0 + r) * a.K + k;
-            return k < a.K ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        uint32_t r, k;
+        uint4 v[kOwnTurns];         // a thread's pieces
+        uint32_t row[kOwnTurns], k[kOwnTurns];
+#pragma unroll
+        for (uint32_t n = 0; n < kOwnTurns; ++n)
+            if (n * blockDim.x < pieces) {
+                const uint32_t i = min(n * blockDim.x + tid, pieces - 1u);
+                row[n] = fastdiv(i, a.rowdiv);
+                k[n] = (i - row[n] * (a.width / 8u)) * 8u;
+                const uint16_t *src = a.x + (uint64_t)(tok0 + row[n]) * a.K + k[n];
+                v[n] = k[n] < a.K ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0u, 0u, 0u, 0u);
+            }
         __syncthreads();            // xmax
-#pragma unroll 4
-        for (uint32_t i0 = warp * 32u; i0 < pieces; i0 += blockDim.x) {
-            uint32_t m = largest8(load(min(i0 + lane, pieces - 1u), r, k));
-            if (__all_sync(0xFFFFFFFFu, r == __shfl_sync(0xFFFFFFFFu, r, 0))) {
-                m = __reduce_max_sync(0xFFFFFFFFu, m);
-                if (lane == 0)
-                    atomicMax(&xmax[r], m);
-            } else
-                atomicMax(&xmax[r], m);
-        }
+#pragma unroll
+        for (uint32_t n = 0; n < kOwnTurns; ++n)
+            if (n * blockDim.x < pieces) {
+                uint32_t m = largest8(v[n]);
+                if (__all_sync(0xFFFFFFFFu, row[n] == __shfl_sync(0xFFFFFFFFu, row[n], 0))) {
+                    m = __reduce_max_sync(0xFFFFFFFFu, m);
+                    if (lane == 0)
+                        atomicMax(&xmax[row[n]], m);
+                } else
+                    atomicMax(&xmax[row[n]], m);
+            }
         __syncthreads();
-#pragma unroll 4
-        for (uint32_t i = tid; i < pieces; i += blockDim.x) {
-            const uint4 v = load(i, r, k);
-            stage8<FMT>(xs + r * a.xstride, k, v, row_factor(xmax[r] << 16));
-        }
+#pragma unroll
+        for (uint32_t n = 0; n < kOwnTurns; ++n)
+            if (n * blockDim.x + tid < pieces)
+                stage8<FMT>(xs + row[n] * a.xstride, k[n], v[n], row_factor(xmax[row[n]] << 16));
         if (tid < ntok) {
             const uint32_t m = xmax[tid] << 16;
             xinv[tid] = 1.0f / row_factor(m);
@@ -390,7 +395,6 @@ linear_kernel(const Args a)
 namespace {
 
 constexpr uint32_t kSmemMax = 226 * 1024;       // dynamic
-constexpr uint32_t kOwnPieces = 1024;   // of 8 values: tokens that every CTA brings into f16 itself
 
 template <int FMT, int NT, typename Out>
 cudaError_t go(const Args &a, dim3 grid, uint32_t warps, size_t smem, cudaStream_t s)
@@ -445,9 +449,9 @@ cudaError_t plan(const LinearArgs &l, int out_f32, int sms, cudaStream_t s)
     while (a.kslog < 3 && warps % (2u << a.kslog) == 0 && (2u << a.kslog) <= a.chunks &&
            ((uint64_t)a.tiles * 2 << a.kslog) <= (uint64_t)ctas * warps)
         ++a.kslog;
-    // A CTA's own work on the tokens costs less than another kernel before it where they
-    // are few.
-    a.x = a.cap * (a.width / 8) <= kOwnPieces ? l.x : nullptr;
+    // A CTA's own work on the tokens costs less than another kernel before it where a
+    // thread can hold its share.
+    a.x = a.cap * (a.width / 8) <= kOwnTurns * 32 * warps ? l.x : nullptr;
     cudaError_t e = cudaSuccess;
     if (!a.x)
         e = launch_dependent(linear_rows_kernel<FMT>, dim3(a.T), 256, 0, s, l.x, a.K, a.width, l.xh, l.xf, l.status);

@@ -480,6 +480,7 @@ class Cache:
         self.fmt, self.pages, self.kv_heads, self.page_tokens, self.head_dim = fmt, pages, heads, tokens, dim
         self.struct = _CacheStruct(*[None if t is None else t.data_ptr() for t in self.tensors], pages, heads, tokens,
                                    dim, FMT[fmt])
+        self._ref, self._index = ctypes.byref(self.struct), k_codes.get_device()
 
     @classmethod
     def empty(cls, pages, kv_heads, page_tokens, head_dim, fmt="mxfp8", k_s2=None, v_s2=None, device="cuda"):
@@ -494,12 +495,18 @@ def _batch(cu, lens, table, seqs, width, dev):
             _buf("table", table, 4 * seqs * width, dev), seqs, width)
 
 
+def _cache_device(cache):
+    if cache._index < 0:
+        raise ValueError("libmxq takes device tensors")
+    return cache._index
+
+
 def _rows(name, t, stride, T, values, dev):
     """Address of T rows of `values` values, `stride` values apart (the last dimensions contiguous)."""
     if t is None:
         return None
-    if T > 0 and (t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
-                  < ((T - 1) * stride + values) * t.element_size()):
+    size = t.itemsize
+    if T > 0 and t.untyped_storage().nbytes() < (t.storage_offset() + (T - 1) * stride + values) * size:
         raise ValueError("%s does not hold %d rows of %d values, %d apart" % (name, T, values, stride))
     if t.get_device() != dev:
         raise ValueError("%s is not on the device of the first tensor" % name)
@@ -509,18 +516,18 @@ def _rows(name, t, stride, T, values, dev):
 def mxq_cache_write(cache, k, k_stride, v, v_stride, T, cu, lens, table, seqs, width, mode, status, stream=None):
     """k and v: bf16 tensors whose row t starts t * stride values behind their first
     value and holds kv_heads * head_dim contiguous ones."""
-    dev, n = _device(cache.k_codes), cache.kv_heads * cache.head_dim
+    dev, n = _cache_device(cache), cache.kv_heads * cache.head_dim
     rc = _enqueue(load().mxq_cache_write,
-                  (cache.struct, _rows("k", k, k_stride, T, n, dev), k_stride, _rows("v", v, v_stride, T, n, dev), v_stride,
+                  (cache._ref, _rows("k", k, k_stride, T, n, dev), k_stride, _rows("v", v, v_stride, T, n, dev), v_stride,
                    T, *_batch(cu, lens, table, seqs, width, dev), SCALE_MODE[mode], _buf("status", status, 4, dev)),
                   dev, stream)
     _check("mxq_cache_write", rc)
 
 
 def mxq_cache_read(cache, cu, lens, table, seqs, width, T, k, v, status, stream=None):
-    dev, n = _device(cache.k_codes), 2 * T * cache.kv_heads * cache.head_dim
+    dev, n = _cache_device(cache), 2 * T * cache.kv_heads * cache.head_dim
     rc = _enqueue(load().mxq_cache_read,
-                  (cache.struct, *_batch(cu, lens, table, seqs, width, dev), T, _buf("k", k, n, dev),
+                  (cache._ref, *_batch(cu, lens, table, seqs, width, dev), T, _buf("k", k, n, dev),
                    _buf("v", v, n, dev), _buf("status", status, 4, dev)), dev, stream)
     _check("mxq_cache_read", rc)
 
@@ -528,9 +535,9 @@ def mxq_cache_read(cache, cu, lens, table, seqs, width, T, k, v, status, stream=
 def mxq_cache_attention(cache, q, q_stride, T, heads, cu, lens, table, seqs, width, max_new, scale, o, lse, status,
                         workspace, stream=None):
     """q: bf16, row t `t * q_stride` values behind the first, heads * head_dim contiguous ones each."""
-    dev, n = _device(cache.k_codes), heads * cache.head_dim
+    dev, n = _cache_device(cache), heads * cache.head_dim
     rc = _enqueue(load().mxq_cache_attention,
-                  (cache.struct, _rows("q", q, q_stride, T, n, dev), q_stride, T, heads,
+                  (cache._ref, _rows("q", q, q_stride, T, n, dev), q_stride, T, heads,
                    *_batch(cu, lens, table, seqs, width, dev), max_new, scale, _buf("o", o, 2 * T * n, dev),
                    _buf("lse", lse, 4 * T * heads, dev), _buf("status", status, 4, dev),
                    _buf("workspace", workspace, 0, dev), _nbytes(workspace)), dev, stream)
