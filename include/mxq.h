@@ -644,8 +644,8 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  * repeated calls give the same bits (the order of the sums follows from the sizes,
  * the lengths of the batch's sequences and the number of SMs).  MXFP8: exact
  * while the block maxima of neighbouring tokens lie within 2^22 of one another (what
- * is smaller is off by at most 2^-41 of the largest); values (v) below 2^-100 count
- * as zeros. */
+ * is smaller is off by at most 2^-41 of the largest); blocks of keys or values whose
+ * largest element is below 2^-100 lose bits, down to zero. */
 MXQ_API mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride,
                                        int64_t T, int64_t heads, const int32_t *cu, const int32_t *lens,
                                        const int32_t *table, int64_t seqs, int64_t width, int64_t max_new,

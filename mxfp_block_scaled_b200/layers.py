@@ -18,7 +18,9 @@ Argument marshalling only; every step runs in libmxq.so.
 * A converted layer is run as it is stored: routed_forward reads the
   experts' codes (a few tokens), fp8_linear quantizes the tokens and
   multiplies in block FP8 (projections and shared experts kept in that
-  format).
+  format).  projection_forward does the same for one matrix in any of the
+  formats, and attention_forward takes a step over a quantized key/value
+  cache: the new tokens are written, then attend to what the cache holds.
 """
 import torch
 
@@ -89,6 +91,43 @@ def fp8_linear(x, w_q, out="bf16", stream=None):
     t = mxq.quantize_fp8(x, stream=stream)
     return mxq.gemm_fp8(t["codes"], t["scales"], w_q["codes"], w_q["scales"], out, status=t["status"],
                         stream=stream)
+
+
+def quantize_projection(w, fmt="nvfp4", mode="four_six", stream=None):
+    """Quantize one matrix w [N, K] (an attention projection, a shared expert's
+    matrix, the output head) for projection_forward.  fmt: "nvfp4" (4/6-optimal or
+    RTN block scales), "mxfp4", "mxfp8" or "fp8_block" (128 x 128).  Returns a dict
+    codes, scales (s2 for "nvfp4"), status, fmt."""
+    if fmt == "nvfp4":
+        q = mxq.quantize_nvfp4(w[None], mode=mode, with_mbits=False, stream=stream)
+        q.update(codes=q["codes"][0], scales=q["scales"][0])
+    elif fmt == "fp8_block":
+        q = mxq.quantize_fp8(w, 128, stream=stream)
+    else:
+        q = mxq.quantize_mx(w, fmt, stream=stream)
+    q["fmt"] = fmt
+    return q
+
+
+def projection_forward(w_q, x, out="bf16", workspace=None, stream=None):
+    """x W^T over a quantize_projection result as it is stored.  x: bf16 [T, K]; the
+    4-bit and MX formats are for a few tokens (mxq.linear, which takes `workspace`),
+    block FP8 for any number (fp8_linear).  Returns a dict with y [T, N] and status."""
+    if w_q["fmt"] == "fp8_block":
+        r = fp8_linear(x, w_q, out=out, stream=stream)
+        return {"y": r["c"], "status": r["status"]}
+    return mxq.linear(x, w_q, w_q["fmt"], out=out, workspace=workspace, stream=stream)
+
+
+def attention_forward(cache, q, k, v, cu, lens, table, max_new, scale=None, mode="rtn", workspace=None, stream=None):
+    """A step of attention over a quantized cache (mxq.Cache): the new tokens' keys and
+    values k, v [T, kv_heads, head_dim] are quantized into their places, then their
+    queries q [T, heads, head_dim] attend to every token of their sequence up to their
+    own, read back from the cache as they were quantized.  cu, lens, table, max_new: the
+    batch (mxq.cache_attention).  Returns dict o, lse, status."""
+    status = mxq.cache_write(cache, k, v, cu, lens, table, mode=mode, stream=stream)
+    return mxq.cache_attention(cache, q, cu, lens, table, max_new, scale=scale, workspace=workspace, status=status,
+                               stream=stream)
 
 
 def unstack_expert(layer_q, e):
