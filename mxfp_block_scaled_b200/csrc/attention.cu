@@ -11,8 +11,8 @@
 
 namespace mxq {
 
-cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint64_t most_keys, uint32_t &ctas,
-                                  cudaStream_t s);
+cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t rows, uint32_t sms, uint64_t most_keys,
+                                  uint32_t &ctas, cudaStream_t s);
 cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t ctas, cudaStream_t s);
 
 namespace {
@@ -20,11 +20,11 @@ namespace {
 // Sequences of up to this many rows are attention_rows.cu's.
 constexpr uint32_t kFewRows = 64;
 constexpr uint32_t kMaxSms = 160;           // the division uses no more (workspace)
-constexpr uint32_t kFewCtas = 4 * kMaxSms;  // of attention_rows.cu
-constexpr uint32_t kFewTile = 16, kTile = 256;
+constexpr uint32_t kFewCtas = 5 * kMaxSms;  // of attention_rows.cu: 5 an SM with tiles of 8 rows, 4 with
+constexpr uint32_t kFewTile = 16, kTile = 256;      // tiles of 16, whose parts are then the larger
 
 size_t left_bytes() { return kFewCtas * sizeof(Unfinished); }
-size_t rows_part_bytes(int64_t dim) { return (size_t)kFewCtas * 2 * kFewTile * (size_t)(dim + 2) * 4; }
+size_t rows_part_bytes(int64_t dim) { return (size_t)(4 * kMaxSms) * 2 * kFewTile * (size_t)(dim + 2) * 4; }
 size_t tiles_part_bytes(int64_t dim) { return (size_t)kMaxSms * 2 * (dim == 256 ? 128 : kTile) * (size_t)(dim + 2) * 4; }
 bool few(int64_t group, int64_t max_new) { return group * max_new <= (int64_t)kFewRows; }
 
@@ -198,11 +198,13 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
         a.over = 0;
         a.upto = many ? kFewRows : 0xFFFFFFFFu;
         a.min_steps = 8;
-        a.tiles = std::max(((many ? kFewRows : a.max_new * a.group) + kFewTile - 1) / kFewTile, 1u);
+        // tiles of 8 rows where no sequence has more, else of 16
+        const uint32_t most = std::max(many ? kFewRows : a.max_new * a.group, 1u), rows_of = most <= 8u ? 8u : kFewTile;
+        a.tiles = (most + rows_of - 1) / rows_of;
         uint32_t n = 0;         // at most kFewCtas
-        e = launch_attention_rows(a, fmt, dim, ctas, (uint64_t)c.c.width << c.c.page_log, n, s);
+        e = launch_attention_rows(a, fmt, dim, rows_of, ctas, (uint64_t)c.c.width << c.c.page_log, n, s);
         if (e == cudaSuccess && n > 0u)
-            e = join<kFewTile>(a, dim, n, s);
+            e = rows_of == 8u ? join<8>(a, dim, n, s) : join<kFewTile>(a, dim, n, s);
     }
     return e;
 }

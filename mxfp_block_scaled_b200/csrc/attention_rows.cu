@@ -34,27 +34,28 @@ namespace mxq {
 
 namespace {
 
-constexpr uint32_t kRows = 16;          // rows of a tile
 constexpr uint32_t kKeys = 32, kLog = 5;    // keys of a step
 constexpr uint32_t kWarps = 4;
 constexpr uint32_t kClusterTurns = 8;       // of a warp, of a tile that a cluster takes
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 struct Shape {
+    static constexpr uint32_t R = 8 * NT;                       // rows of a tile
     static constexpr bool fp4 = FMT == MXQ_FMT_NVFP4;
     static constexpr uint32_t row = fp4 ? D / 2 : D;            // bytes of a key's codes
     static constexpr uint32_t blocks = fp4 ? D / 16 : D / 32;   // and of its scales
     static constexpr uint32_t codes = kKeys * row, scales = kKeys * blocks;
     static constexpr uint32_t stage = 2 * (codes + scales);     // k codes, v codes, k scales, v scales
     static constexpr uint32_t ring = 2 * stage;                 // of a warp
-    static constexpr bool q_regs = D <= 128;                    // queries in registers
+    static constexpr bool q_regs = D * NT <= 256;                    // queries in registers
     static constexpr uint32_t q_pitch = D * 2 + 16;             // bytes of a query row in shared memory
-    static constexpr uint32_t outs = kRows * (D + 4) * 4;       // a warp's outputs, when they are joined
-    static constexpr uint32_t smem = kWarps * ring + kRows * q_pitch;
+    static constexpr uint32_t outs = R * (D + 4) * 4;       // a warp's outputs, when they are joined
+    static constexpr uint32_t smem = kWarps * ring + R * q_pitch;
     static constexpr uint32_t all = smem > kWarps * outs ? smem : kWarps * outs;
-    static constexpr uint32_t most = D == 64 ? 4 : D == 128 ? 3 : 2;        // CTAs of an SM, by registers
+    static constexpr uint32_t most = (D == 64 ? 4 : D == 128 ? 3 : 2) + (NT == 1 ? 1 : 0);      // CTAs of an SM, by registers
     static constexpr uint32_t room = (227 * 1024) / (all + 2048);           // and by shared memory
     static constexpr uint32_t fit = room < most ? room : most;
+    static_assert(fit <= 5 && fit * R <= 64, "the workspace");
 };
 
 // Byte `off` of a stage's codes in shared memory: 16-byte pieces are permuted in
@@ -76,13 +77,22 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t off)
     return off ^ (m << 4);
 }
 
+// 8 x 8 halves: lane 4 r + c has (r, 2 c) and (r, 2 c + 1), and gets (2 c, r) and (2 c + 1, r).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 } // namespace
 
-template <int FMT, int D, bool CLUSTER>
-__global__ void __launch_bounds__(32 * kWarps, Shape<FMT, D>::most)
+template <int FMT, int D, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kWarps, Shape<FMT, D, NT>::fit)
 attention_rows_kernel(const __grid_constant__ AttArgs a)
 {
-    using S = Shape<FMT, D>;
+    using S = Shape<FMT, D, NT>;
+    constexpr uint32_t kRows = S::R;
     using W = Walk<kRows, kLog>;
     constexpr uint32_t kThreads = 32 * kWarps;
     extern __shared__ __align__(128) char smem[];
@@ -216,34 +226,42 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             }
         }
         __syncthreads();
-        // Of this lane's two rows: log2-scale factor and last key.
-        float fq[2];
-        int64_t pos[2];         // rows past the sequence's see every key, and are not stored
+        // Of this lane's rows 2 t4 and 2 t4 + 1 of every 8: log2-scale factor and last key.
+        float fq[NT][2];
+        int64_t pos[NT][2];     // rows past the sequence's see every key, and are not stored
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t row = tile * kRows + g8 + 8 * i;
-            fq[i] = factor[g8 + 8 * i] * a.scale;
-            pos[i] = row < rows ? pos0 + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
-        }
-        // This lane's run of a query: values [t4 D / 4, + D / 4) of rows g8 and g8 + 8.
-        uint2 q0[S::q_regs ? D / 16 : 1], q1[S::q_regs ? D / 16 : 1];
-        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2), *qb = qa + 8 * S::q_pitch;
-        if (S::q_regs) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                q0[i] = lds64(qa + i * 8);
-                q1[i] = lds64(qb + i * 8);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t r = nt * 8 + 2 * t4 + i, row = tile * kRows + r;
+                fq[nt][i] = factor[r] * a.scale;
+                pos[nt][i] = row < rows ? pos0 + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
             }
-        }
+        // This lane's run of a query: values [t4 D / 4, + D / 4) of row g8 of every 8.
+        uint2 q[NT][S::q_regs ? D / 16 : 1];
+        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2);
+        if (S::q_regs)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    q[nt][i] = lds64(qa + nt * 8 * S::q_pitch + i * 8);
         float kfac = 1.0f;
         if (FMT == MXQ_FMT_NVFP4)
             kfac = __ldg(a.c.k_s2 + head);
 
-        float acc[D / 8][4];
+        float acc[D / 16][NT][4];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-        float mx[2] = {kLowest, kLowest}, sum[2] = {0.0f, 0.0f};
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.0f;
+        float mx[NT][2], sum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = mx[nt][1] = kLowest;
+            sum[nt][0] = sum[nt][1] = 0.0f;
+        }
 
         // The loops over parts of a turn are rolled: cold instruction caches are what a short
         // call waits for, and the code of a whole turn would not stay in them.
@@ -259,8 +277,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             const char *ksc = st + 2 * S::codes, *vsc = ksc + S::scales;
             const uint32_t left = k1 - key;             // keys of the turn
 
-            // Scores: 16 keys at a time, columns nt * 8 + ... of which this lane decodes key g8.
-            float s[4][4];
+            // Scores: 16 keys at a time, of which this lane decodes g8 and g8 + 8.
+            float s[2][NT][4];
 #pragma unroll 1
             for (uint32_t half = 0; half < 2u; ++half) {
                 constexpr int nblk = S::fp4 ? D / 64 : (D + 127) / 128;         // blocks of the lane's run
@@ -312,55 +330,56 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         }
                     kf = __uint_as_float(top << 23) * 0x1p-7f;
                 }
-                float c[2][4];
+                float c[NT][4];
+                constexpr int run = S::row / 4;          // bytes of a lane's run of a key
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
-                    const uint32_t row = (kr + nt * 8) * S::row;
-                    constexpr int run = S::row / 4;          // bytes of a lane's run
+                for (int p = 0; p < (run + 15) / 16; ++p) {
+                    uint32_t w[2][4];
 #pragma unroll
-                    for (int p = 0; p < (run + 15) / 16; ++p) {
-                        uint32_t w[4];
+                    for (int n = 0; n < 2; ++n) {
+                        const char *at = st + swizzle<S::row>((kr + n * 8) * S::row + t4 * run + p * 16);
                         if (run >= 16) {
-                            const uint4 v = lds128(st + swizzle<S::row>(row + t4 * run + p * 16));
-                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                            const uint4 v = lds128(at);
+                            w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
                         } else {
-                            const uint2 v = lds64(st + swizzle<S::row>(row + t4 * run));
-                            w[0] = v.x, w[1] = v.y;
+                            const uint2 v = lds64(at);
+                            w[n][0] = v.x, w[n][1] = v.y;
                         }
+                    }
 #pragma unroll
-                        for (int i = 0; i < (run >= 16 ? 4 : 2); ++i) {
-                            uint32_t h[4];
-                            constexpr int per = S::fp4 ? 2 : 1;         // products of a word
+                    for (int i = 0; i < (run >= 16 ? 4 : 2); ++i) {
+                        uint32_t h[2][4];
+                        constexpr int per = S::fp4 ? 2 : 1;         // products of a word
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
                             if (S::fp4)
-                                e2m1x8_unpack(w[i], h);
+                                e2m1x8_unpack(w[n][i], h[n]);
                             else
-                                e4m3x4_unpack(w[i], h[0], h[1]);
+                                e4m3x4_unpack(w[n][i], h[n][0], h[n][1]);
 #pragma unroll
-                            for (int u = 0; u < per; ++u) {
-                                const int step = (p * 4 + i) * per + u;       // of 4 values of each lane
-                                const uint32_t sc = kscale[nt][S::fp4 ? step / 4 : step / 8];
-                                uint2 x0, x1;
-                                if (S::q_regs) {
-                                    x0 = q0[step % (D / 16)];
-                                    x1 = q1[step % (D / 16)];
-                                } else {
-                                    x0 = lds64(qa + step * 8);
-                                    x1 = lds64(qb + step * 8);
-                                }
-                                mma16816(c[nt], x0.x, x1.x, x0.y, x1.y, hmul2_bits(h[2 * u], sc),
-                                         hmul2_bits(h[2 * u + 1], sc));
+                        for (int u = 0; u < per; ++u) {
+                            const int step = (p * 4 + i) * per + u;       // of 4 values of each lane
+                            const int blk = S::fp4 ? step / 4 : step / 8;
+                            const uint32_t a0 = hmul2_bits(h[0][2 * u], kscale[0][blk]), a2 = hmul2_bits(h[0][2 * u + 1], kscale[0][blk]);
+                            const uint32_t a1 = hmul2_bits(h[1][2 * u], kscale[1][blk]), a3 = hmul2_bits(h[1][2 * u + 1], kscale[1][blk]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint2 x = S::q_regs ? q[nt][step % (S::q_regs ? D / 16 : 1)] : lds64(qa + nt * 8 * S::q_pitch + step * 8);
+                                if (step == 0)
+                                    mma16816_first(c[nt], a0, a1, a2, a3, x.x, x.y);
+                                else
+                                    mma16816(c[nt], a0, a1, a2, a3, x.x, x.y);
                             }
                         }
                     }
                 }
-                const float f[2] = {fq[0] * kf, fq[1] * kf};
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s[nt][j] = half ? s[nt][j] : c[nt][j] * f[j >> 1];
-                        s[nt + 2][j] = c[nt][j] * f[j >> 1];
+                        const float v = c[nt][j] * (fq[nt][j & 1] * kf);
+                        s[0][nt][j] = half ? s[0][nt][j] : v;
+                        s[1][nt][j] = v;
                     }
             }
 
@@ -380,65 +399,82 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             }
 
             // Running maximum, which stays unless it grows by more than 2^8; weights.
-            int lim[2];                                 // last key of the turn that a row sees
+            int lim[NT][2], least = kKeys - 1;          // last key of the turn that a row sees
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                lim[i] = (int)max(min(pos[i] - (int64_t)key, (int64_t)min(left, kKeys) - 1), (int64_t)-1);
-            const bool cut = __any_sync(0xFFFFFFFFu, min(lim[0], lim[1]) < (int)kKeys - 1);
-            float alpha[2];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float m = -INFINITY;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                    for (int j = 2 * i; j < 2 * i + 2; ++j) {
-                        if (cut)
-                            s[nt][j] = (int)(nt * 8 + 2 * t4 + (j & 1)) <= lim[i] ? s[nt][j] : -INFINITY;
-                        m = fmaxf(m, s[nt][j]);
-                    }
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) + E;
-                alpha[i] = 1.0f;
-                if (m > mx[i] + 8.0f) {
-                    alpha[i] = ex2(mx[i] - m);
-                    mx[i] = m;
+                for (int i = 0; i < 2; ++i) {
+                    lim[nt][i] = (int)max(min(pos[nt][i] - (int64_t)key, (int64_t)min(left, kKeys) - 1), (int64_t)-1);
+                    least = min(least, lim[nt][i]);
                 }
-                const float off = E - mx[i];
-                float part = 0.0f;
+            const bool cut = __any_sync(0xFFFFFFFFu, least < (int)kKeys - 1);
+            float alpha[NT][2];
+            bool moved = false;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 2 * i; j < 2 * i + 2; ++j) {
-                        s[nt][j] = ex2(s[nt][j] + off);
-                        part += s[nt][j];
+                for (int i = 0; i < 2; ++i) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) {
+                            if (cut)
+                                s[h][nt][j] = (int)(h * 16 + (j >> 1) * 8 + g8) <= lim[nt][i] ? s[h][nt][j] : -INFINITY;
+                            m = fmaxf(m, s[h][nt][j]);
+                        }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                    m += E;
+                    alpha[nt][i] = 1.0f;
+                    if (m > mx[nt][i] + 8.0f) {
+                        alpha[nt][i] = ex2(mx[nt][i] - m);
+                        mx[nt][i] = m;
+                        moved = true;
                     }
-                sum[i] = fmaf(sum[i], alpha[i], part * inv);
-            }
-            if (!first_turn && __any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+                    const float off = E - mx[nt][i];
+                    float part = 0.0f;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    acc[j][0] *= alpha[0];
-                    acc[j][1] *= alpha[0];
-                    acc[j][2] *= alpha[1];
-                    acc[j][3] *= alpha[1];
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) {
+                            s[h][nt][j] = ex2(s[h][nt][j] + off);
+                            part += s[h][nt][j];
+                        }
+                    sum[nt][i] = fmaf(sum[nt][i], alpha[nt][i], part * inv);
                 }
+            if (!first_turn && __any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        acc[j][nt][0] *= alpha[nt][0];
+                        acc[j][nt][1] *= alpha[nt][1];
+                        acc[j][nt][2] *= alpha[nt][0];
+                        acc[j][nt][3] *= alpha[nt][1];
+                    }
             }
             first_turn = false;
-            uint32_t pw[2][4];
+            // A lane has a key's weights for two rows; the products want a row's for two keys.
+            uint32_t pw[2][NT][2];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                pw[kk][0] = half2_bits(s[2 * kk][0], s[2 * kk][1]);
-                pw[kk][1] = half2_bits(s[2 * kk][2], s[2 * kk][3]);
-                pw[kk][2] = half2_bits(s[2 * kk + 1][0], s[2 * kk + 1][1]);
-                pw[kk][3] = half2_bits(s[2 * kk + 1][2], s[2 * kk + 1][3]);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    pw[h][nt][0] = transpose8(half2_bits(s[h][nt][0], s[h][nt][1]));
+                    pw[h][nt][1] = transpose8(half2_bits(s[h][nt][2], s[h][nt][3]));
+                }
 
             // Outputs: 16 keys at a time, columns d = run of this lane.
 #pragma unroll 1
             for (uint32_t kk = 0; kk < 2u; ++kk) {
-                const uint32_t p0 = kk ? pw[1][0] : pw[0][0], p1 = kk ? pw[1][1] : pw[0][1];
-                const uint32_t p2 = kk ? pw[1][2] : pw[0][2], p3 = kk ? pw[1][3] : pw[0][3];
+                uint32_t b[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        b[nt][i] = kk ? pw[1][nt][i] : pw[0][nt][i];
                 constexpr int vblocks = S::fp4 && D == 256 ? 2 : 1;      // of a lane's run of D / 8
                 uint32_t vscale[2][vblocks];        // of the key pairs 2 t4, + 1 and 8 further
 #pragma unroll
@@ -491,19 +527,24 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                             e2m1x8_unpack(((w[2][i] >> 4) & lm) | (w[3][i] & ~lm), b1[1]);
                             const int blk = vblocks == 2 ? i / 2 : 0;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                mma16816(acc[(p * words + i) * 8 + j], p0, p1, p2, p3,
-                                         hmul2_bits(b0[j & 1][j >> 1], vscale[0][blk]),
-                                         hmul2_bits(b1[j & 1][j >> 1], vscale[1][blk]));
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t a0 = hmul2_bits(b0[0][j], vscale[0][blk]), a1 = hmul2_bits(b0[1][j], vscale[0][blk]);
+                                const uint32_t a2 = hmul2_bits(b1[0][j], vscale[1][blk]), a3 = hmul2_bits(b1[1][j], vscale[1][blk]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816(acc[(p * words + i) * 4 + j][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+                            }
                         } else {
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 uint32_t x0, x1, y0, y1;
                                 e4m3x4_unpack(__byte_perm(w[0][i], w[1][i], u ? 0x7362 : 0x5140), x0, x1);
                                 e4m3x4_unpack(__byte_perm(w[2][i], w[3][i], u ? 0x7362 : 0x5140), y0, y1);
-                                const int j = (p * words + i) * 4 + u * 2;
-                                mma16816(acc[j], p0, p1, p2, p3, hmul2_bits(x0, vscale[0][0]), hmul2_bits(y0, vscale[1][0]));
-                                mma16816(acc[j + 1], p0, p1, p2, p3, hmul2_bits(x1, vscale[0][0]), hmul2_bits(y1, vscale[1][0]));
+                                const uint32_t a0 = hmul2_bits(x0, vscale[0][0]), a1 = hmul2_bits(x1, vscale[0][0]);
+                                const uint32_t a2 = hmul2_bits(y0, vscale[1][0]), a3 = hmul2_bits(y1, vscale[1][0]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816(acc[(p * words + i) * 2 + u][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
                             }
                         }
                     }
@@ -515,36 +556,41 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 
         // Join the warps: sums over the lanes of a row first.
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
-            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    sum[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][i], o);
         __syncthreads();
-        if (t4 == 0) {
-            stat[0][warp][g8] = mx[0];
-            stat[0][warp][g8 + 8] = mx[1];
-            stat[1][warp][g8] = sum[0];
-            stat[1][warp][g8 + 8] = sum[1];
-        }
+        if (g8 == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    stat[0][warp][nt * 8 + 2 * t4 + i] = mx[nt][i];
+                    stat[1][warp][nt * 8 + 2 * t4 + i] = sum[nt][i];
+                }
         __syncthreads();
         float *outs = reinterpret_cast<float *>(smem) + warp * (S::outs / 4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t r = g8 + 8 * i;
-            float m = stat[0][0][r];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (uint32_t w = 1; w < kWarps; ++w)
-                m = fmaxf(m, stat[0][w][r]);
-            const float f = ex2(mx[i] - m);
-            // columns 2 t4 and 2 t4 + 1 of each product: the runs of lanes g8 = 2 t4 and 2 t4 + 1
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t r = nt * 8 + 2 * t4 + i;
+                float m = stat[0][0][r];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+                for (uint32_t w = 1; w < kWarps; ++w)
+                    m = fmaxf(m, stat[0][w][r]);
+                const float f = ex2(mx[nt][i] - m);
+                // the run of lanes g8, two values a product
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    const uint32_t jj = S::row == 256 && c ? j ^ 16 : j;
-                    outs[r * (D + 4) + (2 * t4 + c) * (D / 8) + jj] = acc[j][2 * i + c] * f;
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t jj = S::row == 256 ? (2 * j) ^ ((g8 & 1u) * 16u) : 2 * j;
+                    *reinterpret_cast<float2 *>(outs + r * (D + 4) + g8 * (D / 8) + jj) =
+                        make_float2(acc[j][nt][i] * f, acc[j][nt][2 + i] * f);
                 }
-        }
+            }
         __syncthreads();
         const float vfac = FMT == MXQ_FMT_NVFP4 ? __ldg(a.c.v_s2 + head) : 1.0f;
         const bool whole = walk.whole();
@@ -637,11 +683,11 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 
 namespace {
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 cudaError_t run(const AttArgs &a, uint32_t sms, uint32_t &ctas, cudaStream_t s)
 {
-    using S = Shape<FMT, D>;
-    const auto k = attention_rows_kernel<FMT, D, false>;
+    using S = Shape<FMT, D, NT>;
+    const auto k = attention_rows_kernel<FMT, D, NT, false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::all);
     ctas = sms * S::fit;
     return e != cudaSuccess ? e : launch_dependent(k, dim3(ctas), 32 * kWarps, S::all, s, a);
@@ -649,10 +695,10 @@ cudaError_t run(const AttArgs &a, uint32_t sms, uint32_t &ctas, cudaStream_t s)
 
 // Clusters of 1 to 8 CTAs, one a tile, where they fit the card at once.  most_keys: what a
 // sequence can have.
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 cudaError_t run_clusters(const AttArgs &a, uint32_t sms, uint64_t most_keys, bool &taken, cudaStream_t s)
 {
-    using S = Shape<FMT, D>;
+    using S = Shape<FMT, D, NT>;
     const uint64_t clusters = (uint64_t)a.c.seqs * a.c.heads * a.tiles, room = (uint64_t)sms * S::fit;
     uint32_t size = 1;
     while (size < 8u && clusters * size * 2u <= room && (uint64_t)size * kWarps * kKeys < most_keys)
@@ -661,7 +707,7 @@ cudaError_t run_clusters(const AttArgs &a, uint32_t sms, uint64_t most_keys, boo
     taken = clusters <= room && most_keys <= (uint64_t)size * kWarps * kKeys * kClusterTurns;
     if (!taken)
         return cudaSuccess;
-    const auto k = attention_rows_kernel<FMT, D, true>;
+    const auto k = attention_rows_kernel<FMT, D, NT, true>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::all);
     if (e != cudaSuccess)
         return e;
@@ -672,29 +718,35 @@ cudaError_t run_clusters(const AttArgs &a, uint32_t sms, uint64_t most_keys, boo
                        : launch_dependent<8>(k, grid, 32 * kWarps, S::all, s, a);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 cudaError_t either(const AttArgs &a, uint32_t sms, uint64_t most_keys, uint32_t &ctas, cudaStream_t s)
 {
     bool taken = false;
     ctas = 0;
-    const cudaError_t e = run_clusters<FMT, D>(a, sms, most_keys, taken, s);
-    return taken || e != cudaSuccess ? e : run<FMT, D>(a, sms, ctas, s);
+    const cudaError_t e = run_clusters<FMT, D, NT>(a, sms, most_keys, taken, s);
+    return taken || e != cudaSuccess ? e : run<FMT, D, NT>(a, sms, ctas, s);
 }
 
 } // namespace
 
 // `ctas`: of a launch that leaves unfinished tiles, each with its entry in `left`; 0 of
-// one that does not.
-cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t sms, uint64_t most_keys, uint32_t &ctas,
-                                  cudaStream_t s)
+// one that does not.  Tiles of `rows` rows, 8 or 16.
+template <int FMT, int D>
+static cudaError_t sized(const AttArgs &a, uint32_t rows, uint32_t sms, uint64_t most_keys, uint32_t &ctas, cudaStream_t s)
+{
+    return rows == 8u ? either<FMT, D, 1>(a, sms, most_keys, ctas, s) : either<FMT, D, 2>(a, sms, most_keys, ctas, s);
+}
+
+cudaError_t launch_attention_rows(const AttArgs &a, int fmt, int dim, uint32_t rows, uint32_t sms, uint64_t most_keys,
+                                  uint32_t &ctas, cudaStream_t s)
 {
     if (fmt == MXQ_FMT_NVFP4)
-        return dim == 64    ? either<MXQ_FMT_NVFP4, 64>(a, sms, most_keys, ctas, s)
-               : dim == 128 ? either<MXQ_FMT_NVFP4, 128>(a, sms, most_keys, ctas, s)
-                            : either<MXQ_FMT_NVFP4, 256>(a, sms, most_keys, ctas, s);
-    return dim == 64    ? either<MXQ_FMT_MXFP8, 64>(a, sms, most_keys, ctas, s)
-           : dim == 128 ? either<MXQ_FMT_MXFP8, 128>(a, sms, most_keys, ctas, s)
-                        : either<MXQ_FMT_MXFP8, 256>(a, sms, most_keys, ctas, s);
+        return dim == 64    ? sized<MXQ_FMT_NVFP4, 64>(a, rows, sms, most_keys, ctas, s)
+               : dim == 128 ? sized<MXQ_FMT_NVFP4, 128>(a, rows, sms, most_keys, ctas, s)
+                            : sized<MXQ_FMT_NVFP4, 256>(a, rows, sms, most_keys, ctas, s);
+    return dim == 64    ? sized<MXQ_FMT_MXFP8, 64>(a, rows, sms, most_keys, ctas, s)
+           : dim == 128 ? sized<MXQ_FMT_MXFP8, 128>(a, rows, sms, most_keys, ctas, s)
+                        : sized<MXQ_FMT_MXFP8, 256>(a, rows, sms, most_keys, ctas, s);
 }
 
 } // namespace mxq
