@@ -160,16 +160,29 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 at[0] = keys0 ? (((uint64_t)page[0] * a.c.heads + head) << a.c.page_log) + (key & mask) : 0ull;
                 at[1] = keys1 > 16u ? (((uint64_t)page[1] * a.c.heads + head) << a.c.page_log) + ((key + 16u) & mask) : 0ull;
                 constexpr uint32_t pieces = S::row / 16;        // of a key's codes
-                static_assert(pieces * 16 % 32 == 0, "a copy of the warp stays in a run");
+                static_assert(pieces * 16 % 32 == 0 && S::scales % 32 == 0, "a copy of the warp stays in a run");
+                if (keys0 >= kKeys && keys1 >= kKeys) {         // most often: nothing to look at
 #pragma unroll
-                for (uint32_t i = 0; i < pieces; ++i) {
-                    const uint32_t run = i * 32u / (16u * pieces), p = i * 32u + lane - run * 16u * pieces;
-                    const uint32_t r = run * 16u + p / pieces;
-                    const uint64_t src = at[run] * S::row + p * 16u;
-                    const uint32_t dst = st + swizzle<S::row>((i * 32u + lane) * 16u);
-                    const bool ok = r < (run ? keys1 : keys0);
-                    cp16_or_zero(dst, a.c.k_codes + (ok ? src : 0ull), ok);
-                    cp16_or_zero(dst + S::codes, a.c.v_codes + (ok ? src : 0ull), ok);
+                    for (uint32_t run = 0; run < 2u; ++run) {
+                        const uint8_t *kc = a.c.k_codes + at[run] * S::row + lane * 16u, *vc = a.c.v_codes + at[run] * S::row + lane * 16u;
+#pragma unroll
+                        for (uint32_t i = 0; i < pieces / 2; ++i) {
+                            const uint32_t dst = st + swizzle<S::row>(((run * pieces / 2 + i) * 32u + lane) * 16u);
+                            cp16(dst, kc + i * 512u);
+                            cp16(dst + S::codes, vc + i * 512u);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (uint32_t i = 0; i < pieces; ++i) {
+                        const uint32_t run = i * 2u >= pieces, p = i * 32u + lane - run * 16u * pieces;
+                        const uint32_t r = run * 16u + p / pieces;
+                        const uint64_t src = (run ? at[1] : at[0]) * S::row + p * 16u;
+                        const uint32_t dst = st + swizzle<S::row>((i * 32u + lane) * 16u);
+                        const bool ok = r < (run ? keys1 : keys0);
+                        cp16_or_zero(dst, a.c.k_codes + (ok ? src : 0ull), ok);
+                        cp16_or_zero(dst + S::codes, a.c.v_codes + (ok ? src : 0ull), ok);
+                    }
                 }
                 // Scales: 16 bytes are 16 / blocks keys.
 #pragma unroll
@@ -263,8 +276,6 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             sum[nt][0] = sum[nt][1] = 0.0f;
         }
 
-        // The loops over parts of a turn are rolled: cold instruction caches are what a short
-        // call waits for, and the code of a whole turn would not stay in them.
 #pragma unroll 1
         for (; key < k1; key += stride, slot ^= 1u) {
             page[0] = ahead[0];
@@ -279,7 +290,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 
             // Scores: 16 keys at a time, of which this lane decodes g8 and g8 + 8.
             float s[2][NT][4];
-#pragma unroll 1
+#pragma unroll
             for (uint32_t half = 0; half < 2u; ++half) {
                 constexpr int nblk = S::fp4 ? D / 64 : (D + 127) / 128;         // blocks of the lane's run
                 uint32_t kscale[2][nblk];               // f16x2
@@ -376,11 +387,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float v = c[nt][j] * (fq[nt][j & 1] * kf);
-                        s[0][nt][j] = half ? s[0][nt][j] : v;
-                        s[1][nt][j] = v;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        s[half][nt][j] = c[nt][j] * (fq[nt][j & 1] * kf);
             }
 
             // E: the largest power of the values' scales.
@@ -467,14 +475,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 }
 
             // Outputs: 16 keys at a time, columns d = run of this lane.
-#pragma unroll 1
+#pragma unroll
             for (uint32_t kk = 0; kk < 2u; ++kk) {
-                uint32_t b[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        b[nt][i] = kk ? pw[1][nt][i] : pw[0][nt][i];
                 constexpr int vblocks = S::fp4 && D == 256 ? 2 : 1;      // of a lane's run of D / 8
                 uint32_t vscale[2][vblocks];        // of the key pairs 2 t4, + 1 and 8 further
 #pragma unroll
@@ -532,7 +534,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                                 const uint32_t a2 = hmul2_bits(b1[0][j], vscale[1][blk]), a3 = hmul2_bits(b1[1][j], vscale[1][blk]);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma16816(acc[(p * words + i) * 4 + j][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+                                    mma16816(acc[(p * words + i) * 4 + j][nt], a0, a1, a2, a3, pw[kk][nt][0], pw[kk][nt][1]);
                             }
                         } else {
 #pragma unroll
@@ -544,7 +546,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                                 const uint32_t a2 = hmul2_bits(y0, vscale[1][0]), a3 = hmul2_bits(y1, vscale[1][0]);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma16816(acc[(p * words + i) * 2 + u][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+                                    mma16816(acc[(p * words + i) * 2 + u][nt], a0, a1, a2, a3, pw[kk][nt][0], pw[kk][nt][1]);
                             }
                         }
                     }
