@@ -12,7 +12,9 @@
 // atomics, and the division follows from the lengths, the sizes and the number of
 // SMs alone.  Every warp works its CTA's range out for itself, in the same way (out of
 // line: a launch begins with cold instruction caches, and inlined in every role the
-// division was most of a kernel's code).
+// division was most of a kernel's code).  What is out of line takes the arguments from a
+// copy in shared memory: by a reference to the kernel's own they come from global memory,
+// cold and one after the other.
 #pragma once
 
 #include "mxq_cache.cuh"

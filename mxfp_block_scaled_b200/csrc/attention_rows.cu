@@ -1,20 +1,29 @@
 // attention_rows.cu -- attention over a quantized cache where a sequence has few
 // rows: decoding, guessed tokens (sm_100a).  The read of the cache is the work.
 //
-// A tile is up to 16 rows of one sequence and key/value head, a step 32 keys;
-// attention.cuh divides them.  A CTA has 4 warps, which take turns of the steps of a
-// tile, each with its own running maximum, sum and output, joined at the end (in the
-// order of the warps).  Where there are few tiles, a cluster of CTAs takes each instead
-// (CLUSTER), a run of its steps a CTA, and the parts are joined through the CTAs' shared
-// memory: nothing is divided and no second launch is needed, which is most of a short
-// call's time.
+// A tile is up to 8 rows (where no sequence of the call has more) or 16 of one sequence
+// and key/value head, a step 32 keys; attention.cuh divides them.  A CTA has 4 warps,
+// which take turns of the steps of a tile, each with its own running maximum, sum and
+// output, joined at the end (in the order of the warps).  Where there are few tiles and a
+// warp has few turns, a cluster of CTAs takes each tile instead (CLUSTER), a run of its
+// steps a CTA, and the parts are joined through the CTAs' shared memory: nothing is
+// divided and no second launch is needed, which is most of a short call's time.
 //
 // Codes go from global memory to a warp's own two stages of shared memory by
-// cp.async and from there, decoded, into the operands of mma.sync m16n8k16 (f16,
-// fp32 sums).  The order of a head's dimension inside a product is free, so a
-// lane takes a contiguous run of every key's codes, and a contiguous run of the
-// values' columns; pairs of keys are put together a byte (or nibble) at a time
-// before they are decoded, so the values need no transposition.
+// cp.async and from there, decoded, into the left operands of mma.sync m16n8k16 (f16,
+// fp32 sums): 16 keys of S^T = K Q^T, 16 columns of O^T = V^T P^T, so that 8 rows waste
+// nothing.  The order of a head's dimension inside a product is free, so a lane takes a
+// contiguous run of every key's codes, and a contiguous run of the values' columns;
+// pairs of keys are put together a byte (or nibble) at a time before they are decoded, so
+// the values need no transposition; the weights are turned by movmatrix.
+//
+// Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
+// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 72 us (328 MB, 4.5
+// TB/s, 69 % of the measured copy rate), NVFP4 70 us, heads of 64 98 us, 32 sequences with
+// heads of 256 82 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
+// up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 48 us.  One
+// sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
+// wins (12 of 16384 as above by clusters 120 us, 59 us divided).
 //
 // Precision.  E2M1 times its E4M3 scale is exact in f16.  E4M3 codes (MXFP8) are
 // multiplied in f16 by their block's power of two relative to the largest of the
@@ -36,7 +45,7 @@ namespace {
 
 constexpr uint32_t kKeys = 32, kLog = 5;    // keys of a step
 constexpr uint32_t kWarps = 4;
-constexpr uint32_t kClusterTurns = 8;       // of a warp, of a tile that a cluster takes
+constexpr uint32_t kClusterTurns = 8;       // most turns of a warp, of a tile that a cluster takes
 
 template <int FMT, int D, int NT>
 struct Shape {
@@ -97,10 +106,13 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
     constexpr uint32_t kThreads = 32 * kWarps;
     extern __shared__ __align__(128) char smem[];
     __shared__ Range range;
+    __shared__ AttArgs sa;      // for functions out of line
     __shared__ W walks[kWarps];
     __shared__ __align__(16) float stat[2][kWarps][kRows];        // the warps' maxima and sums
     __shared__ __align__(16) float joint[2][kRows];               // the CTA's
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3u;
+    if (!CLUSTER && tid == 0)
+        sa = a;
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
     W &walk = walks[warp];
@@ -128,16 +140,17 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         __syncwarp();
         more = true;
     } else {
-        find_range<W::Div>(a, range);
+        __syncthreads();
+        find_range<W::Div>(sa, range);
         if (tid == 0)
             a.left[blockIdx.x].parts = 0u;
-        more = W::begin(walk, a, range);
+        more = W::begin(walk, sa, range);
     }
 
     char *ring = smem + warp * S::ring;
     const uint32_t ring_s = smem_addr(ring);
     char *qs = smem + kWarps * S::ring;
-    for (; more; more = !CLUSTER && W::next(walk, a)) {
+    for (; more; more = !CLUSTER && W::next(walk, sa)) {
         const uint32_t first = walk.s.first, rows = walk.s.rows, tile = walk.rt, head = walk.head, b = walk.b;
         const int64_t pos0 = walk.s.len - walk.s.n;           // position of the sequence's first new token
         const uint32_t k0 = walk.k0 << kLog, k1 = min(walk.k1 << kLog, walk.keys);

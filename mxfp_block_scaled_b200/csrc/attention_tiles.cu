@@ -2,29 +2,43 @@
 // rows: chunks of a prompt (sm_100a).  The products are the work.
 //
 // A tile is 256 rows (128 for heads of 256 values) of one sequence and key/value
-// head, a step 128 keys (64); attention.cuh divides them among one CTA an SM.  Both
-// products run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P
-// from TMEM.  Four warps decode the cache's codes straight from global memory into
-// f16 tiles in shared memory (two stages of keys, two of values, the same layout for
-// both: rows of a token, 128 bytes wide, 128-byte swizzle; the values' is read as an
-// MN-major operand, so nothing is transposed).  Two groups of four warps take the
-// softmax of 128 rows each, a row a thread, so a row's maximum and sum need no
-// exchange; while one works the tensor cores do the other's products.  One warp
-// issues.  A step of 128 x 128 products costs the tensor cores 512 cycles twice, and
-// a group 128 x 128 exponentials, at 16 a cycle 1024 cycles: both are near full.
+// head, a step 64 keys; attention.cuh divides them among one CTA an SM.  Both products
+// run on tcgen05: S = Q K^T from shared memory into TMEM, O += P V with P from TMEM.
+// Warps 8-10 decode the keys' codes straight from global memory into f16 tiles in
+// shared memory, warps 12-14 the values' (four stages each, two for heads of 256; the
+// same layout for both: rows of a token, 128 bytes wide, 128-byte swizzle; the values' is
+// read as an MN-major operand, so nothing is transposed).  Warps 0-3 and 4-7 are two
+// groups that take the softmax of 128 rows each, a row a thread, so a row's maximum and
+// sum need no exchange; while one works the tensor cores do the other's products.  Warps
+// 11 and 15 issue, one for each group.
 //
-// A unit u is a softmax and its two products.  With two groups at work unit u is
-// step u / 2 of group u % 2, with one (tiles of up to 128 rows) step u; either way its
-// scores are in TMEM buffer u % 2, and S of unit u + 2 is issued behind P V of unit u,
-// which has read the weights that lie over the scores.
+// Scores lie in four TMEM buffers of 64 columns, whose first halves take the weights.
+// With two groups at work each has two of them, with one (tiles of up to 128 rows) it has
+// all four; scores of a step are issued as soon as the product that reads the weights in
+// their place is done, a buffer's count of steps ahead.
 //
-// The output in TMEM is rescaled only where the maximum has grown by more than 2^8
-// (by the softmax group, which has the output to itself between its products);
-// weights are at most 2^8 then, exact powers of two apart from what they would be.
-// MXFP8 powers: as in attention_rows.cu, a largest one for every 32 (16) keys.
+// Weights are taken against the maximum so far; only where a score exceeds it by more
+// than 2^8 is the new maximum found, the step's weights are taken again, and the output
+// in TMEM is rescaled (by the softmax group, which has the output to itself between its
+// products).  Weights are 2^8 at most then, exact powers of two apart from what they
+// would be.  MXFP8 powers: as in attention_rows.cu, a largest one for every 32 (16) keys.
+//
+// Bound: a step of 256 x 64 x 128 costs the tensor cores 1024 cycles and the SM's 16
+// exponentials a cycle 1024 as well, beside which a softmax thread has two operations a
+// score in fp32 and a rounding to f16.  A chunk of 4096 tokens over 20480 of 32 query and
+// 4 key/value heads of 128 takes 1.26 ms (979 TFLOP/s, 60 % of the measured rate of a
+// bf16 product; NVFP4 1.18 ms; heads of 64 1.20 ms, of 256 half the chunk over 10240
+// 0.90 ms).  Steps that brought it there: 2.46 ms with one warp that issued for all and
+// steps of 128 keys; 1.71 with products issued by the groups; 1.54 with steps of 64 keys and
+// an issuing warp a group (a warp is held while its products queue); 1.49 with fewer waits
+// between weights and scores; 1.26 with one copy of each loop and the division of the work
+// out of line (a launch begins with cold instruction caches).  A polynomial in place of
+// part of the exponentials, other shares of registers, and softmax threads that share a
+// row were slower or no faster.  What is left beside the two bounds is about 50 us at a
+// launch's start and 1.7 us a tile.
 //
 // Every wait is bounded (MXQ_DEV_WAIT_TIMEOUT); all roles then leave, the issuing
-// one behind its last product.
+// ones behind their last product.
 #include "attention.cuh"
 #include "mxq_mma.cuh"
 #include "mxq_tcgen05.cuh"
@@ -34,11 +48,10 @@ namespace mxq {
 
 namespace {
 
-constexpr uint32_t kSpin = 1u << 18;        // tests of a barrier before a wait gives up
-// Warps 0-3 and 4-7: softmax groups; 8-10 decode keys, 12-14 values; 11 and 15 issue
-// the groups' products.  (A warp is held while its products queue and at every wait
-// that it makes between them; with one for both groups the tensor cores were idle for
-// more than half of the time.)
+// Tests of a barrier before a wait gives up.  A test suspends for 4 us at most, so that is
+// after a second; a step takes microseconds.  A group that has nothing to do waits for the
+// other's whole tiles, 64 times as long (and leaves at once where the other gives up).
+constexpr uint32_t kSpin = 1u << 18, kIdleSpin = kSpin << 6;
 constexpr uint32_t kCodeWarp = 8;
 constexpr int kThreads = 512;
 
@@ -69,9 +82,9 @@ struct Bars {
 };
 
 // Further tests of a barrier whose first one failed.
-__device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
+__device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status, uint32_t spin)
 {
-    for (uint32_t i = 0; i < kSpin; ++i) {
+    for (uint32_t i = 0; i < spin; ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
         if ((i & 63u) == 63u && *reinterpret_cast<volatile uint32_t *>(&s.abort))
@@ -82,10 +95,10 @@ __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, Bars &s, 
     return false;
 }
 // The whole warp.
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status)
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status, uint32_t spin = kSpin)
 {
     return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity & 1u)) ||
-           __all_sync(0xFFFFFFFFu, wait_more(bar, parity & 1u, s, status));
+           __all_sync(0xFFFFFFFFu, wait_more(bar, parity & 1u, s, status, spin));
 }
 
 // 128 x N products of 16, f16 operands, from shared memory and from TMEM; issued
@@ -170,6 +183,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ Bars bars;
     __shared__ Range range;
+    __shared__ AttArgs sa;      // for functions out of line
     __shared__ W walks[16];     // of the warps
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     char *kt = smem + S::subs * S::qbytes, *vt = kt + S::stages * S::tile;
@@ -193,6 +207,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             mbar_init(&bars.ffull[i], 2 * S::chunks);
         mbar_init(&bars.meet, 8);
         bars.abort = 0;
+        sa = a;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -202,7 +217,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
     }
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    find_range<typename W::Div>(a, range);
+    __syncthreads();
+    find_range<typename W::Div>(sa, range);
     fence_before();
     __syncthreads();
     fence_after();
@@ -223,11 +239,11 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
         const uint64_t qd = operand_desc(smem_addr(smem + wg * S::qbytes)), kd = operand_desc(smem_addr(kt));
         const uint64_t vd = columns_desc(smem_addr(vt), S::panel);
         const uint32_t out = tmem + kOut + wg * D;
-        for (bool more = W::begin(w, a, range); more && ok; more = W::next(w, a)) {
+        for (bool more = W::begin(w, sa, range); more && ok; more = W::next(w, sa)) {
             const Units<S> un(w);
             if (wg == 0u || un.two) {
                 const uint32_t buffers = un.two ? kBufs / 2u : kBufs;       // of this group
-                ok = wait_all(&bars.qfull[wg], q0++, bars, a.c.status);
+                ok = wait_all(&bars.qfull[wg], q0++, bars, a.c.status, kIdleSpin);
                 auto keys_there = [&](uint32_t j) {
                     const uint32_t t = t0 + j;
                     ok = ok && wait_all(&bars.kfull[t % S::stages], t / S::stages, bars, a.c.status);
@@ -295,14 +311,14 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
         uint64_t *full = values ? bars.vfull : bars.kfull, *empty = values ? bars.vempty : bars.kempty;
         char *tiles = values ? vt : kt;
         Raw<FMT, D> raw;
-        bool more = W::begin(w, a, range);
+        bool more = W::begin(w, sa, range);
         uint32_t step = w.k0, t = 0;
         auto settle = [&]() {       // the chunk is number dw from step `step` on: its own step
             while (dw >= S::chunks && more) {
                 dw -= S::chunks;
                 ++t;
                 if (++step == w.k1) {
-                    more = W::next(w, a);
+                    more = W::next(w, sa);
                     step = w.k0;
                 }
             }
@@ -462,10 +478,10 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.meet);
-                ok = wait_all(&bars.meet, met++, bars, a.c.status);
+                ok = wait_all(&bars.meet, met++, bars, a.c.status, kIdleSpin);
             }
         };
-        for (bool more = W::begin(w, a, range); more && ok; more = W::next(w, a)) {
+        for (bool more = W::begin(w, sa, range); more && ok; more = W::next(w, sa)) {
             const Units<S> un(w);
             if (!un.two)
                 meet();
