@@ -18,10 +18,10 @@
 // the values need no transposition; the weights are turned by movmatrix.
 //
 // Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
-// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 72 us (328 MB, 4.5
-// TB/s, 69 % of the measured copy rate), NVFP4 70 us, heads of 64 98 us, 32 sequences with
-// heads of 256 82 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
-// up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 48 us.  One
+// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 69 us (328 MB, 4.8
+// TB/s, 73 % of the measured copy rate), NVFP4 69 us, heads of 64 94 us, 32 sequences with
+// heads of 256 79 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
+// up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 46 us.  One
 // sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
 // wins (12 of 16384 as above by clusters 120 us, 59 us divided).
 //
@@ -147,6 +147,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         more = W::begin(walk, sa, range);
     }
 
+    const uint64_t once = once_policy();
     char *ring = smem + warp * S::ring;
     const uint32_t ring_s = smem_addr(ring);
     char *qs = smem + kWarps * S::ring;
@@ -181,8 +182,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
                         for (uint32_t i = 0; i < pieces / 2; ++i) {
                             const uint32_t dst = st + swizzle<S::row>(((run * pieces / 2 + i) * 32u + lane) * 16u);
-                            cp16(dst, kc + i * 512u);
-                            cp16(dst + S::codes, vc + i * 512u);
+                            cp16_once(dst, kc + i * 512u, true, once);
+                            cp16_once(dst + S::codes, vc + i * 512u, true, once);
                         }
                     }
                 } else {

@@ -147,6 +147,7 @@ linear_kernel(const Args a)
     const uint32_t lg = a.kslog, ks = 1u << lg, teams = warps >> lg, team = warp >> lg, q = warp & (ks - 1u);
     const uint32_t c0 = (a.chunks * q) >> lg, c1 = (a.chunks * (q + 1u)) >> lg;
 
+    const uint64_t once = once_policy();
     const uint32_t piece = lane & 7u;
     const uint32_t pdst = (lane >> 3) * F::pitch + (F::swap ? (piece * 16u) ^ ((lane >> 3 & 1u) * 64u) : piece * 16u);
     constexpr uint32_t spieces = F::groups;                 // scale pieces of a row of a chunk
@@ -166,7 +167,7 @@ linear_kernel(const Args a)
             const bool in = piece * 16u < left;         // zeros behind the row's end
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                cp16_or_zero(dst + 4 * i * F::pitch, pcode[i] + (in ? (uint64_t)pch * kChunk : 0ull), in);
+                cp16_once(dst + 4 * i * F::pitch, pcode[i] + (in ? (uint64_t)pch * kChunk : 0ull), in, once);
             if (!a.direct && srow < 16u && spiece * F::group_bytes < left)
                 cp_small<F::sbytes>(ring_s + pslot * kSlot + kScaleAt + srow * kScalePitch + spiece * F::sbytes,
                                     pscale + pch * (F::groups * F::sbytes));

@@ -33,6 +33,20 @@ __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
 }
 
+// The same of data that is read once: what it displaces in the second-level cache first
+// is its like, not the code and the small operands of the next kernels.
+__device__ __forceinline__ uint64_t once_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void cp16_once(uint32_t dst, const void *src, bool ok, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;"
+                 ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u), "l"(policy) : "memory");
+}
+
 // c += A B: A 16 rows x 16 k (f16), B 16 k x 8 columns (f16).
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
