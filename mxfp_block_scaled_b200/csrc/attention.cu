@@ -17,8 +17,14 @@ cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t 
 
 namespace {
 
-// Sequences of up to this many rows are attention_rows.cu's.
-constexpr uint32_t kFewRows = 64;
+// Sequences of up to this many rows are attention_rows.cu's, and of up to kSomeRows where
+// all have few keys: its 16 rows a tile decode a key again for every tile, while
+// attention_tiles.cu takes 30 us to begin.  Measured, rows against tiles, 2 key/value heads
+// of 128, MXFP8: 64 sequences of up to 4096 with 16 rows 46 against 46 us, 32 rows 58 against
+// 68, 64 rows 92 against 75; one of 30000 with 32 rows 26 against 29, 64 rows 34 against 30;
+// 8 of up to 500 with 64 rows 11 against 39 (8192 keys times heads).
+constexpr uint32_t kFewRows = 32, kSomeRows = 64;
+constexpr uint64_t kFewKeys = 1u << 16;     // times heads, as the table's width bounds them
 constexpr uint32_t kMaxSms = 160;           // the division uses no more (workspace)
 constexpr uint32_t kFewCtas = 5 * kMaxSms;  // of attention_rows.cu: 5 an SM with tiles of 8 rows, 4 with
 constexpr uint32_t kFewTile = 16, kTile = 256;      // tiles of 16, whose parts are then the larger
@@ -183,11 +189,13 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     a.groupdiv = make_fastdiv(a.group);
     const uint32_t ctas = std::min<uint32_t>((uint32_t)sms, kMaxSms);
     a.tiles = 0;
-    const bool many = !few(a.group, c.max_new);
+    const uint64_t keys = ((uint64_t)c.c.width << c.c.page_log) * c.c.seqs * c.c.heads;
+    const uint32_t few_rows = keys <= kFewKeys ? kSomeRows : kFewRows;
+    const bool many = (uint64_t)a.group * c.max_new > few_rows;
     // A lone sequence is one kernel's, whatever it has.
     const bool rows = !many || c.c.seqs > 1u;
     if (many) {
-        a.over = rows ? kFewRows : 0u;
+        a.over = rows ? few_rows : 0u;
         a.upto = 0xFFFFFFFFu;
         a.min_steps = 4;
         e = launch_attention_tiles(a, fmt, dim, ctas, s);
@@ -196,10 +204,10 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     }
     if (rows && e == cudaSuccess) {
         a.over = 0;
-        a.upto = many ? kFewRows : 0xFFFFFFFFu;
+        a.upto = many ? few_rows : 0xFFFFFFFFu;
         a.min_steps = 8;
         // tiles of 8 rows where no sequence has more, else of 16
-        const uint32_t most = std::max(many ? kFewRows : a.max_new * a.group, 1u), rows_of = most <= 8u ? 8u : kFewTile;
+        const uint32_t most = std::max(many ? few_rows : a.max_new * a.group, 1u), rows_of = most <= 8u ? 8u : kFewTile;
         a.tiles = (most + rows_of - 1) / rows_of;
         uint32_t n = 0;         // at most kFewCtas
         e = launch_attention_rows(a, fmt, dim, rows_of, ctas, (uint64_t)c.c.width << c.c.page_log, n, s);
