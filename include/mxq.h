@@ -628,7 +628,8 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  *   heads    a multiple of kv_heads (MXQ_ERR_SHAPE), at most 256 of them to one
  *            (MXQ_ERR_UNSUPPORTED).
  *   max_new  at least the rows of every sequence (a bound known to the host); a
- *            sequence with more is left out and sets MXQ_DEV_INVALID_PAGE.
+ *            sequence with more is left out and sets MXQ_DEV_INVALID_PAGE (as one
+ *            that is longer than its row of the table).
  *   scale    any finite number.
  *   o        out, bf16 [T, heads, head_dim], 16-byte aligned.
  *   lse      out, fp32 [T, heads], or NULL.

@@ -57,7 +57,8 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-// Sequence b as this launch sees it: rows 0 where it is another launch's, or invalid.
+// Sequence b as this launch sees it: rows 0 where it is another launch's, or invalid (one
+// that is longer than its row of the table among them: the length bounds the work).
 struct Sequence {
     uint32_t first, n, rows;
     int64_t len;
@@ -66,14 +67,14 @@ __device__ __forceinline__ Sequence sequence(const AttArgs &a, uint32_t b)
 {
     Sequence s;
     s.n = new_tokens(a.c, b, a.T, s.first);
-    if (s.n > a.max_new) {
+    s.len = max(__ldg(a.c.lens + b), 0);
+    if (s.n > a.max_new || (s.n > 0u && s.len > (int64_t)a.c.width << a.c.page_log)) {
         atomicOr(a.c.status, MXQ_DEV_INVALID_PAGE);
         s.n = 0;
     }
     s.rows = s.n * a.group;
     if (s.rows <= a.over || s.rows > a.upto)
         s.n = s.rows = 0;
-    s.len = max(__ldg(a.c.lens + b), 0);
     return s;
 }
 

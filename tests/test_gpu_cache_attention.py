@@ -137,6 +137,18 @@ def test_bad_pages_leave_the_other_sequences(new, group):
     assert r["status"].item() == mxq.DEV_INVALID_PAGE
 
 
+@pytest.mark.parametrize("new", [1, 90])
+def test_a_sequence_longer_than_its_table_is_left_out(new):
+    """A length that no table holds costs nothing and leaves the other sequence alone."""
+    cache, ln, table = filled("mxfp8", [100, 300], 2, 16, 64, 3)
+    q = torch.randn((2 * new, 4, 64), generator=gen(1), device="cuda").bfloat16()
+    cu = dev32([0, new, 2 * new])
+    for bad in (2 ** 31 - 1, table.shape[1] * 16 + 1):
+        r = mxq.cache_attention(cache, q, cu, dev32([bad, 300]), table, new)
+        assert r["status"].item() == mxq.DEV_INVALID_PAGE and (r["o"][:new] == 0).all()
+        check(r, cache, q, cu, ln, table, 0.125, rows=slice(new, None))
+
+
 @pytest.mark.parametrize("news,most", [([3, 1], 2), ([200, 90], 100)])
 def test_a_sequence_of_more_rows_than_said_is_left_out(news, most):
     cache, ln, table = filled("nvfp4", [300, 300], 1, 16, 128, 3)
