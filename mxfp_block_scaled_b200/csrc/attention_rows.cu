@@ -19,11 +19,13 @@
 //
 // Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
 // 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 69 us (328 MB, 4.8
-// TB/s, 73 % of the measured copy rate), NVFP4 69 us, heads of 64 94 us, 32 sequences with
-// heads of 256 79 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
+// TB/s, 74 % of the measured copy rate), NVFP4 65 us, heads of 64 94 us, 32 sequences with
+// heads of 256 74 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
 // up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 46 us.  One
 // sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
-// wins (12 of 16384 as above by clusters 120 us, 59 us divided).
+// wins (12 of 16384 as above by clusters 120 us, divided 59 then).  Two warps to a turn, each
+// with half of its keys' scores and half of the columns, so that 32 rows fit: 59 us for
+// the 12 of 16384 against 46, the barrier of a turn costs more than a second decoding.
 //
 // Precision.  E2M1 times its E4M3 scale is exact in f16.  E4M3 codes (MXFP8) are
 // multiplied in f16 by their block's power of two relative to the largest of the
@@ -56,8 +58,10 @@ struct Shape {
     static constexpr uint32_t codes = kKeys * row, scales = kKeys * blocks;
     static constexpr uint32_t stage = 2 * (codes + scales);     // k codes, v codes, k scales, v scales
     static constexpr uint32_t ring = 2 * stage;                 // of a warp
-    static constexpr bool q_regs = D * NT <= 256;                    // queries in registers
-    static constexpr uint32_t q_pitch = D * 2 + 16;             // bytes of a query row in shared memory
+    static constexpr bool q_regs = D * NT <= 128;                    // queries in registers
+    // Bytes of a lane's run of a query row in shared memory, and of a row: 8 lanes' loads of
+    // 16 bytes (four runs of two rows) touch every bank once.
+    static constexpr uint32_t q_run = D / 2 + (D == 64 ? 0 : 32), q_pitch = 4 * q_run + 16;
     static constexpr uint32_t outs = R * (D + 4) * 4;       // a warp's outputs, when they are joined
     static constexpr uint32_t smem = kWarps * ring + R * q_pitch;
     static constexpr uint32_t all = smem > kWarps * outs ? smem : kWarps * outs;
@@ -246,7 +250,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 const float f = row_factor(m);
 #pragma unroll
                 for (uint32_t j = 0; j < per / 2; ++j)
-                    *reinterpret_cast<uint32_t *>(qs + r * S::q_pitch + (lane * per + 2 * j) * 2) =
+                    *reinterpret_cast<uint32_t *>(qs + r * S::q_pitch + (lane >> 3) * S::q_run + ((lane & 7u) * per + 2 * j) * 2) =
                         half2_bits(bf16_lo(x[n][j]) * f, bf16_hi(x[n][j]) * f);
                 if (lane == 0)
                     factor[r] = 1.0f / f;
@@ -265,14 +269,14 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 pos[nt][i] = row < rows ? pos0 + fastdiv(row, a.groupdiv) : 0x7FFFFFFF;
             }
         // This lane's run of a query: values [t4 D / 4, + D / 4) of row g8 of every 8.
-        uint2 q[NT][S::q_regs ? D / 16 : 1];
-        const char *qa = qs + g8 * S::q_pitch + t4 * (D / 2);
+        uint4 q[NT][S::q_regs ? D / 32 : 1];        // of two products each
+        const char *qa = qs + g8 * S::q_pitch + t4 * S::q_run;
         if (S::q_regs)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    q[nt][i] = lds64(qa + nt * 8 * S::q_pitch + i * 8);
+                for (int i = 0; i < D / 32; ++i)
+                    q[nt][i] = lds128(qa + nt * 8 * S::q_pitch + i * 16);
         float kfac = 1.0f;
         if (FMT == MXQ_FMT_NVFP4)
             kfac = __ldg(a.c.k_s2 + head);
@@ -389,11 +393,14 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                             const uint32_t a1 = hmul2_bits(h[1][2 * u], kscale[1][blk]), a3 = hmul2_bits(h[1][2 * u + 1], kscale[1][blk]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 x = S::q_regs ? q[nt][step % (S::q_regs ? D / 16 : 1)] : lds64(qa + nt * 8 * S::q_pitch + step * 8);
+                                if (!S::q_regs && step % 2 == 0)
+                                    q[nt][0] = lds128(qa + nt * 8 * S::q_pitch + step * 8);
+                                const uint4 x = q[nt][S::q_regs ? step / 2 : 0];
+                                const uint32_t lo = step % 2 ? x.z : x.x, hi = step % 2 ? x.w : x.y;
                                 if (step == 0)
-                                    mma16816_first(c[nt], a0, a1, a2, a3, x.x, x.y);
+                                    mma16816_first(c[nt], a0, a1, a2, a3, lo, hi);
                                 else
-                                    mma16816(c[nt], a0, a1, a2, a3, x.x, x.y);
+                                    mma16816(c[nt], a0, a1, a2, a3, lo, hi);
                             }
                         }
                     }
