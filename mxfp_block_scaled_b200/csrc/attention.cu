@@ -140,8 +140,9 @@ template <uint32_t R, int D>
 cudaError_t join_of(const AttArgs &a, uint32_t ctas, uint32_t tiles, cudaStream_t s)
 {
     // Few tiles have many parts: eight warps a row (a decoding step over 65536 tokens, 222
-    // parts of each of two tiles, with one 50 us more).
-    if ((uint64_t)tiles * R <= 4096u)
+    // parts of each of two tiles, with one 50 us more; 64 sequences with 3 or 4 parts a tile
+    // 1 us less with one).
+    if (ctas > 8u * tiles)
         return launch_dependent(attention_join_kernel<R, D, 8>, dim3(tiles, R), 256, 0, s, a, ctas);
     return launch_dependent(attention_join_kernel<R, D, 1>, dim3(tiles, R / 8), 256, 0, s, a, ctas);
 }
