@@ -170,7 +170,7 @@ def _workspace(op, n, rows, cols, device):
 
 
 def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _need(name, t, nbytes):
@@ -436,7 +436,7 @@ def mxq_moe_forward(x, T, hidden, topk_ids, topk_weights, topk, fmt, experts, in
 
 
 def mxq_linear(x, T, K, fmt, codes, scales, s2, N, out, y, status, workspace, stream=None):
-    dev = _device(_first(x, status))
+    dev = _device(_first(x, status) if x is None else x)
     nb = N * K // (16 if fmt == "nvfp4" else 32)
     rc = _enqueue(load().mxq_linear,
                   (_buf("x", x, 2 * T * K, dev), T, K, FMT[fmt], _buf("codes", codes, _code_bytes(fmt, N * K), dev),
