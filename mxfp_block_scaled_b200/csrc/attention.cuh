@@ -41,6 +41,7 @@ struct AttArgs {
     uint32_t T, group, max_new;
     uint32_t over, upto;        // the sequences of this launch: those of over < rows <= upto
     uint32_t min_steps;         // of a CTA, where there are few
+    uint32_t extra;             // steps that stand for what a tile costs beside its keys, before its first
     uint32_t tiles;             // of a sequence and head, at most
     float scale;                // softmax scale times log2(e)
     uint16_t *o;
@@ -88,7 +89,7 @@ struct Division {
     }
     static __device__ __forceinline__ uint32_t steps(const AttArgs &a, const Sequence &s, uint32_t rt)
     {
-        return max((keys(a, s, rt) + (1u << LOG) - 1u) >> LOG, 1u);
+        return max((keys(a, s, rt) + (1u << LOG) - 1u) >> LOG, 1u) + a.extra;
     }
     static __device__ __forceinline__ uint32_t tiles(const Sequence &s) { return (s.rows + R - 1u) / R; }
 
@@ -208,9 +209,12 @@ struct Walk {
     uint32_t keys;              // the tile's keys
 
     __device__ __forceinline__ bool whole() const { return k1 - k0 == steps; }
+    // The piece's first step of keys, and the one behind its last.
+    __device__ __forceinline__ uint32_t from(const AttArgs &a) const { return max(k0, a.extra) - a.extra; }
+    __device__ __forceinline__ uint32_t to(const AttArgs &a) const { return max(k1, a.extra) - a.extra; }
 
-    // The piece at the walk's place, of as many steps as the range has left; back to `to`.
-    __device__ __forceinline__ void take(const AttArgs &a, Walk &to)
+    // The piece at the walk's place, of as many steps as the range has left; back to `out`.
+    __device__ __forceinline__ void take(const AttArgs &a, Walk &out)
     {
         steps = Div::steps(a, s, rt);
         keys = Div::keys(a, s, rt);
@@ -218,10 +222,10 @@ struct Walk {
         left -= k1 - k0;
         __syncwarp();
         if ((threadIdx.x & 31u) == 0u)
-            to = *this;
+            out = *this;
         __syncwarp();
     }
-    static __device__ __noinline__ bool begin(Walk &to, const AttArgs &a, const Range &r)
+    static __device__ __noinline__ bool begin(Walk &out, const AttArgs &a, const Range &r)
     {
         Walk w;
         w.left = r.end - r.begin;
@@ -255,12 +259,12 @@ struct Walk {
                 return false;
         }
         w.k0 = (uint32_t)at;
-        w.take(a, to);
+        w.take(a, out);
         return true;
     }
-    static __device__ __noinline__ bool next(Walk &to, const AttArgs &a)
+    static __device__ __noinline__ bool next(Walk &out, const AttArgs &a)
     {
-        Walk w = to;
+        Walk w = out;
         if (w.left == 0)
             return false;
         w.k0 = 0;
@@ -275,7 +279,7 @@ struct Walk {
                 } while (w.s.rows == 0);
             }
         }
-        w.take(a, to);
+        w.take(a, out);
         return true;
     }
 };

@@ -18,10 +18,10 @@
 // the values need no transposition; the weights are turned by movmatrix.
 //
 // Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
-// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 69 us (328 MB, 4.8
-// TB/s, 74 % of the measured copy rate), NVFP4 65 us, heads of 64 94 us, 32 sequences with
-// heads of 256 74 us; with keys as right operands and rows as 16 left ones 98 us.  12 of
-// up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 46 us.  One
+// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 65 us (328 MB, 5.1
+// TB/s, 77 % of the measured copy rate), NVFP4 63 us, heads of 64 88 us, 32 sequences with
+// heads of 256 68 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
+// 12 of up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 42 us.  One
 // sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
 // wins (12 of 16384 as above by clusters 120 us, divided 59 then).  Two warps to a turn, each
 // with half of its keys' scores and half of the columns, so that 32 rows fit: 59 us for
@@ -135,8 +135,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             return;             // all of the cluster
         w.steps = W::Div::steps(a, w.s, tile);
         w.keys = W::Div::keys(a, w.s, tile);
-        w.k0 = (uint32_t)((uint64_t)w.steps * rank / ranks);
-        w.k1 = (uint32_t)((uint64_t)w.steps * (rank + 1u) / ranks);
+        w.k0 = a.extra + (uint32_t)((uint64_t)(w.steps - a.extra) * rank / ranks);
+        w.k1 = a.extra + (uint32_t)((uint64_t)(w.steps - a.extra) * (rank + 1u) / ranks);
         w.left = 0;
         __syncwarp();
         if (lane == 0)
@@ -158,7 +158,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
     for (; more; more = !CLUSTER && W::next(walk, sa)) {
         const uint32_t first = walk.s.first, rows = walk.s.rows, tile = walk.rt, head = walk.head, b = walk.b;
         const int64_t pos0 = walk.s.len - walk.s.n;           // position of the sequence's first new token
-        const uint32_t k0 = walk.k0 << kLog, k1 = min(walk.k1 << kLog, walk.keys);
+        const uint32_t k0 = walk.from(a) << kLog, k1 = min(walk.to(a) << kLog, walk.keys);
         __syncthreads();
         // Pages of a turn's keys, as the table has them: 32 keys lie on one page, or on two of 16
         // tokens.  Looked up a turn before the copies are made, which are a turn ahead themselves.
