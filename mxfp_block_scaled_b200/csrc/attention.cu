@@ -17,12 +17,14 @@ cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t 
 
 namespace {
 
-// Sequences of up to this many rows are attention_rows.cu's, and of up to kSomeRows where
-// all have few keys: its 16 rows a tile decode a key again for every tile, while
-// attention_tiles.cu takes 30 us to begin.  Measured, rows against tiles, 2 key/value heads
-// of 128, MXFP8: 64 sequences of up to 4096 with 16 rows 46 against 46 us, 32 rows 58 against
-// 68, 64 rows 92 against 75; one of 30000 with 32 rows 26 against 29, 64 rows 34 against 30;
-// 8 of up to 500 with 64 rows 11 against 39 (8192 keys times heads).
+// Sequences of up to kSomeRows rows are attention_rows.cu's; of MXFP8, where there are many
+// keys, up to kFewRows: its 16 rows a tile decode a key again for every tile, while
+// attention_tiles.cu takes 30 us to begin.  Measured, rows against tiles, 2 key/value heads.
+// 64 sequences of up to 4096 with 32 rows: MXFP8 45 against 66 us (heads of 128), 83 against
+// 113 (256); NVFP4 42 against 61, 58 against 100.  With 64 rows: MXFP8 70 against 73, 150
+// against 123 (16 of 16384: 58 against 54, 109 against 88); NVFP4 63 against 69, 97 against
+// 110.  8 of up to 500 with 64 rows (8192 keys times heads) 10 against 39, one of 30000
+// (61440) 34 against 30.
 constexpr uint32_t kFewRows = 32, kSomeRows = 64;
 constexpr uint64_t kFewKeys = 1u << 16;     // times heads, as the table's width bounds them
 constexpr uint32_t kMaxSms = 160;           // the division uses no more (workspace)
@@ -191,7 +193,7 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     const uint32_t ctas = std::min<uint32_t>((uint32_t)sms, kMaxSms);
     a.tiles = 0;
     const uint64_t keys = ((uint64_t)c.c.width << c.c.page_log) * c.c.seqs * c.c.heads;
-    const uint32_t few_rows = keys <= kFewKeys ? kSomeRows : kFewRows;
+    const uint32_t few_rows = fmt == MXQ_FMT_NVFP4 || keys <= kFewKeys ? kSomeRows : kFewRows;
     const bool many = (uint64_t)a.group * c.max_new > few_rows;
     // A lone sequence is one kernel's, whatever it has.
     const bool rows = !many || c.c.seqs > 1u;
