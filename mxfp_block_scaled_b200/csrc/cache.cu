@@ -20,7 +20,7 @@
 // The reader moves bytes: 24 sequences of up to 8192 tokens, 4 heads of 128, 258 MB with
 // MXFP8 in 48 us (82 % of a plain copy's rate; 59 with a look-up for each unit), 218 MB
 // with NVFP4 in 42 us.  The writer of NVFP4 is bound by the quantizer's arithmetic (4/6
-// tries two scales), as the tensor quantizer is: 17000 tokens of 8 heads in about 37 us
+// tries two scales), as the tensor quantizer is: 17000 tokens of 8 heads in about 36 us
 // (4/6), 25 (RTN); MXFP8 21 us.
 #include "mx_block.cuh"
 #include "mxq_cache.cuh"
@@ -88,7 +88,7 @@ __device__ __forceinline__ void find_places(const CacheView &c, uint32_t row0, u
 } // namespace
 
 template <int FMT, bool FOUR_SIX, int PER>
-__global__ void __launch_bounds__(256) cache_write_kernel(const WriteArgs a)
+__global__ void __launch_bounds__(256, 3) cache_write_kernel(const WriteArgs a)
 {
     constexpr bool fp4 = FMT == MXQ_FMT_NVFP4;
     __shared__ uint64_t place[kMostRows];
