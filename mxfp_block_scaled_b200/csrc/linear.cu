@@ -53,7 +53,8 @@ struct Args {
     uint32_t slots;             // of a warp's ring
     uint32_t xstride;           // bytes of a staged row
     uint32_t direct;            // scales are read where they lie (rows of them are not 4- or 8-byte aligned)
-    FastDiv griddiv, rowdiv;    // CTAs; 16-byte pieces of a token
+    uint32_t per, rest;         // tasks of a CTA, one more of the first `rest`
+    FastDiv rowdiv;             // 16-byte pieces of a token
 };
 
 template <int FMT>
@@ -143,7 +144,7 @@ linear_kernel(const Args a)
 
     const uint32_t tok0 = blockIdx.y * a.cap, ntok = min(a.cap, a.T - tok0);
     float *part = reinterpret_cast<float *>(xs + a.cap * a.xstride);
-    const uint32_t t0 = fastdiv(a.tiles * blockIdx.x, a.griddiv), t1 = fastdiv(a.tiles * (blockIdx.x + 1u), a.griddiv);
+    const uint32_t t0 = a.per * blockIdx.x + min(blockIdx.x, a.rest), t1 = t0 + a.per + (blockIdx.x < a.rest ? 1u : 0u);
     const uint32_t lg = a.kslog, ks = 1u << lg, teams = warps >> lg, team = warp >> lg, q = warp & (ks - 1u);
     const uint32_t c0 = (a.chunks * q) >> lg, c1 = (a.chunks * (q + 1u)) >> lg;
 
@@ -445,7 +446,8 @@ cudaError_t plan(const LinearArgs &l, int out_f32, int sms, cudaStream_t s)
     a.slots = std::min((kSmemMax - rows - warps * nt * sums) / (warps * kSlot), kMostSlots);
     const uint32_t smem = rows + warps * (a.slots * kSlot + nt * sums);
     const uint32_t ctas = (uint32_t)std::min<uint64_t>((uint64_t)sms, a.tiles);
-    a.griddiv = make_fastdiv(ctas);
+    a.per = a.tiles / ctas;
+    a.rest = a.tiles % ctas;
     a.kslog = 0;
     while (a.kslog < 3 && warps % (2u << a.kslog) == 0 && (2u << a.kslog) <= a.chunks &&
            ((uint64_t)a.tiles * 2 << a.kslog) <= (uint64_t)ctas * warps)

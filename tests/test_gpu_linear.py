@@ -112,6 +112,17 @@ def test_scales_at_odd_addresses_and_the_end_of_y(fmt):
     assert torch.equal(y[:63].view(3, 21), want) and (y[63:] == 7).all()
 
 
+def test_hundreds_of_millions_of_rows():
+    """16-row tasks times CTAs past 32 bits, and codes past the fourth gibibyte."""
+    N, K = 480_000_007, 32
+    codes = torch.empty((N, 16), dtype=torch.uint8, device="cuda").random_(generator=gen(1))
+    scales = torch.empty((N, 1), dtype=torch.uint8, device="cuda").random_(120, 131, generator=gen(2))
+    x = torch.randn((1, K), generator=gen(3), device="cuda").bfloat16()
+    y = mxq.linear(x, {"codes": codes, "scales": scales}, "mxfp4")["y"][0]
+    rows = torch.cat((torch.arange(64), torch.arange(N - 64, N), torch.randint(0, N, (20000,), generator=torch.Generator().manual_seed(4)))).cuda()
+    check(y[rows][None], x, {"codes": codes[rows], "scales": scales[rows], "fmt": "mxfp4"}, "bf16")
+
+
 def test_empty_sizes():
     w = {"codes": torch.empty((9, 0), dtype=torch.uint8, device="cuda"), "scales": torch.empty((9, 0), dtype=torch.uint8, device="cuda")}
     x = torch.empty((2, 0), dtype=torch.bfloat16, device="cuda")
