@@ -626,7 +626,7 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  *   q        bf16, row t at q + t q_stride (values): [heads, head_dim].  16-byte
  *            aligned, q_stride a multiple of 8 and at least heads * head_dim.
  *   heads    a multiple of kv_heads (MXQ_ERR_SHAPE), at most 256 of them to one
- *            (MXQ_ERR_UNSUPPORTED).
+ *            (MXQ_ERR_UNSUPPORTED); T heads below 2^31 (MXQ_ERR_SHAPE).
  *   max_new  at least the rows of every sequence (a bound known to the host); a
  *            sequence with more is left out and sets MXQ_DEV_INVALID_PAGE (as one
  *            that is longer than its row of the table).

@@ -50,8 +50,8 @@ namespace {
 
 // Tests of a barrier before a wait gives up.  A test suspends for 4 us at most, so that is
 // after a second; a step takes microseconds.  A group that has nothing to do waits for the
-// other's whole tiles, 64 times as long (and leaves at once where the other gives up).
-constexpr uint32_t kSpin = 1u << 18, kIdleSpin = kSpin << 6;
+// other's whole tiles, 8 times as long (and leaves at once where the other gives up).
+constexpr uint32_t kSpin = 1u << 18, kIdleSpin = kSpin << 3;
 constexpr uint32_t kCodeWarp = 8;
 constexpr int kThreads = 512;
 

@@ -90,6 +90,7 @@ def test_batches_that_every_call_refuses(lib, name, spec, over, code):
     ("mxq_cache_read", READ, dict(k=None), ARG), ("mxq_cache_read", READ, dict(v=P + 8), ALIGN),
     ("mxq_cache_attention", ATT, dict(heads=0), ARG), ("mxq_cache_attention", ATT, dict(heads=3), SHAPE),
     ("mxq_cache_attention", ATT, dict(heads=2 * 257, qs=1 << 16), UNSUPPORTED),
+    ("mxq_cache_attention", ATT, dict(T=1 << 29), SHAPE), ("mxq_cache_attention", ATT, dict(T=(1 << 31) - 1, heads=512, qs=1 << 15), SHAPE),
     ("mxq_cache_attention", ATT, dict(max_new=-1), ARG), ("mxq_cache_attention", ATT, dict(qs=248), SHAPE),
     ("mxq_cache_attention", ATT, dict(qs=260), ALIGN), ("mxq_cache_attention", ATT, dict(scale=NAN), ARG),
     ("mxq_cache_attention", ATT, dict(scale=INF), ARG), ("mxq_cache_attention", ATT, dict(q=None), ARG),

@@ -7,6 +7,7 @@ the sum; exponentials and the running rescaling add 2^-18; MXFP8 codes far below
 neighbour's and weights below f16's normal numbers add keys 2^-25 of the largest term.  The
 result is then rounded to bf16 (2^-8)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -234,6 +235,41 @@ def test_captured_replayed_and_side_by_side(new):
         graph.replay()
         for i, scale in enumerate((0.1, 0.2)):
             assert torch.equal(o[i], mxq.cache_attention(cache, q, cu, ln, table, new, scale=scale)["o"])
+
+
+def test_host_threads_with_streams_of_their_own():
+    """Calls of different sizes from several threads at once, against the same calls one by one."""
+    work = []
+    for seed, (lens, new, group, dim, fmt) in enumerate((([3000, 70], 1, 8, 128, "mxfp8"), ([900], 300, 2, 64, "nvfp4"),
+                                                         ([40] * 9, 4, 3, 256, "nvfp4"), ([2000, 10], 33, 4, 256, "mxfp8"))):
+        cache, ln, table = filled(fmt, lens, 2, 16, dim, seed)
+        q = torch.randn((new * len(lens), 2 * group, dim), generator=gen(seed), device="cuda").bfloat16()
+        w = layers.quantize_projection(torch.randn((700, 256), generator=gen(seed), device="cuda").bfloat16(), fmt)
+        x = torch.randn((new, 256), generator=gen(seed), device="cuda").bfloat16()
+        cu = dev32([i * new for i in range(len(lens) + 1)])
+        work.append(lambda stream, c=(cache, q, cu, ln, table, new), x=x, w=w, fmt=fmt: (
+            mxq.cache_attention(*c, stream=stream)["o"], mxq.linear(x, w, fmt, stream=stream)["y"]))
+    want = [f(None) for f in work]
+    torch.cuda.synchronize()
+    got, failed = [[None] * 20 for _ in work], []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            for n in range(20):
+                got[i][n] = work[i](stream)
+            stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for a, b in zip(got, want):
+        for o, y in a:
+            assert torch.equal(o, b[0]) and torch.equal(y, b[1])
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
