@@ -23,7 +23,7 @@
 namespace mxq {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e30f;       // a running maximum before the first key
+constexpr float kLowest = -3e38f;       // a running maximum before the first key
 
 // What a CTA leaves of the tile that it begins and does not finish (parts 0: none).
 struct Unfinished {

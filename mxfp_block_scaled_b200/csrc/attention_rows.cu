@@ -18,9 +18,9 @@
 // the values need no transposition; the weights are turned by movmatrix.
 //
 // Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
-// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 65 us (328 MB, 5.1
-// TB/s, 77 % of the measured copy rate), NVFP4 63 us, heads of 64 88 us, 32 sequences with
-// heads of 256 68 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
+// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 66 us (328 MB, 5.0
+// TB/s, 76 % of the measured copy rate), NVFP4 62 us, heads of 64 88 us, 32 sequences with
+// heads of 256 70 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
 // 12 of up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 42 us.  One
 // sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
 // wins (12 of 16384 as above by clusters 120 us, divided 59 then).  Two warps to a turn, each
@@ -450,25 +450,25 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         for (int j = i; j < 4; j += 2) {
                             if (cut)
                                 s[h][nt][j] = (int)(h * 16 + (j >> 1) * 8 + g8) <= lim[nt][i] ? s[h][nt][j] : -INFINITY;
+                            // (rounded once, here: the largest weight is 1 whatever the scores' size)
+                            s[h][nt][j] += E;
                             m = fmaxf(m, s[h][nt][j]);
                         }
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1)
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                    m += E;
                     alpha[nt][i] = 1.0f;
                     if (m > mx[nt][i] + 8.0f) {
                         alpha[nt][i] = ex2(mx[nt][i] - m);
                         mx[nt][i] = m;
                         moved = true;
                     }
-                    const float off = E - mx[nt][i];
                     float part = 0.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int j = i; j < 4; j += 2) {
-                            s[h][nt][j] = ex2(s[h][nt][j] + off);
+                            s[h][nt][j] = ex2(s[h][nt][j] - mx[nt][i]);
                             part += s[h][nt][j];
                         }
                     sum[nt][i] = fmaf(sum[nt][i], alpha[nt][i], part * inv);

@@ -26,9 +26,9 @@
 // Bound: a step of 256 x 64 x 128 costs the tensor cores 1024 cycles and the SM's 16
 // exponentials a cycle 1024 as well, beside which a softmax thread has two operations a
 // score in fp32 and a rounding to f16.  A chunk of 4096 tokens over 20480 of 32 query and
-// 4 key/value heads of 128 takes 1.26 ms (979 TFLOP/s, 60 % of the measured rate of a
-// bf16 product; NVFP4 1.18 ms; heads of 64 1.20 ms, of 256 half the chunk over 10240
-// 0.90 ms).  Steps that brought it there: 2.46 ms with one warp that issued for all and
+// 4 key/value heads of 128 takes 1.32 ms (935 TFLOP/s, 57 % of the measured rate of a
+// bf16 product; NVFP4 1.18 ms; heads of 64 1.24 ms, of 256 half the chunk over 10240
+// 0.92 ms).  Steps that brought it there: 2.46 ms with one warp that issued for all and
 // steps of 128 keys; 1.71 with products issued by the groups; 1.54 with steps of 64 keys and
 // an issuing warp a group (a warp is held while its products queue); 1.49 with fewer waits
 // between weights and scores; 1.26 with one copy of each loop and the division of the work
@@ -575,7 +575,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                     const int col = g * S::mine + x;
                                     m = fmaxf(m, __uint_as_float(v[col / 32][col % 32]));
                                 }
-                                top = fmaxf(top, fmaf(m, fac(g), e(g)));
+                                top = fmaxf(top, S::fp4 ? m * fac(g) : fmaf(m, fac(g), e(g)));
                             }
                             if (top > mx + 8.0f) {
                                 alpha = ex2(mx - top);
@@ -587,14 +587,17 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                         high = -INFINITY;
 #pragma unroll
                         for (int g = 0; g < groups; ++g) {
-                            const float fg = fac(g), bg = e(g) - mx;
-                            const float2 f2 = make_float2(fg, fg), b2 = make_float2(bg, bg);
+                            const float fg = fac(g), eg = e(g);
+                            const float2 f2 = make_float2(fg, fg), e2 = make_float2(eg, eg);
                             float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int x = 0; x < (int)S::mine / 2; ++x) {
                                 const int col = g * S::mine + 2 * x;
-                                float2 s = __ffma2_rn(make_float2(__uint_as_float(v[col / 32][col % 32]),
-                                                                  __uint_as_float(v[col / 32][col % 32 + 1])), f2, b2);
+                                float2 s = make_float2(__uint_as_float(v[col / 32][col % 32]), __uint_as_float(v[col / 32][col % 32 + 1]));
+                                // Rounded as the maximum was, so that the largest weight is 1 whatever the
+                                // scores' size (in one operation, 4 % faster with MXFP8, scores past 2^28
+                                // could give weights without bound).
+                                s = __fadd2_rn(S::fp4 ? __fmul2_rn(s, f2) : __ffma2_rn(s, f2, e2), make_float2(-mx, -mx));
                                 high = fmaxf(fmaxf(high, s.x), s.y);
                                 s.x = ex2(s.x);
                                 s.y = ex2(s.y);

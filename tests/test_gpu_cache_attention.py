@@ -118,6 +118,23 @@ def test_queries_and_values_of_very_different_sizes(fmt, new):
     check(mxq.cache_attention(cache, q, cu, ln, table, new), cache, q, cu, ln, table, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("new", [1, 5, 80])
+@pytest.mark.parametrize("low,high", [(-30, 4), (-90, -60), (30, 60), (60, 90)])
+def test_tokens_of_very_different_sizes(new, low, high):
+    """MXFP8 scales that lie up to 2^34 apart from one token and block to the next, and far
+    from 1; scores of ordinary size, of 2^30 and of 2^60 and more, of both signs."""
+    lens, dim = [600], 128
+    cache, ln, table = filled("mxfp8", lens, 1, 32, dim, 13)
+    g = gen(14)
+    k, v = (torch.randn((600, 1, dim // 32, 32), generator=g, device="cuda")
+            * torch.exp2(torch.randint(low, high + 1, (600, 1, dim // 32, 1), generator=g, device="cuda").float()) for _ in range(2))
+    mxq.cache_write(cache, k.view(600, 1, dim).bfloat16(), v.view(600, 1, dim).bfloat16(), dev32([0, 600]), ln, table)
+    q = torch.randn((new, 4, dim), generator=g, device="cuda").bfloat16()
+    cu = dev32([0, new])
+    for scale in (dim ** -0.5, 2.0 ** -high, 2.0 ** (24 - high), -2.0 ** (24 - high)):
+        check(mxq.cache_attention(cache, q, cu, ln, table, new, scale=scale), cache, q, cu, ln, table, scale)
+
+
 @pytest.mark.parametrize("new,group", [(2, 4), (70, 2)])
 def test_bad_pages_leave_the_other_sequences(new, group):
     lens = [100, 200, 90, 400]
