@@ -637,7 +637,8 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  *            then undefined); MXQ_DEV_WAIT_TIMEOUT.
  *   workspace at least mxq_cache_attention_workspace_bytes(...), 256-byte aligned.
  *            Two calls that overlap in time need one each.
- * A row without a key (its position is negative) gives zeros and -Inf.  Rows of no
+ * A row without a key (its position is negative) gives zeros and -Inf; one whose query
+ * holds Inf or NaN is undefined, the others are not touched by it.  Rows of no
  * sequence are left as they were.  What pages hold behind a sequence's last
  * position does not matter, NaN patterns included.  Codes and scales of the
  * positions read are taken to be finite, as mxq_cache_write leaves them.

@@ -147,6 +147,11 @@ def test_nonfinite_values_and_scales_are_reported():
         cache.v_s2[1] = s2
         assert mxq.cache_write(cache, x, x, cu, ln, table).item() == mxq.DEV_INVALID_SCALE
         assert (cache.v_codes[:, 1] == 0xA5).all() and not (cache.v_codes[1, 0, :4] == 0xA5).all()
+    cache = make_cache("nvfp4", 2, 2, 16, 64)       # a scale of zero: a head of zeros
+    cache.v_s2[1] = 0.0
+    assert mxq.cache_write(cache, x, x, cu, ln, table).item() == 0
+    assert (cache.v_codes[1, 1, :4] == 0).all() and (cache.v_scales[1, 1, :4] == 0).all()
+    assert (mxq.cache_read(cache, cu, ln, table, 4)["v"][:, 1] == 0).all()
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])

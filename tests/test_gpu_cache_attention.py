@@ -135,6 +135,23 @@ def test_tokens_of_very_different_sizes(new, low, high):
         check(mxq.cache_attention(cache, q, cu, ln, table, new, scale=scale), cache, q, cu, ln, table, scale)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+@pytest.mark.parametrize("new,group", [(1, 4), (3, 8), (150, 2)])
+def test_a_nonfinite_query_leaves_the_others(fmt, new, group):
+    cache, ln, table = filled(fmt, [900, 400], 1, 16, 128, 3)
+    q = torch.randn((2 * new, group, 128), generator=gen(1), device="cuda").bfloat16()
+    cu = dev32([0, new, 2 * new])
+    want = mxq.cache_attention(cache, q, cu, ln, table, new)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        z = q.clone()
+        z[new // 2, 1, 77] = bad
+        r = mxq.cache_attention(cache, z, cu, ln, table, new)
+        keep = torch.ones((2 * new, group), dtype=torch.bool, device="cuda")
+        keep[new // 2, 1] = False
+        assert torch.equal(r["o"][keep], want["o"][keep]) and torch.equal(r["lse"][keep], want["lse"][keep])
+        assert r["status"].item() == 0
+
+
 @pytest.mark.parametrize("new,group", [(2, 4), (70, 2)])
 def test_bad_pages_leave_the_other_sequences(new, group):
     lens = [100, 200, 90, 400]
