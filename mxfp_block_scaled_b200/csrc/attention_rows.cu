@@ -458,7 +458,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                     for (int o = 4; o < 32; o <<= 1)
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                     alpha[nt][i] = 1.0f;
-                    if (m > mx[nt][i] + 8.0f) {
+                    if (m - mx[nt][i] > 8.0f) {         // the weights' own difference, rounded as theirs
                         alpha[nt][i] = ex2(mx[nt][i] - m);
                         mx[nt][i] = m;
                         moved = true;

@@ -577,7 +577,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                 }
                                 top = fmaxf(top, S::fp4 ? m * fac(g) : fmaf(m, fac(g), e(g)));
                             }
-                            if (top > mx + 8.0f) {
+                            if (top - mx > 8.0f) {      // the weights' own difference, rounded as theirs
                                 alpha = ex2(mx - top);
                                 mx = top;
                                 sum *= alpha;
