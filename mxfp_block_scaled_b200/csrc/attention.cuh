@@ -23,7 +23,13 @@
 namespace mxq {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -3e38f;       // a running maximum before the first key
+// Weights are 2^(s - r), s a row's scores in powers of two.  The reference r is kTop below the
+// row's maximum when it is taken, and stays until a score lies more than kLag above it: the largest
+// weight is 2^kTop to 2^kLag, the top of f16's range, so that a weight keeps 11 bits down to 2^-21
+// of the largest and some down to 2^-31.  (The range is one of long contexts: with a maximum of 1,
+// 2^18 tokens whose weights are 2^-25 of a first token's lost all that they give.)
+constexpr float kTop = 7.0f, kLag = 15.0f;
+constexpr float kLowest = -3e38f;       // a reference before the first key
 
 // What a CTA leaves of the tile that it begins and does not finish (parts 0: none).
 struct Unfinished {

@@ -427,7 +427,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 inv = __uint_as_float((uint32_t)(261 - (int)vtop) << 23);      // 2^-E, vtop at least 27 (and at most 254)
             }
 
-            // Running maximum, which stays unless it grows by more than 2^8; weights.
+            // The reference (attention.cuh), and weights.
             int lim[NT][2], least = kKeys - 1;          // last key of the turn that a row sees
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -450,7 +450,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         for (int j = i; j < 4; j += 2) {
                             if (cut)
                                 s[h][nt][j] = (int)(h * 16 + (j >> 1) * 8 + g8) <= lim[nt][i] ? s[h][nt][j] : -INFINITY;
-                            // (rounded once, here: the largest weight is 1 whatever the scores' size)
+                            // (rounded once, here: no weight is above 2^kLag whatever the scores' size)
                             s[h][nt][j] += E;
                             m = fmaxf(m, s[h][nt][j]);
                         }
@@ -458,7 +458,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                     for (int o = 4; o < 32; o <<= 1)
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                     alpha[nt][i] = 1.0f;
-                    if (m - mx[nt][i] > 8.0f) {         // the weights' own difference, rounded as theirs
+                    if (m - mx[nt][i] > kLag) {         // the weights' own difference, rounded as theirs
+                        m -= kTop;
                         alpha[nt][i] = ex2(mx[nt][i] - m);
                         mx[nt][i] = m;
                         moved = true;

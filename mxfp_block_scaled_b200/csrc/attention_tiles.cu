@@ -17,11 +17,10 @@
 // all four; scores of a step are issued as soon as the product that reads the weights in
 // their place is done, a buffer's count of steps ahead.
 //
-// Weights are taken against the maximum so far; only where a score exceeds it by more
-// than 2^8 is the new maximum found, the step's weights are taken again, and the output
+// Weights are taken against a reference (attention.cuh); only where a score lies too far
+// above it is the maximum found, the step's weights are taken again, and the output
 // in TMEM is rescaled (by the softmax group, which has the output to itself between its
-// products).  Weights are 2^8 at most then, exact powers of two apart from what they
-// would be.  MXFP8 powers: as in attention_rows.cu, a largest one for every 32 (16) keys.
+// products).  MXFP8 powers: as in attention_rows.cu, a largest one for every 32 (16) keys.
 //
 // Bound: a step of 256 x 64 x 128 costs the tensor cores 1024 cycles and the SM's 16
 // exponentials a cycle 1024 as well, beside which a softmax thread has two operations a
@@ -545,8 +544,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     // 0, which times -Inf would be NaN), of the values.
                     auto fac = [&](int g) { return S::fp4 ? fq : fmaxf(fq * bars.kfac[t % kRing][g], 0x1p-126f); };
                     auto e = [&](int g) { return S::fp4 ? 0.0f : bars.vexp[t % kRing][g]; };
-                    // Weights against the maximum so far, which stays unless a row's grows by more
-                    // than 2^8; then (and at first) the maximum is found first, and the weights
+                    // Weights against the reference so far, unless a row's lie more than kLag above
+                    // it; then (and at first) the maximum is found first, and the weights
                     // from the scores again.  (One copy of each loop: cold instruction caches are
                     // what a short call waits for.)
                     uint32_t p[groups][S::mine / 2];
@@ -577,7 +576,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                 }
                                 top = fmaxf(top, S::fp4 ? m * fac(g) : fmaf(m, fac(g), e(g)));
                             }
-                            if (top - mx > 8.0f) {      // the weights' own difference, rounded as theirs
+                            if (top - mx > kLag) {      // the weights' own difference, rounded as theirs
+                                top -= kTop;
                                 alpha = ex2(mx - top);
                                 mx = top;
                                 sum *= alpha;
@@ -594,7 +594,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             for (int x = 0; x < (int)S::mine / 2; ++x) {
                                 const int col = g * S::mine + 2 * x;
                                 float2 s = make_float2(__uint_as_float(v[col / 32][col % 32]), __uint_as_float(v[col / 32][col % 32 + 1]));
-                                // Rounded as the maximum was, so that the largest weight is 1 whatever the
+                                // Rounded as the maximum was, so that no weight is above 2^kLag whatever the
                                 // scores' size (in one operation, 4 % faster with MXFP8, scores past 2^28
                                 // could give weights without bound).
                                 s = __fadd2_rn(S::fp4 ? __fmul2_rn(s, f2) : __ffma2_rn(s, f2, e2), make_float2(-mx, -mx));
@@ -606,7 +606,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             }
                             total = S::fp4 ? total + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t % kRing][g], total);
                         }
-                        if (find || !__any_sync(0xFFFFFFFFu, high > 8.0f))
+                        if (find || !__any_sync(0xFFFFFFFFu, high > kLag))
                             break;
                         find = true;
                     }

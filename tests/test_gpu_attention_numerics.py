@@ -1,9 +1,17 @@
 """Attention over the quantized cache where its numbers reach far: scores whose neighbours in
-fp32 lie 16 apart."""
+fp32 lie 16 apart, weights far below the largest, values of very different sizes.
+
+Bounds as in test_gpu_cache_attention.py, without its allowance for what lies far below the
+largest term.  In its place, of weights: they are rounded to f16, whose step below its normal
+numbers is 2^-24, and the largest one of a row stands at 2^4 or above, so each is off by 2^-29
+of the largest at most."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
+import cache_ref as ref
 from mxfp_block_scaled_b200 import mxq
 from test_gpu_cache import dev32, gen
 
@@ -38,6 +46,31 @@ def attend(cache, q, ln, table, scale):
     r = mxq.cache_attention(cache, q, dev32([0, new]), ln, table, new, scale=scale)
     assert r["status"].item() == 0
     return r
+
+
+def check(r, cache, q, ln, table, scale, more=0.0):
+    """Every output and lse; `more`: a further allowance of outputs."""
+    cu = [0, q.shape[0]]
+    o, lse, weight, spread = ref.attention(cache, q, cu, ln.tolist(), table, scale)
+    eps = 2 * (cache.head_dim + 8) * 2.0 ** -23 * spread
+    largest = largest_weight(cache, q, ln, table, scale, lse)
+    size = ref.sequence_values(cache, 0, ln, table)[1].abs().amax(0)        # [1, dim], of a column
+    bound = 1.01 * (o.abs() * 2.0 ** -8 + weight * (2.0 ** -11 + eps[..., None] + 2.0 ** -18) * (1 + 2.0 ** -8)) \
+        + int(ln[0]) * 2.0 ** -28 * largest[..., None] * size + more + 1e-30
+    worst = ((r["o"].double() - o).abs() / bound).max().item()
+    assert worst <= 1, worst
+    off = ((r["lse"].double() - lse).abs() / (eps + 2.0 ** -18 + lse.abs() * 2.0 ** -22)).max().item()
+    assert off <= 1, off
+
+
+def largest_weight(cache, q, ln, table, scale, lse):
+    """The largest softmax weight of each row, [T, heads]."""
+    k = ref.sequence_values(cache, 0, ln, table)[0][:, 0]
+    new = q.shape[0]
+    s = scale * torch.einsum("ihd,jd->ihj", q.double(), k)
+    pos = int(ln[0]) - new + torch.arange(new, device=q.device)
+    s.masked_fill_((torch.arange(k.shape[0], device=q.device)[None] > pos[:, None])[:, None], -math.inf)
+    return torch.exp(s.amax(-1) - lse)
 
 
 def scale_with(bits):
@@ -85,3 +118,25 @@ def test_scores_whose_neighbours_lie_sixteen_apart(fmt, new):
         assert torch.isfinite(r["o"].float()).all() and torch.isfinite(r["lse"]).all(), bits
         assert (r["o"].float() >= 1).all() and (r["o"].float() <= 2).all(), bits
     assert found >= 4
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("every", [1 << 30, 32])
+@pytest.mark.parametrize("below", [16.3, 22.7, 24.6, 26.2])
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+def test_weights_far_below_the_largest(fmt, below, every, new):
+    """A first token that takes the weight (or one in 32 tokens) and has no value, and many whose
+    weights are 2^-below of its: the output is theirs."""
+    n, dim = 1 << 18, 64
+    cache, ln, table = one_sequence(fmt, n, dim)
+    k, v = rows_of(cache.k_codes, n), rows_of(cache.v_codes, n)
+    sink = torch.arange(n, device="cuda") % every == 0
+    one = 0x38 if fmt == "mxfp8" else 0x02
+    k[:, 0] = torch.where(sink, one, 0).to(torch.uint8)
+    codes = torch.tensor([0x38, 0x3C, 0x40, 0x30] if fmt == "mxfp8" else [0x22, 0x33, 0x44, 0x21], device="cuda", dtype=torch.uint8)
+    v[:] = codes[torch.randint(0, 4, v.shape, generator=gen(1), device="cuda")]
+    v[sink] = 0
+    q = torch.zeros((new, 1, dim), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = below / LOG2E
+    check(attend(cache, q, ln, table, scale), cache, q, ln, table, scale)
