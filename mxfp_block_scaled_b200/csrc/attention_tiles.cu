@@ -574,7 +574,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                     const int col = g * S::mine + x;
                                     m = fmaxf(m, __uint_as_float(v[col / 32][col % 32]));
                                 }
-                                top = fmaxf(top, S::fp4 ? m * fac(g) : fmaf(m, fac(g), e(g)));
+                                top = fmaxf(top, fmaf(m, fac(g), e(g)));
                             }
                             if (top - mx > kLag) {      // the weights' own difference, rounded as theirs
                                 top -= kTop;
@@ -588,7 +588,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
                         for (int g = 0; g < groups; ++g) {
                             const float fg = fac(g), eg = e(g);
-                            const float2 f2 = make_float2(fg, fg), e2 = make_float2(eg, eg);
+                            const float2 f2 = make_float2(fg, fg), e2 = make_float2(eg, eg);    // (NVFP4: a zero)
                             float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int x = 0; x < (int)S::mine / 2; ++x) {
@@ -596,8 +596,9 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                 float2 s = make_float2(__uint_as_float(v[col / 32][col % 32]), __uint_as_float(v[col / 32][col % 32 + 1]));
                                 // Rounded as the maximum was, so that no weight is above 2^kLag whatever the
                                 // scores' size (in one operation, 4 % faster with MXFP8, scores past 2^28
-                                // could give weights without bound).
-                                s = __fadd2_rn(S::fp4 ? __fmul2_rn(s, f2) : __ffma2_rn(s, f2, e2), make_float2(-mx, -mx));
+                                // could give weights without bound).  A packed product and sum are made one
+                                // operation by the compiler; this form leaves it nothing to join.
+                                s = __fadd2_rn(__ffma2_rn(s, f2, e2), make_float2(-mx, -mx));
                                 high = fmaxf(fmaxf(high, s.x), s.y);
                                 s.x = ex2(s.x);
                                 s.y = ex2(s.y);

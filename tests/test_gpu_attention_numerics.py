@@ -14,6 +14,7 @@ import torch
 import cache_ref as ref
 from mxfp_block_scaled_b200 import mxq
 from test_gpu_cache import dev32, gen
+from test_gpu_cache_attention import filled
 
 pytestmark = pytest.mark.gpu
 LOG2E = 1.4426950408889634
@@ -118,6 +119,21 @@ def test_scores_whose_neighbours_lie_sixteen_apart(fmt, new):
         assert torch.isfinite(r["o"].float()).all() and torch.isfinite(r["lse"]).all(), bits
         assert (r["o"].float() >= 1).all() and (r["o"].float() <= 2).all(), bits
     assert found >= 4
+
+
+@pytest.mark.parametrize("new", [1, 5, 80])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+def test_scores_of_any_size(fmt, dim, new):
+    """Scores up to 2^60 that are no round numbers: a product rounded in one place and not in
+    another would leave weights without bound.  Outputs lie between the values."""
+    cache, ln, table = filled(fmt, [3000], 1, 32, dim, 17, spread=0)
+    q = torch.randn((new, 4, dim), generator=gen(5), device="cuda").bfloat16()
+    v = ref.sequence_values(cache, 0, ln, table)[1].abs().amax()
+    for power in (20, 24, 25, 26, 27, 28, 29, 30, 33, 40, 57):
+        for scale in (1.37 * 2.0 ** power, -1.61 * 2.0 ** power):
+            r = attend(cache, q, ln, table, scale)
+            assert torch.isfinite(r["lse"]).all() and (r["o"].double().abs() <= v * (1 + 2.0 ** -8)).all(), scale
 
 
 @pytest.mark.parametrize("new", [1, 70])
