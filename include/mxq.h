@@ -645,10 +645,14 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  * Scores, maxima, sums and outputs are fp32, weights are rounded to 11 bits above
  * 2^-21 of a row's largest and are off by at most 2^-32 of it below;
  * repeated calls give the same bits (the order of the sums follows from the sizes,
- * the lengths of the batch's sequences and the number of SMs).  MXFP8: exact
- * while the block maxima of neighbouring tokens lie within 2^22 of one another (what
- * is smaller is off by at most 2^-41 of the largest); blocks of keys or values whose
- * largest element is below 2^-100 lose bits, down to zero. */
+ * the lengths of the batch's sequences and the number of SMs).  MXFP8: a
+ * token's codes enter the products exactly while its block scales are within 2^21 of
+ * the largest one of the head among 64 tokens (from a position that is a multiple of
+ * 64 on); below that they lose bits, and keys 2^-31, values 2^-24 of the largest may
+ * count as zeros.  Weights below 2^-17 of a row's largest are then off by at most
+ * 2^-28 of it.  Other tokens' sizes do not matter (up to 2^60 between the values
+ * of a sequence).  Blocks of keys or values whose largest element is below 2^-100
+ * lose bits, down to zero. */
 MXQ_API mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride,
                                        int64_t T, int64_t heads, const int32_t *cu, const int32_t *lens,
                                        const int32_t *table, int64_t seqs, int64_t width, int64_t max_new,

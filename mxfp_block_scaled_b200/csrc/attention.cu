@@ -38,7 +38,8 @@ bool few(int64_t group, int64_t max_new) { return group * max_new <= (int64_t)kF
 
 } // namespace
 
-// Parts of unfinished tiles, added up in their order.  Of the `ctas` CTAs of the kernel
+// Parts of unfinished tiles, each its own keys' output, weighed by their sums and added up in
+// their order.  Of the `ctas` CTAs of the kernel
 // before, blockIdx.x counts those that began one; blockIdx.y its rows, 8 / WPR to a CTA.
 // WPR warps share a row's parts, and their sums are added in the order of the warps;
 // lanes have its columns.
@@ -46,7 +47,7 @@ template <uint32_t R, int D, uint32_t WPR>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttArgs a, uint32_t ctas)
 {
     __shared__ uint32_t found, count[8];
-    __shared__ float sums[8][D + 1];
+    __shared__ float sums[8][D];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
@@ -83,12 +84,26 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     for (int j = 0; j < per; ++j)
         v[j] = 0.0f;
     if (in) {
-        // maximum over the parts: the first is the CTA's second, the others their CTAs' first
-        for (uint32_t i = lane; i < u.parts; i += 32u)
-            m = fmaxf(m, part_of<R, D>(a, cta + i, i == 0u)[R * D + r * 2u]);
+        // maximum and sum over the parts: the first is the CTA's second, the others their CTAs' first
+        auto stat = [&](uint32_t i) {
+            return *reinterpret_cast<const float2 *>(part_of<R, D>(a, cta + i, i == 0u) + R * D + r * 2u);
+        };
+        const float2 own = lane < u.parts ? stat(lane) : make_float2(kLowest, 0.0f);
+        m = own.x;
+        for (uint32_t i = lane + 32u; i < u.parts; i += 32u)
+            m = fmaxf(m, stat(i).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        l = own.y * ex2(own.x - m);
+        for (uint32_t i = lane + 32u; i < u.parts; i += 32u) {
+            const float2 st = stat(i);
+            l = fmaf(st.y, ex2(st.x - m), l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        const float inv = inverse(l);
 #pragma unroll 8
         for (uint32_t i = q; i < u.parts; i += WPR) {
             const float *p = part_of<R, D>(a, cta + i, i == 0u);
@@ -100,8 +115,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < per; j += 4)
                     *reinterpret_cast<float4 *>(x + j) = *reinterpret_cast<const float4 *>(p + r * D + lane * per + j);
-            const float f = ex2(st.x - m);
-            l = fmaf(st.y, f, l);
+            const float f = st.y * ex2(st.x - m) * inv;
 #pragma unroll
             for (int j = 0; j < per; ++j)
                 v[j] = fmaf(x[j], f, v[j]);
@@ -111,24 +125,20 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < per; ++j)
             sums[warp][lane * per + j] = v[j];
-        if (lane == 0)
-            sums[warp][D] = l;
         __syncthreads();
         if (q != 0u)
             return;
 #pragma unroll
-        for (uint32_t w = 1; w < WPR; ++w) {
-            l += sums[warp + w][D];
+        for (uint32_t w = 1; w < WPR; ++w)
 #pragma unroll
             for (int j = 0; j < per; ++j)
                 v[j] += sums[warp + w][lane * per + j];
-        }
     }
     if (!in)
         return;
     const uint32_t row = u.row0 + r, i = fastdiv(row, a.groupdiv), h = u.head * a.group + row - i * a.group;
     const uint64_t out = (uint64_t)(u.first + i) * (a.c.heads * a.group) + h;
-    const float f = l == 0.0f ? 0.0f : (a.c.v_s2 ? __ldg(a.c.v_s2 + u.head) : 1.0f) / l;
+    const float f = a.c.v_s2 ? __ldg(a.c.v_s2 + u.head) : 1.0f;
 #pragma unroll
     for (int j = 0; j < per; j += 2)
         *reinterpret_cast<__nv_bfloat162 *>(a.o + out * D + lane * per + j) = __floats2bfloat162_rn(v[j] * f, v[j + 1] * f);

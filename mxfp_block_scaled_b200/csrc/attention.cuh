@@ -53,7 +53,7 @@ struct AttArgs {
     uint16_t *o;
     float *lse;
     Unfinished *left;           // [CTA]
-    float *part;                // [CTA][2][R][dim] outputs, [R][2] maxima and sums
+    float *part;                // [CTA][2][R][dim] outputs of its keys alone, [R][2] references and sums
     FastDiv groupdiv;
 };
 
@@ -63,6 +63,37 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// 1 / x, off by a unit of the last place; 0 for a sum of no keys.
+__device__ __forceinline__ float inverse(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return x == 0.0f ? 0.0f : r;
+}
+
+// MXFP8 values enter the products relative to a power of two, 2^(ref - 134) where `ref` is a
+// scale byte: codes times 2^(their scale - ref + 7), in f16.  It follows the scales of the keys at
+// hand, and the output so far is rescaled where it moves (fp32, exact): no power enters the weights or
+// their sum, so a large value takes nothing from tokens that are multiplied apart from it.  What
+// kZeros and below count as is left to it; and it stays within 2^60 of the largest so far, so that no
+// output leaves fp32.
+constexpr uint32_t kZeros = 27, kSpan = 60;
+struct ValueRef {
+    uint32_t ref = kZeros, most = kZeros;
+
+    // For keys whose largest scale is `top`, which may lie `slack` below the reference: the factor of
+    // the output so far.
+    __device__ __forceinline__ float follow(uint32_t top, uint32_t slack)
+    {
+        const uint32_t was = ref;
+        if (top > ref || (top + slack < ref && top > kZeros))
+            ref = max(top, max(most, kSpan) - kSpan);
+        most = max(most, ref);
+        return __uint_as_float((uint32_t)max(127 + (int)was - (int)ref, 0) << 23);
+    }
+    __device__ __forceinline__ float unit() const { return __uint_as_float((ref - 7u) << 23); }
+};
 
 // Sequence b as this launch sees it: rows 0 where it is another launch's, or invalid (one
 // that is longer than its row of the table among them: the length bounds the work).

@@ -30,12 +30,12 @@
 // Precision.  E2M1 times its E4M3 scale is exact in f16.  E4M3 codes (MXFP8) are
 // multiplied in f16 by their block's power of two relative to the largest of the
 // warp's 32 keys, 2^7 at most: exact while the blocks' maxima lie within 2^22 of one
-// another, below that off by 2^-25 / 57344 of the largest.  The largest one's power
-// itself multiplies the scores in fp32, and for the values it enters the running
-// maximum, m = max(s + E): weights are w = 2^(s + E - m), so an output needs no
-// second factor.  Queries are held in f16 times a power of two of the row (as the
+// another, below that off by 2^-25 / 57344 of the largest, and zero from 2^-32 on.  The
+// largest one's power itself multiplies the scores in fp32.  Values: relative to a
+// reference of the warp and the 32 columns of the block (ValueRef), so columns do not
+// share it; it may stand one above the 32 keys' largest, exact within 2^21 then.  Queries are held in f16 times a power of two of the row (as the
 // layer's tokens, moe.cu); weights are rounded to f16's 11 bits, an eighth of the bf16
-// result's own step; scores, maxima, sums and outputs are fp32.
+// result's own step; scores, references, sums and outputs are fp32.
 #include "attention.cuh"
 #include "mxq_cluster.cuh"
 #include "mxq_mma.cuh"
@@ -287,7 +287,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.0f;
-        float mx[NT][2], sum[NT][2];
+        float mx[NT][2], sum[NT][2];        // references and sums
+        ValueRef vref;                      // of the block of this lane's columns (MXFP8)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mx[nt][0] = mx[nt][1] = kLowest;
@@ -338,7 +339,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         }
                     }
                 } else {
-                    uint32_t e[2][nblk], top = 27u;     // 2^-100 at least: what is below counts as zeros
+                    uint32_t e[2][nblk], top = kZeros;      // what is below counts as zeros (2^-100)
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -409,22 +410,24 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        s[half][nt][j] = c[nt][j] * (fq[nt][j & 1] * kf);
+                        // (rounded here, not with the subtraction below: no weight is above 2^kLag
+                    // whatever the scores' size)
+                    s[half][nt][j] = __fmul_rn(c[nt][j], fq[nt][j & 1] * kf);
             }
 
-            // E: the largest power of the values' scales.
-            float E = 0.0f, inv = 1.0f;
-            uint32_t vtop = 27u;
+            // The largest scale of the values of this lane's block; lanes of a g8 have a quarter each.
+            float shift = 1.0f;
             if (!S::fp4) {
+                uint32_t vtop = 0u;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t r = (i >> 1) * 8 + 2 * t4 + (i & 1), blk = D == 64 ? g8 >> 2 : D == 128 ? g8 >> 1 : g8;
                     const uint32_t e = *reinterpret_cast<const uint8_t *>(vsc + r * S::blocks + blk);
                     vtop = max(vtop, r < left ? e : 0u);
                 }
-                vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
-                E = (float)((int)vtop - 134);
-                inv = __uint_as_float((uint32_t)(261 - (int)vtop) << 23);      // 2^-E, vtop at least 27 (and at most 254)
+                vtop = max(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, 1));
+                vtop = max(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, 2));
+                shift = vref.follow(vtop, 1u);
             }
 
             // The reference (attention.cuh), and weights.
@@ -438,7 +441,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 }
             const bool cut = __any_sync(0xFFFFFFFFu, least < (int)kKeys - 1);
             float alpha[NT][2];
-            bool moved = false;
+            bool moved = shift != 1.0f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -450,8 +453,6 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         for (int j = i; j < 4; j += 2) {
                             if (cut)
                                 s[h][nt][j] = (int)(h * 16 + (j >> 1) * 8 + g8) <= lim[nt][i] ? s[h][nt][j] : -INFINITY;
-                            // (rounded once, here: no weight is above 2^kLag whatever the scores' size)
-                            s[h][nt][j] += E;
                             m = fmaxf(m, s[h][nt][j]);
                         }
 #pragma unroll
@@ -472,17 +473,17 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                             s[h][nt][j] = ex2(s[h][nt][j] - mx[nt][i]);
                             part += s[h][nt][j];
                         }
-                    sum[nt][i] = fmaf(sum[nt][i], alpha[nt][i], part * inv);
+                    sum[nt][i] = fmaf(sum[nt][i], alpha[nt][i], part);
                 }
             if (!first_turn && __any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        acc[j][nt][0] *= alpha[nt][0];
-                        acc[j][nt][1] *= alpha[nt][1];
-                        acc[j][nt][2] *= alpha[nt][0];
-                        acc[j][nt][3] *= alpha[nt][1];
+                        acc[j][nt][0] *= alpha[nt][0] * shift;
+                        acc[j][nt][1] *= alpha[nt][1] * shift;
+                        acc[j][nt][2] *= alpha[nt][0] * shift;
+                        acc[j][nt][3] *= alpha[nt][1] * shift;
                     }
             }
             first_turn = false;
@@ -515,8 +516,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                         if (S::fp4)
                             vscale[i][j] = e4m3x2_to_f16x2(w0 | (w1 << 8));
                         else
-                            vscale[i][j] = half2_bits(__uint_as_float((uint32_t)max((int)(w0 + 134u) - (int)vtop, 0) << 23),
-                                                      __uint_as_float((uint32_t)max((int)(w1 + 134u) - (int)vtop, 0) << 23));
+                            vscale[i][j] = half2_bits(__uint_as_float((uint32_t)max((int)(w0 + 134u) - (int)vref.ref, 0) << 23),
+                                                      __uint_as_float((uint32_t)max((int)(w1 + 134u) - (int)vref.ref, 0) << 23));
                     }
                 constexpr int run = S::row / 8;          // bytes of a lane's run of columns
                 constexpr int words = run < 16 ? run / 4 : 4;
@@ -597,33 +598,44 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 }
         __syncthreads();
         float *outs = reinterpret_cast<float *>(smem) + warp * (S::outs / 4);
+        // Row r's reference and sum of all warps.
+        auto row_stat = [&](uint32_t r, float &l) {
+            float m = stat[0][0][r];
+#pragma unroll
+            for (uint32_t w = 1; w < kWarps; ++w)
+                m = fmaxf(m, stat[0][w][r]);
+            l = 0.0f;
+#pragma unroll
+            for (uint32_t w = 0; w < kWarps; ++w)
+                l = fmaf(stat[1][w][r], ex2(stat[0][w][r] - m), l);
+            return m;
+        };
+        // Each warp's share of the CTA's output: divided by the sum here, so that values near the
+        // end of fp32's range stay in it.
+        const float unit = S::fp4 ? 1.0f : vref.unit();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t r = nt * 8 + 2 * t4 + i;
-                float m = stat[0][0][r];
-#pragma unroll
-                for (uint32_t w = 1; w < kWarps; ++w)
-                    m = fmaxf(m, stat[0][w][r]);
-                const float f = ex2(mx[nt][i] - m);
+                float l;
+                const float m = row_stat(r, l), f = ex2(mx[nt][i] - m) * inverse(l);
                 // the run of lanes g8, two values a product
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     const uint32_t jj = S::row == 256 ? (2 * j) ^ ((g8 & 1u) * 16u) : 2 * j;
                     *reinterpret_cast<float2 *>(outs + r * (D + 4) + g8 * (D / 8) + jj) =
-                        make_float2(acc[j][nt][i] * f, acc[j][nt][2 + i] * f);
+                        make_float2(acc[j][nt][i] * f * unit, acc[j][nt][2 + i] * f * unit);
                 }
             }
         __syncthreads();
         const float vfac = FMT == MXQ_FMT_NVFP4 ? __ldg(a.c.v_s2 + head) : 1.0f;
         const bool whole = walk.whole();
         float *part = part_of<kRows, D>(a, blockIdx.x, walk.k0 == 0u);
-        auto put = [&](uint32_t r, uint32_t d, float m, float l, float4 v) {        // 4 columns of a finished row
+        auto put = [&](uint32_t r, uint32_t d, float m, float l, float4 v) {        // 4 columns of a finished row; m, l where d is 0
             const uint32_t row = tile * kRows + r, it = fastdiv(row, a.groupdiv), h = head * a.group + row - it * a.group;
             const uint64_t out = (uint64_t)(first + it) * (a.c.heads * a.group) + h;
-            const float f = l == 0.0f ? 0.0f : vfac / l;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * vfac, v.y * vfac), hi = __floats2bfloat162_rn(v.z * vfac, v.w * vfac);
             *reinterpret_cast<uint2 *>(a.o + out * D + d) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             if (d == 0 && a.lse)
@@ -636,15 +648,12 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             const uint32_t r = i / (D / 4), d = i % (D / 4) * 4;
             if (tile * kRows + r >= rows)
                 continue;
-            float m = stat[0][0][r];
-#pragma unroll
-            for (uint32_t w = 1; w < kWarps; ++w)
-                m = fmaxf(m, stat[0][w][r]);
-            float l = 0.0f;
+            float m = 0.0f, l = 0.0f;
+            if (d == 0)
+                m = row_stat(r, l);
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (uint32_t w = 0; w < kWarps; ++w) {
-                l = fmaf(stat[1][w][r], ex2(stat[0][w][r] - m), l);
                 const float4 x = *reinterpret_cast<const float4 *>(all + w * (S::outs / 4) + r * (D + 4) + d);
                 v.x += x.x;
                 v.y += x.y;
@@ -673,21 +682,30 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
                 const uint32_t r = i / (D / 4), d = i % (D / 4) * 4;
                 if (tile * kRows + r >= rows)
                     continue;
-                float m = kLowest;
-                for (uint32_t c = 0; c < ranks; ++c)
-                    m = fmaxf(m, peer_f(&joint[0][r], c));
-                float l = 0.0f;
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                for (uint32_t c = 0; c < ranks; ++c) {
-                    const float f = ex2(peer_f(&joint[0][r], c) - m);
-                    const float4 x = peer_f4(reinterpret_cast<const float4 *>(sum4 + r * (D + 4) + d), c);
-                    l = fmaf(peer_f(&joint[1][r], c), f, l);
-                    v.x = fmaf(x.x, f, v.x);
-                    v.y = fmaf(x.y, f, v.y);
-                    v.z = fmaf(x.z, f, v.z);
-                    v.w = fmaf(x.w, f, v.w);
+                float share[8], m = kLowest, l = 0.0f;      // of the CTAs (8 at most)
+#pragma unroll
+                for (uint32_t c = 0; c < 8u; ++c) {
+                    share[c] = c < ranks ? peer_f(&joint[0][r], c) : kLowest;
+                    m = fmaxf(m, share[c]);
                 }
+#pragma unroll
+                for (uint32_t c = 0; c < 8u; ++c)
+                    if (c < ranks) {
+                        share[c] = peer_f(&joint[1][r], c) * ex2(share[c] - m);
+                        l += share[c];
+                    }
+                const float f = inverse(l);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (uint32_t c = 0; c < 8u; ++c)
+                    if (c < ranks) {
+                        const float4 x = peer_f4(reinterpret_cast<const float4 *>(sum4 + r * (D + 4) + d), c);
+                        const float g = share[c] * f;
+                        v.x = fmaf(x.x, g, v.x);
+                        v.y = fmaf(x.y, g, v.y);
+                        v.z = fmaf(x.z, g, v.z);
+                        v.w = fmaf(x.w, g, v.w);
+                    }
                 put(r, d, m, l, v);
             }
             cluster_sync_all();         // every CTA's sums have been read

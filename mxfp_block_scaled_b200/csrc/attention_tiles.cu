@@ -20,7 +20,12 @@
 // Weights are taken against a reference (attention.cuh); only where a score lies too far
 // above it is the maximum found, the step's weights are taken again, and the output
 // in TMEM is rescaled (by the softmax group, which has the output to itself between its
-// products).  MXFP8 powers: as in attention_rows.cu, a largest one for every 32 (16) keys.
+// products).  MXFP8 powers: keys as in attention_rows.cu, a largest one for every 32 (16) keys.
+// Values the same, the largest scale rounded up to an even one (exact within 2^21); all columns of
+// a step share a reference (ValueRef, which may stand 2^4 above a step's largest), and the
+// weights of keys whose own largest is not the reference are multiplied by the difference,
+// in f16: of a step's 64 keys, values 2^-24 of the largest count as zeros.  (Even ones, so that
+// neighbouring chunks mostly have the same.)
 //
 // Bound: a step of 256 x 64 x 128 costs the tensor cores 1024 cycles and the SM's 16
 // exponentials a cycle 1024 as well, beside which a softmax thread has two operations a
@@ -77,7 +82,8 @@ constexpr uint32_t kRing = 16;              // steps whose powers are kept; deco
 struct Bars {
     uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], odone[2], qfull[2], ffull[kRing], meet, drain[2];
     uint32_t tmem, abort;
-    float kfac[kRing][4], vexp[kRing][4], vinv[kRing][4];       // by step and chunk: powers of keys, values
+    float kfac[kRing][4];       // by step and chunk: powers of the keys,
+    uint32_t vtop[kRing][4];    // largest scales of the values
 };
 
 // Further tests of a barrier whose first one failed.
@@ -431,7 +437,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             load();
         }
         while (more) {
-            uint32_t top = 27u;     // 2^-100 at least: what is below counts as zeros
+            uint32_t top = values ? kZeros - 1u : kZeros;       // what is below counts as zeros (2^-100)
             if (!S::fp4) {
                 uint32_t m = raw.s[0];
 #pragma unroll
@@ -439,6 +445,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     m = __vmaxu4(m, raw.s[i]);
                 m = __vmaxu4(m, m >> 16);
                 top = __reduce_max_sync(0xFFFFFFFFu, max(top, max(m & 0xFFu, (m >> 8) & 0xFFu)));
+                top = values ? (top + 1u) & ~1u : top;
             }
             // The next chunk's place; its pages are on the way while this one is stored.
             const uint32_t now = t, chunk = dw;
@@ -450,10 +457,9 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             if (!wait_all(&empty[now % S::stages], now / S::stages + 1u, bars, a.c.status))
                 break;
             if (!S::fp4 && lane == 0) {         // the slot was read long ago (kRing)
-                if (values) {
-                    bars.vexp[now % kRing][chunk] = (float)((int)top - 134);
-                    bars.vinv[now % kRing][chunk] = __uint_as_float((uint32_t)(261 - (int)top) << 23);
-                } else
+                if (values)
+                    bars.vtop[now % kRing][chunk] = top;
+                else
                     bars.kfac[now % kRing][chunk] = __uint_as_float(top << 23) * 0x1p-7f;
                 mbar_arrive(&bars.ffull[now % kRing]);
             }
@@ -521,6 +527,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 const int64_t base = (int64_t)w.k0 << S::log, pos = in ? w.s.len - w.s.n + i : 0x7FFFFFFFll;
                 const int last = (int)max(min(pos, (int64_t)w.keys - 1) - base, (int64_t)-1);
                 float mx = kLowest, sum = 0.0f;
+                ValueRef vref;
                 const uint32_t steps = un.steps;
                 const bool two = un.two;
                 // phases of this group's buffers: of the even ones and the odd ones of its units
@@ -530,8 +537,24 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     const uint32_t phase = two ? (j & 1u ? p1 : p0) + (j >> 1)
                                                : (buf & 2u ? (buf & 1u ? buf0[3] : buf0[2]) : (buf & 1u ? buf0[1] : buf0[0])) + (j >> 2);
                     const uint32_t at = tmem + buf * S::keys + lanes;
-                    ok = (S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a.c.status)) &&
-                         wait_all(&bars.sfull[buf], phase, bars, a.c.status);
+                    ok = S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a.c.status);
+                    if (!ok)
+                        break;
+                    // The reference of the values, before the scores are there.
+                    float shift = 1.0f;
+                    bool level = true;      // all of the step's keys have it
+                    if constexpr (!S::fp4) {
+                        uint32_t largest = 0, smallest = 255u;
+#pragma unroll
+                        for (int g = 0; g < S::chunks; ++g) {
+                            const uint32_t v = bars.vtop[t % kRing][g];
+                            largest = max(largest, v);
+                            smallest = min(smallest, v);
+                        }
+                        shift = vref.follow(largest, 4u);
+                        level = smallest == vref.ref;
+                    }
+                    ok = wait_all(&bars.sfull[buf], phase, bars, a.c.status);
                     if (!ok)
                         break;
                     fence_after();
@@ -541,9 +564,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     const int lim = last - (int)(j << S::log);
                     const bool cut = __any_sync(0xFFFFFFFFu, lim < (int)S::keys - 1);
                     // Of a chunk's columns: powers of the keys (with the row's own factor, kept above
-                    // 0, which times -Inf would be NaN), of the values.
+                    // 0, which times -Inf would be NaN).
                     auto fac = [&](int g) { return S::fp4 ? fq : fmaxf(fq * bars.kfac[t % kRing][g], 0x1p-126f); };
-                    auto e = [&](int g) { return S::fp4 ? 0.0f : bars.vexp[t % kRing][g]; };
                     // Weights against the reference so far, unless a row's lie more than kLag above
                     // it; then (and at first) the maximum is found first, and the weights
                     // from the scores again.  (One copy of each loop: cold instruction caches are
@@ -574,7 +596,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                     const int col = g * S::mine + x;
                                     m = fmaxf(m, __uint_as_float(v[col / 32][col % 32]));
                                 }
-                                top = fmaxf(top, fmaf(m, fac(g), e(g)));
+                                top = fmaxf(top, __fmul_rn(m, fac(g)));
                             }
                             if (top - mx > kLag) {      // the weights' own difference, rounded as theirs
                                 top -= kTop;
@@ -587,8 +609,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                         high = -INFINITY;
 #pragma unroll
                         for (int g = 0; g < groups; ++g) {
-                            const float fg = fac(g), eg = e(g);
-                            const float2 f2 = make_float2(fg, fg), e2 = make_float2(eg, eg);    // (NVFP4: a zero)
+                            const float fg = fac(g);
+                            const float2 f2 = make_float2(fg, fg);
                             float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int x = 0; x < (int)S::mine / 2; ++x) {
@@ -597,21 +619,31 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                 // Rounded as the maximum was, so that no weight is above 2^kLag whatever the
                                 // scores' size (in one operation, 4 % faster with MXFP8, scores past 2^28
                                 // could give weights without bound).  A packed product and sum are made one
-                                // operation by the compiler; this form leaves it nothing to join.
-                                s = __fadd2_rn(__ffma2_rn(s, f2, e2), make_float2(-mx, -mx));
+                                // operation by the compiler; with a zero added there is nothing to join.
+                                s = __fadd2_rn(__ffma2_rn(s, f2, make_float2(0.0f, 0.0f)), make_float2(-mx, -mx));
                                 high = fmaxf(fmaxf(high, s.x), s.y);
                                 s.x = ex2(s.x);
                                 s.y = ex2(s.y);
                                 part = __fadd2_rn(part, s);
                                 p[g][x] = half2_bits(s.x, s.y);
                             }
-                            total = S::fp4 ? total + (part.x + part.y) : fmaf(part.x + part.y, bars.vinv[t % kRing][g], total);
+                            total += part.x + part.y;
                         }
                         if (find || !__any_sync(0xFFFFFFFFu, high > kLag))
                             break;
                         find = true;
                     }
                     sum += total;
+                    if (!level) {
+#pragma unroll
+                        for (int g = 0; g < groups; ++g) {
+                            const float f = __uint_as_float((127u - min(vref.ref - bars.vtop[t % kRing][g], 30u)) << 23);
+                            const uint32_t f2 = half2_bits(f, f);
+#pragma unroll
+                            for (int x = 0; x < (int)S::mine / 2; ++x)
+                                p[g][x] = hmul2_bits(p[g][x], f2);
+                        }
+                    }
 #pragma unroll
                     for (int g = 0; g < groups; ++g) {
                         if constexpr (S::mine == 32)
@@ -621,16 +653,16 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                                          ::"r"(at + g * 8), "r"(p[g][0]), "r"(p[g][1]), "r"(p[g][2]), "r"(p[g][3]),
                                            "r"(p[g][4]), "r"(p[g][5]), "r"(p[g][6]), "r"(p[g][7]) : "memory");
                     }
-                    // Where a row's maximum has grown the output is rescaled, once the product before
+                    // Where a reference has moved the output is rescaled, once the product before
                     // this one is done.  (A wait is for a barrier's next phase.  Of two groups each has
                     // two buffers of scores, so with these scores the product before that one is done;
                     // a group alone has four, and waits at every step.)
-                    const bool grown = j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
-                    if (j > 0 && (grown || !two)) {
+                    const bool moved = j > 0 && (shift != 1.0f || __any_sync(0xFFFFFFFFu, alpha != 1.0f));
+                    if (j > 0 && (moved || !two)) {
                         if (!(ok = wait_all(&bars.pv[wg], pv0 + j - 1u, bars, a.c.status)))
                             break;
                     }
-                    if (grown) {
+                    if (moved) {
                         fence_after();
                         const uint32_t out = tmem + kOut + wg * D + lanes;
 #pragma unroll 1
@@ -640,7 +672,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             tmem_ld_wait(o);
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * (alpha * shift));
                             tmem_st32(out + c * 32, o);
                         }
                     }
@@ -661,7 +693,9 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 const bool in1 = row1 < w.s.rows, whole = w.whole();
                 const uint64_t to = (uint64_t)(w.s.first + i1) * (a.c.heads * a.group) + h1;
                 float *part = part_of<S::rows, D>(a, blockIdx.x, w.k0 == 0u);
-                const float f2 = sum == 0.0f ? 0.0f : (S::fp4 ? __ldg(a.c.v_s2 + w.head) : 1.0f) / sum;
+                // A part is its own keys' output (the join has the factor of NVFP4).
+                const float f2 = (S::fp4 && whole ? __ldg(a.c.v_s2 + w.head) : 1.0f) * inverse(sum);
+                const float unit = S::fp4 ? 1.0f : vref.unit();
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -676,17 +710,18 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             uint32_t b[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(o[x * 8 + y * 2]) * f2,
-                                                                              __uint_as_float(o[x * 8 + y * 2 + 1]) * f2);
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(o[x * 8 + y * 2]) * f2 * unit,
+                                                                              __uint_as_float(o[x * 8 + y * 2 + 1]) * f2 * unit);
                                 b[y] = *reinterpret_cast<const uint32_t *>(&p);
                             }
                             dst[x] = make_uint4(b[0], b[1], b[2], b[3]);
                         }
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(part + (wg * 128u + r) * D + c * 32);
+                        float4 *dst = reinterpret_cast<float4 *>(part + (wg * 128u + r) * D + c * 32);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            dst[x] = make_uint4(o[x * 4], o[x * 4 + 1], o[x * 4 + 2], o[x * 4 + 3]);
+                            dst[x] = make_float4(__uint_as_float(o[x * 4]) * f2 * unit, __uint_as_float(o[x * 4 + 1]) * f2 * unit,
+                                                 __uint_as_float(o[x * 4 + 2]) * f2 * unit, __uint_as_float(o[x * 4 + 3]) * f2 * unit);
                     }
                 }
                 if (in1 && whole && a.lse)
