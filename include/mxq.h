@@ -48,7 +48,8 @@
  *     scale is negative or not finite (that group's outputs are undefined),
  *     MXQ_DEV_INVALID_EXPERT when an expert id is not below the number of
  *     experts (it is left out), MXQ_DEV_INVALID_PAGE when a token's page is
- *     not one of the cache's (see mxq_cache).  `status` may be NULL on the MX entry point
+ *     not one of the cache's, or a batch's rows are not the call's (see
+ *     mxq_cache).  `status` may be NULL on the MX entry point
  *     only (the check is then skipped); elsewhere it is required.
  *   - Input bf16 data must be 16-byte aligned; code and scale outputs
  *     must be 16-byte aligned; fp32 / fp64 arrays naturally aligned.
@@ -567,6 +568,10 @@ MXQ_API mxq_status mxq_linear(const uint16_t *x, int64_t T, int64_t K, mxq_fmt f
  *   cu       int32 [seqs + 1], ascending: rows cu[b] .. cu[b + 1] - 1 of the
  *            call's tensors are sequence b's.  Rows before cu[0] and from
  *            cu[seqs] on belong to none: nothing is read or written for them.
+ *            A sequence whose entries descend, are negative or lie behind the call's
+ *            rows is left out by every call and sets MXQ_DEV_INVALID_PAGE (of a batch in
+ *            which they descend mxq_cache_write and mxq_cache_read may leave out
+ *            others, too).
  *   lens     int32 [seqs]: tokens the sequence has in the cache once its rows
  *            are in it.  Row i of a sequence of n rows stands for position
  *            lens[b] - n + i; a row whose position is negative has no place.

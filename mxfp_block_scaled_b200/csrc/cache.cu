@@ -72,13 +72,19 @@ __device__ __forceinline__ Unit unit_at(uint32_t in, const Split &s)
     return u;
 }
 
-// Places of the CTA's rows (kNowhere: none), by all threads.
-__device__ __forceinline__ void find_places(const CacheView &c, uint32_t row0, uint32_t n, uint64_t (&place)[kMostRows])
+// Places of the CTA's rows (kNowhere: none), by all threads.  The first CTA looks at every
+// sequence's rows, for those that are none of the call's are no row's here.
+__device__ __forceinline__ void find_places(const CacheView &c, uint32_t row0, uint32_t n, uint32_t T, uint64_t (&place)[kMostRows])
 {
+    if (blockIdx.x == 0)
+        for (uint32_t b = threadIdx.x; b < c.seqs; b += blockDim.x) {
+            uint32_t first;
+            new_tokens(c, b, T, first);
+        }
     for (uint32_t i0 = threadIdx.x & ~31u; i0 < n; i0 += blockDim.x) {
         const uint32_t i = i0 + (threadIdx.x & 31u);
         uint64_t at;
-        const bool ok = find_place(c, row0 + min(i, n - 1u), at);
+        const bool ok = find_place(c, row0 + min(i, n - 1u), T, at);
         if (i < n)
             place[i] = ok ? at : kNowhere;
     }
@@ -123,7 +129,7 @@ __global__ void __launch_bounds__(256, 3) cache_write_kernel(const WriteArgs a)
                 v[i][1] = __ldg(p + 1);
             }
             if (!looked)
-                find_places(a.c, row0, rows, place);
+                find_places(a.c, row0, rows, a.s.T, place);
             looked = true;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a)
     cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t row0 = blockIdx.x * a.s.rows, rows = min(a.s.rows, a.s.T - row0);
     const uint32_t off = fastdiv(threadIdx.x, a.s.perdiv);
-    find_places(a.c, row0, rows, place);
+    find_places(a.c, row0, rows, a.s.T, place);
     if (off >= a.s.pass)
         return;
     for (uint32_t in = threadIdx.x - off * a.s.per; in < a.s.per; in += blockDim.x) {

@@ -42,12 +42,21 @@ __device__ __forceinline__ uint32_t find_sequence(const CacheView &c, uint32_t r
     return __ldg(c.cu + lo) <= (int64_t)row && (int64_t)row < __ldg(c.cu + lo + 1) ? lo : c.seqs;
 }
 
-// New tokens of sequence b: at most `T`, none where cu descends.
+// Rows r0 .. r1 - 1 are rows of the call, which has T.
+__device__ __forceinline__ bool rows_ok(int32_t r0, int32_t r1, uint32_t T)
+{
+    return r0 >= 0 && r1 >= r0 && (uint32_t)r1 <= T;
+}
+
+// New tokens of sequence b; none, and the status bit, where cu descends or leaves the call's rows.
 __device__ __forceinline__ uint32_t new_tokens(const CacheView &c, uint32_t b, uint32_t T, uint32_t &first)
 {
-    const int64_t r0 = __ldg(c.cu + b), r1 = __ldg(c.cu + b + 1);
+    const int32_t r0 = __ldg(c.cu + b), r1 = __ldg(c.cu + b + 1);
     first = (uint32_t)r0;
-    return r0 >= 0 && r1 > r0 && r1 <= (int64_t)T ? (uint32_t)(r1 - r0) : 0u;
+    if (rows_ok(r0, r1, T))
+        return (uint32_t)(r1 - r0);
+    atomicOr(c.status, MXQ_DEV_INVALID_PAGE);
+    return 0u;
 }
 
 // What the table says of position `pos` of sequence b: a page, or a number that is none
@@ -71,14 +80,16 @@ __device__ __forceinline__ uint32_t find_page(const CacheView &c, uint32_t b, ui
 
 // Number of the (page, head, token) row of codes that holds row `row`'s token;
 // false where the row has no place: behind the last sequence, before the
-// sequence's first position, or on an invalid page.  All lanes of a warp call, as above.
-__device__ __forceinline__ bool find_place(const CacheView &c, uint32_t row, uint64_t &at)
+// sequence's first position, of a sequence that leaves the call's T rows, or on an
+// invalid page.  All lanes of a warp call, as above.
+__device__ __forceinline__ bool find_place(const CacheView &c, uint32_t row, uint32_t T, uint64_t &at)
 {
     const uint32_t b = find_sequence(c, row);
     if (b == c.seqs)
         return false;
-    const int64_t pos = (int64_t)__ldg(c.lens + b) - __ldg(c.cu + b + 1) + row;
-    if (pos < 0)
+    const int32_t end = __ldg(c.cu + b + 1);
+    const int64_t pos = (int64_t)__ldg(c.lens + b) - end + row;
+    if (pos < 0 || !rows_ok(__ldg(c.cu + b), end, T))
         return false;
     const uint32_t page = find_page(c, b, (uint32_t)pos);
     at = (((uint64_t)page * c.heads) << c.page_log) + ((uint32_t)pos & ((1u << c.page_log) - 1u));
