@@ -35,6 +35,18 @@ MXQ_API void mxq_test_stall_next_single_pass(int on);
  * by exactly one launch, of any thread of the process. */
 MXQ_API void mxq_test_stall_next_product(int on);
 
+/* Make the next mxq_cache_attention launch that works on tiles (sequences of
+ * many rows; the kernel for few rows has no waits and ignores the request)
+ * stall on purpose: its first CTA's step t never has its keys (`on` = 1 + 2 t)
+ * or its values (`on` = 2 + 2 t) reported as there, so that the waits of
+ * every role of that CTA run into a limit, a shorter one than usual.  (A step
+ * that the CTA does not have stalls nothing.)  The launch then ORs
+ * MXQ_DEV_WAIT_TIMEOUT into *status, waits for its products in flight and
+ * returns; the results of that call are undefined and the device stays
+ * usable.  `on` = 0 withdraws a pending request.  Taken by exactly one launch, of
+ * any thread of the process. */
+MXQ_API void mxq_test_stall_next_attention(int on);
+
 #ifdef __cplusplus
 }
 #endif

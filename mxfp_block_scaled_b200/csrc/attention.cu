@@ -200,6 +200,7 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
     a.left = static_cast<Unfinished *>(c.workspace);
     a.part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + left_bytes());
     a.groupdiv = make_fastdiv(a.group);
+    a.spin = a.stall = 0;       // the tiles' own
     const uint32_t ctas = std::min<uint32_t>((uint32_t)sms, kMaxSms);
     a.tiles = 0;
     const uint64_t keys = ((uint64_t)c.c.width << c.c.page_log) * c.c.seqs * c.c.heads;

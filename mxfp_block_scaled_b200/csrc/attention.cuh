@@ -55,6 +55,8 @@ struct AttArgs {
     Unfinished *left;           // [CTA]
     float *part;                // [CTA][2][R][dim] outputs of its keys alone, [R][2] references and sums
     FastDiv groupdiv;
+    uint32_t spin;              // tests of a barrier before a wait gives up (tiles)
+    uint32_t stall;             // test hook: CTA 0 withholds 1 + 2 t: keys, 2 + 2 t: values of its step t
 };
 
 __device__ __forceinline__ float ex2(float x)

@@ -46,16 +46,22 @@
 #include "attention.cuh"
 #include "mxq_mma.cuh"
 #include "mxq_tcgen05.cuh"
+#include "mxq_test.h"
 #include <algorithm>
+#include <atomic>
 
 namespace mxq {
 
 namespace {
 
+// Test hook (include/mxq_test.h): the next launch stalls on purpose.
+std::atomic<int> g_stall_attention{0};
+
 // Tests of a barrier before a wait gives up.  A test suspends for 4 us at most, so that is
 // after a second; a step takes microseconds.  A group that has nothing to do waits for the
 // other's whole tiles, 8 times as long (and leaves at once where the other gives up).
-constexpr uint32_t kSpin = 1u << 18, kIdleSpin = kSpin << 3;
+// (In a launch that was told to stall a sixteenth of that.)
+constexpr uint32_t kSpin = 1u << 18, kStalledSpin = 1u << 14, kIdle = 8;
 constexpr uint32_t kCodeWarp = 8;
 constexpr int kThreads = 512;
 
@@ -100,10 +106,10 @@ __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, Bars &s, 
     return false;
 }
 // The whole warp.
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bars &s, uint32_t *status, uint32_t spin = kSpin)
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bars &s, const AttArgs &a, uint32_t times = 1)
 {
     return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity & 1u)) ||
-           __all_sync(0xFFFFFFFFu, wait_more(bar, parity & 1u, s, status, spin));
+           __all_sync(0xFFFFFFFFu, wait_more(bar, parity & 1u, s, a.c.status, a.spin * times));
 }
 
 // 128 x N products of 16, f16 operands, from shared memory and from TMEM; issued
@@ -248,10 +254,10 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             const Units<S> un(w);
             if (wg == 0u || un.two) {
                 const uint32_t buffers = un.two ? kBufs / 2u : kBufs;       // of this group
-                ok = wait_all(&bars.qfull[wg], q0++, bars, a.c.status, kIdleSpin);
+                ok = wait_all(&bars.qfull[wg], q0++, bars, a, kIdle);
                 auto keys_there = [&](uint32_t j) {
                     const uint32_t t = t0 + j;
-                    ok = ok && wait_all(&bars.kfull[t % S::stages], t / S::stages, bars, a.c.status);
+                    ok = ok && wait_all(&bars.kfull[t % S::stages], t / S::stages, bars, a);
                 };
                 // Scores of step j; a group alone makes up for the other's arrivals.
                 auto scores = [&](uint32_t j) {
@@ -277,8 +283,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     const uint32_t t = t0 + j, stage = t % S::stages, buf = un.buffer(wg, j);
                     if (j + buffers < un.steps)
                         keys_there(j + buffers);
-                    ok = ok && wait_all(&bars.vfull[stage], t / S::stages, bars, a.c.status) &&
-                         wait_all(&bars.pfull[buf], buf0[buf] + un.use(j), bars, a.c.status);
+                    ok = ok && wait_all(&bars.vfull[stage], t / S::stages, bars, a) &&
+                         wait_all(&bars.pfull[buf], buf0[buf] + un.use(j), bars, a);
                     if (!ok)
                         break;
                     fence_after();
@@ -293,7 +299,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     if (j + 1u == un.steps)
                         umma_commit(&bars.odone[wg], one);
                     // The weights have been read, and the next scores may take their place.
-                    ok = wait_all(&bars.pv[wg], pv0 + j, bars, a.c.status);
+                    ok = wait_all(&bars.pv[wg], pv0 + j, bars, a);
                     if (j + buffers < un.steps)
                         scores(j + buffers);
                 }
@@ -454,7 +460,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             if (more)
                 pages();
             // a fresh barrier passes the wait for its odd phase
-            if (!wait_all(&empty[now % S::stages], now / S::stages + 1u, bars, a.c.status))
+            if (!wait_all(&empty[now % S::stages], now / S::stages + 1u, bars, a))
                 break;
             if (!S::fp4 && lane == 0) {         // the slot was read long ago (kRing)
                 if (values)
@@ -466,7 +472,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             store(top, chunk, tiles + now % S::stages * S::tile);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0)
+            const bool held = a.stall == 1u + 2u * now + values && blockIdx.x == 0 && chunk == 0;
+            if (lane == 0 && !held)
                 mbar_arrive(&full[now % S::stages]);
             if (more)
                 load();
@@ -483,7 +490,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.meet);
-                ok = wait_all(&bars.meet, met++, bars, a.c.status, kIdleSpin);
+                ok = wait_all(&bars.meet, met++, bars, a, kIdle);
             }
         };
         for (bool more = W::begin(w, sa, range); more && ok; more = W::next(w, sa)) {
@@ -537,7 +544,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     const uint32_t phase = two ? (j & 1u ? p1 : p0) + (j >> 1)
                                                : (buf & 2u ? (buf & 1u ? buf0[3] : buf0[2]) : (buf & 1u ? buf0[1] : buf0[0])) + (j >> 2);
                     const uint32_t at = tmem + buf * S::keys + lanes;
-                    ok = S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a.c.status);
+                    ok = S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a);
                     if (!ok)
                         break;
                     // The reference of the values, before the scores are there.
@@ -554,7 +561,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                         shift = vref.follow(largest, 4u);
                         level = smallest == vref.ref;
                     }
-                    ok = wait_all(&bars.sfull[buf], phase, bars, a.c.status);
+                    ok = wait_all(&bars.sfull[buf], phase, bars, a);
                     if (!ok)
                         break;
                     fence_after();
@@ -659,7 +666,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     // a group alone has four, and waits at every step.)
                     const bool moved = j > 0 && (shift != 1.0f || __any_sync(0xFFFFFFFFu, alpha != 1.0f));
                     if (j > 0 && (moved || !two)) {
-                        if (!(ok = wait_all(&bars.pv[wg], pv0 + j - 1u, bars, a.c.status)))
+                        if (!(ok = wait_all(&bars.pv[wg], pv0 + j - 1u, bars, a)))
                             break;
                     }
                     if (moved) {
@@ -685,7 +692,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 if (!ok)
                     break;
                 // The tile's output, or this CTA's part of it.
-                if (!(ok = wait_all(&bars.odone[wg], pieces++, bars, a.c.status)))
+                if (!(ok = wait_all(&bars.odone[wg], pieces++, bars, a)))
                     break;
                 fence_after();
                 const uint32_t out = tmem + kOut + wg * D + lanes, row1 = w.rt * S::rows + wg * 128u + r;
@@ -748,7 +755,9 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 meet();
         }
     }
+    // Whichever way a warp came here, what it stored into TMEM is there before TMEM is given back.
     __syncwarp();
+    tmem_st_wait();
     fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -760,9 +769,11 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
 namespace {
 
 template <int FMT, int D>
-cudaError_t run(const AttArgs &a, uint32_t ctas, cudaStream_t s)
+cudaError_t run(AttArgs a, uint32_t ctas, cudaStream_t s)
 {
     using S = Shape<FMT, D>;
+    a.stall = g_stall_attention.load() ? (uint32_t)g_stall_attention.exchange(0) : 0u;
+    a.spin = a.stall ? kStalledSpin : kSpin;
     const auto k = attention_tiles_kernel<FMT, D>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
     return e != cudaSuccess ? e : launch_dependent(k, dim3(ctas), kThreads, S::smem, s, a);
@@ -782,3 +793,8 @@ cudaError_t launch_attention_tiles(const AttArgs &a, int fmt, int dim, uint32_t 
 }
 
 } // namespace mxq
+
+extern "C" MXQ_API void mxq_test_stall_next_attention(int on)
+{
+    mxq::g_stall_attention.store(on > 0 ? on : 0);
+}
