@@ -635,7 +635,9 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  *   max_new  at least the rows of every sequence (a bound known to the host); a
  *            sequence with more is left out and sets MXQ_DEV_INVALID_PAGE (as one
  *            that is longer than its row of the table).
- *   scale    any finite number.
+ *   scale    finite, 2^127 at most in magnitude.  |scale| times the largest elements of
+ *            a query and of a key, and times that of the query alone, are taken to be
+ *            below 2^120.
  *   o        out, bf16 [T, heads, head_dim], 16-byte aligned.
  *   lse      out, fp32 [T, heads], or NULL.
  *   status   required.  MXQ_DEV_INVALID_PAGE as above (the sequence's rows are

@@ -881,7 +881,7 @@ mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_
         st = attention_sizes(cache, T, heads, max_new);
     if (st != MXQ_OK)
         return st;
-    if (!(scale - scale == 0.0f))
+    if (!(scale - scale == 0.0f) || scale > 0x1p127f || scale < -0x1p127f)      // (it is multiplied by log2(e))
         return MXQ_ERR_INVALID_ARG;
     if (q_stride < heads * cache->head_dim || q_stride > INT64_MAX / 0x80000000ll)
         return MXQ_ERR_SHAPE;
