@@ -504,12 +504,16 @@ def _cache_device(cache):
 
 
 def _rows(name, t, stride, T, values, dev):
-    """Address of T rows of `values` values, `stride` values apart (the last dimensions contiguous)."""
+    """Address of T bf16 rows of `values` contiguous values, `stride` values apart: a contiguous
+    buffer, or one whose first dimension is the rows."""
     if t is None:
         return None
-    size = t.itemsize
-    if T > 0 and t.untyped_storage().nbytes() < (t.storage_offset() + (T - 1) * stride + values) * size:
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s holds %s, not bf16" % (name, t.dtype))
+    if T > 0 and t.untyped_storage().nbytes() < (t.storage_offset() + (T - 1) * stride + values) * 2:
         raise ValueError("%s does not hold %d rows of %d values, %d apart" % (name, T, values, stride))
+    if T > 0 and not t.is_contiguous() and not (t.stride(0) == stride and t[0].numel() == values and t[0].is_contiguous()):
+        raise ValueError("the rows of %s are not of %d contiguous values, %d apart" % (name, values, stride))
     if t.get_device() != dev:
         raise ValueError("%s is not on the device of the first tensor" % name)
     return t.data_ptr()
