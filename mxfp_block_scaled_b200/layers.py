@@ -110,13 +110,24 @@ def quantize_projection(w, fmt="nvfp4", mode="four_six", stream=None):
 
 
 def projection_forward(w_q, x, out="bf16", workspace=None, stream=None):
-    """x W^T over a quantize_projection result as it is stored.  x: bf16 [T, K]; the
-    4-bit and MX formats are for a few tokens (mxq.linear, which takes `workspace`),
-    block FP8 for any number (fp8_linear).  Returns a dict with y [T, N] and status."""
+    """x W^T over a quantize_projection result as it is stored.  x: bf16 [T, K], any
+    number of tokens; the 4-bit and MX formats are made for a few (mxq.linear, which takes
+    `workspace`, a linear_workspace of min(T, mxq.LINEAR_MAX_TOKENS) tokens; a prompt of more
+    goes through it in pieces), block FP8 for many (fp8_linear).  Returns a dict with y [T, N]
+    and status."""
     if w_q["fmt"] == "fp8_block":
         r = fp8_linear(x, w_q, out=out, stream=stream)
         return {"y": r["c"], "status": r["status"]}
-    return mxq.linear(x, w_q, w_q["fmt"], out=out, workspace=workspace, stream=stream)
+    T, most = x.shape[0], mxq.LINEAR_MAX_TOKENS
+    if T <= most:
+        return mxq.linear(x, w_q, w_q["fmt"], out=out, workspace=workspace, stream=stream)
+    with mxq._on(stream):
+        y = torch.empty((T, w_q["codes"].shape[0]), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=x.device)
+        status = torch.zeros(1, dtype=torch.int32, device=x.device)
+        workspace = mxq.linear_workspace(most, x.shape[1], x.device) if workspace is None else workspace
+    for t in range(0, T, most):
+        mxq.linear(x[t:t + most], w_q, w_q["fmt"], out=out, workspace=workspace, stream=stream, y=y[t:t + most], status=status)
+    return {"y": y, "status": status}
 
 
 def attention_forward(cache, q, k, v, cu, lens, table, max_new, scale=None, mode="rtn", workspace=None, stream=None):

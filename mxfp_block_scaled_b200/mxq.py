@@ -805,12 +805,16 @@ def linear_workspace(T, K, device="cuda"):
     return torch.empty(max(load().mxq_linear_workspace_bytes(T, K), 256), dtype=torch.uint8, device=device)
 
 
-def linear(x, w, fmt, out="bf16", workspace=None, stream=None):
+LINEAR_MAX_TOKENS = 2048        # of one call of mxq_linear
+
+
+def linear(x, w, fmt, out="bf16", workspace=None, stream=None, y=None, status=None):
     """x w^T for a few tokens over a quantized matrix.  x: bf16 [T, K]; w: a dict with
     codes, scales (and s2 [1] for "nvfp4") of the matrix [N, K] as quantize_nvfp4 (of
     [1, N, K]) or quantize_mx return it with linear scales; workspace: a
-    linear_workspace to use again, not by two calls at once.  Returns dict y [T, N]
-    (bf16, or fp32 for out="f32"), status."""
+    linear_workspace to use again, not by two calls at once; y: the result's tensor, where
+    the caller has one.  Returns dict y [T, N] (bf16, or fp32 for out="f32"), status (a
+    given one is added to)."""
     _bf16(x)
     per = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32}.get(fmt)
     if per is None:
@@ -825,10 +829,12 @@ def linear(x, w, fmt, out="bf16", workspace=None, stream=None):
     _typed("scales", scales, torch.uint8, (N, K // per))
     if fmt == "nvfp4":
         _typed("s2", w["s2"], torch.float32, (1,))
-    dev = x.device
+    dev, dtype = x.device, torch.float32 if out == "f32" else torch.bfloat16
+    if y is not None:
+        _typed("y", y, dtype, (T, N))
     with _on(stream):
-        res = {"y": torch.empty((T, N), dtype=torch.float32 if out == "f32" else torch.bfloat16, device=dev),
-               "status": torch.zeros(1, dtype=torch.int32, device=dev)}
+        res = {"y": torch.empty((T, N), dtype=dtype, device=dev) if y is None else y,
+               "status": torch.zeros(1, dtype=torch.int32, device=dev) if status is None else status}
         mxq_linear(x, T, K, fmt, codes, scales, w["s2"] if fmt == "nvfp4" else None, N, out, res["y"], res["status"],
                    linear_workspace(T, K, dev) if workspace is None else workspace, stream)
     return res
