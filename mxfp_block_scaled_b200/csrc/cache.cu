@@ -252,8 +252,13 @@ uint32_t split(Split &s, const CacheView &c, int dim, uint32_t unit, uint32_t T)
 template <int PER, typename K1, typename KN, typename A>
 cudaError_t go(K1 one, KN several, A &a, uint32_t threads, cudaStream_t s)
 {
-    constexpr uint64_t full = 148 * 2048;
-    const bool few = (uint64_t)a.s.T * a.s.per <= full;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    const bool few = (uint64_t)a.s.T * a.s.per <= (uint64_t)sms * 2048u;
     a.s.rows = a.s.pass * (few ? 1u : (uint32_t)PER);
     return launch_dependent(few ? one : several, dim3((a.s.T + a.s.rows - 1u) / a.s.rows), threads, 0, s, a);
 }
