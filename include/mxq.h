@@ -649,7 +649,8 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  * sequence are left as they were.  What pages hold behind a sequence's last
  * position does not matter, NaN patterns included.  Codes and scales of the
  * positions read are taken to be finite, as mxq_cache_write leaves them.
- * Scores, maxima, sums and outputs are fp32, weights are rounded to 11 bits above
+ * Scores, maxima, sums and outputs are fp32 (the products' sums cut to it, by up to 2^-12
+ * in all, of same signs), weights are rounded to 11 bits above
  * 2^-21 of a row's largest and are off by at most 2^-32 of it below;
  * repeated calls give the same bits (the order of the sums follows from the sizes,
  * the lengths of the batch's sequences and the number of SMs).  MXFP8: a

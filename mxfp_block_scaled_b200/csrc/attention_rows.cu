@@ -47,6 +47,7 @@ namespace {
 
 constexpr uint32_t kKeys = 32, kLog = 5;    // keys of a step
 constexpr uint32_t kWarps = 4;
+constexpr uint32_t kMostSteps = 4096;       // of a piece: 2^15 keys a warp
 constexpr uint32_t kClusterTurns = 8;       // most turns of a warp, of a tile that a cluster takes
 
 template <int FMT, int D, int NT>
@@ -98,6 +99,54 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return r;
 }
 
+// What the pieces of a tile before this one left in `part` is added to the warps' outputs
+// `outs` and to their references and sums `stat` (the first warp's are then all).  All threads,
+// between barriers.
+template <uint32_t R, int D, uint32_t OUTS>
+__device__ __noinline__ void add_earlier(float *outs, float *stat, const float *part)
+{
+    constexpr uint32_t kThreads = 32 * kWarps;
+    static_assert(R <= kThreads, "a row a thread");
+    const uint32_t tid = threadIdx.x;
+    for (uint32_t i = tid; i < R * (D + 4) / 4; i += kThreads) {      // the row's reference and sum as columns D and on
+        const uint32_t r = i / (D / 4 + 1), d = i % (D / 4 + 1) * 4;
+        const float2 st = *reinterpret_cast<const float2 *>(part + R * D + r * 2);
+        float m = st.x, own = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w)
+            m = fmaxf(m, stat[w * R + r]);
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w)
+            own = fmaf(stat[(kWarps + w) * R + r], ex2(stat[w * R + r] - m), own);
+        const float share = st.y * ex2(st.x - m), f = inverse(share + own), g = share * f, h = own * f;
+        if (d == D) {
+            outs[r * (D + 4) + D] = m;
+            outs[r * (D + 4) + D + 1] = share + own;
+            continue;
+        }
+        float4 v = *reinterpret_cast<const float4 *>(part + r * D + d);
+        v = make_float4(v.x * g, v.y * g, v.z * g, v.w * g);
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) {
+            float4 *at = reinterpret_cast<float4 *>(outs + w * OUTS + r * (D + 4) + d);
+            const float4 x = *at;
+            v = make_float4(fmaf(x.x, h, v.x), fmaf(x.y, h, v.y), fmaf(x.z, h, v.z), fmaf(x.w, h, v.w));
+            *at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        *reinterpret_cast<float4 *>(outs + r * (D + 4) + d) = v;
+    }
+    __syncthreads();
+    if (tid < R) {
+        const float top = outs[tid * (D + 4) + D], l = outs[tid * (D + 4) + D + 1];
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) {
+            stat[w * R + tid] = w ? kLowest : top;
+            stat[(kWarps + w) * R + tid] = w ? 0.0f : l;
+        }
+    }
+    __syncthreads();
+}
+
 } // namespace
 
 template <int FMT, int D, int NT, bool CLUSTER>
@@ -106,7 +155,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
 {
     using S = Shape<FMT, D, NT>;
     constexpr uint32_t kRows = S::R;
-    using W = Walk<kRows, kLog>;
+    using W = Walk<kRows, kLog, kMostSteps>;
     constexpr uint32_t kThreads = 32 * kWarps;
     extern __shared__ __align__(128) char smem[];
     __shared__ Range range;
@@ -137,6 +186,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         w.keys = W::Div::keys(a, w.s, tile);
         w.k0 = a.extra + (uint32_t)((uint64_t)(w.steps - a.extra) * rank / ranks);
         w.k1 = a.extra + (uint32_t)((uint64_t)(w.steps - a.extra) * (rank + 1u) / ranks);
+        w.begun = w.k0;
         w.left = 0;
         __syncwarp();
         if (lane == 0)
@@ -631,7 +681,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
         __syncthreads();
         const float vfac = FMT == MXQ_FMT_NVFP4 ? __ldg(a.c.v_s2 + head) : 1.0f;
         const bool whole = walk.whole();
-        float *part = part_of<kRows, D>(a, blockIdx.x, walk.k0 == 0u);
+        float *part = part_of<kRows, D>(a, blockIdx.x, walk.slot());
         auto put = [&](uint32_t r, uint32_t d, float m, float l, float4 v) {        // 4 columns of a finished row; m, l where d is 0
             const uint32_t row = tile * kRows + r, it = fastdiv(row, a.groupdiv), h = head * a.group + row - it * a.group;
             const uint64_t out = (uint64_t)(first + it) * (a.c.heads * a.group) + h;
@@ -641,6 +691,8 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             if (d == 0 && a.lse)
                 a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         };
+        if (!CLUSTER && walk.earlier())
+            add_earlier<kRows, D, S::outs / 4>(reinterpret_cast<float *>(smem), &stat[0][0][0], part);
         const float *all = reinterpret_cast<const float *>(smem);
         float *sum4 = reinterpret_cast<float *>(smem);      // CLUSTER: the CTA's outputs, over the first warp's
 #pragma unroll 1
@@ -710,7 +762,7 @@ attention_rows_kernel(const __grid_constant__ AttArgs a)
             }
             cluster_sync_all();         // every CTA's sums have been read
         }
-        if (!CLUSTER && tid == 0 && walk.k0 == 0u && !whole) {
+        if (!CLUSTER && tid == 0 && walk.unfinished()) {
             Unfinished u = {};
             u.first = first;
             u.row0 = tile * kRows;

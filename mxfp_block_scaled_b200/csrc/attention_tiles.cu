@@ -63,6 +63,7 @@ std::atomic<int> g_stall_attention{0};
 // (In a launch that was told to stall a sixteenth of that.)
 constexpr uint32_t kSpin = 1u << 18, kStalledSpin = 1u << 14, kIdle = 8;
 constexpr uint32_t kCodeWarp = 8;
+constexpr uint32_t kMostSteps = 512;        // of a piece: 2^15 keys
 constexpr int kThreads = 512;
 
 template <int FMT, int D>
@@ -89,7 +90,7 @@ struct Bars {
     uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], odone[2], qfull[2], ffull[kRing], meet, drain[2];
     uint32_t tmem, abort;
     float kfac[kRing][4];       // by step and chunk: powers of the keys,
-    uint32_t vtop[kRing][4];    // largest scales of the values
+    uint32_t vtop[kRing];       // by step, a byte a chunk: scales that the values are relative to
 };
 
 // Further tests of a barrier whose first one failed.
@@ -157,6 +158,33 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// What the pieces of a tile before this one left of this thread's row is added to its output in
+// TMEM, which is then that of all of them, and no sum any more; their reference and sum.
+template <int D>
+__device__ __noinline__ float2 add_earlier(uint32_t out, const float4 *row, const float2 *stat, float mx, float sum, float unit)
+{
+    const float2 st = *stat;
+    const float top = fmaxf(st.x, mx), share = st.y * ex2(st.x - top), own = ex2(mx - top), all = fmaf(sum, own, share);
+    const float f = own * inverse(all), g = share * inverse(all);
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(out + c * 32, o);
+        tmem_ld_wait(o);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float4 e = row[c * 8 + x];
+            o[x * 4] = __float_as_uint(fmaf(e.x, g, __uint_as_float(o[x * 4]) * f * unit));
+            o[x * 4 + 1] = __float_as_uint(fmaf(e.y, g, __uint_as_float(o[x * 4 + 1]) * f * unit));
+            o[x * 4 + 2] = __float_as_uint(fmaf(e.z, g, __uint_as_float(o[x * 4 + 2]) * f * unit));
+            o[x * 4 + 3] = __float_as_uint(fmaf(e.w, g, __uint_as_float(o[x * 4 + 3]) * f * unit));
+        }
+        tmem_st32(out + c * 32, o);
+    }
+    tmem_st_wait();
+    return make_float2(top, all);
+}
+
 // How the units of a piece lie: `two` groups, or the first alone.
 template <typename S>
 struct Units {
@@ -190,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_tiles_kernel(const __grid_constant__ AttArgs a)
 {
     using S = Shape<FMT, D>;
-    using W = Walk<S::rows, S::log>;
+    using W = Walk<S::rows, S::log, kMostSteps>;
     extern __shared__ __align__(1024) char smem_raw[];
     __shared__ Bars bars;
     __shared__ Range range;
@@ -214,8 +242,10 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             mbar_init(&bars.qfull[i], 4);
             mbar_init(&bars.drain[i], 1);
         }
-        for (uint32_t i = 0; i < kRing; ++i)
+        for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bars.ffull[i], 2 * S::chunks);
+            bars.vtop[i] = 0;
+        }
         mbar_init(&bars.meet, 8);
         bars.abort = 0;
         sa = a;
@@ -451,7 +481,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     m = __vmaxu4(m, raw.s[i]);
                 m = __vmaxu4(m, m >> 16);
                 top = __reduce_max_sync(0xFFFFFFFFu, max(top, max(m & 0xFFu, (m >> 8) & 0xFFu)));
-                top = values ? (top + 1u) & ~1u : top;
+                top = values ? min((top + 1u) & ~1u, 254u) : top;
             }
             // The next chunk's place; its pages are on the way while this one is stored.
             const uint32_t now = t, chunk = dw;
@@ -464,7 +494,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 break;
             if (!S::fp4 && lane == 0) {         // the slot was read long ago (kRing)
                 if (values)
-                    bars.vtop[now % kRing][chunk] = top;
+                    reinterpret_cast<uint8_t *>(&bars.vtop[now % kRing])[chunk] = (uint8_t)top;
                 else
                     bars.kfac[now % kRing][chunk] = __uint_as_float(top << 23) * 0x1p-7f;
                 mbar_arrive(&bars.ffull[now % kRing]);
@@ -547,19 +577,18 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     ok = S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a);
                     if (!ok)
                         break;
-                    // The reference of the values, before the scores are there.
-                    float shift = 1.0f;
-                    bool level = true;      // all of the step's keys have it
+                    // The reference of the values, before the scores are there; mostly all chunks have
+                    // it.  alpha: the factor of the output so far.
+                    float alpha = 1.0f;
+                    bool level = true;
                     if constexpr (!S::fp4) {
-                        uint32_t largest = 0, smallest = 255u;
-#pragma unroll
-                        for (int g = 0; g < S::chunks; ++g) {
-                            const uint32_t v = bars.vtop[t % kRing][g];
-                            largest = max(largest, v);
-                            smallest = min(smallest, v);
+                        constexpr uint32_t all = S::chunks == 2 ? 0x0101u : 0x01010101u;
+                        const uint32_t tops = bars.vtop[t % kRing];
+                        level = tops == vref.ref * all;
+                        if (!level) {
+                            const uint32_t m = __vmaxu4(tops, tops >> 16);
+                            alpha = vref.follow(max(m & 0xFFu, (m >> 8) & 0xFFu), 4u);
                         }
-                        shift = vref.follow(largest, 4u);
-                        level = smallest == vref.ref;
                     }
                     ok = wait_all(&bars.sfull[buf], phase, bars, a);
                     if (!ok)
@@ -578,7 +607,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     // from the scores again.  (One copy of each loop: cold instruction caches are
                     // what a short call waits for.)
                     uint32_t p[groups][S::mine / 2];
-                    float alpha = 1.0f, total, high;
+                    float total, high;
 #pragma unroll 1
                     for (bool find = j == 0;;) {
                         uint32_t v[parts][32];
@@ -607,9 +636,10 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             }
                             if (top - mx > kLag) {      // the weights' own difference, rounded as theirs
                                 top -= kTop;
-                                alpha = ex2(mx - top);
+                                const float f = ex2(mx - top);
                                 mx = top;
-                                sum *= alpha;
+                                sum *= f;
+                                alpha *= f;
                             }
                         }
                         total = 0.0f;
@@ -644,7 +674,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     if (!level) {
 #pragma unroll
                         for (int g = 0; g < groups; ++g) {
-                            const float f = __uint_as_float((127u - min(vref.ref - bars.vtop[t % kRing][g], 30u)) << 23);
+                            const uint32_t below = vref.ref - ((bars.vtop[t % kRing] >> (8 * g)) & 0xFFu);
+                            const float f = __uint_as_float((127u - min(below, 30u)) << 23);
                             const uint32_t f2 = half2_bits(f, f);
 #pragma unroll
                             for (int x = 0; x < (int)S::mine / 2; ++x)
@@ -664,7 +695,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     // this one is done.  (A wait is for a barrier's next phase.  Of two groups each has
                     // two buffers of scores, so with these scores the product before that one is done;
                     // a group alone has four, and waits at every step.)
-                    const bool moved = j > 0 && (shift != 1.0f || __any_sync(0xFFFFFFFFu, alpha != 1.0f));
+                    const bool moved = j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
                     if (j > 0 && (moved || !two)) {
                         if (!(ok = wait_all(&bars.pv[wg], pv0 + j - 1u, bars, a)))
                             break;
@@ -679,7 +710,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                             tmem_ld_wait(o);
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * (alpha * shift));
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
                             tmem_st32(out + c * 32, o);
                         }
                     }
@@ -699,45 +730,55 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 const uint32_t i1 = fastdiv(row1, a.groupdiv), h1 = w.head * a.group + row1 - i1 * a.group;
                 const bool in1 = row1 < w.s.rows, whole = w.whole();
                 const uint64_t to = (uint64_t)(w.s.first + i1) * (a.c.heads * a.group) + h1;
-                float *part = part_of<S::rows, D>(a, blockIdx.x, w.k0 == 0u);
-                // A part is its own keys' output (the join has the factor of NVFP4).
-                const float f2 = (S::fp4 && whole ? __ldg(a.c.v_s2 + w.head) : 1.0f) * inverse(sum);
-                const float unit = S::fp4 ? 1.0f : vref.unit();
+                float *part = part_of<S::rows, D>(a, blockIdx.x, w.slot());
+                // A part is its own keys' output (the join has the factor of NVFP4); with those of the
+                // pieces before, of the same tile, which this thread has left.
+                float4 *rowp = reinterpret_cast<float4 *>(part + (wg * 128u + r) * D);
+                float2 *statp = reinterpret_cast<float2 *>(part + S::rows * D + (wg * 128u + r) * 2u);
+                float f2 = inverse(sum), unit = S::fp4 ? 1.0f : vref.unit();
+                if (w.earlier()) {
+                    const float2 st = add_earlier<D>(out, rowp, statp, mx, sum, unit);
+                    mx = st.x;
+                    sum = st.y;
+                    f2 = unit = 1.0f;
+                }
+                if (S::fp4 && whole)
+                    f2 *= __ldg(a.c.v_s2 + w.head);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(out + c * 32, o);
                     tmem_ld_wait(o);
-                    if (!in1)
-                        continue;
-                    if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.o + to * D + c * 32);
+                    if (in1) {
+                        if (whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(a.o + to * D + c * 32);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t b[4];
+                            for (int x = 0; x < 4; ++x) {
+                                uint32_t b[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(o[x * 8 + y * 2]) * f2 * unit,
-                                                                              __uint_as_float(o[x * 8 + y * 2 + 1]) * f2 * unit);
-                                b[y] = *reinterpret_cast<const uint32_t *>(&p);
+                                for (int y = 0; y < 4; ++y) {
+                                    const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(o[x * 8 + y * 2]) * f2 * unit,
+                                                                                  __uint_as_float(o[x * 8 + y * 2 + 1]) * f2 * unit);
+                                    b[y] = *reinterpret_cast<const uint32_t *>(&p);
+                                }
+                                dst[x] = make_uint4(b[0], b[1], b[2], b[3]);
                             }
-                            dst[x] = make_uint4(b[0], b[1], b[2], b[3]);
-                        }
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(part + (wg * 128u + r) * D + c * 32);
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            dst[x] = make_float4(__uint_as_float(o[x * 4]) * f2 * unit, __uint_as_float(o[x * 4 + 1]) * f2 * unit,
-                                                 __uint_as_float(o[x * 4 + 2]) * f2 * unit, __uint_as_float(o[x * 4 + 3]) * f2 * unit);
+                            for (int x = 0; x < 8; ++x)
+                                rowp[c * 8 + x] = make_float4(__uint_as_float(o[x * 4]) * f2 * unit, __uint_as_float(o[x * 4 + 1]) * f2 * unit,
+                                                              __uint_as_float(o[x * 4 + 2]) * f2 * unit, __uint_as_float(o[x * 4 + 3]) * f2 * unit);
+                        }
                     }
+                    __syncwarp();       // (the next read is the whole warp's)
                 }
                 if (in1 && whole && a.lse)
                     a.lse[to] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
                 if (in1 && !whole)
-                    *reinterpret_cast<float2 *>(part + S::rows * D + (wg * 128u + r) * 2u) = make_float2(mx, sum);
+                    *statp = make_float2(mx, sum);
                 fence_before();     // the loads of the output, before the next tile's products
             }
-            if (threadIdx.x == 0 && w.k0 == 0u && !w.whole()) {
+            if (threadIdx.x == 0 && w.unfinished()) {
                 Unfinished u = {};
                 u.first = w.s.first;
                 u.row0 = w.rt * S::rows;
