@@ -654,12 +654,11 @@ MXQ_API size_t mxq_cache_attention_workspace_bytes(const mxq_cache *cache, int64
  * 2^-21 of a row's largest and are off by at most 2^-32 of it below;
  * repeated calls give the same bits (the order of the sums follows from the sizes,
  * the lengths of the batch's sequences and the number of SMs).  MXFP8: a
- * token's codes enter the products exactly while its block scales are within 2^21 of
+ * token's codes enter the products exactly while its block scales are within 2^18 of
  * the largest one of the head among 64 tokens (from a position that is a multiple of
- * 64 on); below that they lose bits, and keys 2^-31, values 2^-24 of the largest may
- * count as zeros.  Weights below 2^-17 of a row's largest are then off by at most
- * 2^-28 of it.  Other tokens' sizes do not matter (up to 2^60 between the values
- * of a sequence).  Blocks of keys or values whose largest element is below 2^-100
+ * 64 on); below that they lose bits, and from 2^-27 of the largest on they may count
+ * as zeros.  Other tokens' sizes do not matter (up to 2^60 between the values of a
+ * sequence).  Blocks of keys or values whose largest element is below 2^-100
  * lose bits, down to zero. */
 MXQ_API mxq_status mxq_cache_attention(const mxq_cache *cache, const uint16_t *q, int64_t q_stride,
                                        int64_t T, int64_t heads, const int32_t *cu, const int32_t *lens,

@@ -88,11 +88,17 @@ struct ValueRef {
     // the output so far.
     __device__ __forceinline__ float follow(uint32_t top, uint32_t slack)
     {
-        const uint32_t was = ref;
-        if (top > ref || (top + slack < ref && top > kZeros))
-            ref = max(top, max(most, kSpan) - kSpan);
+        if (top <= ref && (top + slack >= ref || top <= kZeros))
+            return 1.0f;
+        const float f = move(max(top, max(most, kSpan) - kSpan));
         most = max(most, ref);
-        return __uint_as_float((uint32_t)max(127 + (int)was - (int)ref, 0) << 23);
+        return f;
+    }
+    __device__ __forceinline__ float move(uint32_t to)
+    {
+        const float f = __uint_as_float((uint32_t)max(127 + (int)ref - (int)to, 0) << 23);
+        ref = to;
+        return f;
     }
     __device__ __forceinline__ float unit() const { return __uint_as_float((ref - 7u) << 23); }
 };

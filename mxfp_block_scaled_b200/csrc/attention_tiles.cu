@@ -21,11 +21,12 @@
 // above it is the maximum found, the step's weights are taken again, and the output
 // in TMEM is rescaled (by the softmax group, which has the output to itself between its
 // products).  MXFP8 powers: keys as in attention_rows.cu, a largest one for every 32 (16) keys.
-// Values the same, the largest scale rounded up to an even one (exact within 2^21); all columns of
-// a step share a reference (ValueRef, which may stand 2^4 above a step's largest), and the
-// weights of keys whose own largest is not the reference are multiplied by the difference,
-// in f16: of a step's 64 keys, values 2^-24 of the largest count as zeros.  (Even ones, so that
-// neighbouring chunks mostly have the same.)
+// Values are relative to a reference of the step (ValueRef), which may stand 2^4 above its largest
+// scale (exact within 2^18 then).  The warps that decode keys, ahead of the others, tell the
+// largest scales of the values of their chunks (heads of 256, whose decoding is what a step waits
+// for: warp 15 does, 976 us for 2048 tokens over 10240 otherwise); those that decode values follow
+// them step by step, so that all use the same, and the softmax has no more to do than rescale
+// the output where it moved.
 //
 // Bound: a step of 256 x 64 x 128 costs the tensor cores 1024 cycles and the SM's 16
 // exponentials a cycle 1024 as well, beside which a softmax thread has two operations a
@@ -87,10 +88,12 @@ struct Shape {
 constexpr uint32_t kBufs = 4;               // of scores, in TMEM
 constexpr uint32_t kRing = 16;              // steps whose powers are kept; decoding is fewer ahead
 struct Bars {
-    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], odone[2], qfull[2], ffull[kRing], meet, drain[2];
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], sfull[kBufs], pfull[kBufs], pv[2], odone[2], qfull[2], ffull[kRing];
+    uint64_t tfull[kRing], tempty[kRing], meet, drain[2];
     uint32_t tmem, abort;
     float kfac[kRing][4];       // by step and chunk: powers of the keys,
-    uint32_t vtop[kRing];       // by step, a byte a chunk: scales that the values are relative to
+    uint32_t vtop[kRing];       // by step: largest scales of the values, a byte a chunk
+    uint32_t vref[kRing];       // and what they are relative to
 };
 
 // Further tests of a barrier whose first one failed.
@@ -209,6 +212,7 @@ struct Raw {
     uint4 c[S::loads];
     // NVFP4: the two scales of each piece.  MXFP8: the scales of key lane % mine.
     uint32_t s[S::fp4 ? S::loads : (S::blocks + 3) / 4];
+    uint32_t v[S::fp4 || S::subs == 1 ? 1 : (S::blocks + 3) / 4];       // MXFP8, of a warp of keys: the scales of the same token's values
 };
 
 } // namespace
@@ -244,6 +248,8 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
         }
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bars.ffull[i], 2 * S::chunks);
+            mbar_init(&bars.tfull[i], S::subs == 2 ? S::chunks : 1);
+            mbar_init(&bars.tempty[i], 3);
             bars.vtop[i] = 0;
         }
         mbar_init(&bars.meet, 8);
@@ -270,8 +276,45 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
     constexpr uint32_t kOut = kBufs * S::keys;
     static_assert(kOut + S::subs * D <= 512, "TMEM");
 
+    // Largest of the warp's bytes.
+    auto largest = [](uint32_t m) {
+        m = __vmaxu4(m, m >> 16);
+        return __reduce_max_sync(0xFFFFFFFFu, max(kZeros, max(m & 0xFFu, (m >> 8) & 0xFFu)));
+    };
+
     W &w = walks[warp];
-    if (warp >= kCodeWarp && (warp & 3u) == 3u) {    // issue
+    if (!S::fp4 && S::subs == 1 && warp == kCodeWarp + 7u) {        // tells the largest scales of the values
+        bool more = W::begin(w, sa, range);
+        uint32_t step = w.k0, t = 0;
+        uint2 s[2];
+        auto load = [&]() {
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                const uint32_t key = (step << S::log) + lane + 32u * i;
+                const uint32_t page = key < w.keys ? table_entry(a.c, w.b, key) : a.c.pages;
+                const uint64_t at = (((uint64_t)page * a.c.heads + w.head) << a.c.page_log) + (key & ((1u << a.c.page_log) - 1u));
+                s[i] = page < a.c.pages ? __ldg(reinterpret_cast<const uint2 *>(a.c.v_scales + at * S::blocks)) : make_uint2(0u, 0u);
+            }
+        };
+        if (more)
+            load();
+        for (; more; ++t) {
+            const uint32_t m = __vmaxu4(__vmaxu4(s[0].x, s[0].y), __vmaxu4(s[1].x, s[1].y));
+            if (++step == w.k1) {
+                more = W::next(w, sa);
+                step = w.k0;
+            }
+            if (more)
+                load();
+            const uint32_t top = largest(m);
+            if (!wait_all(&bars.tempty[t % kRing], t / kRing + 1u, bars, a))        // (a fresh barrier passes)
+                break;
+            if (lane == 0) {
+                bars.vtop[t % kRing] = top;
+                mbar_arrive(&bars.tfull[t % kRing]);
+            }
+        }
+    } else if (warp >= kCodeWarp && (warp & 3u) == 3u) {    // issue
         const uint32_t one = elect_one(), wg = (warp - kCodeWarp) >> 2;
         uint32_t t0 = 0, buf0[kBufs] = {0, 0, 0, 0}, q0 = 0, pv0 = 0;
         bool ok = wg < S::subs;
@@ -347,21 +390,33 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
         // Three warps take the chunks of keys in turn, three those of values.
         const bool values = warp >= kCodeWarp + 4u;
         constexpr uint32_t stride = 3;
-        uint32_t dw = warp & 3u;
+        uint32_t dw = (warp & 3u) + S::chunks;
         const uint8_t *codes = values ? a.c.v_codes : a.c.k_codes, *scales = values ? a.c.v_scales : a.c.k_scales;
         uint64_t *full = values ? bars.vfull : bars.kfull, *empty = values ? bars.vempty : bars.kempty;
         char *tiles = values ? vt : kt;
         Raw<FMT, D> raw;
         bool more = W::begin(w, sa, range);
-        uint32_t step = w.k0, t = 0;
+        uint32_t step = w.k0 - 1u, t = 0u - 1u;     // before the first
+        // Steps that the warp passes on its way from a chunk to its next.
+        constexpr uint32_t kPass = S::chunks == 2 ? 2 : 1;
+        struct Passed {
+            bool on, first;         // it is one; the first of a piece
+            uint32_t t;
+        } passed[kPass];
+        ValueRef vref;
         auto settle = [&]() {       // the chunk is number dw from step `step` on: its own step
-            while (dw >= S::chunks && more) {
+#pragma unroll
+            for (uint32_t n = 0; n < kPass; ++n) {
+                passed[n].on = dw >= S::chunks && more;
+                if (!passed[n].on)
+                    continue;
                 dw -= S::chunks;
-                ++t;
                 if (++step == w.k1) {
                     more = W::next(w, sa);
                     step = w.k0;
                 }
+                passed[n].t = ++t;
+                passed[n].first = step == w.k0;
             }
         };
         if (more)
@@ -382,13 +437,23 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             page[1] = S::mine > 16 && a.c.page_log == 4u && key + 16u < w.keys ? table_entry(a.c, w.b, key + 16u) : a.c.pages;
         };
         // MXFP8: a key's scales.
-        auto key_scales = [&](const uint8_t *p, bool in) {
+        auto read_scales = [&](auto &s, const uint8_t *p, bool in) {
             if (S::blocks == 2)
-                raw.s[0] = in ? __ldg(reinterpret_cast<const uint16_t *>(p)) : 0u;
-            else
-#pragma unroll
-                for (uint32_t i = 0; i < sizeof(raw.s) / 4; ++i)
-                    raw.s[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+                s[0] = in ? __ldg(reinterpret_cast<const uint16_t *>(p)) : 0u;
+            else if (S::blocks == 4)
+                s[0] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+            else {
+                const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
+                s[0] = x.x;
+                s[sizeof(s) / 4 - 1] = x.y;
+            }
+        };
+        auto key_scales = [&](uint64_t at, bool in) {
+            if constexpr (!S::fp4) {
+                read_scales(raw.s, scales + at * S::blocks, in);
+                if (S::subs == 2 && !values)
+                    read_scales(raw.v, a.c.v_scales + at * S::blocks, in);
+            }
         };
         auto load = [&]() {
             const uint32_t key = (step << S::log) + dw * S::mine, mask = (1u << a.c.page_log) - 1u;
@@ -404,7 +469,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     for (uint32_t i = 0; i < S::loads; ++i)
                         raw.s[i] = __ldg(reinterpret_cast<const uint16_t *>(sc + i * rows_a_load * S::blocks) + piece0);
                 } else
-                    key_scales(scales + (at - row0 + lane % S::mine) * S::blocks, true);
+                    key_scales(at - row0 + lane % S::mine, true);
                 return;
             }
             const bool short_pages = S::mine > 16 && a.c.page_log == 4u;
@@ -423,7 +488,7 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                 const uint32_t row = lane % S::mine, pg = short_pages && row >= 16u ? page[1] : page[0];
                 const bool in = key + row < w.keys && pg < a.c.pages;
                 const uint64_t at = in ? (((uint64_t)pg * a.c.heads + w.head) << a.c.page_log) + ((key + row) & mask) : 0ull;
-                key_scales(scales + at * S::blocks, in);
+                key_scales(at, in);
             }
         };
         // The chunk into its f16 tile.  top: see attention_rows.cu.
@@ -473,15 +538,36 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             load();
         }
         while (more) {
-            uint32_t top = values ? kZeros - 1u : kZeros;       // what is below counts as zeros (2^-100)
-            if (!S::fp4) {
+            uint32_t top = 0, vtop = 0;     // what the chunk's codes are relative to; of the values
+            if (!S::fp4 && !values) {
                 uint32_t m = raw.s[0];
 #pragma unroll
                 for (uint32_t i = 1; i < sizeof(raw.s) / 4; ++i)
                     m = __vmaxu4(m, raw.s[i]);
-                m = __vmaxu4(m, m >> 16);
-                top = __reduce_max_sync(0xFFFFFFFFu, max(top, max(m & 0xFFu, (m >> 8) & 0xFFu)));
-                top = values ? min((top + 1u) & ~1u, 254u) : top;
+                top = largest(m);
+                if (S::subs == 2)
+                    vtop = largest(raw.v[0]);
+            }
+            if (!S::fp4 && values) {
+                bool ok = true;
+#pragma unroll
+                for (uint32_t n = 0; n < kPass; ++n)
+                    if (passed[n].on && ok) {
+                        ok = wait_all(&bars.tfull[passed[n].t % kRing], passed[n].t / kRing, bars, a);
+                        uint32_t m = bars.vtop[passed[n].t % kRing];
+                        if (S::subs == 1) {     // (warps of keys are not far enough ahead to need it)
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&bars.tempty[passed[n].t % kRing]);
+                        }
+                        m = __vmaxu4(m, m >> 16);
+                        if (passed[n].first)
+                            vref = ValueRef();
+                        vref.follow(max(m & 0xFFu, (m >> 8) & 0xFFu), 4u);
+                    }
+                if (!ok)
+                    break;
+                top = vref.ref;
             }
             // The next chunk's place; its pages are on the way while this one is stored.
             const uint32_t now = t, chunk = dw;
@@ -492,11 +578,16 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
             // a fresh barrier passes the wait for its odd phase
             if (!wait_all(&empty[now % S::stages], now / S::stages + 1u, bars, a))
                 break;
-            if (!S::fp4 && lane == 0) {         // the slot was read long ago (kRing)
+            if (!S::fp4 && lane == 0) {         // the slots were read long ago (kRing)
                 if (values)
-                    reinterpret_cast<uint8_t *>(&bars.vtop[now % kRing])[chunk] = (uint8_t)top;
-                else
+                    bars.vref[now % kRing] = top;       // of every chunk the same
+                else {
                     bars.kfac[now % kRing][chunk] = __uint_as_float(top << 23) * 0x1p-7f;
+                    if (S::subs == 2) {
+                        reinterpret_cast<uint8_t *>(&bars.vtop[now % kRing])[chunk] = (uint8_t)vtop;
+                        mbar_arrive(&bars.tfull[now % kRing]);
+                    }
+                }
                 mbar_arrive(&bars.ffull[now % kRing]);
             }
             store(top, chunk, tiles + now % S::stages * S::tile);
@@ -577,19 +668,9 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                     ok = S::fp4 || wait_all(&bars.ffull[t % kRing], t / kRing, bars, a);
                     if (!ok)
                         break;
-                    // The reference of the values, before the scores are there; mostly all chunks have
-                    // it.  alpha: the factor of the output so far.
-                    float alpha = 1.0f;
-                    bool level = true;
-                    if constexpr (!S::fp4) {
-                        constexpr uint32_t all = S::chunks == 2 ? 0x0101u : 0x01010101u;
-                        const uint32_t tops = bars.vtop[t % kRing];
-                        level = tops == vref.ref * all;
-                        if (!level) {
-                            const uint32_t m = __vmaxu4(tops, tops >> 16);
-                            alpha = vref.follow(max(m & 0xFFu, (m >> 8) & 0xFFu), 4u);
-                        }
-                    }
+                    float alpha = 1.0f;     // factor of the output so far
+                    if constexpr (!S::fp4)
+                        alpha = vref.move(bars.vref[t % kRing]);
                     ok = wait_all(&bars.sfull[buf], phase, bars, a);
                     if (!ok)
                         break;
@@ -671,17 +752,6 @@ attention_tiles_kernel(const __grid_constant__ AttArgs a)
                         find = true;
                     }
                     sum += total;
-                    if (!level) {
-#pragma unroll
-                        for (int g = 0; g < groups; ++g) {
-                            const uint32_t below = vref.ref - ((bars.vtop[t % kRing] >> (8 * g)) & 0xFFu);
-                            const float f = __uint_as_float((127u - min(below, 30u)) << 23);
-                            const uint32_t f2 = half2_bits(f, f);
-#pragma unroll
-                            for (int x = 0; x < (int)S::mine / 2; ++x)
-                                p[g][x] = hmul2_bits(p[g][x], f2);
-                        }
-                    }
 #pragma unroll
                     for (int g = 0; g < groups; ++g) {
                         if constexpr (S::mine == 32)

@@ -54,7 +54,7 @@ def check_row(o, lse, q, cache, pos, scale):
     eps = 2 * (cache.head_dim + 8) * 2.0 ** -23 * scale * (q.double().abs() @ k.abs().t()).amax(-1)
     largest = torch.exp(s - want_lse[:, None]).amax(-1)
     bound = 1.01 * (want * 2.0 ** -8 + want * (2.0 ** -11 + 2.0 ** -12 + eps[:, None] + 2.0 ** -18) * (1 + 2.0 ** -8)) \
-        + (pos + 1) * 2.0 ** -28 * largest[:, None] * v.max()
+        + (pos + 1) * 2.0 ** -32 * largest[:, None] * v.max()
     worst = ((o.double() - want).abs() / bound).max().item()
     assert worst <= 1, worst
     assert ((lse.double() - want_lse).abs() <= eps + 2.0 ** -16 + want_lse.abs() * 2.0 ** -22).all()
