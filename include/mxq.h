@@ -540,8 +540,9 @@ MXQ_API size_t mxq_linear_workspace_bytes(int64_t T, int64_t K);
  * T at most 2048, K at most 65536 (MXQ_ERR_UNSUPPORTED).  T or N 0 does nothing,
  * K 0 gives zeros.  Sums are fp32 in a fixed order (it follows from the sizes and
  * the number of SMs): repeated calls give the same bits, and a token's row does not
- * depend on the others' values.  They are formed over the token's row scaled so
- * that its largest element is about 2^15; block scales (NVFP4: s2) above about 2^80
+ * depend on the others' values.  They are formed over the token's row in f16, scaled so
+ * that its largest element is about 2^15: elements are exact down to 2^-31 of the
+ * largest, and off by at most 2^-39 of it below.  Block scales (NVFP4: s2) above about 2^80
  * may overflow, and below about 2^-100 sums lose bits. */
 MXQ_API mxq_status mxq_linear(const uint16_t *x, int64_t T, int64_t K, mxq_fmt fmt, const uint8_t *codes,
                               const uint8_t *scales, const float *s2, int64_t N, mxq_out out, void *y,
