@@ -512,8 +512,14 @@ def _rows(name, t, stride, T, values, dev):
         raise ValueError("%s holds %s, not bf16" % (name, t.dtype))
     if T > 0 and t.untyped_storage().nbytes() < (t.storage_offset() + (T - 1) * stride + values) * 2:
         raise ValueError("%s does not hold %d rows of %d values, %d apart" % (name, T, values, stride))
-    if T > 0 and not t.is_contiguous() and not (t.stride(0) == stride and t[0].numel() == values and t[0].is_contiguous()):
-        raise ValueError("the rows of %s are not of %d contiguous values, %d apart" % (name, values, stride))
+    if T > 0 and not t.is_contiguous():
+        shape, strides = t.shape, t.stride()
+        n, ok = 1, strides[0] == stride
+        for d in range(len(shape) - 1, 0, -1):
+            ok &= strides[d] == n or shape[d] == 1
+            n *= shape[d]
+        if not ok or n != values:
+            raise ValueError("the rows of %s are not of %d contiguous values, %d apart" % (name, values, stride))
     if t.get_device() != dev:
         raise ValueError("%s is not on the device of the first tensor" % name)
     return t.data_ptr()
