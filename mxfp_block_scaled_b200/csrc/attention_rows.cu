@@ -18,10 +18,10 @@
 // the values need no transposition; the weights are turned by movmatrix.
 //
 // Bound: the arithmetic of the decoding beside HBM.  64 sequences of up to 32768 tokens,
-// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 66 us (328 MB, 5.0
-// TB/s, 76 % of the measured copy rate), NVFP4 62 us, heads of 64 88 us, 32 sequences with
-// heads of 256 70 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
-// 12 of up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 42 us.  One
+// 2 key/value heads of 128 for 16 query heads, one token each: MXFP8 67 us (328 MB, 4.9
+// TB/s, 75 % of the measured copy rate), NVFP4 63 us, heads of 64 57 us, 32 sequences with
+// heads of 256 73 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
+// 12 of up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 41 us.  One
 // sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
 // wins (12 of 16384 as above by clusters 120 us, divided 59 then).  Two warps to a turn, each
 // with half of its keys' scores and half of the columns, so that 32 rows fit: 59 us for

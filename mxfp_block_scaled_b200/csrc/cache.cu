@@ -19,9 +19,10 @@
 //
 // The reader moves bytes: 24 sequences of up to 8192 tokens, 4 heads of 128, 258 MB with
 // MXFP8 in 48 us (82 % of a plain copy's rate; 59 with a look-up for each unit), 218 MB
-// with NVFP4 in 42 us.  The writer of NVFP4 is bound by the quantizer's arithmetic (4/6
-// tries two scales), as the tensor quantizer is: 17000 tokens of 8 heads in about 36 us
-// (4/6), 25 (RTN); MXFP8 21 us.
+// with NVFP4 in 42 us.  The writer of NVFP4 waits for itself: a thread has a block of 16
+// and, with 4/6, two scales for it, and a quarter of the SM's warps are not enough to hide that
+// chain (issue slots 53 % full).  17000 tokens of 8 heads take about 36 us (4/6), 25 (RTN);
+// MXFP8 21 us.
 #include "mx_block.cuh"
 #include "mxq_cache.cuh"
 #include "mxq_internal.h"
