@@ -20,11 +20,11 @@ namespace {
 // Sequences of up to kSomeRows rows are attention_rows.cu's; of MXFP8, where there are many
 // keys, up to kFewRows: its 16 rows a tile decode a key again for every tile, while
 // attention_tiles.cu takes 30 us to begin.  Measured, rows against tiles, 2 key/value heads.
-// 64 sequences of up to 4096 with 32 rows: MXFP8 45 against 66 us (heads of 128), 83 against
-// 113 (256); NVFP4 42 against 61, 58 against 100.  With 64 rows: MXFP8 70 against 73, 150
-// against 123 (16 of 16384: 58 against 54, 109 against 88); NVFP4 63 against 69, 97 against
-// 110.  8 of up to 500 with 64 rows (8192 keys times heads) 10 against 39, one of 30000
-// (61440) 34 against 30.
+// 64 sequences of up to 4096 with 32 rows: MXFP8 40 against 53 us (heads of 128), 72 against
+// 89 (256); NVFP4 37 against 51, 52 against 71.  With 64 rows: MXFP8 59 against 58, 129
+// against 100 (16 of 16384: 47 against 48, 85 against 69); NVFP4 53 against 54, 82 against
+// 79.  8 of up to 500 with 64 rows (8192 keys times heads) 10 against 32, one of 30000
+// (61440) 36 against 32.
 constexpr uint32_t kFewRows = 32, kSomeRows = 64;
 constexpr uint64_t kFewKeys = 1u << 16;     // times heads, as the table's width bounds them
 constexpr uint32_t kMaxSms = 160;           // the division uses no more (workspace)
@@ -225,9 +225,9 @@ cudaError_t launch_attention(const AttentionCall &c, int fmt, int dim, cudaStrea
         const uint32_t most = std::max(many ? few_rows : a.max_new * a.group, 1u), rows_of = most <= 8u ? 8u : kFewTile;
         a.tiles = (most + rows_of - 1) / rows_of;
         // A tile's start costs a CTA about as much as 8 steps (its queries, the first copies,
-        // the join of its warps).  Measured without and with: 64 sequences of up to 32768 67.3 and
-        // 65.8 us, 64 of up to 4096 with 32 rows of 256 77 and 61; one sequence of 65536, with
-        // few tiles to the CTAs, 27.3 and 28.
+        // the join of its warps).  Measured without and with: 64 sequences of up to 32768 69.3 and
+        // 66.6 us, 64 of up to 4096 with 32 rows of 256 90 and 72; one sequence of 65536, with
+        // few tiles to the CTAs, 28.2 and 28.2.
         a.extra = (uint64_t)c.c.seqs * c.c.heads * a.tiles * 16u >= ctas ? 8u : 0u;
         uint32_t n = 0;         // at most kFewCtas
         e = launch_attention_rows(a, fmt, dim, rows_of, ctas, (uint64_t)c.c.width << c.c.page_log, n, s);

@@ -22,7 +22,7 @@
 // TB/s, 75 % of the measured copy rate), NVFP4 63 us, heads of 64 57 us, 32 sequences with
 // heads of 256 73 us; with keys as right operands and rows as 16 left ones MXFP8 took 98 us.
 // 12 of up to 16384, heads of 256, 4 tokens each (two tiles of 16 rows), NVFP4: 41 us.  One
-// sequence of 5000: 11 us, 21 us without clusters; beyond 8 turns a warp the division
+// sequence of 5000: 11 us, 17 us without clusters; beyond 8 turns a warp the division
 // wins (12 of 16384 as above by clusters 120 us, divided 59 then).  Two warps to a turn, each
 // with half of its keys' scores and half of the columns, so that 32 rows fit: 59 us for
 // the 12 of 16384 against 46, the barrier of a turn costs more than a second decoding.
