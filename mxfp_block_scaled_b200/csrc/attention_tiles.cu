@@ -33,15 +33,16 @@
 // score in fp32 and a rounding to f16.  A chunk of 4096 tokens over 20480 of 32 query and
 // 4 key/value heads of 128 takes 1.35 ms (916 TFLOP/s, 56 % of the measured rate of a
 // bf16 product; NVFP4 1.28 ms; heads of 64 1.25 ms, of 256 half the chunk over 10240
-// 0.91 ms).  Each is busy for 42 to 44 % of that: a step takes 2500 cycles, in a group's chain from
-// scores to weights and products issued one behind the other.  Steps that brought it there: 2.46 ms with one warp that issued for all and
-// steps of 128 keys; 1.71 with products issued by the groups; 1.54 with steps of 64 keys and
-// an issuing warp a group (a warp is held while its products queue); 1.49 with fewer waits
-// between weights and scores; 1.26 with one copy of each loop and the division of the work
-// out of line (a launch begins with cold instruction caches); scores rounded before the
-// reference is subtracted and references of the values brought it back to 1.35.  A polynomial in place of
-// part of the exponentials, other shares of registers, and softmax threads that share a
-// row were slower or no faster.
+// 0.91 ms).  Each is busy for 42 to 44 % of that: a step takes 2500 cycles, in a group's
+// chain from scores to weights and products issued one behind the other.  Steps that
+// brought it there: 2.46 ms with one warp that issued for all and steps of 128 keys; 1.71
+// with products issued by the groups; 1.54 with steps of 64 keys and an issuing warp a group
+// (a warp is held while its products queue); 1.49 with fewer waits between weights and
+// scores; 1.26 with one copy of each loop and the division of the work out of line (a launch
+// begins with cold instruction caches); scores rounded before the reference is subtracted
+// and references of the values brought it back to 1.35.  A polynomial in place of part of the
+// exponentials, other shares of registers, and softmax threads that share a row were slower
+// or no faster.
 //
 // Every wait is bounded (MXQ_DEV_WAIT_TIMEOUT); all roles then leave, the issuing
 // ones behind their last product.
